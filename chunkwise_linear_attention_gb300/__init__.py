@@ -6,8 +6,10 @@ shared library has not been built the import of a function fails loudly;
 there is no CPU fallback.
 
 All tensors must be CUDA tensors, contiguous, with the dtype the C ABI names
-(float32, or bfloat16 passed as its bit pattern).  Outputs and the workspace
-are allocated with torch when not supplied.
+(float32, or bfloat16 passed as its bit pattern; float16 too where an entry
+point takes a dtype).  The window_attn_* tensors may be strided over batch,
+heads and tokens.  Outputs and the workspace are allocated with torch when not
+supplied.
 """
 from __future__ import annotations
 
@@ -43,6 +45,7 @@ def lib():
                     "(needs nvcc); there is no fallback implementation")
             L = ctypes.CDLL(LIB_PATH)
             P, I64, SZ, INT = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+            F = ctypes.c_float
             sig = {
                 "cla_status_string": ([INT], ctypes.c_char_p),
                 "cla_last_error_message": ([], ctypes.c_char_p),
@@ -80,6 +83,17 @@ def lib():
                 "cla_delta_fwd_ckpt": ([P] * 9 + [I64] * 5 + [INT, P, SZ, P], INT),
                 "cla_delta_bwd_ckpt": ([P] * 15 + [I64] * 5 + [INT, P, SZ, P], INT),
                 "cla_state_compose": ([P] * 4 + [I64] * 7 + [P], INT),
+                "cla_gated_scan_ckpt_elems": ([I64, I64, I64], SZ),
+                "cla_gated_scan_workspace_size": ([I64, I64, I64], SZ),
+                "cla_gated_scan_fwd": ([P] * 10 + [F, INT] + [I64] * 3 + [P, SZ, P], INT),
+                "cla_gated_scan_bwd": ([P] * 15 + [F, INT] + [I64] * 3 + [P, SZ, P], INT),
+                "cla_gated_scan_step": ([P] * 7 + [F, INT, I64, I64, P], INT),
+                "cla_window_attn_fwd": ([P] * 6 + [F, I64, I64, INT] + [I64] * 5 + [P, P], INT),
+                "cla_window_attn_bwd_workspace_size": ([I64] * 7, SZ),
+                "cla_window_attn_bwd": ([P] * 10 + [F, I64, I64, INT] + [I64] * 5 + [P, P, SZ, P], INT),
+                "cla_window_cache_write": ([P] * 5 + [I64, I64, INT] + [I64] * 4 + [P, P], INT),
+                "cla_window_attn_step_workspace_size": ([I64] * 6, SZ),
+                "cla_window_attn_step": ([P] * 7 + [F, I64, I64, INT] + [I64] * 4 + [P, P, SZ, P], INT),
             }
             for name, (args, res) in sig.items():
                 f = getattr(L, name)
@@ -122,10 +136,10 @@ class _T:
     """A tensor argument of an entry point (None stays NULL), checked by _launch for what the
     C ABI cannot check: dtype and shape (the sizes the call passes), then device and layout."""
 
-    __slots__ = ("t", "dtype", "name", "shape")
+    __slots__ = ("t", "dtype", "name", "shape", "strided")
 
-    def __init__(self, t, dtype, name, shape=None):
-        self.t, self.dtype, self.name, self.shape = t, dtype, name, shape
+    def __init__(self, t, dtype, name, shape=None, strided=False):
+        self.t, self.dtype, self.name, self.shape, self.strided = t, dtype, name, shape, strided
 
     def check_meta(self):
         t = self.t
@@ -140,7 +154,10 @@ class _T:
             raise ValueError(f"{self.name} must be a CUDA tensor")
         if t.device != device:
             raise ValueError(f"{self.name} is on {t.device}, the call's first tensor on {device}")
-        if not t.is_contiguous():
+        if self.strided:  # the entry point takes the outer strides
+            if t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{self.name} must be contiguous in its last dimension")
+        elif not t.is_contiguous():
             raise ValueError(f"{self.name} must be contiguous")
 
 
@@ -591,3 +608,187 @@ def delta_bwd(q, k, v, log_decay, beta, S0, dO, dST=None, *, chunk=64, dq=None, 
     else:
         _launch("cla_delta_bwd_ckpt", dev, args + (_delta_ckpt_arg(ckpt, B, H, T, dkk, dvv, chunk),) + tail, stream)
     return dq, dk, dv, dlog_decay, dbeta, dS0
+
+
+# ---------------------------------------------------------------- gated scan
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _dtype_code(t, name, allowed):
+    if t.dtype not in allowed:
+        raise ValueError(f"{name} must be one of {', '.join(map(str, allowed))}, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _reset_arg(reset, shape):
+    """A reset mask: bool or uint8 (the C ABI reads bytes)."""
+    return _T(reset, torch.bool if reset is not None and reset.dtype == torch.bool else torch.uint8, "reset", shape)
+
+
+def gated_scan_workspace_size(B, T, D) -> int:
+    return int(lib().cla_gated_scan_workspace_size(B, T, D))
+
+
+def gated_scan_ckpt_elems(B, T, D) -> int:
+    return int(lib().cla_gated_scan_ckpt_elems(B, T, D))
+
+
+def gated_scan_ckpt(x):
+    """A device buffer (fp32) for the checkpoint of a gated_scan_fwd on x [B, T, D]."""
+    return torch.empty(max(gated_scan_ckpt_elems(*_dims(x, 3, "x")), 1), dtype=torch.float32, device=x.device)
+
+
+def _gated_ckpt_arg(ckpt, B, T, D):
+    need = gated_scan_ckpt_elems(B, T, D)
+    if ckpt is not None and ckpt.numel() < need:
+        raise ValueError(f"ckpt: need at least {need} fp32 values, got {ckpt.numel()}")
+    return _T(ckpt, torch.float32, "ckpt")
+
+
+def gated_scan_fwd(x, rgate, igate, lam, h0=None, *, reset=None, lens=None, c=8.0, h=None, hT=None, ckpt=None,
+                   workspace=None, stream=None):
+    """h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(igate_t) x_t with a = exp(-c softplus(lam) sigmoid(rgate)) over axis 1
+    of [B, T, D] (fp32, bf16 or fp16); returns (h, hT).  reset [B, T]: tokens that start afresh; lens [B] int32: lengths
+    of a right-padded batch.  With ckpt (see gated_scan_ckpt) it also saves states for gated_scan_bwd."""
+    B, T, D = _dims(x, 3, "x")
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    code = _dtype_code(x, "x", _DTYPES)
+    h = _out(h, (B, T, D), dt, dev)
+    hT = _out(hT, (B, D), f32, dev)
+    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace)
+    bt, bd = (B, T, D), (B, D)
+    _launch("cla_gated_scan_fwd", dev, (
+        _T(x, dt, "x", bt), _T(rgate, dt, "rgate", bt), _T(igate, dt, "igate", bt), _T(lam, f32, "lam", (D,)),
+        _T(h0, f32, "h0", bd), _reset_arg(reset, (B, T)), _T(lens, torch.int32, "lens", (B,)), _T(h, dt, "h", bt),
+        _T(hT, f32, "hT", bd), _gated_ckpt_arg(ckpt, B, T, D), float(c), code, B, T, D,
+        _T(ws, None, "workspace"), _nbytes(ws)), stream)
+    return h, hT
+
+
+def gated_scan_bwd(x, rgate, igate, lam, h0, dh, dhT=None, *, reset=None, lens=None, c=8.0, dx=None, drgate=None,
+                   digate=None, dlam=None, dh0=None, ckpt=None, workspace=None, stream=None):
+    """Adjoint of gated_scan_fwd; returns (dx, drgate, digate, dlam, dh0).  ckpt: what a gated_scan_fwd on the same
+    inputs saved, or None to rebuild the states."""
+    B, T, D = _dims(x, 3, "x")
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    code = _dtype_code(x, "x", _DTYPES)
+    bt, bd = (B, T, D), (B, D)
+    dx, drgate, digate = (_out(t, bt, dt, dev) for t in (dx, drgate, digate))
+    dlam = _out(dlam, (D,), f32, dev)
+    dh0 = _out(dh0, bd, f32, dev)
+    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace)
+    _launch("cla_gated_scan_bwd", dev, (
+        _T(x, dt, "x", bt), _T(rgate, dt, "rgate", bt), _T(igate, dt, "igate", bt), _T(lam, f32, "lam", (D,)),
+        _T(h0, f32, "h0", bd), _reset_arg(reset, (B, T)), _T(lens, torch.int32, "lens", (B,)),
+        _gated_ckpt_arg(ckpt, B, T, D), _T(dh, dt, "dh", bt), _T(dhT, f32, "dhT", bd), _T(dx, dt, "dx", bt),
+        _T(drgate, dt, "drgate", bt), _T(digate, dt, "digate", bt), _T(dlam, f32, "dlam", (D,)),
+        _T(dh0, f32, "dh0", bd), float(c), code, B, T, D, _T(ws, None, "workspace"), _nbytes(ws)), stream)
+    return dx, drgate, digate, dlam, dh0
+
+
+def gated_scan_step(x, rgate, igate, lam, h, *, reset=None, c=8.0, y=None, stream=None):
+    """One token of gated_scan_fwd for each of B sequences ([B, D]); updates the state h [B, D] fp32 in place and
+    returns it rounded to x's dtype."""
+    B, D = _dims(x, 2, "x")
+    dt, dev, bd = x.dtype, x.device, (B, D)
+    code = _dtype_code(x, "x", _DTYPES)
+    y = _out(y, bd, dt, dev)
+    _launch("cla_gated_scan_step", dev, (
+        _T(x, dt, "x", bd), _T(rgate, dt, "rgate", bd), _T(igate, dt, "igate", bd), _T(lam, torch.float32, "lam", (D,)),
+        _reset_arg(reset, (B,)), _T(h, torch.float32, "h", bd), _T(y, dt, "y", bd), float(c), code, B, D), stream)
+    return y
+
+
+# ---------------------------------------------------------------- sliding-window attention with sinks
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _strides(*tensors):
+    """The tensors' outer strides as the C ABI takes them; None when all are dense."""
+    if all(t.is_contiguous() for t in tensors):
+        return None
+    flat = [s for t in tensors for s in t.stride()[:-1]]
+    return (ctypes.c_int64 * len(flat))(*flat)
+
+
+def _scale(scale, d):
+    return float(d) ** -0.5 if scale is None else float(scale)
+
+
+def window_attn_fwd(q, k, v, *, window, sinks=0, lens=None, scale=None, o=None, lse=None, stream=None):
+    """Softmax attention of token t over s <= t with t - s < window or s < sinks: q [B, H, T, d], k and v
+    [B, Hkv, T, d] (bf16 or fp16, d 64 or 128, H a multiple of Hkv; strided views are taken as they are).  lens [B]
+    int32: lengths of a right-padded batch.  scale: d ** -0.5 when None.  Returns (o, lse [B, H, T] fp32)."""
+    B, H, T, d = _dims(q, 4, "q")
+    Hkv = _dims(k, 4, "k")[1]
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q, "q", _HALF)
+    o = _out(o, (B, H, T, d), dt, dev)
+    lse = _out(lse, (B, H, T), torch.float32, dev)
+    hs, ks = (B, H, T, d), (B, Hkv, T, d)
+    _launch("cla_window_attn_fwd", dev, (
+        _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True),
+        _T(lens, torch.int32, "lens", (B,)), _T(o, dt, "o", hs, True), _T(lse, torch.float32, "lse", (B, H, T)),
+        _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, T, d, _strides(q, k, v, o)), stream)
+    return o, lse
+
+
+def window_attn_bwd_workspace_size(B, H, Hkv, T, d, window, sinks=0) -> int:
+    return int(lib().cla_window_attn_bwd_workspace_size(B, H, Hkv, T, d, int(window), int(sinks)))
+
+
+def window_attn_bwd(q, k, v, o, lse, dO, *, window, sinks=0, lens=None, scale=None, dq=None, dk=None, dv=None,
+                    workspace=None, stream=None):
+    """Adjoint of window_attn_fwd from its outputs (o, lse) and dO; returns (dq, dk, dv)."""
+    B, H, T, d = _dims(q, 4, "q")
+    Hkv = _dims(k, 4, "k")[1]
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q, "q", _HALF)
+    hs, ks = (B, H, T, d), (B, Hkv, T, d)
+    dq = _out(dq, hs, dt, dev)
+    dk, dv = _out(dk, ks, dt, dev), _out(dv, ks, dt, dev)
+    ws = _ws(window_attn_bwd_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace)
+    _launch("cla_window_attn_bwd", dev, (
+        _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True),
+        _T(lens, torch.int32, "lens", (B,)), _T(o, dt, "o", hs, True), _T(lse, torch.float32, "lse", (B, H, T)),
+        _T(dO, dt, "dO", hs, True), _T(dq, dt, "dq", hs, True), _T(dk, dt, "dk", ks, True), _T(dv, dt, "dv", ks, True),
+        _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, T, d, _strides(q, k, v, o, dO, dq, dk, dv),
+        _T(ws, None, "workspace"), _nbytes(ws)), stream)
+    return dq, dk, dv
+
+
+def window_cache_write(k, v, kcache, vcache, *, window, sinks=0, lens=None, stream=None):
+    """Writes the prompts' keys and values ([B, Hkv, T, d], from position 0) into the rolling cache
+    [B, Hkv, sinks + window, d] that window_attn_step reads: token p in slot p while p < sinks, else in slot
+    sinks + (p - sinks) % window, the last one that falls on a slot; slots without one stay as they were."""
+    B, Hkv, T, d = _dims(k, 4, "k")
+    dev, dt = k.device, k.dtype
+    code = _dtype_code(k, "k", _HALF)
+    ks, cs = (B, Hkv, T, d), (B, Hkv, int(sinks) + int(window), d)
+    _launch("cla_window_cache_write", dev, (
+        _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True), _T(lens, torch.int32, "lens", (B,)),
+        _T(kcache, dt, "kcache", cs), _T(vcache, dt, "vcache", cs), int(window), int(sinks), code, B, Hkv, T, d,
+        _strides(k, v)), stream)
+
+
+def window_attn_step_workspace_size(B, H, Hkv, d, window, sinks=0) -> int:
+    return int(lib().cla_window_attn_step_workspace_size(B, H, Hkv, d, int(window), int(sinks)))
+
+
+def window_attn_step(q, k, v, kcache, vcache, pos, *, window, sinks=0, scale=None, o=None, workspace=None, stream=None):
+    """One token for each of B sequences: writes k and v [B, Hkv, d] into the rolling cache (see window_cache_write) and
+    returns the attention of q [B, H, d] over what it then holds.  pos [B] int32: tokens before this one; negative: a
+    row without a sequence (o is 0, its cache is left alone)."""
+    B, H, d = _dims(q, 3, "q")
+    Hkv = _dims(k, 3, "k")[1]
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q, "q", _HALF)
+    o = _out(o, (B, H, d), dt, dev)
+    cs = (B, Hkv, int(sinks) + int(window), d)
+    ws = _ws(window_attn_step_workspace_size(B, H, Hkv, d, window, sinks), dev, workspace)
+    _launch("cla_window_attn_step", dev, (
+        _T(q, dt, "q", (B, H, d), True), _T(k, dt, "k", (B, Hkv, d), True), _T(v, dt, "v", (B, Hkv, d), True),
+        _T(kcache, dt, "kcache", cs), _T(vcache, dt, "vcache", cs), _T(pos, torch.int32, "pos", (B,)),
+        _T(o, dt, "o", (B, H, d)), _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, d, _strides(q, k, v),
+        _T(ws, None, "workspace"), _nbytes(ws)), stream)
+    return o

@@ -581,6 +581,161 @@ int cla_state_compose(const float *alpha, const float *dS, const float *edge,
                       float *out, int64_t P, int64_t BH, int64_t n, int64_t A,
                       int64_t first, int64_t count, int64_t step, void *stream);
 
+/* ======================================================================== */
+/* Gated scan (gates formed inside)                                         */
+/* ======================================================================== */
+
+/* Element types of the entry points below that take a `dtype`. */
+typedef enum { CLA_F32 = 0, CLA_BF16 = 1, CLA_F16 = 2 } cla_dtype;
+
+/* Time steps between the states the forward saves for the backward. */
+#define CLA_GATED_SCAN_CKPT_CHUNK 64
+
+/* Elements (fp32) of the checkpoint [B, ceil(T/64), D]. */
+size_t cla_gated_scan_ckpt_elems(int64_t B, int64_t T, int64_t D);
+
+/* Bytes of workspace for cla_gated_scan_fwd / _bwd. */
+size_t cla_gated_scan_workspace_size(int64_t B, int64_t T, int64_t D);
+
+/* Forward of the diagonal recurrence whose decays and inputs come from gates:
+ *   r = sigmoid(rgate), i = sigmoid(igate), L = -c softplus(lam) r, a = e^L,
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t.
+ *   x, rgate, igate [B, T, D] dtype
+ *   lam    [D]    fp32
+ *   h0     [B, D] fp32 [opt] initial state (NULL = 0)
+ *   reset  [B, T] bytes [opt]: nonzero starts afresh there, h_t = i_t x_t (the
+ *          first token of each document of a packed sequence).  Nothing before
+ *          it reaches the states from it on, infinities and NaN included.
+ *   lens   [B]    int32 [opt]: tokens of each sequence of a right-padded batch
+ *          (clamped to [0, T]); behind them h is 0, the state is kept and the
+ *          inputs are not used
+ *   h      [B, T, D] dtype out: the states, rounded to dtype (kept in fp32
+ *          inside)
+ *   hT     [B, D] fp32 [opt] out: the state after the last token
+ *   ckpt   [B, ceil(T/64), D] fp32 [opt] out: the state entering every 64-step
+ *          chunk, for the backward
+ *   c      a positive finite number; the decay of a fully open gate is
+ *          exp(-c softplus(lam)); decays below 2^-126 count as 2^-126
+ * B * D must be below 2^31. */
+int cla_gated_scan_fwd(const void *x, const void *rgate, const void *igate,
+                       const float *lam, const float *h0, const uint8_t *reset,
+                       const int32_t *lens, void *h, float *hT, float *ckpt,
+                       float c, int dtype, int64_t B, int64_t T, int64_t D,
+                       void *ws, size_t ws_bytes, void *stream);
+
+/* Backward: gradients on everything the forward read, from dh (dtype) and dhT.
+ * The states are rebuilt from `ckpt`, or, when it is NULL, from a forward scan
+ * into the workspace.
+ *   dh     [B, T, D] dtype;  dhT [B, D] fp32 [opt]
+ *   dx, drgate, digate [B, T, D] dtype out, 0 behind a sequence's length
+ *   dlam   [D] fp32 [opt] out, summed in a fixed order
+ *   dh0    [B, D] fp32 [opt] out
+ * The other arguments are the forward's. */
+int cla_gated_scan_bwd(const void *x, const void *rgate, const void *igate,
+                       const float *lam, const float *h0, const uint8_t *reset,
+                       const int32_t *lens, const float *ckpt, const void *dh,
+                       const float *dhT, void *dx, void *drgate, void *digate,
+                       float *dlam, float *dh0, float c, int dtype, int64_t B,
+                       int64_t T, int64_t D, void *ws, size_t ws_bytes,
+                       void *stream);
+
+/* One token of the recurrence for each of B sequences.
+ *   x, rgate, igate [B, D] dtype;  lam [D] fp32;  reset [B] bytes [opt]
+ *   h      [B, D] fp32 in and out: the state
+ *   y      [B, D] dtype out: the new state, rounded */
+int cla_gated_scan_step(const void *x, const void *rgate, const void *igate,
+                        const float *lam, const uint8_t *reset, float *h, void *y,
+                        float c, int dtype, int64_t B, int64_t D, void *stream);
+
+/* ======================================================================== */
+/* Sliding-window attention with sinks                                      */
+/* ======================================================================== */
+
+/* Softmax attention for the layers a stack of recurrent layers is interleaved
+ * with.  Token t sees s <= t where t - s < window or s < sinks.  H query heads
+ * share Hkv key heads, H a multiple of Hkv: query head h reads key head
+ * h / (H / Hkv).
+ *
+ * Strides: `strides` points at one {batch, head, token} triple of element
+ * strides (host memory, int64) per [B, heads, T, d] tensor, in the order of the
+ * arguments; NULL means all are dense.  The last dimension is dense always.  A
+ * stride of a dimension longer than 1 must be positive, and of a 16-byte
+ * multiple; the tensors of one call must not overlap its outputs.
+ *
+ * Forward:
+ *   q      [B, H, T, d] dtype (bf16 or fp16);  k, v [B, Hkv, T, d] dtype
+ *   lens   [B] int32 [opt]: tokens of each sequence of a right-padded batch
+ *          (clamped to [0, T]); behind them o is 0 and lse is -inf, and what
+ *          q, k and v hold there is not used, NaN included.  Within a sequence
+ *          v and k must be finite: an infinity or NaN may reach rows that do
+ *          not see its token.
+ *   o      [B, H, T, d] dtype out
+ *   lse    [B, H, T] fp32 out: log of the sum of exponentials of the scaled
+ *          logits, natural base (dense)
+ *   scale  the logits' factor, a finite number
+ *   strides [opt]: of q, k, v, o
+ * d in {64, 128}; window >= 1; sinks >= 0. */
+int cla_window_attn_fwd(const void *q, const void *k, const void *v,
+                        const int32_t *lens, void *o, float *lse, float scale,
+                        int64_t window, int64_t sinks, int dtype, int64_t B,
+                        int64_t H, int64_t Hkv, int64_t T, int64_t d,
+                        const int64_t *strides, void *stream);
+
+/* Bytes of workspace for cla_window_attn_bwd. */
+size_t cla_window_attn_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv,
+                                          int64_t T, int64_t d, int64_t window,
+                                          int64_t sinks);
+
+/* Backward: with P = exp(scale q k^T - lse) and dS = P (dO v^T - rowsum(dO o)),
+ * dq = scale dS k, dk = scale dS^T q, dv = P^T dO, the gradients of a shared
+ * key head summed over its query heads in a fixed order (no float atomics).
+ *   o, lse as the forward returned them;  dO [B, H, T, d] dtype
+ *   dq     [B, H, T, d] dtype out;  dk, dv [B, Hkv, T, d] dtype out; all 0
+ *          behind a sequence's length
+ *   strides [opt]: of q, k, v, o, dO, dq, dk, dv */
+int cla_window_attn_bwd(const void *q, const void *k, const void *v,
+                        const int32_t *lens, const void *o, const float *lse,
+                        const void *dO, void *dq, void *dk, void *dv, float scale,
+                        int64_t window, int64_t sinks, int dtype, int64_t B,
+                        int64_t H, int64_t Hkv, int64_t T, int64_t d,
+                        const int64_t *strides, void *ws, size_t ws_bytes,
+                        void *stream);
+
+/* The cache of such a layer holds sinks + window slots per sequence and key
+ * head: token p in slot p while p < sinks, else in slot
+ * sinks + (p - sinks) mod window, over the token that left the window.
+ *
+ * Writes the tokens of prompts that start at position 0 into it: of each slot
+ * the last token that falls on it.  Slots that no token reaches are left as
+ * they were.
+ *   k, v   [B, Hkv, T, d] dtype;  lens as above
+ *   kcache, vcache [B, Hkv, sinks + window, d] dtype, dense, in and out
+ *   strides [opt]: of k, v */
+int cla_window_cache_write(const void *k, const void *v, const int32_t *lens,
+                           void *kcache, void *vcache, int64_t window,
+                           int64_t sinks, int dtype, int64_t B, int64_t Hkv,
+                           int64_t T, int64_t d, const int64_t *strides,
+                           void *stream);
+
+/* Bytes of workspace for cla_window_attn_step. */
+size_t cla_window_attn_step_workspace_size(int64_t B, int64_t H, int64_t Hkv,
+                                           int64_t d, int64_t window, int64_t sinks);
+
+/* One token for each of B sequences: writes its key and value into the cache
+ * and attends over what the cache then holds.
+ *   q      [B, H, d];  k, v [B, Hkv, d] dtype
+ *   kcache, vcache as above, in and out
+ *   pos    [B] int32: tokens of the sequence before this one, its position.  A
+ *          negative entry marks a row without a sequence: its o is 0 and its
+ *          cache is left alone.
+ *   o      [B, H, d] dtype out, dense
+ *   strides [opt]: {batch, head} pairs of q, k, v, under the rules above */
+int cla_window_attn_step(const void *q, const void *k, const void *v, void *kcache,
+                         void *vcache, const int32_t *pos, void *o, float scale,
+                         int64_t window, int64_t sinks, int dtype, int64_t B,
+                         int64_t H, int64_t Hkv, int64_t d, const int64_t *strides,
+                         void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
