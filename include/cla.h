@@ -589,9 +589,9 @@ int cla_state_compose(const float *alpha, const float *dS, const float *edge,
 typedef enum { CLA_F32 = 0, CLA_BF16 = 1, CLA_F16 = 2 } cla_dtype;
 
 /* Time steps between the states the forward saves for the backward. */
-#define CLA_GATED_SCAN_CKPT_CHUNK 64
+#define CLA_GATED_SCAN_CKPT_CHUNK 32
 
-/* Elements (fp32) of the checkpoint [B, ceil(T/64), D]. */
+/* Elements (fp32) of the checkpoint [B, ceil(T/32), D]. */
 size_t cla_gated_scan_ckpt_elems(int64_t B, int64_t T, int64_t D);
 
 /* Bytes of workspace for cla_gated_scan_fwd / _bwd. */
@@ -612,11 +612,11 @@ size_t cla_gated_scan_workspace_size(int64_t B, int64_t T, int64_t D);
  *   h      [B, T, D] dtype out: the states, rounded to dtype (kept in fp32
  *          inside)
  *   hT     [B, D] fp32 [opt] out: the state after the last token
- *   ckpt   [B, ceil(T/64), D] fp32 [opt] out: the state entering every 64-step
+ *   ckpt   [B, ceil(T/32), D] fp32 [opt] out: the state entering every 32-step
  *          chunk, for the backward
  *   c      a positive finite number; the decay of a fully open gate is
  *          exp(-c softplus(lam)); decays below 2^-126 count as 2^-126
- * B * D must be below 2^31. */
+ * B * D must be below 2^31, B * T * D below 10^12. */
 int cla_gated_scan_fwd(const void *x, const void *rgate, const void *igate,
                        const float *lam, const float *h0, const uint8_t *reset,
                        const int32_t *lens, void *h, float *hT, float *ckpt,

@@ -52,7 +52,7 @@ def test_gated_scan_pointers(lib):
 
 
 def test_gated_scan_sizes(lib):
-    assert lib.cla_gated_scan_ckpt_elems(3, 129, 10) == 3 * 3 * 10
+    assert lib.cla_gated_scan_ckpt_elems(3, 129, 10) == 3 * 5 * 10
     assert lib.cla_gated_scan_ckpt_elems(3, 0, 10) == 0 and lib.cla_gated_scan_ckpt_elems(-1, 5, 5) == 0
     assert lib.cla_gated_scan_workspace_size(2, 100, 64) >= 256 and lib.cla_gated_scan_workspace_size(2, -1, 64) == 0
 
