@@ -88,7 +88,8 @@ def lib():
                 "cla_gated_scan_fwd": ([P] * 10 + [F, INT] + [I64] * 3 + [P, SZ, P], INT),
                 "cla_gated_scan_bwd": ([P] * 15 + [F, INT] + [I64] * 3 + [P, SZ, P], INT),
                 "cla_gated_scan_step": ([P] * 7 + [F, INT, I64, I64, P], INT),
-                "cla_window_attn_fwd": ([P] * 6 + [F, I64, I64, INT] + [I64] * 5 + [P, P], INT),
+                "cla_window_attn_workspace_size": ([I64] * 7, SZ),
+                "cla_window_attn_fwd": ([P] * 6 + [F, I64, I64, INT] + [I64] * 5 + [P, P, SZ, P], INT),
                 "cla_window_attn_bwd_workspace_size": ([I64] * 7, SZ),
                 "cla_window_attn_bwd": ([P] * 10 + [F, I64, I64, INT] + [I64] * 5 + [P, P, SZ, P], INT),
                 "cla_window_cache_write": ([P] * 5 + [I64, I64, INT] + [I64] * 4 + [P, P], INT),
@@ -715,7 +716,11 @@ def _scale(scale, d):
     return float(d) ** -0.5 if scale is None else float(scale)
 
 
-def window_attn_fwd(q, k, v, *, window, sinks=0, lens=None, scale=None, o=None, lse=None, stream=None):
+def window_attn_workspace_size(B, H, Hkv, T, d, window, sinks=0) -> int:
+    return int(lib().cla_window_attn_workspace_size(B, H, Hkv, T, d, int(window), int(sinks)))
+
+
+def window_attn_fwd(q, k, v, *, window, sinks=0, lens=None, scale=None, o=None, lse=None, workspace=None, stream=None):
     """Softmax attention of token t over s <= t with t - s < window or s < sinks: q [B, H, T, d], k and v
     [B, Hkv, T, d] (bf16 or fp16, d 64 or 128, H a multiple of Hkv; strided views are taken as they are).  lens [B]
     int32: lengths of a right-padded batch.  scale: d ** -0.5 when None.  Returns (o, lse [B, H, T] fp32)."""
@@ -725,11 +730,13 @@ def window_attn_fwd(q, k, v, *, window, sinks=0, lens=None, scale=None, o=None, 
     code = _dtype_code(q, "q", _HALF)
     o = _out(o, (B, H, T, d), dt, dev)
     lse = _out(lse, (B, H, T), torch.float32, dev)
+    ws = _ws(window_attn_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace)
     hs, ks = (B, H, T, d), (B, Hkv, T, d)
     _launch("cla_window_attn_fwd", dev, (
         _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True),
         _T(lens, torch.int32, "lens", (B,)), _T(o, dt, "o", hs, True), _T(lse, torch.float32, "lse", (B, H, T)),
-        _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, T, d, _strides(q, k, v, o)), stream)
+        _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, T, d, _strides(q, k, v, o),
+        _T(ws, None, "workspace"), _nbytes(ws)), stream)
     return o, lse
 
 

@@ -9,32 +9,15 @@
 // dS = P (dO v^T - delta), delta_t = dO_t . o_t, dq = scale dS k,
 // dk = scale dS^T q, dv = P^T dO.
 //
-// One warp walks the visible tokens of one row (forward, dq) or the tokens
-// that see one key (dk, dv); a lane holds d / 32 columns.
+// Forward and backward run on the tensor cores (window_attn_tc.cuh).
 #include <math.h>
 
 #include "cla_internal.cuh"
 #include "elem_io.cuh"
+#include "window_attn_tc.cuh"
 
 namespace cla {
 namespace {
-
-struct Str3 {
-    long long b, h, t;
-};
-
-struct WaArgs {
-    const int32_t *lens;
-    float scale;
-    long long T, window, sinks;
-    int B, H, Hkv;
-};
-
-__device__ __forceinline__ long long wa_len(const WaArgs &g, int b) {
-    if (g.lens == nullptr) return g.T;
-    const long long n = g.lens[b];
-    return n < 0 ? 0 : (n > g.T ? g.T : n);
-}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -60,101 +43,6 @@ __device__ __forceinline__ float dot(const float (&a)[N], const float (&b)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) s = fmaf(a[i], b[i], s);
     return warp_sum(s);
-}
-
-template <typename E, int N>
-__global__ void wa_fwd_kernel(const E *q, const E *k, const E *v, E *o, float *lse, Str3 sq, Str3 sk, Str3 sv, Str3 so,
-                              WaArgs g) {
-    const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (row >= (long long)g.B * g.H * g.T) return;
-    const long long t = row % g.T;
-    const int h = (int)(row / g.T % g.H), b = (int)(row / g.T / g.H), hk = h / (g.H / g.Hkv);
-    float acc[N], qv[N], kv[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    if (t < wa_len(g, b)) {
-        row_ld(q + b * sq.b + h * sq.h + t * sq.t, qv);
-        const long long lo = t - g.window + 1 > 0 ? t - g.window + 1 : 0;
-        for (long long s = 0; s <= t; s = (s + 1 >= g.sinks && s + 1 < lo) ? lo : s + 1) {
-            if (s < lo && s >= g.sinks) continue;
-            row_ld(k + b * sk.b + hk * sk.h + s * sk.t, kv);
-            const float x = dot(qv, kv) * g.scale;
-            const float mn = fmaxf(m, x), f = expf(m - mn), p = expf(x - mn);
-            row_ld(v + b * sv.b + hk * sv.h + s * sv.t, kv);
-            l = l * f + p;
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(p, kv[i], acc[i] * f);
-            m = mn;
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] /= l;
-    }
-    row_st(o + b * so.b + h * so.h + t * so.t, acc);
-    if ((threadIdx.x & 31) == 0) lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
-}
-
-template <typename E, int N>
-__global__ void wa_dq_kernel(const E *q, const E *k, const E *v, const E *o, const float *lse, const E *dO, E *dq,
-                             float *delta, Str3 sq, Str3 sk, Str3 sv, Str3 so, Str3 sd, Str3 sdq, WaArgs g) {
-    const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (row >= (long long)g.B * g.H * g.T) return;
-    const long long t = row % g.T;
-    const int h = (int)(row / g.T % g.H), b = (int)(row / g.T / g.H), hk = h / (g.H / g.Hkv);
-    float acc[N], qv[N], gv[N], kv[N], vv[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    if (t < wa_len(g, b)) {
-        row_ld(q + b * sq.b + h * sq.h + t * sq.t, qv);
-        row_ld(dO + b * sd.b + h * sd.h + t * sd.t, gv);
-        row_ld(o + b * so.b + h * so.h + t * so.t, vv);
-        const float dl = dot(gv, vv), e = lse[row];
-        if ((threadIdx.x & 31) == 0) delta[row] = dl;
-        const long long lo = t - g.window + 1 > 0 ? t - g.window + 1 : 0;
-        for (long long s = 0; s <= t; s = (s + 1 >= g.sinks && s + 1 < lo) ? lo : s + 1) {
-            if (s < lo && s >= g.sinks) continue;
-            row_ld(k + b * sk.b + hk * sk.h + s * sk.t, kv);
-            row_ld(v + b * sv.b + hk * sv.h + s * sv.t, vv);
-            const float p = expf(dot(qv, kv) * g.scale - e);
-            const float ds = p * (dot(gv, vv) - dl) * g.scale;
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(ds, kv[i], acc[i]);
-        }
-    }
-    row_st(dq + b * sdq.b + h * sdq.h + t * sdq.t, acc);
-}
-
-template <typename E, int N>
-__global__ void wa_dkv_kernel(const E *q, const E *k, const E *v, const float *lse, const float *delta, const E *dO,
-                              E *dk, E *dv, Str3 sq, Str3 sk, Str3 sv, Str3 sd, Str3 sdk, Str3 sdv, WaArgs g) {
-    const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (row >= (long long)g.B * g.Hkv * g.T) return;
-    const long long s = row % g.T;
-    const int hk = (int)(row / g.T % g.Hkv), b = (int)(row / g.T / g.Hkv), G = g.H / g.Hkv;
-    float ak[N], av[N], qv[N], gv[N], kv[N], vv[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) ak[i] = av[i] = 0.f;
-    const long long n = wa_len(g, b);
-    if (s < n) {
-        row_ld(k + b * sk.b + hk * sk.h + s * sk.t, kv);
-        row_ld(v + b * sv.b + hk * sv.h + s * sv.t, vv);
-        const long long end = s < g.sinks || g.window > n - s ? n : s + g.window;
-        for (int h = hk * G; h < (hk + 1) * G; ++h)
-            for (long long t = s; t < end; ++t) {
-                const long long at = ((long long)b * g.H + h) * g.T + t;
-                row_ld(q + b * sq.b + h * sq.h + t * sq.t, qv);
-                row_ld(dO + b * sd.b + h * sd.h + t * sd.t, gv);
-                const float p = expf(dot(qv, kv) * g.scale - lse[at]);
-                const float ds = p * (dot(gv, vv) - delta[at]) * g.scale;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    ak[i] = fmaf(ds, qv[i], ak[i]);
-                    av[i] = fmaf(p, gv[i], av[i]);
-                }
-            }
-    }
-    row_st(dk + b * sdk.b + hk * sdk.h + s * sdk.t, ak);
-    row_st(dv + b * sdv.b + hk * sdv.h + s * sdv.t, av);
 }
 
 // One 16-byte piece of a cache slot per thread.
@@ -226,7 +114,8 @@ int wa_check(const char *fn, int64_t B, int64_t H, int64_t Hkv, int64_t T, int64
     if (dtype != CLA_BF16 && dtype != CLA_F16) return fail(CLA_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
     if (d != 64 && d != 128) return fail(CLA_ERR_UNSUPPORTED, "%s: head dimension %lld", fn, (long long)d);
     if (!product_below({B, H}, 2147483648.0) || T > kMaxTokens || !product_below({B, H, T, d}, 1e15) ||
-        !product_below({B, Hkv, d, window}, 1e15) || !product_below({B, Hkv, d, sinks}, 1e15))
+        !product_below({B, H, T}, 128.0 * 2147483648.0) || !product_below({B, Hkv, d, window}, 1e15) ||
+        !product_below({B, Hkv, d, sinks}, 1e15))
         return fail(CLA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     return CLA_OK;
 }
@@ -241,8 +130,8 @@ int wa_strides(const char *fn, const int64_t *strides, const char *const *names,
         }
         const int64_t *s = strides + 3 * i, size[3] = {B, heads[i], T};
         for (int j = 0; j < 3; ++j)
-            if (size[j] > 1 && (s[j] <= 0 || s[j] % 8 != 0 || s[j] > (int64_t)1e15 / size[j]))
-                return fail(CLA_ERR_INVALID_ARG, "%s: stride %lld of %s: a positive multiple of 8 elements is needed", fn,
+            if (size[j] > 1 && (s[j] <= 0 || s[j] % 8 != 0 || s[j] >= (int64_t)1 << 39))
+                return fail(CLA_ERR_INVALID_ARG, "%s: stride %lld of %s: a positive multiple of 8 below 2^39 elements is needed", fn,
                             (long long)s[j], names[i]);
         out[i] = Str3{B > 1 ? s[0] : 0, heads[i] > 1 ? s[1] : 0, T > 1 ? s[2] : 0};
     }
@@ -250,6 +139,86 @@ int wa_strides(const char *fn, const int64_t *strides, const char *const *names,
 }
 
 unsigned warps_grid(long long warps) { return (unsigned)((warps + 3) / 4); }
+
+// Multiprocessors of the current device, asked for once per device.
+int wa_blocks(const char *fn, long long items, unsigned *blocks) {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    CLA_CUDA_TRY(cudaGetDevice(&dev), fn);
+    if (dev < 64) n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        CLA_CUDA_TRY(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev), fn);
+        if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    }
+    *blocks = (unsigned)(items < n ? items : n);
+    return CLA_OK;
+}
+
+long long wa_tiles(long long T) { return (T + kWT - 1) / kWT; }
+
+template <int D, bool BF>
+int wa_fwd(const char *fn, const WaMaps &m, void *o, float *lse, const Str3 &so, const WaArgs &g, WsHeader *hdr, cudaStream_t s) {
+    static std::atomic<unsigned long long> done{0};
+    constexpr int smem = FwdCfg<D>::SMEM > kMinSmem ? FwdCfg<D>::SMEM : kMinSmem;
+    const long long G = g.H / g.Hkv, tiles = wa_tiles(g.T);
+    const long long items = (long long)g.B * g.Hkv * (G % 2 == 0 ? G / 2 * tiles : G * ((tiles + 1) / 2));
+    unsigned blocks;
+    if (int st = set_max_dynamic_smem(done, (const void *)wa_fwd_kernel<D, BF>, smem)) return st;
+    if (int st = wa_blocks(fn, items, &blocks)) return st;
+    wa_fwd_kernel<D, BF><<<blocks, FwdCfg<D>::THREADS, smem, s>>>(m, o, lse, so, g, (int)items, hdr);
+    return check_launch(fn);
+}
+
+// Tiles with sinks are seen by every later query tile.  Their lists are cut into pieces of what a
+// tile without sinks has (at least 8), while there are few such tiles: 64 pieces a key head bound
+// the partial sums to 64 x 2 x 128 x d floats.
+DkvPlan wa_plan(int64_t H, int64_t Hkv, int64_t T, int64_t window, int64_t sinks) {
+    DkvPlan p{0, 1, 0, nullptr};
+    const long long G = Hkv ? H / Hkv : 0, tiles = wa_tiles(T), st = wa_tiles(sinks < T ? sinks : T);
+    const long long span = wa_tiles(window < T ? window : T) + 1, all = G * tiles;
+    long long piece = G * (span < tiles ? span : tiles);
+    if (piece < 8) piece = 8;
+    if (st == 0 || st > 16 || 2 * all <= 3 * piece) return p;
+    const long long most = 64 / st;
+    if ((all + piece - 1) / piece > most) piece = (all + most - 1) / most;
+    p.sink_tiles = (int)st;
+    p.piece = (int)piece;
+    p.pieces = (int)((all + piece - 1) / piece);
+    return p;
+}
+size_t wa_part_bytes(const DkvPlan &p, int64_t B, int64_t Hkv, int64_t d) {
+    return (size_t)(B * Hkv) * p.sink_tiles * p.pieces * 2 * kWT * d * 4;
+}
+
+template <int D, bool BF>
+int wa_bwd(const char *fn, const WaMaps &m, const void *o, const void *dO, const float *lse, void *dq, void *dk, void *dv,
+           const Str3 *r, const WaArgs &g, DkvPlan pl, void *ws, cudaStream_t s) {
+    static std::atomic<unsigned long long> done_q{0}, done_kv{0};
+    constexpr int smem_q = DqCfg<D>::SMEM > kMinSmem ? DqCfg<D>::SMEM : kMinSmem;
+    constexpr int smem_kv = DkvCfg<D>::SMEM > kMinSmem ? DkvCfg<D>::SMEM : kMinSmem;
+    char *p = static_cast<char *>(ws);
+    WsHeader *hdr = reinterpret_cast<WsHeader *>(p);
+    float *delta = reinterpret_cast<float *>(p + sizeof(WsHeader));
+    pl.part = reinterpret_cast<float *>(p + sizeof(WsHeader) + align_up((size_t)g.B * g.H * g.T * 4, 16));
+    if (int st = set_max_dynamic_smem(done_q, (const void *)wa_dq_kernel<D, BF>, smem_q)) return st;
+    if (int st = set_max_dynamic_smem(done_kv, (const void *)wa_dkv_kernel<D, BF>, smem_kv)) return st;
+    const long long tiles = wa_tiles(g.T);
+    long long items = (long long)g.B * g.H * tiles;
+    unsigned blocks;
+    if (int st = wa_blocks(fn, items, &blocks)) return st;
+    wa_dq_kernel<D, BF><<<blocks, DqCfg<D>::THREADS, smem_q, s>>>(m, o, dO, lse, dq, delta, r[3], r[4], r[5], g, (int)items, hdr);
+    if (int st = check_launch(fn)) return st;
+    items = (long long)g.B * g.Hkv * (tiles + (long long)pl.sink_tiles * (pl.pieces - 1));
+    if (int st = wa_blocks(fn, items, &blocks)) return st;
+    wa_dkv_kernel<D, BF><<<blocks, DkvCfg<D>::THREADS, smem_kv, s>>>(m, lse, delta, dk, dv, r[6], r[7], g, pl, (int)items, hdr);
+    if (int st = check_launch(fn)) return st;
+    if (pl.sink_tiles > 0) {
+        const long long n = (long long)g.B * g.Hkv * pl.sink_tiles * 2 * kWT * (D / 2);
+        wa_join_kernel<D, BF><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(dk, dv, r[6], r[7], g, pl);
+        return check_launch(fn);
+    }
+    return CLA_OK;
+}
 
 }  // namespace
 }  // namespace cla
@@ -272,29 +241,46 @@ using namespace cla;
 
 extern "C" int cla_window_attn_fwd(const void *q, const void *k, const void *v, const int32_t *lens, void *o, float *lse,
                                    float scale, int64_t window, int64_t sinks, int dtype, int64_t B, int64_t H,
-                                   int64_t Hkv, int64_t T, int64_t d, const int64_t *strides, void *stream) {
+                                   int64_t Hkv, int64_t T, int64_t d, const int64_t *strides, void *ws,
+                                   size_t ws_bytes, void *stream) {
     const char *fn = "cla_window_attn_fwd";
     clear_error();
     if (int st = wa_check(fn, B, H, Hkv, T, d, window, sinks, dtype, scale)) return st;
-    if (B * H * T == 0) return CLA_OK;
-    if (!q || !k || !v || !o || !lse) return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (B * H * T > 0 && (!q || !k || !v || !o || !lse)) return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned_or_null({q, k, v, o}, 16) || !aligned_or_null({lse, lens}, 4))
         return fail(CLA_ERR_INVALID_ARG, "%s: a pointer is misaligned", fn);
+    if (ws == nullptr || !aligned16(ws) || ws_bytes < sizeof(WsHeader))
+        return fail(CLA_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, sizeof(WsHeader));
     static const char *const names[] = {"q", "k", "v", "o"};
     const int64_t heads[] = {H, Hkv, Hkv, H};
     Str3 r[4];
     if (int st = wa_strides(fn, strides, names, heads, 4, B, T, d, r)) return st;
     const WaArgs g{lens, scale, T, window < T ? window : T, sinks < T ? sinks : T, (int)B, (int)H, (int)Hkv};
     cudaStream_t s = (cudaStream_t)stream;
-    WA_DISPATCH(wa_fwd_kernel, warps_grid(B * H * T), (const E *)q, (const E *)k, (const E *)v, (E *)o, lse, r[0], r[1],
-                r[2], r[3], g);
-    return CLA_OK;
+    WsHeader *hdr = static_cast<WsHeader *>(ws);
+    if (B * H * T == 0) {
+        CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(WsHeader), s), fn);
+        return CLA_OK;
+    }
+    const bool bf = dtype == CLA_BF16;
+    WaMaps m;
+    if (!make_map_bht(&m.q, q, bf, d, T, H, B, r[0]) || !make_map_bht(&m.k, k, bf, d, T, Hkv, B, r[1]) ||
+        !make_map_bht(&m.v, v, bf, d, T, Hkv, B, r[2]))
+        return fail(CLA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
+    m.g = m.q;
+    if (d == 128) return bf ? wa_fwd<128, true>(fn, m, o, lse, r[3], g, hdr, s) : wa_fwd<128, false>(fn, m, o, lse, r[3], g, hdr, s);
+    return bf ? wa_fwd<64, true>(fn, m, o, lse, r[3], g, hdr, s) : wa_fwd<64, false>(fn, m, o, lse, r[3], g, hdr, s);
+}
+
+extern "C" size_t cla_window_attn_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d, int64_t window,
+                                                 int64_t sinks) {
+    return wa_check("cla_window_attn_workspace_size", B, H, Hkv, T, d, window, sinks, CLA_BF16, 1.f) == CLA_OK ? sizeof(WsHeader) : 0;
 }
 
 extern "C" size_t cla_window_attn_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d,
                                                      int64_t window, int64_t sinks) {
     if (wa_check("cla_window_attn_bwd_workspace_size", B, H, Hkv, T, d, window, sinks, CLA_BF16, 1.f) != CLA_OK) return 0;
-    return sizeof(WsHeader) + align_up((size_t)(B * H * T) * 4, 16);
+    return sizeof(WsHeader) + align_up((size_t)(B * H * T) * 4, 16) + wa_part_bytes(wa_plan(H, Hkv, T, window, sinks), B, Hkv, d);
 }
 
 extern "C" int cla_window_attn_bwd(const void *q, const void *k, const void *v, const int32_t *lens, const void *o,
@@ -304,8 +290,7 @@ extern "C" int cla_window_attn_bwd(const void *q, const void *k, const void *v, 
     const char *fn = "cla_window_attn_bwd";
     clear_error();
     if (int st = wa_check(fn, B, H, Hkv, T, d, window, sinks, dtype, scale)) return st;
-    if (B * H * T == 0) return CLA_OK;
-    if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv)
+    if (B * H * T > 0 && (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv))
         return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned_or_null({q, k, v, o, dO, dq, dk, dv}, 16) || !aligned_or_null({lse, lens}, 4))
         return fail(CLA_ERR_INVALID_ARG, "%s: a pointer is misaligned", fn);
@@ -319,12 +304,18 @@ extern "C" int cla_window_attn_bwd(const void *q, const void *k, const void *v, 
     const WaArgs g{lens, scale, T, window < T ? window : T, sinks < T ? sinks : T, (int)B, (int)H, (int)Hkv};
     cudaStream_t s = (cudaStream_t)stream;
     CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(WsHeader), s), fn);
-    float *delta = reinterpret_cast<float *>(static_cast<char *>(ws) + sizeof(WsHeader));
-    WA_DISPATCH(wa_dq_kernel, warps_grid(B * H * T), (const E *)q, (const E *)k, (const E *)v, (const E *)o, lse,
-                (const E *)dO, (E *)dq, delta, r[0], r[1], r[2], r[3], r[4], r[5], g);
-    WA_DISPATCH(wa_dkv_kernel, warps_grid(B * Hkv * T), (const E *)q, (const E *)k, (const E *)v, lse, delta,
-                (const E *)dO, (E *)dk, (E *)dv, r[0], r[1], r[2], r[4], r[6], r[7], g);
-    return CLA_OK;
+    if (B * H * T == 0) return CLA_OK;
+    const bool bf = dtype == CLA_BF16;
+    WaMaps m;
+    if (!make_map_bht(&m.q, q, bf, d, T, H, B, r[0]) || !make_map_bht(&m.k, k, bf, d, T, Hkv, B, r[1]) ||
+        !make_map_bht(&m.v, v, bf, d, T, Hkv, B, r[2]) || !make_map_bht(&m.g, dO, bf, d, T, H, B, r[4]))
+        return fail(CLA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
+    const DkvPlan pl = wa_plan(H, Hkv, T, window, sinks);
+    if (d == 128)
+        return bf ? wa_bwd<128, true>(fn, m, o, dO, lse, dq, dk, dv, r, g, pl, ws, s)
+                  : wa_bwd<128, false>(fn, m, o, dO, lse, dq, dk, dv, r, g, pl, ws, s);
+    return bf ? wa_bwd<64, true>(fn, m, o, dO, lse, dq, dk, dv, r, g, pl, ws, s)
+              : wa_bwd<64, false>(fn, m, o, dO, lse, dq, dk, dv, r, g, pl, ws, s);
 }
 
 extern "C" int cla_window_cache_write(const void *k, const void *v, const int32_t *lens, void *kcache, void *vcache,

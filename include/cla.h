@@ -679,7 +679,12 @@ int cla_window_attn_fwd(const void *q, const void *k, const void *v,
                         const int32_t *lens, void *o, float *lse, float scale,
                         int64_t window, int64_t sinks, int dtype, int64_t B,
                         int64_t H, int64_t Hkv, int64_t T, int64_t d,
-                        const int64_t *strides, void *stream);
+                        const int64_t *strides, void *ws, size_t ws_bytes,
+                        void *stream);
+
+/* Bytes of workspace for cla_window_attn_fwd; 0 for what the call refuses. */
+size_t cla_window_attn_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t T,
+                                      int64_t d, int64_t window, int64_t sinks);
 
 /* Bytes of workspace for cla_window_attn_bwd. */
 size_t cla_window_attn_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv,

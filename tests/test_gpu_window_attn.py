@@ -59,6 +59,13 @@ def test_heads(cla, B, H, K):
     check(cla, *inputs(B, H, K, 200, 64, BF16), 70, 3)
 
 
+@pytest.mark.parametrize("T,window,sinks,d", [(1500, 65, 4, 64), (1300, 10, 200, 128)])
+def test_long_lists_of_the_sinks(cla, T, window, sinks, d):
+    """Every later query sees the sinks: their gradients come from many more tiles than a window has."""
+    lens = torch.tensor([T, 700], dtype=torch.int32).cuda()
+    check(cla, *inputs(2, 4, 1, T, d, BF16), window, sinks, lens)
+
+
 @pytest.mark.parametrize("B,H,K,T", [(0, 2, 1, 5), (2, 0, 0, 5), (2, 2, 1, 0)])
 def test_nothing_to_do(cla, B, H, K, T):
     q, k, v, dO = inputs(B, H, K, T, 64, BF16)

@@ -61,8 +61,10 @@ def _arr(s):
     return None if s is None else (ctypes.c_int64 * len(s))(*s)
 
 
-def wfwd(lib, q=A, o=A, lse=A, lens=None, scale=0.1, window=16, sinks=2, dtype=1, B=2, H=4, K=2, T=100, d=64, strides=None):
-    return lib.cla_window_attn_fwd(q, A, A, lens, o, lse, scale, window, sinks, dtype, B, H, K, T, d, _arr(strides), None)
+def wfwd(lib, q=A, o=A, lse=A, lens=None, scale=0.1, window=16, sinks=2, dtype=1, B=2, H=4, K=2, T=100, d=64, strides=None,
+         ws=WS, n=BIG):
+    return lib.cla_window_attn_fwd(q, A, A, lens, o, lse, scale, window, sinks, dtype, B, H, K, T, d, _arr(strides), ws, n,
+                                   None)
 
 
 def wbwd(lib, q=A, o=A, lse=A, lens=None, scale=0.1, window=16, sinks=2, dtype=1, B=2, H=4, K=2, T=100, d=64, strides=None,
@@ -87,7 +89,7 @@ COMMON = [(dict(B=-1), 1), (dict(H=-4), 1), (dict(K=-2), 1), (dict(H=5), 1), (di
 
 
 @pytest.mark.parametrize("call,kw,status", [(c, kw, st) for c in (wfwd, wbwd, wstep) for kw, st in COMMON] + [
-    (wfwd, dict(T=-1), 1), (wbwd, dict(T=-1), 1), (wfwd, dict(T=1 << 31), 2), (wbwd, dict(ws=None), 5), (wbwd, dict(ws=ODD), 5),
+    (wfwd, dict(T=-1), 1), (wbwd, dict(T=-1), 1), (wfwd, dict(T=1 << 31), 2), (wfwd, dict(ws=None), 5), (wfwd, dict(n=255), 5), (wbwd, dict(ws=None), 5), (wbwd, dict(ws=ODD), 5),
     (wbwd, dict(n=64), 5), (wstep, dict(ws=None), 5), (wstep, dict(n=8), 5), (wstep, dict(lens=None), 1),
     (wfwd, dict(strides=[64 * 400, 64 * 100, 0] * 4), 1), (wfwd, dict(strides=[64 * 400, 64 * 100, 4] * 4), 1),
     (wstep, dict(window=1 << 60), 2), (wstep, dict(sinks=1 << 60), 2)])
@@ -107,6 +109,8 @@ def test_window_cache_refusals(lib):
 
 def test_window_sizes(lib):
     assert lib.cla_window_attn_bwd_workspace_size(2, 4, 2, 100, 64, 16, 2) >= 256 + 2 * 4 * 100 * 4
+    assert lib.cla_window_attn_workspace_size(2, 4, 2, 100, 64, 16, 2) == 256
+    assert lib.cla_window_attn_workspace_size(2, 4, 2, 100, 65, 16, 2) == 0
     assert lib.cla_window_attn_bwd_workspace_size(2, 4, 3, 100, 64, 16, 2) == 0
     assert lib.cla_window_attn_step_workspace_size(2, 4, 2, 64, 16, 2) >= 256
     assert lib.cla_window_attn_step_workspace_size(2, 4, 2, 65, 16, 2) == 0
