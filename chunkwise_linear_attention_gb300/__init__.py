@@ -93,8 +93,7 @@ def lib():
                 "cla_window_attn_bwd_workspace_size": ([I64] * 7, SZ),
                 "cla_window_attn_bwd": ([P] * 10 + [F, I64, I64, INT] + [I64] * 5 + [P, P, SZ, P], INT),
                 "cla_window_cache_write": ([P] * 5 + [I64, I64, INT] + [I64] * 4 + [P, P], INT),
-                "cla_window_attn_step_workspace_size": ([I64] * 6, SZ),
-                "cla_window_attn_step": ([P] * 7 + [F, I64, I64, INT] + [I64] * 4 + [P, P, SZ, P], INT),
+                "cla_window_attn_step": ([P] * 7 + [F, I64, I64, INT] + [I64] * 4 + [P, P], INT),
             }
             for name, (args, res) in sig.items():
                 f = getattr(L, name)
@@ -778,11 +777,7 @@ def window_cache_write(k, v, kcache, vcache, *, window, sinks=0, lens=None, stre
         _strides(k, v)), stream)
 
 
-def window_attn_step_workspace_size(B, H, Hkv, d, window, sinks=0) -> int:
-    return int(lib().cla_window_attn_step_workspace_size(B, H, Hkv, d, int(window), int(sinks)))
-
-
-def window_attn_step(q, k, v, kcache, vcache, pos, *, window, sinks=0, scale=None, o=None, workspace=None, stream=None):
+def window_attn_step(q, k, v, kcache, vcache, pos, *, window, sinks=0, scale=None, o=None, stream=None):
     """One token for each of B sequences: writes k and v [B, Hkv, d] into the rolling cache (see window_cache_write) and
     returns the attention of q [B, H, d] over what it then holds.  pos [B] int32: tokens before this one; negative: a
     row without a sequence (o is 0, its cache is left alone)."""
@@ -792,10 +787,8 @@ def window_attn_step(q, k, v, kcache, vcache, pos, *, window, sinks=0, scale=Non
     code = _dtype_code(q, "q", _HALF)
     o = _out(o, (B, H, d), dt, dev)
     cs = (B, Hkv, int(sinks) + int(window), d)
-    ws = _ws(window_attn_step_workspace_size(B, H, Hkv, d, window, sinks), dev, workspace)
     _launch("cla_window_attn_step", dev, (
         _T(q, dt, "q", (B, H, d), True), _T(k, dt, "k", (B, Hkv, d), True), _T(v, dt, "v", (B, Hkv, d), True),
         _T(kcache, dt, "kcache", cs), _T(vcache, dt, "vcache", cs), _T(pos, torch.int32, "pos", (B,)),
-        _T(o, dt, "o", (B, H, d)), _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, d, _strides(q, k, v),
-        _T(ws, None, "workspace"), _nbytes(ws)), stream)
+        _T(o, dt, "o", (B, H, d)), _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, d, _strides(q, k, v)), stream)
     return o

@@ -13,37 +13,11 @@
 #include <math.h>
 
 #include "cla_internal.cuh"
-#include "elem_io.cuh"
 #include "window_attn_tc.cuh"
+#include "window_step.cuh"
 
 namespace cla {
 namespace {
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-template <typename E, int N>
-__device__ __forceinline__ void row_ld(const E *p, float (&v)[N]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = to_f32(p[lane * N + i]);
-}
-template <typename E, int N>
-__device__ __forceinline__ void row_st(E *p, const float (&v)[N]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[lane * N + i] = from_f32<E>(v[i]);
-}
-template <int N>
-__device__ __forceinline__ float dot(const float (&a)[N], const float (&b)[N]) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s = fmaf(a[i], b[i], s);
-    return warp_sum(s);
-}
 
 // One 16-byte piece of a cache slot per thread.
 __global__ void wa_write_kernel(const char *k, const char *v, char *kc, char *vc, Str3 sk, Str3 sv, WaArgs g, int pieces) {
@@ -59,48 +33,6 @@ __global__ void wa_write_kernel(const char *k, const char *v, char *kc, char *vc
     if (p >= n) return;
     reinterpret_cast<uint4 *>(kc)[i] = *reinterpret_cast<const uint4 *>(k + 2 * (b * sk.b + h * sk.h + p * sk.t) + 16 * piece);
     reinterpret_cast<uint4 *>(vc)[i] = *reinterpret_cast<const uint4 *>(v + 2 * (b * sv.b + h * sv.h + p * sv.t) + 16 * piece);
-}
-
-// A warp per (b, query head) walks the cache; the new token comes from k and v themselves, and
-// the first query head of a key head writes it into its slot.
-template <typename E, int N>
-__global__ void wa_step_kernel(const E *q, const E *k, const E *v, E *kc, E *vc, const int32_t *pos, E *o, Str3 sq,
-                               Str3 sk, Str3 sv, WaArgs g) {
-    const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (row >= (long long)g.B * g.H) return;
-    const int h = (int)(row % g.H), b = (int)(row / g.H), G = g.H / g.Hkv, hk = h / G;
-    const long long S = g.sinks + g.window, p = pos[b];
-    float acc[N], qv[N], kn[N], vn[N], x[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    if (p >= 0) {
-        const long long mine = p < g.sinks ? p : g.sinks + (p - g.sinks) % g.window, n = p + 1 < S ? p + 1 : S;
-        row_ld(q + b * sq.b + h * sq.h, qv);
-        row_ld(k + b * sk.b + hk * sk.h, kn);
-        row_ld(v + b * sv.b + hk * sv.h, vn);
-        E *kb = kc + ((long long)b * g.Hkv + hk) * S * (32 * N), *vb = vc + ((long long)b * g.Hkv + hk) * S * (32 * N);
-        float m = dot(qv, kn) * g.scale, l = 1.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = vn[i];
-        for (long long s = 0; s < n; ++s) {
-            if (s == mine) continue;
-            row_ld(kb + s * (32 * N), x);
-            const float z = dot(qv, x) * g.scale;
-            const float mn = fmaxf(m, z), f = expf(m - mn), e = expf(z - mn);
-            row_ld(vb + s * (32 * N), x);
-            l = l * f + e;
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(e, x[i], acc[i] * f);
-            m = mn;
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] /= l;
-        if (h == hk * G) {
-            row_st(kb + mine * (32 * N), kn);
-            row_st(vb + mine * (32 * N), vn);
-        }
-    }
-    row_st(o + row * (32 * N), acc);
 }
 
 // ------------------------------------------------------------------ host checks
@@ -138,8 +70,6 @@ int wa_strides(const char *fn, const int64_t *strides, const char *const *names,
     return CLA_OK;
 }
 
-unsigned warps_grid(long long warps) { return (unsigned)((warps + 3) / 4); }
-
 // Multiprocessors of the current device, asked for once per device.
 int wa_blocks(const char *fn, long long items, unsigned *blocks) {
     static std::atomic<int> known[64];
@@ -153,6 +83,9 @@ int wa_blocks(const char *fn, long long items, unsigned *blocks) {
     *blocks = (unsigned)(items < n ? items : n);
     return CLA_OK;
 }
+
+// The step's blocks are made at least this many by splitting the slots, where there are so many.
+constexpr long long kStepBlocks = 912;
 
 long long wa_tiles(long long T) { return (T + kWT - 1) / kWT; }
 
@@ -224,20 +157,6 @@ int wa_bwd(const char *fn, const WaMaps &m, const void *o, const void *dO, const
 }  // namespace cla
 
 using namespace cla;
-
-#define WA_DISPATCH(kernel, grid, ...)                                                                              \
-    do {                                                                                                            \
-        if (dtype == CLA_BF16) {                                                                                    \
-            using E = __nv_bfloat16;                                                                                \
-            if (d == 64) kernel<E, 2><<<grid, 128, 0, s>>>(__VA_ARGS__);                                            \
-            else kernel<E, 4><<<grid, 128, 0, s>>>(__VA_ARGS__);                                                    \
-        } else {                                                                                                    \
-            using E = __half;                                                                                       \
-            if (d == 64) kernel<E, 2><<<grid, 128, 0, s>>>(__VA_ARGS__);                                            \
-            else kernel<E, 4><<<grid, 128, 0, s>>>(__VA_ARGS__);                                                    \
-        }                                                                                                           \
-        if (int st = check_launch(fn)) return st;                                                                   \
-    } while (0)
 
 extern "C" int cla_window_attn_fwd(const void *q, const void *k, const void *v, const int32_t *lens, void *o, float *lse,
                                    float scale, int64_t window, int64_t sinks, int dtype, int64_t B, int64_t H,
@@ -341,27 +260,44 @@ extern "C" int cla_window_cache_write(const void *k, const void *v, const int32_
     return check_launch(fn);
 }
 
-extern "C" size_t cla_window_attn_step_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t d, int64_t window,
-                                                      int64_t sinks) {
-    if (wa_check("cla_window_attn_step_workspace_size", B, H, Hkv, 1, d, window, sinks, CLA_BF16, 1.f) != CLA_OK) return 0;
-    return sizeof(WsHeader);
+template <int D, bool BF, int NG>
+static int wa_step(const char *fn, const void *q, const void *k, const void *v, void *kc, void *vc, const int32_t *pos, void *o,
+                   const Str3 *r, StepArgs g, cudaStream_t s) {
+    const int G = g.H / g.Hkv;
+    g.groups = (G + 8 * NG - 1) / (8 * NG);
+    const long long units = (long long)g.B * g.Hkv * g.groups;
+    const long long tiles = (g.slots + 15) / 16;
+    g.splits = 1;
+    while (g.splits < 8 && units * g.splits < kStepBlocks && tiles > g.splits * kStepWarps) g.splits *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * g.splits));
+    cfg.blockDim = dim3(kStepWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)g.splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    CLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, wa_step_kernel<D, BF, NG>, (const uint16_t *)q, (const uint16_t *)k, (const uint16_t *)v,
+                                    (uint16_t *)kc, (uint16_t *)vc, pos, (uint16_t *)o, r[0], r[1], r[2], g),
+                 fn);
+    return check_launch(fn);
 }
 
 extern "C" int cla_window_attn_step(const void *q, const void *k, const void *v, void *kcache, void *vcache,
                                     const int32_t *pos, void *o, float scale, int64_t window, int64_t sinks, int dtype,
-                                    int64_t B, int64_t H, int64_t Hkv, int64_t d, const int64_t *strides, void *ws,
-                                    size_t ws_bytes, void *stream) {
+                                    int64_t B, int64_t H, int64_t Hkv, int64_t d, const int64_t *strides, void *stream) {
     const char *fn = "cla_window_attn_step";
     clear_error();
     if (int st = wa_check(fn, B, H, Hkv, 1, d, window, sinks, dtype, scale)) return st;
+    if (sinks + window > kMaxTokens || !product_below({B, H}, 1 << 27))
+        return fail(CLA_ERR_UNSUPPORTED, "%s: sinks + window must be at most 2^31 - 512, B * H below 2^27", fn);
     if (B * H == 0) return CLA_OK;
     if (!q || !k || !v || !kcache || !vcache || !pos || !o)
         return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned_or_null({q, k, v, kcache, vcache, o}, 16) || !aligned_or_null({pos}, 4))
         return fail(CLA_ERR_INVALID_ARG, "%s: a pointer is misaligned", fn);
-    const size_t need = cla_window_attn_step_workspace_size(B, H, Hkv, d, window, sinks);
-    if (ws == nullptr || !aligned16(ws) || ws_bytes < need)
-        return fail(CLA_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
     static const char *const names[] = {"q", "k", "v"};
     const int64_t heads[] = {H, Hkv, Hkv};
     Str3 r[3];
@@ -369,9 +305,12 @@ extern "C" int cla_window_attn_step(const void *q, const void *k, const void *v,
     if (strides != nullptr)
         for (int i = 0; i < 3; ++i) full[3 * i] = strides[2 * i], full[3 * i + 1] = strides[2 * i + 1], full[3 * i + 2] = d;
     if (int st = wa_strides(fn, strides ? full : nullptr, names, heads, 3, B, 1, d, r)) return st;
-    const WaArgs g{nullptr, scale, 1, window, sinks, (int)B, (int)H, (int)Hkv};
+    const StepArgs g{scale * 1.4426950408889634f, window, sinks + window, (int)sinks, (int)B, (int)H, (int)Hkv, 1, 1};
     cudaStream_t s = (cudaStream_t)stream;
-    WA_DISPATCH(wa_step_kernel, warps_grid(B * H), (const E *)q, (const E *)k, (const E *)v, (E *)kcache, (E *)vcache, pos,
-                (E *)o, r[0], r[1], r[2], g);
-    return CLA_OK;
+    const bool bf = dtype == CLA_BF16, wide = H / Hkv > 8;
+#define CLA_STEP(D, BF) \
+    (wide ? wa_step<D, BF, 2>(fn, q, k, v, kcache, vcache, pos, o, r, g, s) : wa_step<D, BF, 1>(fn, q, k, v, kcache, vcache, pos, o, r, g, s))
+    if (d == 128) return bf ? CLA_STEP(128, true) : CLA_STEP(128, false);
+    return bf ? CLA_STEP(64, true) : CLA_STEP(64, false);
+#undef CLA_STEP
 }

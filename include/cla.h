@@ -722,10 +722,6 @@ int cla_window_cache_write(const void *k, const void *v, const int32_t *lens,
                            int64_t T, int64_t d, const int64_t *strides,
                            void *stream);
 
-/* Bytes of workspace for cla_window_attn_step. */
-size_t cla_window_attn_step_workspace_size(int64_t B, int64_t H, int64_t Hkv,
-                                           int64_t d, int64_t window, int64_t sinks);
-
 /* One token for each of B sequences: writes its key and value into the cache
  * and attends over what the cache then holds.
  *   q      [B, H, d];  k, v [B, Hkv, d] dtype
@@ -734,12 +730,13 @@ size_t cla_window_attn_step_workspace_size(int64_t B, int64_t H, int64_t Hkv,
  *          negative entry marks a row without a sequence: its o is 0 and its
  *          cache is left alone.
  *   o      [B, H, d] dtype out, dense
- *   strides [opt]: {batch, head} pairs of q, k, v, under the rules above */
+ *   strides [opt]: {batch, head} pairs of q, k, v, under the rules above
+ * sinks + window is at most 2^31 - 512, B * H below 2^27. */
 int cla_window_attn_step(const void *q, const void *k, const void *v, void *kcache,
                          void *vcache, const int32_t *pos, void *o, float scale,
                          int64_t window, int64_t sinks, int dtype, int64_t B,
                          int64_t H, int64_t Hkv, int64_t d, const int64_t *strides,
-                         void *ws, size_t ws_bytes, void *stream);
+                         void *stream);
 
 #ifdef __cplusplus
 }

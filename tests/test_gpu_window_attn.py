@@ -159,7 +159,8 @@ def test_cache_write(cla, T, window, sinks):
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("B,H,K,d,window,sinks", [(1, 1, 1, 64, 1, 0), (4, 4, 2, 64, 30, 3), (5, 8, 1, 128, 200, 4),
-                                                  (3, 6, 6, 128, 1500, 0), (2, 32, 2, 64, 5000, 16), (4, 5, 1, 64, 3, 100)])
+                                                  (3, 6, 6, 128, 1500, 0), (2, 32, 2, 64, 5000, 16), (4, 5, 1, 64, 3, 100),
+                                                  (2, 40, 1, 128, 130, 1), (1, 9, 1, 64, 33, 0)])
 def test_step(cla, B, H, K, d, window, sinks, dtype):
     g = torch.Generator().manual_seed(9)
     S = sinks + window
@@ -222,18 +223,17 @@ def test_step_in_a_graph(cla):
     q, k, v, kc, vc = rnd(B, H, d), rnd(B, K, d), rnd(B, K, d), rnd(B, K, W + n, d), rnd(B, K, W + n, d)
     pos = torch.tensor([0, 640], dtype=torch.int32).cuda()
     kw = dict(window=W, sinks=n)
-    ws = torch.empty(cla.window_attn_step_workspace_size(B, H, K, d, W, n), dtype=torch.uint8, device="cuda")
     k1, v1 = kc.clone(), vc.clone()
     s = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(s):
-        cla.window_attn_step(q, k, v, k1, v1, pos, workspace=ws, **kw)
+        cla.window_attn_step(q, k, v, k1, v1, pos, **kw)
     s.synchronize()
     k1.copy_(kc), v1.copy_(vc)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=s):
-        o = cla.window_attn_step(q, k, v, k1, v1, pos, workspace=ws, **kw)
+        o = cla.window_attn_step(q, k, v, k1, v1, pos, **kw)
     for _ in range(70):
         want = cla.window_attn_step(q, k, v, kc, vc, pos, **kw)
         graph.replay()

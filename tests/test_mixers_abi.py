@@ -74,10 +74,9 @@ def wbwd(lib, q=A, o=A, lse=A, lens=None, scale=0.1, window=16, sinks=2, dtype=1
                                    n, None)
 
 
-def wstep(lib, q=A, o=A, lse=A, lens=A, scale=0.1, window=16, sinks=2, dtype=1, B=2, H=4, K=2, T=1, d=64, strides=None,
-          ws=WS, n=BIG):
+def wstep(lib, q=A, o=A, lse=A, lens=A, scale=0.1, window=16, sinks=2, dtype=1, B=2, H=4, K=2, T=1, d=64, strides=None):
     s = None if strides is None else [x for i in range(3) for x in strides[3 * i:3 * i + 2]]
-    return lib.cla_window_attn_step(q, A, A, lse, A, lens, o, scale, window, sinks, dtype, B, H, K, d, _arr(s), ws, n, None)
+    return lib.cla_window_attn_step(q, A, A, lse, A, lens, o, scale, window, sinks, dtype, B, H, K, d, _arr(s), None)
 
 
 COMMON = [(dict(B=-1), 1), (dict(H=-4), 1), (dict(K=-2), 1), (dict(H=5), 1), (dict(K=0), 1), (dict(window=0), 1),
@@ -90,7 +89,7 @@ COMMON = [(dict(B=-1), 1), (dict(H=-4), 1), (dict(K=-2), 1), (dict(H=5), 1), (di
 
 @pytest.mark.parametrize("call,kw,status", [(c, kw, st) for c in (wfwd, wbwd, wstep) for kw, st in COMMON] + [
     (wfwd, dict(T=-1), 1), (wbwd, dict(T=-1), 1), (wfwd, dict(T=1 << 31), 2), (wfwd, dict(ws=None), 5), (wfwd, dict(n=255), 5), (wbwd, dict(ws=None), 5), (wbwd, dict(ws=ODD), 5),
-    (wbwd, dict(n=64), 5), (wstep, dict(ws=None), 5), (wstep, dict(n=8), 5), (wstep, dict(lens=None), 1),
+    (wbwd, dict(n=64), 5), (wstep, dict(lens=None), 1),
     (wfwd, dict(strides=[64 * 400, 64 * 100, 0] * 4), 1), (wfwd, dict(strides=[64 * 400, 64 * 100, 4] * 4), 1),
     (wstep, dict(window=1 << 60), 2), (wstep, dict(sinks=1 << 60), 2)])
 def test_window_refusals(lib, call, kw, status):
@@ -112,8 +111,6 @@ def test_window_sizes(lib):
     assert lib.cla_window_attn_workspace_size(2, 4, 2, 100, 64, 16, 2) == 256
     assert lib.cla_window_attn_workspace_size(2, 4, 2, 100, 65, 16, 2) == 0
     assert lib.cla_window_attn_bwd_workspace_size(2, 4, 3, 100, 64, 16, 2) == 0
-    assert lib.cla_window_attn_step_workspace_size(2, 4, 2, 64, 16, 2) >= 256
-    assert lib.cla_window_attn_step_workspace_size(2, 4, 2, 65, 16, 2) == 0
 
 
 def test_binding_refusals():
@@ -138,8 +135,7 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="v must have shape"):
         cla.window_attn_fwd(q, q, q[:, :1], window=4)
     with pytest.raises(ValueError, match="kcache must have shape"):
-        cla.window_attn_step(q[:, :, 0], q[:, :, 0], q[:, :, 0], q, q, torch.zeros(1, dtype=torch.int32), window=4, sinks=1,
-                             workspace=torch.zeros(512, dtype=torch.uint8))
+        cla.window_attn_step(q[:, :, 0], q[:, :, 0], q[:, :, 0], q, q, torch.zeros(1, dtype=torch.int32), window=4, sinks=1)
 
 
 # ------------------------------------------------------------------ the 64-bit forms themselves
