@@ -184,14 +184,33 @@ def _launch(fn, device, args, stream):
     """Calls entry point `fn` with the tensors' device current: `args` are plain values and _T
     tensor arguments, every one of which is checked (dtype and shape of all of them first)
     before its pointer is taken; raises ClaError on a non-OK status."""
-    tensors = [a for a in args if isinstance(a, _T) and a.t is not None]
-    for a in tensors:
-        a.check_meta()
-    for a in tensors:
-        a.check_place(device)
-    cargs = [(None if a.t is None else ctypes.c_void_p(a.t.data_ptr())) if isinstance(a, _T) else a for a in args]
-    with torch.cuda.device(device):
-        _check(fn, getattr(lib(), fn)(*cargs, _stream(stream, device)))
+    cargs, good = [], device.type == "cuda"
+    for a in args:  # one quick pass; what does not pass it is looked at again for its message
+        if type(a) is _T:
+            t = a.t
+            if t is None:
+                a = None
+            else:
+                good = (good and (t.dtype is a.dtype or a.dtype is None) and (a.shape is None or t.shape == a.shape)
+                        and t.device == device and (t.is_contiguous() or a.strided and t.stride(-1) == 1))
+                a = t.data_ptr()
+        cargs.append(a)
+    if not good:
+        tensors = [a for a in args if type(a) is _T and a.t is not None]
+        for a in tensors:
+            a.check_meta()
+        for a in tensors:
+            a.check_place(device)
+    call = getattr(_lib or lib(), fn)
+    index = device.index
+    if index == torch.cuda.current_device():
+        # the current stream's handle, without the Stream object around it
+        status = call(*cargs, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, device))
+    else:
+        with torch.cuda.device(device):
+            status = call(*cargs, _stream(stream, device))
+    if status != CLA_OK:
+        _check(fn, status)
 
 
 def check_status(workspace, stream=None) -> None:

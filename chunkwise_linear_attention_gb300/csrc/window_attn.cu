@@ -20,16 +20,16 @@ namespace cla {
 namespace {
 
 // One 16-byte piece of a cache slot per thread.
-__global__ void wa_write_kernel(const char *k, const char *v, char *kc, char *vc, Str3 sk, Str3 sv, WaArgs g, int pieces) {
-    const long long S = g.sinks + g.window;
+__global__ void wa_write_kernel(const char *k, const char *v, const int32_t *lens, char *kc, char *vc, Str3 sk, Str3 sv, int B,
+                                int Hkv, int T, long long window, long long sinks, int pieces) {
+    const long long S = sinks + window;
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= (long long)g.B * g.Hkv * S * pieces) return;
+    if (i >= (long long)B * Hkv * S * pieces) return;
     const int piece = (int)(i % pieces);
     const long long slot = i / pieces % S, bh = i / pieces / S;
-    const int h = (int)(bh % g.Hkv), b = (int)(bh / g.Hkv);
-    const long long n = wa_len(g, b);
-    long long p = slot;
-    if (slot >= g.sinks && slot < n) p += (n - 1 - slot) / g.window * g.window;
+    const int h = (int)(bh % Hkv), b = (int)(bh / Hkv), n = lens == nullptr ? T : min(max(lens[b], 0), T);
+    long long p = slot;  // the last token that falls on the slot
+    if (slot >= sinks && slot < n) p += (n - 1 - slot) / window * window;
     if (p >= n) return;
     reinterpret_cast<uint4 *>(kc)[i] = *reinterpret_cast<const uint4 *>(k + 2 * (b * sk.b + h * sk.h + p * sk.t) + 16 * piece);
     reinterpret_cast<uint4 *>(vc)[i] = *reinterpret_cast<const uint4 *>(v + 2 * (b * sv.b + h * sv.h + p * sv.t) + 16 * piece);
@@ -174,7 +174,7 @@ extern "C" int cla_window_attn_fwd(const void *q, const void *k, const void *v, 
     const int64_t heads[] = {H, Hkv, Hkv, H};
     Str3 r[4];
     if (int st = wa_strides(fn, strides, names, heads, 4, B, T, d, r)) return st;
-    const WaArgs g{lens, scale, T, window < T ? window : T, sinks < T ? sinks : T, (int)B, (int)H, (int)Hkv};
+    const WaArgs g{lens, scale, (int)T, (int)(window < T ? window : T), (int)(sinks < T ? sinks : T), (int)B, (int)H, (int)Hkv};
     cudaStream_t s = (cudaStream_t)stream;
     WsHeader *hdr = static_cast<WsHeader *>(ws);
     if (B * H * T == 0) {
@@ -220,7 +220,7 @@ extern "C" int cla_window_attn_bwd(const void *q, const void *k, const void *v, 
     const int64_t heads[] = {H, Hkv, Hkv, H, H, H, Hkv, Hkv};
     Str3 r[8];
     if (int st = wa_strides(fn, strides, names, heads, 8, B, T, d, r)) return st;
-    const WaArgs g{lens, scale, T, window < T ? window : T, sinks < T ? sinks : T, (int)B, (int)H, (int)Hkv};
+    const WaArgs g{lens, scale, (int)T, (int)(window < T ? window : T), (int)(sinks < T ? sinks : T), (int)B, (int)H, (int)Hkv};
     cudaStream_t s = (cudaStream_t)stream;
     CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(WsHeader), s), fn);
     if (B * H * T == 0) return CLA_OK;
@@ -252,11 +252,11 @@ extern "C" int cla_window_cache_write(const void *k, const void *v, const int32_
     Str3 r[2];
     if (int st = wa_strides(fn, strides, names, heads, 2, B, T, d, r)) return st;
     const int pieces = (int)(d / 8);
-    const WaArgs g{lens, 1.f, T, window, sinks, (int)B, (int)Hkv, (int)Hkv};
     const long long total = B * Hkv * (sinks + window) * pieces;
     if (total / 256 >= 2147483647ll) return fail(CLA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     wa_write_kernel<<<(unsigned)((total + 255) / 256), 256, 0, (cudaStream_t)stream>>>(
-        (const char *)k, (const char *)v, (char *)kcache, (char *)vcache, r[0], r[1], g, pieces);
+        (const char *)k, (const char *)v, lens, (char *)kcache, (char *)vcache, r[0], r[1], (int)B, (int)Hkv, (int)T, window, sinks,
+        pieces);
     return check_launch(fn);
 }
 
