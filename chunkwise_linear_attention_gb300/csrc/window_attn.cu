@@ -102,52 +102,38 @@ int wa_fwd(const char *fn, const WaMaps &m, void *o, float *lse, const Str3 &so,
     return check_launch(fn);
 }
 
-// Tiles with sinks are seen by every later query tile.  Their lists are cut into pieces of what a
-// tile without sinks has (at least 8), while there are few such tiles: 64 pieces a key head bound
-// the partial sums to 64 x 2 x 128 x d floats.
-DkvPlan wa_plan(int64_t H, int64_t Hkv, int64_t T, int64_t window, int64_t sinks) {
-    DkvPlan p{0, 1, 0, nullptr};
-    const long long G = Hkv ? H / Hkv : 0, tiles = wa_tiles(T), st = wa_tiles(sinks < T ? sinks : T);
-    const long long span = wa_tiles(window < T ? window : T) + 1, all = G * tiles;
-    long long piece = G * (span < tiles ? span : tiles);
-    if (piece < 8) piece = 8;
-    if (st == 0 || st > 16 || 2 * all <= 3 * piece) return p;
-    const long long most = 64 / st;
-    if ((all + piece - 1) / piece > most) piece = (all + most - 1) / most;
-    p.sink_tiles = (int)st;
-    p.piece = (int)piece;
-    p.pieces = (int)((all + piece - 1) / piece);
-    return p;
-}
-size_t wa_part_bytes(const DkvPlan &p, int64_t B, int64_t Hkv, int64_t d) {
-    return (size_t)(B * Hkv) * p.sink_tiles * p.pieces * 2 * kWT * d * 4;
+// Blocks of the dk/dv kernel: at most one a multiprocessor, and at least 2 steps each.  The partial
+// sums are sized for this many whatever the device.
+constexpr int kDkvBlocks = 152;
+long long wa_dkv_blocks(int64_t B, int64_t H, int64_t T, int64_t window, int64_t sinks) {
+    const Lists l((int)T, (int)(window < T ? window : T), (int)(sinks < T ? sinks : T));
+    const long long n = (B * H * l.before(l.n) + 1) / 2;
+    return n < kDkvBlocks ? n : kDkvBlocks;
 }
 
 template <int D, bool BF>
 int wa_bwd(const char *fn, const WaMaps &m, const void *o, const void *dO, const float *lse, void *dq, void *dk, void *dv,
-           const Str3 *r, const WaArgs &g, DkvPlan pl, void *ws, cudaStream_t s) {
+           const Str3 *r, const WaArgs &g, void *ws, cudaStream_t s) {
     static std::atomic<unsigned long long> done_q{0}, done_kv{0};
     constexpr int smem_q = DqCfg<D>::SMEM > kMinSmem ? DqCfg<D>::SMEM : kMinSmem;
     constexpr int smem_kv = DkvCfg<D>::SMEM > kMinSmem ? DkvCfg<D>::SMEM : kMinSmem;
     char *p = static_cast<char *>(ws);
     WsHeader *hdr = reinterpret_cast<WsHeader *>(p);
     float *delta = reinterpret_cast<float *>(p + sizeof(WsHeader));
-    pl.part = reinterpret_cast<float *>(p + sizeof(WsHeader) + align_up((size_t)g.B * g.H * g.T * 4, 16));
+    float *parts = reinterpret_cast<float *>(p + sizeof(WsHeader) + align_up((size_t)g.B * g.H * g.T * 4, 16));
     if (int st = set_max_dynamic_smem(done_q, (const void *)wa_dq_kernel<D, BF>, smem_q)) return st;
     if (int st = set_max_dynamic_smem(done_kv, (const void *)wa_dkv_kernel<D, BF>, smem_kv)) return st;
-    const long long tiles = wa_tiles(g.T);
-    long long items = (long long)g.B * g.H * tiles;
+    const long long items = (long long)g.B * g.H * wa_tiles(g.T);
     unsigned blocks;
     if (int st = wa_blocks(fn, items, &blocks)) return st;
     wa_dq_kernel<D, BF><<<blocks, DqCfg<D>::THREADS, smem_q, s>>>(m, o, dO, lse, dq, delta, r[3], r[4], r[5], g, (int)items, hdr);
     if (int st = check_launch(fn)) return st;
-    items = (long long)g.B * g.Hkv * (tiles + (long long)pl.sink_tiles * (pl.pieces - 1));
-    if (int st = wa_blocks(fn, items, &blocks)) return st;
-    wa_dkv_kernel<D, BF><<<blocks, DkvCfg<D>::THREADS, smem_kv, s>>>(m, lse, delta, dk, dv, r[6], r[7], g, pl, (int)items, hdr);
+    if (int st = wa_blocks(fn, wa_dkv_blocks(g.B, g.H, g.T, g.window, g.sinks), &blocks)) return st;
+    CutList *cuts = reinterpret_cast<CutList *>(parts + (size_t)wa_dkv_blocks(g.B, g.H, g.T, g.window, g.sinks) * 4 * kWT * D);
+    wa_dkv_kernel<D, BF><<<blocks, DkvCfg<D>::THREADS, smem_kv, s>>>(m, lse, delta, dk, dv, parts, cuts, r[6], r[7], g, hdr);
     if (int st = check_launch(fn)) return st;
-    if (pl.sink_tiles > 0) {
-        const long long n = (long long)g.B * g.Hkv * pl.sink_tiles * 2 * kWT * (D / 2);
-        wa_join_kernel<D, BF><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(dk, dv, r[6], r[7], g, pl);
+    if (blocks > 1) {
+        wa_join_kernel<D, BF><<<dim3(blocks - 1, kJoinY), 256, 0, s>>>(parts, cuts, dk, dv, r[6], r[7], g.T, (int)blocks);
         return check_launch(fn);
     }
     return CLA_OK;
@@ -199,7 +185,8 @@ extern "C" size_t cla_window_attn_workspace_size(int64_t B, int64_t H, int64_t H
 extern "C" size_t cla_window_attn_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d,
                                                      int64_t window, int64_t sinks) {
     if (wa_check("cla_window_attn_bwd_workspace_size", B, H, Hkv, T, d, window, sinks, CLA_BF16, 1.f) != CLA_OK) return 0;
-    return sizeof(WsHeader) + align_up((size_t)(B * H * T) * 4, 16) + wa_part_bytes(wa_plan(H, Hkv, T, window, sinks), B, Hkv, d);
+    return sizeof(WsHeader) + align_up((size_t)(B * H * T) * 4, 16) +
+           (size_t)wa_dkv_blocks(B, H, T, window, sinks) * (4 * kWT * d * 4 + sizeof(CutList));
 }
 
 extern "C" int cla_window_attn_bwd(const void *q, const void *k, const void *v, const int32_t *lens, const void *o,
@@ -229,12 +216,11 @@ extern "C" int cla_window_attn_bwd(const void *q, const void *k, const void *v, 
     if (!make_map_bht(&m.q, q, bf, d, T, H, B, r[0]) || !make_map_bht(&m.k, k, bf, d, T, Hkv, B, r[1]) ||
         !make_map_bht(&m.v, v, bf, d, T, Hkv, B, r[2]) || !make_map_bht(&m.g, dO, bf, d, T, H, B, r[4]))
         return fail(CLA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
-    const DkvPlan pl = wa_plan(H, Hkv, T, window, sinks);
     if (d == 128)
-        return bf ? wa_bwd<128, true>(fn, m, o, dO, lse, dq, dk, dv, r, g, pl, ws, s)
-                  : wa_bwd<128, false>(fn, m, o, dO, lse, dq, dk, dv, r, g, pl, ws, s);
-    return bf ? wa_bwd<64, true>(fn, m, o, dO, lse, dq, dk, dv, r, g, pl, ws, s)
-              : wa_bwd<64, false>(fn, m, o, dO, lse, dq, dk, dv, r, g, pl, ws, s);
+        return bf ? wa_bwd<128, true>(fn, m, o, dO, lse, dq, dk, dv, r, g, ws, s)
+                  : wa_bwd<128, false>(fn, m, o, dO, lse, dq, dk, dv, r, g, ws, s);
+    return bf ? wa_bwd<64, true>(fn, m, o, dO, lse, dq, dk, dv, r, g, ws, s)
+              : wa_bwd<64, false>(fn, m, o, dO, lse, dq, dk, dv, r, g, ws, s);
 }
 
 extern "C" int cla_window_cache_write(const void *k, const void *v, const int32_t *lens, void *kcache, void *vcache,

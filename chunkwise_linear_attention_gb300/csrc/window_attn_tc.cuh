@@ -144,13 +144,16 @@ __device__ __forceinline__ void mma_scores(uint32_t acc, uint32_t a, uint32_t b,
     for (int kk = 0; kk < D / 16; ++kk)
         mma_ss_w(acc, da + Tile<D>::kstep(kk), db + Tile<D>::kstep(kk), idesc16<BF>(kWT, 0) | negate, kk ? 1u : 0u);
 }
-// acc (+)= P X: P [128 x 128] packed in tensor memory, X a tile [128 tokens][D].
-template <int D, bool BF>
+// acc (+)= P X: P [128 x 128] in tensor memory, X a tile [128 tokens][D].  P lies packed over the
+// scores it came from in pieces of C columns, each at the start of its C score columns: a thread
+// then writes only where it has read itself, and the threads of a row need not wait for another.
+template <int D, bool BF, int C>
 __device__ __forceinline__ void mma_apply(uint32_t acc, uint32_t p, uint32_t x, bool add) {
     const uint64_t dx = Tile<D>::nmajor(x);
 #pragma unroll
     for (int kk = 0; kk < kWT / 16; ++kk)
-        mma_ts_w(acc, p + kk * 8, dx + Tile<D>::nstep(kk), idesc16<BF>(D, 1), (add || kk) ? 1u : 0u);
+        mma_ts_w(acc, p + (kk / (C / 16)) * C + (kk % (C / 16)) * 8, dx + Tile<D>::nstep(kk), idesc16<BF>(D, 1),
+                 (add || kk) ? 1u : 0u);
 }
 
 __device__ __forceinline__ uint32_t tmem_alloc_all(uint32_t *slot) {
@@ -186,12 +189,10 @@ __device__ __forceinline__ bool misplaced(uint32_t base, WsHeader *hdr) {
     if (threadIdx.x == 0) atomicOr(&hdr->error, kErrTimeout);
     return true;
 }
-// Between the N warps that share a lane quarter: what any has read of tensor memory is read.
+// Between the N warps that share a lane quarter, and so their rows.
 template <int N>
 __device__ __forceinline__ void quarter_sync(int id) {
-    tc_fence_before();
     asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(32 * N) : "memory");
-    tc_fence_after();
 }
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {  // one arrival of a warp whose lanes are all done
     __syncwarp();
@@ -262,34 +263,26 @@ __device__ __forceinline__ void zero_row(void *out, long long at) {
 // rarely and by the warps that own it; sums and outputs are fp32.
 template <int D>
 struct FwdCfg {
-    static constexpr int STAGES = D == 128 ? 5 : 8;
-    static constexpr int SMEM = (2 + STAGES) * Tile<D>::BYTES + kSmall;
+    static constexpr int STAGES = D == 128 ? 3 : 8;  // of keys and values, beside two pairs of query tiles
+    static constexpr int SMEM = (4 + STAGES) * Tile<D>::BYTES + kSmall;
     static constexpr int THREADS = 576;  // 16 math warps, products, loads
 };
 
 struct FwdItem {
     int b, hk, h, t0, step_h, step_t;  // the second tile: head h + step_h at t0 + step_t
 };
+// Items go from the last query tiles, which see the most, to the first: dealt out in turn they
+// leave the blocks with almost equal shares.
 __device__ __forceinline__ FwdItem fwd_item(const WaArgs &g, int item, int tiles) {
     FwdItem w;
-    const int G = g.H / g.Hkv;
-    if ((G & 1) == 0) {
-        const int pr = item % (G / 2), r = item / (G / 2), bh = r / tiles;
-        w.b = bh / g.Hkv;
-        w.hk = bh % g.Hkv;
-        w.h = w.hk * G + 2 * pr;
-        w.t0 = (r % tiles) * kWT;
-        w.step_h = 1;
-        w.step_t = 0;
-    } else {
-        const int pairs = (tiles + 1) / 2, r = item / G, bh = r / pairs;
-        w.b = bh / g.Hkv;
-        w.hk = bh % g.Hkv;
-        w.h = w.hk * G + item % G;
-        w.t0 = (r % pairs) * 2 * kWT;
-        w.step_h = 0;
-        w.step_t = kWT;
-    }
+    const int G = g.H / g.Hkv, even = (G & 1) == 0, per = even ? G / 2 : G, bh = item / per % (g.B * g.Hkv);
+    const int last = (even ? tiles : (tiles + 1) / 2) - 1, tt = last - item / per / (g.B * g.Hkv);
+    w.b = bh / g.Hkv;
+    w.hk = bh % g.Hkv;
+    w.h = w.hk * G + item % per * (even ? 2 : 1);
+    w.t0 = tt * (even ? kWT : 2 * kWT);
+    w.step_h = even ? 1 : 0;
+    w.step_t = even ? 0 : kWT;
     return w;
 }
 // The key tiles of both: the first's range begins no later than the second's, and is empty only
@@ -311,17 +304,17 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
               int items, WsHeader *hdr) {
     constexpr int ST = FwdCfg<D>::STAGES, TB = Tile<D>::BYTES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t sq = smem_u32(smem_raw), skv = sq + 2 * TB;
-    Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 + ST) * TB);
-    static_assert(2 * ST + 8 <= 32, "barriers");
+    const uint32_t sq = smem_u32(smem_raw), skv = sq + 4 * TB;
+    Small &sm = *reinterpret_cast<Small *>(smem_raw + (4 + ST) * TB);
+    static_assert(2 * ST + 10 <= 32, "barriers");
     float(*s_row)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [tile][half][row]: maxima, in the end sums
     if (misplaced(sq, hdr)) return;
     const int warp = threadIdx.x >> 5, tiles = (g.T + kWT - 1) / kWT;
     const uint32_t b0 = smem_u32(sm.bars);
-    const uint32_t q_full = b0, q_empty = b0 + 8, o_full = b0 + 16, s_full = b0 + 24, p_ready = b0 + 40;  // the last two x 2
-    const uint32_t kv_full = b0 + 64, kv_empty = kv_full + 8 * ST;
+    const uint32_t q_full = b0, q_empty = b0 + 16, o_full = b0 + 32, s_full = b0 + 48, p_ready = b0 + 64;  // two each
+    const uint32_t kv_full = b0 + 80, kv_empty = kv_full + 8 * ST;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(b0 + 8 * i, 1);
+        for (int i = 0; i < 8; ++i) mbar_init(b0 + 8 * i, 1);
         mbar_init(p_ready, 8);
         mbar_init(p_ready + 8, 8);
         for (int i = 0; i < 2 * ST; ++i) mbar_init(kv_full + 8 * i, 1);
@@ -341,12 +334,13 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
                 const FwdItem w = fwd_item(g, item, tiles);
                 const FwdTiles kt(g, w, wa_len(g, w.b));
                 if (kt.count == 0) continue;
-                if (it > 0) wait(q_empty, it - 1, 21);
+                const uint32_t qb = it & 1;
+                if (it > 1) wait(q_empty + 8 * qb, it / 2 - 1, 21);
                 if (*wait.dead != 0u) break;
                 const bool two = kt.b.hi >= kt.b.lo;
-                mbar_expect_tx(q_full, two ? 2 * TB : TB);
-                Tile<D>::load(sq, &maps.q, w.t0, w.h, w.b, q_full);
-                if (two) Tile<D>::load(sq + TB, &maps.q, w.t0 + w.step_t, w.h + w.step_h, w.b, q_full);
+                mbar_expect_tx(q_full + 8 * qb, two ? 2 * TB : TB);
+                Tile<D>::load(sq + 2 * qb * TB, &maps.q, w.t0, w.h, w.b, q_full + 8 * qb);
+                if (two) Tile<D>::load(sq + (2 * qb + 1) * TB, &maps.q, w.t0 + w.step_t, w.h + w.step_h, w.b, q_full + 8 * qb);
                 for (int i = 0; i < 2 * kt.count; ++i, ++n) {
                     const uint32_t s = n % ST;
                     if (n >= ST) wait(kv_empty + 8 * s, n / ST - 1, 22);
@@ -356,56 +350,67 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
                 }
                 ++it;
             }
-            if (*wait.dead != 0u) drain(q_full, it, 1), drain(kv_full, n, ST);
+            if (*wait.dead != 0u) drain(q_full, it, 2), drain(kv_full, n, ST);
         }
         __syncwarp();
     } else if (warp == 16) {
         // ------------------------------------------------------------ products
-        uint32_t n = 0, it = 0, np[2] = {0, 0};
+        // One stream of steps over all items: for each of the two tiles the output of the step
+        // before, then the scores of this one, so that a tile begins the next item while the other
+        // still ends the last.
+        uint32_t j = 0, it = 0, np[2] = {0, 0};  // steps, items, probabilities taken
         const uint32_t negate = g.scale < 0.f ? kNegateA : 0u;
+        bool owed[2] = {false, false}, begun[2] = {false, false}, ends[2] = {false, false};
+        int rows = kWT;  // of the values of the step before, that lie in the sequence
+        auto settle = [&](int u, bool &got) {  // o += P v of the step before
+            if (!owed[u]) return;
+            const uint32_t s = (2 * j - 1) % ST;
+            if (!got) {
+                wait(kv_full + 8 * s, (2 * j - 1) / ST, 24);
+                if (g.lens != nullptr && rows < kWT) Tile<D>::zero_rows(skv + s * TB, rows);
+                got = true;
+            }
+            wait(p_ready + 8 * u, np[u]++, 25);
+            tc_fence_after();
+            mma_apply<D, BF, 64>(tO + 128 * u, tS + 128 * u, skv + s * TB, begun[u]);
+            begun[u] = !ends[u];
+            if (ends[u]) mma_commit_w(o_full + 8 * u);
+            owed[u] = false;
+        };
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             const FwdItem w = fwd_item(g, item, tiles);
             const int len = wa_len(g, w.b);
             const FwdTiles kt(g, w, len);
-            const int count = kt.count;
-            if (count == 0) continue;
-            bool begun[2] = {false, false};
-            wait(q_full, it, 23);
-            // step i: for each of the two tiles the output of key tile i - 1, then the scores of i
-            for (int i = 0; i <= count; ++i) {
-                const uint32_t sk = (n + 2 * i) % ST, sv = (n + 2 * i - 1) % ST;
-                const int ti = kt.tile(i), tp = kt.tile(i - 1);
+            if (kt.count == 0) continue;
+            const uint32_t qb = it & 1;
+            for (int i = 0; i < kt.count; ++i, ++j) {
+                const uint32_t s = 2 * j % ST;
+                const int tile = kt.tile(i);
                 bool got_v = false, got_k = false;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const KeyTiles &mine = u == 0 ? kt.a : kt.b;
-                    if (i > 0 && mine.has(tp)) {
-                        if (!got_v) {
-                            wait(kv_full + 8 * sv, (n + 2 * i - 1) / ST, 24);
-                            if (g.lens != nullptr && len - tp * kWT < kWT) Tile<D>::zero_rows(skv + sv * TB, len - tp * kWT);
-                            got_v = true;
-                        }
-                        wait(p_ready + 8 * u, np[u]++, 25);
-                        tc_fence_after();
-                        mma_apply<D, BF>(tO + 128 * u, tS + 128 * u, skv + sv * TB, begun[u]);
-                        begun[u] = true;
-                    }
-                    if (i < count && mine.has(ti)) {
-                        if (!got_k) wait(kv_full + 8 * sk, (n + 2 * i) / ST, 26);
-                        got_k = true;
-                        tc_fence_after();
-                        mma_scores<D, BF>(tS + 128 * u, sq + u * TB, skv + sk * TB, negate);
-                        mma_commit_w(s_full + 8 * u);
-                    }
+                    settle(u, got_v);
+                    if (!mine.has(tile)) continue;
+                    if (i == 0) wait(q_full + 8 * qb, it / 2, 23);
+                    if (!got_k) wait(kv_full + 8 * s, 2 * j / ST, 26);
+                    got_k = true;
+                    tc_fence_after();
+                    mma_scores<D, BF>(tS + 128 * u, sq + (2 * qb + u) * TB, skv + s * TB, negate);
+                    mma_commit_w(s_full + 8 * u);
+                    owed[u] = true;
+                    ends[u] = tile == mine.hi;
                 }
-                if (i > 0) mma_commit_w(kv_empty + 8 * sv);
-                if (i < count) mma_commit_w(kv_empty + 8 * sk);
-                if (i == count - 1) mma_commit_w(q_empty);
+                if (j > 0) mma_commit_w(kv_empty + 8 * ((2 * j - 1) % ST));
+                mma_commit_w(kv_empty + 8 * s);
+                rows = len - tile * kWT;
             }
-            mma_commit_w(o_full);
-            n += 2 * count;
+            mma_commit_w(q_empty + 8 * qb);
             ++it;
         }
+        bool got = false;
+        settle(0, got);
+        settle(1, got);
     } else {
         // ------------------------------------------------------------ probabilities and output
         const int u = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + (threadIdx.x & 31);
@@ -414,7 +419,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
         // the scores of a negative factor come negated, and a factor of 0 must leave masked scores at -inf
         const float c = fmaxf(fabsf(g.scale) * 1.4426950408889634f, 1e-30f);
         float *own = &s_row[u][half][row], *other = &s_row[u][half ^ 1][row];
-        uint32_t ns = 0, it = 0;
+        uint32_t ns = 0, no = 0;
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             const FwdItem w = fwd_item(g, item, tiles);
             const int len = wa_len(g, w.b), t0 = w.t0 + u * w.step_t, t = t0 + row;
@@ -450,7 +455,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
                 }
                 float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 *own = top;
-                quarter_sync<2>(id);  // also: both halves hold their scores, P may be written over them
+                quarter_sync<2>(id);
                 top = fmaxf(top, *other) * c;
                 const bool move = top > m + 8.f;
                 if (__any_sync(~0u, move)) {
@@ -483,15 +488,15 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
                         sum[j & 1] = __fadd2_rn(sum[j & 1], e);
                         p[j] = pack16<BF>(e);
                     }
-                    tmem_st16(ts + 32 * half + 16 * k, p);
+                    tmem_st16(ts + 64 * half + 16 * k, p);
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(p_ready + 8 * u);
             }
-            if (kt.count > 0) {
-                wait(o_full, it++, 28);
+            if (!first) {
+                wait(o_full + 8 * u, no++, 28);
                 tc_fence_after();
             }
             if (t0 < g.T) {  // the same for the whole tile
@@ -523,9 +528,10 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
 // scores of i + 1, and when its dS is there, dP of i + 1 and then dq += dS k.
 template <int D>
 struct DqCfg {
-    static constexpr int KST = D == 128 ? 3 : 5, VST = D == 128 ? 2 : 4;
-    static constexpr int SMEM = (2 + KST + VST) * Tile<D>::BYTES + kSmall;
-    static constexpr int THREADS = 576;  // 16 math warps, products, loads
+    // pairs of q and dO tiles: two where they fit, so that an item begins while the last one ends
+    static constexpr int QST = D == 128 ? 1 : 2, KST = D == 128 ? 3 : 5, VST = D == 128 ? 2 : 4;
+    static constexpr int SMEM = (2 * QST + KST + VST) * Tile<D>::BYTES + kSmall;
+    static constexpr int THREADS = 640;  // 16 math warps, products, loads, two for the rows' statistics
 };
 
 template <int D, bool BF>
@@ -533,20 +539,22 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
 wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, const void *__restrict__ dO,
              const float *__restrict__ lse, void *__restrict__ dq, float *__restrict__ delta, Str3 so, Str3 sg, Str3 sdq,
              WaArgs g, int items, WsHeader *hdr) {
-    constexpr int KST = DqCfg<D>::KST, VST = DqCfg<D>::VST, TB = Tile<D>::BYTES;
+    constexpr int QST = DqCfg<D>::QST, KST = DqCfg<D>::KST, VST = DqCfg<D>::VST, TB = Tile<D>::BYTES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t sq = smem_u32(smem_raw), sg_ = sq + TB, sk = sq + 2 * TB, sv = sk + KST * TB;
-    Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 + KST + VST) * TB);
-    static_assert(8 + 2 * (KST + VST) <= 32, "barriers");
-    float(*s_delta)[kWT] = reinterpret_cast<float(*)[kWT]>(sm.f);
+    const uint32_t sq = smem_u32(smem_raw), sk = sq + 2 * QST * TB, sv = sk + KST * TB;  // q, dO in turn
+    Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 * QST + KST + VST) * TB);
+    static_assert(13 + 2 * (KST + VST) <= 32, "barriers");
+    float(*s_stat)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [item's parity][delta, lse log2 e][row]
     if (misplaced(sq, hdr)) return;
     const int warp = threadIdx.x >> 5, tiles = (g.T + kWT - 1) / kWT, G = g.H / g.Hkv;
     const uint32_t b0 = smem_u32(sm.bars);
-    const uint32_t q_full = b0, q_empty = b0 + 8, acc_full = b0 + 16, dp_full = b0 + 24, s_full = b0 + 32, ds_ready = b0 + 48;
-    const uint32_t k_full = b0 + 64, k_empty = k_full + 8 * KST, v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST;
+    const uint32_t q_full = b0, q_empty = b0 + 16, acc_full = b0 + 32, dp_full = b0 + 40, s_full = b0 + 48, ds_ready = b0 + 64;
+    const uint32_t st_full = b0 + 72, st_empty = b0 + 88;  // two each, by the item's parity
+    const uint32_t k_full = b0 + 104, k_empty = k_full + 8 * KST, v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 6; ++i) mbar_init(b0 + 8 * i, 1);
+        for (int i = 0; i < 8; ++i) mbar_init(b0 + 8 * i, 1);
         mbar_init(ds_ready, 16);
+        for (int i = 0; i < 2; ++i) mbar_init(st_full + 8 * i, 2), mbar_init(st_empty + 8 * i, 16);
         for (int i = 0; i < 2 * (KST + VST); ++i) mbar_init(k_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = 0u;
@@ -554,13 +562,13 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
     const uint32_t tmem = tmem_alloc_all(&sm.tmem);
     const Waits wait{&sm.dead, hdr};
     const uint32_t tS = tmem, tP = tmem + 256, tA = tmem + 384;
-    // items: the heads of a group next to each other, then the tiles
+    // items: all heads of the last tile, then of the one before it (as in the forward)
     auto place = [&](int item, int &b, int &h, int &hk, int &t0) {
-        const int gi = item % G, r = item / G, bh = r / tiles;
-        t0 = r % tiles * kWT;
-        hk = bh % g.Hkv;
-        b = bh / g.Hkv;
-        h = hk * G + gi;
+        const int bh = item % (g.B * g.H);
+        t0 = (tiles - 1 - item / (g.B * g.H)) * kWT;
+        b = bh / g.H;
+        h = bh % g.H;
+        hk = h / G;
     };
 
     if (warp == 17) {
@@ -572,11 +580,12 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 const KeyTiles kt = key_tiles(g, t0, wa_len(g, b));
                 if (kt.hi < kt.lo) continue;
                 const int ns = min(kt.sinks, kt.lo), count = kt.hi - kt.lo + 1 + ns;
-                if (it > 0) wait(q_empty, it - 1, 31);
+                const uint32_t qb = it % QST;
+                if (it >= QST) wait(q_empty + 8 * qb, it / QST - 1, 31);
                 if (*wait.dead != 0u) break;
-                mbar_expect_tx(q_full, 2 * TB);
-                Tile<D>::load(sq, &maps.q, t0, h, b, q_full);
-                Tile<D>::load(sg_, &maps.g, t0, h, b, q_full);
+                mbar_expect_tx(q_full + 8 * qb, 2 * TB);
+                Tile<D>::load(sq + 2 * qb * TB, &maps.q, t0, h, b, q_full + 8 * qb);
+                Tile<D>::load(sq + (2 * qb + 1) * TB, &maps.g, t0, h, b, q_full + 8 * qb);
                 for (int i = 0; i < count; ++i, ++n) {
                     const int s0 = (i < ns ? i : kt.lo + i - ns) * kWT;
                     const uint32_t a = n % KST, c = n % VST;
@@ -590,7 +599,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 }
                 ++it;
             }
-            if (*wait.dead != 0u) drain(q_full, it, 1), drain(k_full, n, KST), drain(v_full, n, VST);
+            if (*wait.dead != 0u) drain(q_full, it, QST), drain(k_full, n, KST), drain(v_full, n, VST);
         }
         __syncwarp();
     } else if (warp == 16) {
@@ -602,22 +611,23 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
             const KeyTiles kt = key_tiles(g, t0, len);
             if (kt.hi < kt.lo) continue;
             const int ns = min(kt.sinks, kt.lo), count = kt.hi - kt.lo + 1 + ns;
+            const uint32_t qb = it % QST;
             auto scores = [&](uint32_t j, int i) {  // key tile i of the item, number j of the block
                 wait(k_full + 8 * (j % KST), j / KST, 34);
                 const int left = len - (i < ns ? i : kt.lo + i - ns) * kWT;
                 if (g.lens != nullptr && left < kWT) Tile<D>::zero_rows(sk + (j % KST) * TB, left);
                 tc_fence_after();
-                mma_scores<D, BF>(tS + 128 * (j & 1), sq, sk + (j % KST) * TB);
+                mma_scores<D, BF>(tS + 128 * (j & 1), sq + 2 * qb * TB, sk + (j % KST) * TB);
                 mma_commit_w(s_full + 8 * (j & 1));
             };
             auto grads = [&](uint32_t j) {
                 wait(v_full + 8 * (j % VST), j / VST, 35);
                 tc_fence_after();
-                mma_scores<D, BF>(tP, sg_, sv + (j % VST) * TB);
+                mma_scores<D, BF>(tP, sq + (2 * qb + 1) * TB, sv + (j % VST) * TB);
                 mma_commit_w(dp_full);
                 mma_commit_w(v_empty + 8 * (j % VST));
             };
-            wait(q_full, it, 36);
+            wait(q_full + 8 * qb, it / QST, 36);
             scores(n, 0);
             grads(n);
             for (int i = 0; i < count; ++i, ++n) {
@@ -625,46 +635,76 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 wait(ds_ready, n, 37);
                 tc_fence_after();
                 if (i + 1 < count) grads(n + 1);
-                if (i + 1 == count) mma_commit_w(q_empty);
-                mma_apply<D, BF>(tA, tS + 128 * (n & 1), sk + (n % KST) * TB, i > 0);
+                if (i + 1 == count) mma_commit_w(q_empty + 8 * qb);
+                mma_apply<D, BF, 32>(tA, tS + 128 * (n & 1), sk + (n % KST) * TB, i > 0);
                 mma_commit_w(k_empty + 8 * (n % KST));
             }
             mma_commit_w(acc_full);
             ++it;
         }
+    } else if (warp >= 18) {
+        // ------------------------------------------------------------ delta = dO . o and lse of the next item's rows
+        // A warp takes 64 rows, D / 8 lanes a row (16 bytes each), eight rows in flight a lane.
+        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an access
+        const int lane = threadIdx.x & 31, first = (warp - 18) * 64 + lane / LPR, col = lane % LPR * 8;
+        uint32_t all = 0;
+        for (int item = blockIdx.x; item < items; item += gridDim.x, ++all) {
+            int b, h, hk, t0;
+            place(item, b, h, hk, t0);
+            const int len = wa_len(g, b);
+            const uint16_t *x = static_cast<const uint16_t *>(o) + b * so.b + h * so.h + col;
+            const uint16_t *y = static_cast<const uint16_t *>(dO) + b * sg.b + h * sg.h + col;
+            const long long at = ((long long)b * g.H + h) * g.T;
+            if (all > 1) wait(st_empty + 8 * (all & 1), all / 2 - 1, 42);
+            float *dst = s_stat[all & 1][0], *dst2 = s_stat[all & 1][1];
+            for (int r0 = 0; r0 < 64; r0 += 8 * RPI) {
+                uint4 xv[8], yv[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int t = t0 + first + r0 + k * RPI;
+                    xv[k] = t < len ? __ldg(reinterpret_cast<const uint4 *>(x + t * so.t)) : make_uint4(0u, 0u, 0u, 0u);
+                    yv[k] = t < len ? __ldg(reinterpret_cast<const uint4 *>(y + t * sg.t)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t aw[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w}, ew[4] = {yv[k].x, yv[k].y, yv[k].z, yv[k].w};
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 p = unpack16<BF>(aw[j]), q = unpack16<BF>(ew[j]);
+                        sum = fmaf(p.x, q.x, fmaf(p.y, q.y, sum));
+                    }
+#pragma unroll
+                    for (int s = LPR / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
+                    const int row = first + r0 + k * RPI, t = t0 + row;
+                    if (lane % LPR == 0) {
+                        dst[row] = sum;
+                        if (t < g.T) delta[at + t] = sum;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int row = (warp - 18) * 64 + lane + 32 * k, t = t0 + row;
+                dst2[row] = t < len ? __ldg(lse + at + t) * 1.4426950408889634f : INFINITY;
+            }
+            warp_arrive(st_full + 8 * (all & 1));
+        }
     } else {
         const int part = warp >> 2, quarter = warp & 3, row = quarter * 32 + (threadIdx.x & 31);  // columns 32 part ..
         const uint32_t lanes = (uint32_t)quarter << 21;
         const float c = g.scale * 1.4426950408889634f;
-        uint32_t n = 0, it = 0;
+        uint32_t n = 0, it = 0, all = 0;
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             int b, h, hk, t0;
             place(item, b, h, hk, t0);
             const int len = wa_len(g, b), t = t0 + row;
             const KeyTiles kt = key_tiles(g, t0, len);
             const bool live = t < len;
-            const long long at = ((long long)b * g.H + h) * g.T + t;
-            // delta = dO . o of the row, a quarter of the columns by each of its four threads
-            float sum = 0.f;
-            if (live) {
-                const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(o) + b * so.b + h * so.h + t * so.t) + part * (D / 32);
-                const uint4 *y = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(dO) + b * sg.b + h * sg.h + t * sg.t) + part * (D / 32);
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                    const uint4 a = __ldg(x + k), e = __ldg(y + k);
-                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, ew[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 p = unpack16<BF>(aw[j]), q = unpack16<BF>(ew[j]);
-                        sum = fmaf(p.x, q.x, fmaf(p.y, q.y, sum));
-                    }
-                }
-            }
-            s_delta[part][row] = sum;
-            quarter_sync<4>(1 + quarter);
-            const float dl = (s_delta[0][row] + s_delta[1][row]) + (s_delta[2][row] + s_delta[3][row]);
-            const float ls = live ? lse[at] * 1.4426950408889634f : INFINITY;
-            if (part == 0 && t < g.T) delta[at] = dl;
+            wait(st_full + 8 * (all & 1), all / 2, 41);
+            const float dl = s_stat[all & 1][0][row], ls = s_stat[all & 1][1][row];
+            warp_arrive(st_empty + 8 * (all & 1));
+            ++all;
             const int ns = min(kt.sinks, kt.lo), count = kt.hi < kt.lo ? 0 : kt.hi - kt.lo + 1 + ns;
             for (int i = 0; i < count; ++i, ++n) {
                 const int s0 = (i < ns ? i : kt.lo + i - ns) * kWT;
@@ -695,9 +735,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 }
 #pragma unroll
                 for (int k = 0; k < 16; ++k) ds[k] = pack16<BF>(x[k]);
-                // the threads of a row write where others of them have read scores
-                quarter_sync<4>(1 + quarter);
-                tmem_st16(ts + 16 * part, ds);
+                tmem_st16(ts + 32 * part, ds);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(ds_ready);
@@ -711,51 +749,185 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 zero_row<D / 4>(dq, out);
             }
             tc_fence_before();
-            quarter_sync<4>(1 + quarter);  // s_delta is free
         }
     }
     tmem_free_all(tmem);
 }
 
 // ------------------------------------------------------------------ backward: dk, dv
-// One key tile at a time against the query tiles that see it, head by head of the group.  The
-// scores are transposed (a row is a key), so that P^T and dS^T are A operands from tensor memory:
-// S^T = K Q^T, dP^T = V dO^T, dv += P^T dO, dk += dS^T Q, with P^T over S^T and dS^T over dP^T.
-// Each half of the elementwise work runs beside two products: forming P beside dk += and the next
-// dP, forming dS beside dv += and the next S.  A tile with sinks is seen by every later query
-// tile: its list is cut into pieces that leave fp32 partial sums, joined in their order.
+// A key tile against the query tiles that see it, head by head of the group.  The scores are
+// transposed (a row is a key), so that P^T and dS^T are A operands from tensor memory: S^T = K Q^T,
+// dP^T = V dO^T, dv += P^T dO, dk += dS^T Q, with P^T over S^T and dS^T over dP^T.  Each half of
+// the elementwise work runs beside two products: forming P beside dk += and the next dP, forming
+// dS beside dv += and the next S.
+//
+// The lists of the key tiles, one behind the other (sequence, key head, tile), are cut into equal
+// shares, one a block: few tiles with long lists (sinks are seen by every later query) and a
+// number of tiles that the blocks do not divide cost nothing.  A list that is cut leaves fp32
+// partial sums, which wa_join_kernel adds in their order; where the cuts are depends on the sizes
+// and lengths alone.
 template <int D>
 struct DkvCfg {
-    static constexpr int ST = D == 128 ? 2 : 4;
-    static constexpr int SMEM = (2 + 2 * ST) * Tile<D>::BYTES + kSmall;
+    // stages of q and dO each, and pairs of k and v tiles: two where they fit, so that a list
+    // begins while the last one ends
+    static constexpr int ST = D == 128 ? 2 : 4, KVST = D == 128 ? 1 : 2;
+    static constexpr int SMEM = (2 * KVST + 2 * ST) * Tile<D>::BYTES + kSmall;
     static constexpr int THREADS = 608;  // 16 math warps, products, loads, statistics
 };
 
-struct DkvPlan {
-    int sink_tiles, pieces, piece;  // tiles that are cut, pieces of each, query tiles of a piece
-    float *part;                    // [b][hk][sink tile][piece][dk, dv][128][D]
+// The lists of a sequence of n tiles: tile k is seen by n - k query tiles if it has sinks (k < st),
+// else by at most `span` of them.
+struct Lists {
+    int n, st, span;
+    __host__ __device__ __forceinline__ Lists(int len, int window, int sinks)
+        : n((int)(((long long)len + kWT - 1) / kWT)), st(0), span((int)(((long long)window + kWT - 2) / kWT) + 1) {
+        st = (int)(((long long)sinks + kWT - 1) / kWT);
+        if (st > n) st = n;
+    }
+    __host__ __device__ __forceinline__ int of(int k) const { return k < st || n - k < span ? n - k : span; }
+    __host__ __device__ __forceinline__ long long all(long long x) const { return x * n - x * (x - 1) / 2; }
+    __host__ __device__ __forceinline__ long long banded(long long x) const {
+        const long long full = n - span + 1 > 0 ? n - span + 1 : 0;
+        return x <= full ? x * span : full * span + all(x) - all(full);
+    }
+    __host__ __device__ __forceinline__ long long before(int k) const {  // query tiles in the lists of tiles below k
+        return k <= st ? all(k) : all(st) + banded(k) - banded(st);
+    }
+};
+
+// A place in the chain of lists: step i of `tile`'s (query tile tile + i % f of head i / f).
+struct Place {
+    int b, hk, tile, i;
+};
+// The whole chain's length, and the place of its step `pos`; by one warp, the result in all lanes.
+__device__ __forceinline__ long long chain_length(const WaArgs &g) {
+    if (g.lens == nullptr) {
+        const Lists l(g.T, g.window, g.sinks);
+        return (long long)g.B * g.H * l.before(l.n);
+    }
+    long long sum = 0;
+    for (int b = threadIdx.x & 31; b < g.B; b += 32) {
+        const Lists l(wa_len(g, b), g.window, g.sinks);
+        sum += g.H * l.before(l.n);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    return sum;
+}
+__device__ __forceinline__ Place chain_place(const WaArgs &g, long long pos) {
+    Place p{0, 0, 0, 0};
+    if (g.lens == nullptr) {
+        const Lists l(g.T, g.window, g.sinks);
+        const long long u = g.H * l.before(l.n);
+        p.b = (int)(pos / u);
+        pos -= p.b * u;
+    } else {
+        for (int b = 0; b < g.B; b += 32) {
+            const int mine = b + (threadIdx.x & 31);
+            long long u = 0;
+            if (mine < g.B) {
+                const Lists l(wa_len(g, mine), g.window, g.sinks);
+                u = g.H * l.before(l.n);
+            }
+            long long run = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(~0u, run, o);
+                if ((int)(threadIdx.x & 31) >= o) run += x;
+            }
+            const unsigned int in = __ballot_sync(~0u, pos < run);
+            if (in != 0u) {
+                const int at = __ffs(in) - 1;
+                p.b = b + at;
+                pos -= __shfl_sync(~0u, run - u, at);
+                break;
+            }
+            pos -= __shfl_sync(~0u, run, 31);
+        }
+    }
+    const Lists l(wa_len(g, p.b), g.window, g.sinks);
+    const int G = g.H / g.Hkv;
+    const long long head = G * l.before(l.n);
+    p.hk = (int)(pos / head);
+    pos -= p.hk * head;
+    int lo = 0, hi = l.n - 1;  // the last tile whose list begins at or before pos
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (G * l.before(mid) <= pos) lo = mid;
+        else hi = mid - 1;
+    }
+    p.tile = lo;
+    p.i = (int)(pos - G * l.before(lo));
+    return p;
+}
+// Walks a block's share, a tile's part of it at a time: steps [i0, i1) of `list` of that tile.
+struct Walk {
+    const WaArgs &g;
+    long long left;
+    Place p;
+    int len, f, i0, i1, list;
+    __device__ __forceinline__ Walk(const WaArgs &a, const Place &start, long long steps) : g(a), left(steps), p(start), i1(start.i), list(0) {
+        len = wa_len(g, p.b);
+    }
+    __device__ __forceinline__ bool next() {
+        if (left <= 0) return false;
+        if (list != 0) {  // not the first: the tile before was walked to its end
+            i1 = 0;
+            if (++p.tile * (long long)kWT >= len) {
+                p.tile = 0;
+                if (++p.hk == g.Hkv) {
+                    p.hk = 0;
+                    do len = wa_len(g, ++p.b);
+                    while (len == 0);
+                }
+            }
+        }
+        const Lists l(len, g.window, g.sinks);
+        f = l.of(p.tile);
+        list = f * (g.H / g.Hkv);
+        i0 = i1;
+        i1 = left < list - i0 ? i0 + (int)left : list;
+        left -= i1 - i0;
+        return true;
+    }
+};
+
+// What a block tells wa_join_kernel: the tile whose list it leaves before its end (tile < 0: none;
+// its sums are part 1), and whether it joins a list after its start (part 0), and ends it.
+struct CutList {
+    int b, hk, tile;
+    int joins;  // 0: no, 1: and leaves it before its end too, 2: to its end
 };
 
 template <int D, bool BF>
 __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
 wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse, const float *__restrict__ delta,
-              void *__restrict__ dk, void *__restrict__ dv, Str3 sdk, Str3 sdv, WaArgs g, DkvPlan pl, int items,
-              WsHeader *hdr) {
-    constexpr int ST = DkvCfg<D>::ST, TB = Tile<D>::BYTES;
+              void *__restrict__ dk, void *__restrict__ dv, float *__restrict__ parts, CutList *__restrict__ cuts, Str3 sdk,
+              Str3 sdv, WaArgs g, WsHeader *hdr) {
+    constexpr int ST = DkvCfg<D>::ST, KVST = DkvCfg<D>::KVST, TB = Tile<D>::BYTES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t sk = smem_u32(smem_raw), sv = sk + TB, sq = sk + 2 * TB, sg = sq + ST * TB;
-    Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 + 2 * ST) * TB);
-    static_assert(8 + 4 * ST + 4 <= 32, "barriers");
+    const uint32_t sk = smem_u32(smem_raw), sq = sk + 2 * KVST * TB, sg = sq + ST * TB;  // k, v in turn
+    Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 * KVST + 2 * ST) * TB);
+    static_assert(10 + 4 * ST + 4 <= 32, "barriers");
     float(*s_stat)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [slot][lse log2 e, delta][query]
     if (misplaced(sk, hdr)) return;
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, G = g.H / g.Hkv;
     const uint32_t b0 = smem_u32(sm.bars);
-    const uint32_t kv_full = b0, kv_empty = b0 + 8, acc_full = b0 + 16, s_full = b0 + 24, dp_full = b0 + 32;
-    const uint32_t p_ready = b0 + 40, ds_ready = b0 + 48;
-    const uint32_t q_full = b0 + 64, q_empty = q_full + 8 * ST, g_full = q_empty + 8 * ST, g_empty = g_full + 8 * ST;
+    const uint32_t kv_full = b0, kv_empty = b0 + 16, acc_full = b0 + 32, s_full = b0 + 40, dp_full = b0 + 48;
+    const uint32_t p_ready = b0 + 56, ds_ready = b0 + 64;
+    const uint32_t q_full = b0 + 80, q_empty = q_full + 8 * ST, g_full = q_empty + 8 * ST, g_empty = g_full + 8 * ST;
     const uint32_t st_full = g_empty + 8 * ST, st_empty = st_full + 16;
+    if (warp == 1) {  // this block's share of the chain
+        const long long total = chain_length(g), p0 = total * blockIdx.x / gridDim.x, p1 = total * (blockIdx.x + 1) / gridDim.x;
+        Place p{0, 0, 0, 0};
+        if (p1 > p0) p = chain_place(g, p0);
+        if (threadIdx.x == 32) {
+            *reinterpret_cast<Place *>(sm.pad) = p;
+            *reinterpret_cast<long long *>(sm.pad + 4) = p1 - p0;
+        }
+    }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(b0 + 8 * i, 1);
+        for (int i = 0; i < 7; ++i) mbar_init(b0 + 8 * i, 1);
         mbar_init(p_ready, 16);
         mbar_init(ds_ready, 16);
         for (int i = 0; i < 4 * ST; ++i) mbar_init(q_full + 8 * i, 1);
@@ -766,72 +938,55 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
     const uint32_t tmem = tmem_alloc_all(&sm.tmem);
     const Waits wait{&sm.dead, hdr};
     const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
-    const int tiles = (g.T + kWT - 1) / kWT, G = g.H / g.Hkv;
-    const int per = pl.sink_tiles * pl.pieces + (tiles - pl.sink_tiles);  // items of a (batch, key head)
-    struct Item {
-        int b, hk, tile, piece, nq, i0, i1;  // piece < 0: whole; query tiles tile + i % nq of head i / nq, i in [i0, i1)
-        int len;
+    Walk w(g, *reinterpret_cast<const Place *>(sm.pad), *reinterpret_cast<const long long *>(sm.pad + 4));
+    // the head and the query tile of a step, without a division in the loops
+    struct Step {
+        int h, qt;
     };
-    auto place = [&](int item) {
-        Item w;
-        const int bh = item / per, r = item % per;
-        w.b = bh / g.Hkv;
-        w.hk = bh % g.Hkv;
-        const bool cut = r < pl.sink_tiles * pl.pieces;
-        w.tile = cut ? r / pl.pieces : r - pl.sink_tiles * (pl.pieces - 1);
-        w.piece = cut ? r % pl.pieces : -1;
-        w.len = wa_len(g, w.b);
-        const int s0 = w.tile * kWT;
-        if (s0 >= w.len) {
-            w.nq = w.i0 = w.i1 = 0;
-            return w;
-        }
-        // the last query that the tile's last key is in the window of, where the sequence reaches it
-        const int room = w.len - 1 - s0, reach = kWT - 1 + g.window - 1;
-        w.nq = (s0 + (s0 < g.sinks || reach < 0 || reach > room ? room : reach)) / kWT - w.tile + 1;
-        w.i0 = cut ? min(w.piece * pl.piece, G * w.nq) : 0;
-        w.i1 = cut ? min(w.i0 + pl.piece, G * w.nq) : G * w.nq;
-        return w;
+    auto first_step = [&]() { return Step{w.p.hk * G + w.i0 / w.f, w.p.tile + w.i0 % w.f}; };
+    auto advance = [&](Step &s) {
+        if (++s.qt == w.p.tile + w.f) s.qt = w.p.tile, ++s.h;
     };
 
     if (warp == 17) {
         if ((threadIdx.x & 31) == 0) {
             uint32_t n = 0, it = 0;
-            for (int item = blockIdx.x; item < items; item += gridDim.x) {
-                const Item w = place(item);
-                if (w.i0 >= w.i1) continue;
-                if (it > 0) wait(kv_empty, it - 1, 41);
+            while (w.next()) {
+                const uint32_t kb = it % KVST;
+                if (it >= KVST) wait(kv_empty + 8 * kb, it / KVST - 1, 51);
                 if (*wait.dead != 0u) break;
-                mbar_expect_tx(kv_full, 2 * TB);
-                Tile<D>::load(sk, &maps.k, w.tile * kWT, w.hk, w.b, kv_full);
-                Tile<D>::load(sv, &maps.v, w.tile * kWT, w.hk, w.b, kv_full);
-                for (int i = w.i0; i < w.i1; ++i, ++n) {
+                mbar_expect_tx(kv_full + 8 * kb, 2 * TB);
+                Tile<D>::load(sk + 2 * kb * TB, &maps.k, w.p.tile * kWT, w.p.hk, w.p.b, kv_full + 8 * kb);
+                Tile<D>::load(sk + (2 * kb + 1) * TB, &maps.v, w.p.tile * kWT, w.p.hk, w.p.b, kv_full + 8 * kb);
+                Step x = first_step();
+                for (int i = w.i0; i < w.i1; ++i, ++n, advance(x)) {
                     const uint32_t s = n % ST;
-                    const int t0 = (w.tile + i % w.nq) * kWT;
-                    const int h = w.hk * G + i / w.nq;
                     if (n >= ST) wait(q_empty + 8 * s, n / ST - 1, 42);
                     if (*wait.dead != 0u) break;
                     mbar_expect_tx(q_full + 8 * s, TB);
-                    Tile<D>::load(sq + s * TB, &maps.q, t0, h, w.b, q_full + 8 * s);
+                    Tile<D>::load(sq + s * TB, &maps.q, x.qt * kWT, x.h, w.p.b, q_full + 8 * s);
                     if (n >= ST) wait(g_empty + 8 * s, n / ST - 1, 43);
                     mbar_expect_tx(g_full + 8 * s, TB);
-                    Tile<D>::load(sg + s * TB, &maps.g, t0, h, w.b, g_full + 8 * s);
+                    Tile<D>::load(sg + s * TB, &maps.g, x.qt * kWT, x.h, w.p.b, g_full + 8 * s);
                 }
                 ++it;
             }
-            if (*wait.dead != 0u) drain(kv_full, it, 1), drain(q_full, n, ST), drain(g_full, n, ST);
+            if (*wait.dead != 0u) drain(kv_full, it, KVST), drain(q_full, n, ST), drain(g_full, n, ST);
         }
         __syncwarp();
     } else if (warp == 18) {
         // ------------------------------------------------------------ the rows' statistics, a tile ahead
         const int lane = threadIdx.x & 31;
         uint32_t n = 0;
-        for (int item = blockIdx.x; item < items; item += gridDim.x) {
-            const Item w = place(item);
-            for (int i = w.i0; i < w.i1; ++i, ++n) {
+        CutList cut{0, 0, -1, 0};
+        while (w.next()) {
+            if (w.i0 > 0) cut.joins = w.i1 < w.list ? 1 : 2;
+            else if (w.i1 < w.list) cut.b = w.p.b, cut.hk = w.p.hk, cut.tile = w.p.tile;
+            Step x = first_step();
+            for (int i = w.i0; i < w.i1; ++i, ++n, advance(x)) {
                 const uint32_t s = n & 1;
-                const int t0 = (w.tile + i % w.nq) * kWT;
-                const long long at = ((long long)w.b * g.H + w.hk * G + i / w.nq) * g.T + t0;
+                const int t0 = x.qt * kWT;
+                const long long at = ((long long)w.p.b * g.H + x.h) * g.T + t0;
                 float a[4], d[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -849,46 +1004,46 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                 warp_arrive(st_full + 8 * s);
             }
         }
+        if (lane == 0) cuts[blockIdx.x] = cut;
     } else if (warp == 16) {
         uint32_t n = 0, it = 0;
-        for (int item = blockIdx.x; item < items; item += gridDim.x) {
-            const Item w = place(item);
-            if (w.i0 >= w.i1) continue;
-            auto scores = [&](uint32_t j, int i) {
+        while (w.next()) {
+            const uint32_t kb = it % KVST, kt = sk + 2 * kb * TB;
+            auto scores = [&](uint32_t j, int qt) {
                 const uint32_t s = j % ST;
                 wait(q_full + 8 * s, j / ST, 45);
-                const int left = w.len - (w.tile + i % w.nq) * kWT;
-                if (g.lens != nullptr && left < kWT) Tile<D>::zero_rows(sq + s * TB, left);
+                if (g.lens != nullptr && w.len - qt * kWT < kWT) Tile<D>::zero_rows(sq + s * TB, w.len - qt * kWT);
                 tc_fence_after();
-                mma_scores<D, BF>(tS, sk, sq + s * TB);
+                mma_scores<D, BF>(tS, kt, sq + s * TB);
                 mma_commit_w(s_full);
             };
-            auto grads = [&](uint32_t j, int i) {
+            auto grads = [&](uint32_t j, int qt) {
                 const uint32_t s = j % ST;
                 wait(g_full + 8 * s, j / ST, 46);
-                const int left = w.len - (w.tile + i % w.nq) * kWT;
-                if (g.lens != nullptr && left < kWT) Tile<D>::zero_rows(sg + s * TB, left);
+                if (g.lens != nullptr && w.len - qt * kWT < kWT) Tile<D>::zero_rows(sg + s * TB, w.len - qt * kWT);
                 tc_fence_after();
-                mma_scores<D, BF>(tP, sv, sg + s * TB);
+                mma_scores<D, BF>(tP, kt + TB, sg + s * TB);
                 mma_commit_w(dp_full);
             };
-            wait(kv_full, it, 47);
-            scores(n, w.i0);
-            grads(n, w.i0);
+            Step x = first_step();
+            wait(kv_full + 8 * kb, it / KVST, 47);
+            scores(n, x.qt);
+            grads(n, x.qt);
             for (int i = w.i0; i < w.i1; ++i, ++n) {
                 const uint32_t s = n % ST;
+                advance(x);  // to step i + 1
                 wait(p_ready, n, 48);
                 tc_fence_after();
-                mma_apply<D, BF>(tV, tS, sg + s * TB, i > w.i0);
+                mma_apply<D, BF, 32>(tV, tS, sg + s * TB, i > w.i0);
                 mma_commit_w(g_empty + 8 * s);
-                if (i + 1 < w.i1) scores(n + 1, i + 1);
+                if (i + 1 < w.i1) scores(n + 1, x.qt);
                 wait(ds_ready, n, 49);
                 tc_fence_after();
-                mma_apply<D, BF>(tK, tP, sq + s * TB, i > w.i0);
+                mma_apply<D, BF, 32>(tK, tP, sq + s * TB, i > w.i0);
                 mma_commit_w(q_empty + 8 * s);
-                if (i + 1 < w.i1) grads(n + 1, i + 1);
+                if (i + 1 < w.i1) grads(n + 1, x.qt);
             }
-            mma_commit_w(kv_empty);
+            mma_commit_w(kv_empty + 8 * kb);
             mma_commit_w(acc_full);
             ++it;
         }
@@ -896,12 +1051,14 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
         const int part = warp >> 2, quarter = warp & 3, row = quarter * 32 + (threadIdx.x & 31);  // queries 32 part ..
         const uint32_t lanes = (uint32_t)quarter << 21;
         const float c = g.scale * 1.4426950408889634f;
+        // dk by the first eight warps, dv by the others, half of the columns each
+        const int which = part >> 1, col = (part & 1) * (D / 2);
         uint32_t n = 0, it = 0;
-        for (int item = blockIdx.x; item < items; item += gridDim.x) {
-            const Item w = place(item);
-            const int s0 = w.tile * kWT, key = s0 + row;
-            for (int i = w.i0; i < w.i1; ++i, ++n) {
-                const int t0 = (w.tile + i % w.nq) * kWT;
+        while (w.next()) {
+            const int s0 = w.p.tile * kWT, key = s0 + row;
+            Step st = first_step();
+            for (int i = w.i0; i < w.i1; ++i, ++n, advance(st)) {
+                const int t0 = st.qt * kWT;
                 const uint32_t sl = n & 1;
                 wait(st_full + 8 * sl, n >> 1, 50);
                 wait(s_full, n, 51);
@@ -928,8 +1085,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                 }
 #pragma unroll
                 for (int k = 0; k < 16; ++k) p[k] = pack16<BF>(x[k]);
-                quarter_sync<4>(1 + quarter);  // the threads of a row write where others of them have read
-                tmem_st16(tS + lanes + 16 * part, p);
+                tmem_st16(tS + lanes + 32 * part, p);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(p_ready);
@@ -944,73 +1100,91 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                     p[2 * k] = pack16<BF>(__fmul2_rn(x[2 * k], __fadd2_rn(y[2 * k], make_float2(-z.x, -z.y))));
                     p[2 * k + 1] = pack16<BF>(__fmul2_rn(x[2 * k + 1], __fadd2_rn(y[2 * k + 1], make_float2(-z.z, -z.w))));
                 }
-                quarter_sync<4>(1 + quarter);
-                tmem_st16(tP + lanes + 16 * part, p);
+                tmem_st16(tP + lanes + 32 * part, p);
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(ds_ready);
                 warp_arrive(st_empty + 8 * sl);
             }
-            const bool any = w.i0 < w.i1, write = key < g.T, zero = key >= w.len;
-            if (any) {
-                wait(acc_full, it++, 53);
-                tc_fence_after();
-            }
-            // dk by the first eight warps, dv by the others, half of the columns each
-            const int which = part >> 1, col = (part & 1) * (D / 2);
+            const bool write = key < g.T, zero = key >= w.len;
+            wait(acc_full, it++, 53);
+            tc_fence_after();
             const uint32_t acc = (which == 0 ? tK : tV) + lanes + col;
             const float f = which == 0 ? g.scale : 1.f;
-            if (w.piece < 0) {
-                void *out = which == 0 ? dk : dv;
+            if (w.i0 == 0 && w.i1 == w.list) {
                 const Str3 st = which == 0 ? sdk : sdv;
-                const long long at = w.b * st.b + w.hk * st.h + key * st.t + col;
-                if (any) store_row<D / 2, BF>(acc, out, at, f, write, zero);
-                else if (write) zero_row<D / 2>(out, at);
+                store_row<D / 2, BF>(acc, which == 0 ? dk : dv, w.p.b * st.b + w.p.hk * st.h + key * st.t + col, f, write, zero);
             } else {
+                // part 0 of a block: a list it joins after its start; part 1: one it leaves before its end
                 float4 *p = reinterpret_cast<float4 *>(
-                    pl.part + (((((long long)w.b * g.Hkv + w.hk) * pl.sink_tiles + w.tile) * pl.pieces + w.piece) * 2 + which) * (kWT * D) + row * D + col);
+                    parts + ((2ll * blockIdx.x + (w.i0 > 0 ? 0 : 1)) * 2 + which) * (kWT * D) + row * D + col);
 #pragma unroll
-                for (int k = 0; k < D / 2; k += 32) {
-                    uint32_t r[32];
-                    if (any) {
-                        tmem_ld32(acc + k, r);
-                        tmem_ld_wait();
-                    }
+                for (int k = 0; k < D / 2; k += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(acc + k, r);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        p[k / 4 + j] = any && !zero ? make_float4(__uint_as_float(r[4 * j]) * f, __uint_as_float(r[4 * j + 1]) * f,
-                                                                  __uint_as_float(r[4 * j + 2]) * f, __uint_as_float(r[4 * j + 3]) * f)
-                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int j = 0; j < 4; ++j)
+                        p[k / 4 + j] = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                            : make_float4(__uint_as_float(r[4 * j]) * f, __uint_as_float(r[4 * j + 1]) * f,
+                                                          __uint_as_float(r[4 * j + 2]) * f, __uint_as_float(r[4 * j + 3]) * f);
                 }
             }
             tc_fence_before();
+        }
+        // the tiles behind a sequence's length, which are in no list
+        if (g.lens != nullptr) {
+            const int tiles = (g.T + kWT - 1) / kWT;
+            const long long units = (long long)g.B * g.Hkv * tiles;
+            for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+                const int tile = (int)(u % tiles), hk = (int)(u / tiles % g.Hkv), b = (int)(u / tiles / g.Hkv);
+                const int key = tile * kWT + row;
+                if (tile * kWT < wa_len(g, b) || key >= g.T) continue;
+                const Str3 st = which == 0 ? sdk : sdv;
+                zero_row<D / 2>(which == 0 ? dk : dv, b * st.b + hk * st.h + key * st.t + col);
+            }
         }
     }
     tmem_free_all(tmem);
 }
 
-// Adds the pieces of the cut tiles in their order: a thread for two columns of a row of dk or dv.
+// Adds the parts of a list that was cut, in their order: block (x, y) those of the list that block x
+// of wa_dkv_kernel left, y a share of them.
+constexpr int kJoinY = 8;
 template <int D, bool BF>
-__global__ void wa_join_kernel(void *__restrict__ dk, void *__restrict__ dv, Str3 sdk, Str3 sdv, WaArgs g, DkvPlan pl) {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    constexpr int C = D / 2;
-    const int col = (int)(i % C), row = (int)(i / C % kWT), which = (int)(i / C / kWT % 2);
-    const long long u = i / C / kWT / 2;
-    const int tile = (int)(u % pl.sink_tiles);
-    const long long bh = u / pl.sink_tiles;
-    if (bh >= (long long)g.B * g.Hkv) return;
-    const long long key = (long long)tile * kWT + row;
-    if (key >= g.T) return;
-    const float2 *p = reinterpret_cast<const float2 *>(pl.part + ((u * pl.pieces * 2 + which) * kWT + row) * D) + col;
-    float2 s = make_float2(0.f, 0.f);
-    for (int k = 0; k < pl.pieces; ++k) {
-        const float2 x = p[(long long)k * (kWT * D)];
-        s.x += x.x;
-        s.y += x.y;
+__global__ void __launch_bounds__(256) wa_join_kernel(const float *__restrict__ parts, const CutList *__restrict__ cuts,
+                                                      void *__restrict__ dk, void *__restrict__ dv, Str3 sdk, Str3 sdv, int T,
+                                                      int blocks) {
+    const int x0 = blockIdx.x;
+    const CutList c = cuts[x0];
+    if (c.tile < 0) return;
+    constexpr int C = D / 4, N = 2 * kWT * C, PER = N / (256 * kJoinY);
+    const float4 *src = reinterpret_cast<const float4 *>(parts);
+    const int i0 = blockIdx.y * 256 + threadIdx.x;
+    float4 s[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) s[k] = src[(2ll * x0 + 1) * N + i0 + k * 256 * kJoinY];
+    for (int x = x0 + 1; x < blocks; ++x) {
+        const int joins = cuts[x].joins;
+        if (joins == 0) continue;  // a block without a share
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const float4 y = src[2ll * x * N + i0 + k * 256 * kJoinY];
+            s[k].x += y.x;
+            s[k].y += y.y;
+            s[k].z += y.z;
+            s[k].w += y.w;
+        }
+        if (joins == 2) break;
     }
-    const Str3 st = which == 0 ? sdk : sdv;
-    uint16_t *out = static_cast<uint16_t *>(which == 0 ? dk : dv);
-    *reinterpret_cast<uint32_t *>(out + (bh / g.Hkv) * st.b + (bh % g.Hkv) * st.h + key * st.t + 2 * col) = pack16<BF>(s);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int i = i0 + k * 256 * kJoinY, col = i % C, row = i / C % kWT, which = i / C / kWT, key = c.tile * kWT + row;
+        if (key >= T) continue;
+        const Str3 st = which == 0 ? sdk : sdv;
+        uint16_t *out = static_cast<uint16_t *>(which == 0 ? dk : dv) + c.b * st.b + c.hk * st.h + key * st.t + 4 * col;
+        *reinterpret_cast<uint2 *>(out) = make_uint2(pack16<BF>(make_float2(s[k].x, s[k].y)), pack16<BF>(make_float2(s[k].z, s[k].w)));
+    }
 }
 
 // 4-D map over [B][heads][T][d] with the tensor's own strides, boxes of 64 columns x 128 tokens.

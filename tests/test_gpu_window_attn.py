@@ -66,6 +66,16 @@ def test_long_lists_of_the_sinks(cla, T, window, sinks, d):
     check(cla, *inputs(2, 4, 1, T, d, BF16), window, sinks, lens)
 
 
+@pytest.mark.parametrize("H,K,T,window,sinks", [(2, 1, 200, 60, 1), (3, 3, 300, 1, 0), (1, 1, 130, 500, 0)])
+def test_many_ragged_sequences(cla, H, K, T, window, sinks):
+    """Batches of more sequences than a warp has lanes, empty ones in front, between and behind."""
+    B = 71
+    lens = torch.randint(0, T + 1, (B,), generator=torch.Generator().manual_seed(T), dtype=torch.int32)
+    lens[0] = lens[1] = lens[33] = lens[70] = 0
+    check(cla, *inputs(B, H, K, T, 64, BF16), window, sinks, lens.cuda())
+    check(cla, *inputs(B, H, K, T, 64, BF16), window, sinks, torch.zeros(B, dtype=torch.int32).cuda())
+
+
 @pytest.mark.parametrize("B,H,K,T", [(0, 2, 1, 5), (2, 0, 0, 5), (2, 2, 1, 0)])
 def test_nothing_to_do(cla, B, H, K, T):
     q, k, v, dO = inputs(B, H, K, T, 64, BF16)
