@@ -132,33 +132,30 @@ def _dims(t, n, name):
     return tuple(t.shape)
 
 
-class _T:
+def _T(t, dtype, name, shape=None, strided=False):
     """A tensor argument of an entry point (None stays NULL), checked by _launch for what the
-    C ABI cannot check: dtype and shape (the sizes the call passes), then device and layout."""
+    C ABI cannot check: dtype and shape (the sizes the call passes), then device and layout.
+    A plain tuple: a call makes up to fifteen of them."""
+    return (t, dtype, name, shape, strided)
 
-    __slots__ = ("t", "dtype", "name", "shape", "strided")
 
-    def __init__(self, t, dtype, name, shape=None, strided=False):
-        self.t, self.dtype, self.name, self.shape, self.strided = t, dtype, name, shape, strided
+def _check_meta(t, dtype, name, shape, strided):
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
-    def check_meta(self):
-        t = self.t
-        if self.dtype is not None and t.dtype != self.dtype:
-            raise ValueError(f"{self.name} must be {self.dtype}, got {t.dtype}")
-        if self.shape is not None and tuple(t.shape) != tuple(self.shape):
-            raise ValueError(f"{self.name} must have shape {tuple(self.shape)}, got {tuple(t.shape)}")
 
-    def check_place(self, device):
-        t = self.t
-        if not t.is_cuda:
-            raise ValueError(f"{self.name} must be a CUDA tensor")
-        if t.device != device:
-            raise ValueError(f"{self.name} is on {t.device}, the call's first tensor on {device}")
-        if self.strided:  # the entry point takes the outer strides
-            if t.shape[-1] > 1 and t.stride(-1) != 1:
-                raise ValueError(f"{self.name} must be contiguous in its last dimension")
-        elif not t.is_contiguous():
-            raise ValueError(f"{self.name} must be contiguous")
+def _check_place(device, t, dtype, name, shape, strided):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's first tensor on {device}")
+    if strided:  # the entry point takes the outer strides
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _nbytes(t):
@@ -186,24 +183,25 @@ def _launch(fn, device, args, stream):
     before its pointer is taken; raises ClaError on a non-OK status."""
     cargs, good = [], device.type == "cuda"
     for a in args:  # one quick pass; what does not pass it is looked at again for its message
-        if type(a) is _T:
-            t = a.t
+        if type(a) is tuple:
+            t, dtype, _, shape, strided = a
             if t is None:
                 a = None
             else:
-                good = (good and (t.dtype is a.dtype or a.dtype is None) and (a.shape is None or t.shape == a.shape)
-                        and t.device == device and (t.is_contiguous() or a.strided and t.stride(-1) == 1))
+                if ((t.dtype is not dtype and dtype is not None) or (shape is not None and t.shape != shape)
+                        or t.device != device or not (t.is_contiguous() or strided and t.stride(-1) == 1)):
+                    good = False
                 a = t.data_ptr()
         cargs.append(a)
     if not good:
-        tensors = [a for a in args if type(a) is _T and a.t is not None]
+        tensors = [a for a in args if type(a) is tuple and a[0] is not None]
         for a in tensors:
-            a.check_meta()
+            _check_meta(*a)
         for a in tensors:
-            a.check_place(device)
+            _check_place(device, *a)
     call = getattr(_lib or lib(), fn)
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         # the current stream's handle, without the Stream object around it
         status = call(*cargs, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, device))
     else:
