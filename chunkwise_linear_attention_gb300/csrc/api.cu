@@ -47,6 +47,18 @@ int set_smem_carveout_max(std::atomic<unsigned long long> &done, const void *fun
     return CLA_OK;
 }
 
+int multiprocessors(const char *fn, int *n) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    CLA_CUDA_TRY(cudaGetDevice(&dev), fn);
+    *n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*n == 0) {
+        CLA_CUDA_TRY(cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev), fn);
+        if (dev < 64) known[dev].store(*n, std::memory_order_relaxed);
+    }
+    return CLA_OK;
+}
+
 }  // namespace cla
 
 extern "C" const char *cla_status_string(int status) {

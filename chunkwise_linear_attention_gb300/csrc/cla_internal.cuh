@@ -27,6 +27,9 @@ int set_max_dynamic_smem(std::atomic<unsigned long long> &done, const void *func
 // kernels whose resident blocks per SM are bounded by shared memory.
 int set_smem_carveout_max(std::atomic<unsigned long long> &done, const void *func);
 
+// Multiprocessors of the current device, asked for once per device.
+int multiprocessors(const char *fn, int *n);
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned16_or_null(const void *p) { return p == nullptr || aligned16(p); }

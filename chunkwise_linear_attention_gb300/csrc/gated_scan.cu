@@ -13,15 +13,17 @@
 // where L / m -> 0 as L -> 0: writing the gradients with dL L instead of dL
 // leaves no division by a vanishing m.
 //
-// Decomposition (one warp = one chunk of 8 L steps x 16 channels): lane =
-// (sub, cg), cg in 0..3 picks 4 adjacent channels and sub in 0..7 a run of L
-// steps.  Every input is read once; a lane keeps its run's decays and inputs
-// in registers, composes them, composes across the 8 runs by shuffles, and
-// publishes the chunk's pair.  The state entering a chunk is folded from the
-// published pairs of its group's earlier chunks (32 chunks a group, eight
-// lanes at a time) and the state at the end of the group before.  That order
-// is fixed by the chunk's place alone, so the result does not depend on which
-// block came first, and only one wait per 32 chunks is on the serial path.
+// Decomposition.  A warp takes 8 L steps x 16 channels: lane = (sub, cg), cg in
+// 0..3 picks 4 adjacent channels and sub in 0..7 a run of L steps.  Every
+// input is read once; a lane keeps its run's decays and inputs in registers,
+// composes them, then the 8 runs compose by shuffles, the block's warps (most
+// of them one behind the other in time) in shared memory, and the blocks
+// through pairs that they publish.  The state entering a block's steps is
+// folded from the published pairs of its group's earlier blocks (8 a group,
+// one a sub) and the state at the end of the group before.  That
+// order is fixed by the place in the sequence alone, so the result does not
+// depend on which block came first, and only one wait per 8 blocks is on the
+// serial path.
 #include <math.h>
 
 #include "cla_internal.cuh"
@@ -31,8 +33,9 @@ namespace cla {
 namespace {
 
 constexpr int kGsCkpt = CLA_GATED_SCAN_CKPT_CHUNK;
-constexpr int kGsGroup = 32;  // chunks of a group
-constexpr int kGsWarps = 4;
+constexpr int kGsGroup = 8;  // block chunks of a group: a lane looks at one pair, all at once
+constexpr int kFwdWarps = 4, kFwdBlocks = 4;  // warps a block and blocks a multiprocessor
+constexpr int kBwdWarps = 4, kBwdBlocks = 3;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }
@@ -60,35 +63,38 @@ struct Gate2 {
     float2 a, y, m, rm, r1, i, i1;  // a, log2 a, m, 1 / m, 1 - r, i, 1 - i
 };
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // The gates of two channels at once (the paired fp32 instructions round each lane as the scalar
-// ones do).  Both sigmoids share one reciprocal, of (1 + e^-|rgate|)(1 + e^-igate): a closed
-// rgate keeps its relative accuracy down to the smallest float, since m grows with the root of
-// it, and igate does not close below 2^-120.  a = 2^y and 1 - a come from one
-// split y = k + f, 2^f = 1 + t: a = 2^k + 2^k t and 1 - a = (1 - 2^k) - 2^k t, which for decays
-// near 1 (k = 0) is -t itself, with no digits lost, where 1 - a^2 from a rounded a would keep
-// only those above 2^-24 / (1 - a).  The polynomial is a least-maximum-error fit of 2^f on
-// [-1/2, 1/2] with p(0) = 1 (Lawson's reweighted least squares, degree 6, 2e-9).  NaN passes
-// through: the clamps are comparisons that a NaN fails.
+// ones do).  e^-g is held at 2^126, so that 1 - sigmoid(g) = e^-g sigmoid(g) stays finite: a gate
+// does not close below 2^-126.  a = 2^y and 1 - a come from one split y = k + f, 2^f = 1 + t:
+// a = 2^k + 2^k t and 1 - a = (1 - 2^k) - 2^k t, which for decays near 1 (k = 0) is -t itself,
+// with no digits lost, where 1 - a^2 from a rounded a would keep only those above
+// 2^-24 / (1 - a).  The polynomial is a least-maximum-error fit of 2^f on [-1/2, 1/2] with
+// p(0) = 1 (Lawson's reweighted least squares, degree 6, 2e-9).  NaN passes through.
 __device__ __forceinline__ Gate2 gate2(float2 rg, float2 ig, float2 nl2) {
     constexpr float kP1 = 6.931471825e-01f, kP2 = 2.402264774e-01f, kP3 = 5.550332367e-02f, kP4 = 9.618437849e-03f,
                     kP5 = 1.339887269e-03f, kP6 = 1.535334159e-04f, kMagic = 12582912.0f;
     Gate2 q;
-    float2 pi = mul2(ig, f2(-kLog2e));
-    pi.x = pi.x > 120.f ? 120.f : pi.x;
-    pi.y = pi.y > 120.f ? 120.f : pi.y;
-    const float2 er = make_float2(ex2a(-fabsf(rg.x) * kLog2e), ex2a(-fabsf(rg.y) * kLog2e));
-    const float2 ei = make_float2(ex2a(pi.x), ex2a(pi.y));
+    const float2 pr = mul2(rg, f2(-kLog2e)), pi = mul2(ig, f2(-kLog2e));
+    const float2 er = make_float2(ex2a(min_nan(pr.x, 126.f)), ex2a(min_nan(pr.y, 126.f)));
+    const float2 ei = make_float2(ex2a(min_nan(pi.x, 126.f)), ex2a(min_nan(pi.y, 126.f)));
     const float2 br = add2(er, f2(1.f)), bi = add2(ei, f2(1.f));
-    const float2 pp = mul2(br, bi);
-    const float2 R = make_float2(rcpa(pp.x), rcpa(pp.y));
-    const float2 big = mul2(R, bi), small = mul2(er, big);  // sigmoid(|rgate|) and 1 - it
-    const float2 r = make_float2(rg.x >= 0.f ? big.x : small.x, rg.y >= 0.f ? big.y : small.y);
-    q.r1 = make_float2(rg.x >= 0.f ? small.x : big.x, rg.y >= 0.f ? small.y : big.y);
-    q.i = mul2(R, br);
+    const float2 r = make_float2(rcpa(br.x), rcpa(br.y));
+    q.i = make_float2(rcpa(bi.x), rcpa(bi.y));
+    q.r1 = mul2(er, r);
     q.i1 = mul2(ei, q.i);
     float2 y = mul2(nl2, r);
-    y.x = y.x < -126.f ? -126.f : y.x;
-    y.y = y.y < -126.f ? -126.f : y.y;
+    y = make_float2(max_nan(y.x, -126.f), max_nan(y.y, -126.f));
     q.y = y;
     const float2 km = add2(y, f2(kMagic));
     const float2 k = add2(km, f2(-kMagic));
@@ -99,12 +105,13 @@ __device__ __forceinline__ Gate2 gate2(float2 rg, float2 ig, float2 nl2) {
     t = fma2(t, f, f2(kP2));
     t = fma2(t, f, f2(kP1));
     t = mul2(t, f);
-    const float2 sc = make_float2(__int_as_float((__float_as_int(km.x) << 23) + 0x3f800000),
-                                  __int_as_float((__float_as_int(km.y) << 23) + 0x3f800000));
-    q.a = fma2(sc, t, sc);
-    const float2 ns = mul2(sc, f2(-1.f));
-    float2 om = fma2(ns, t, add2(ns, f2(1.f)));  // 1 - a
-    om = mul2(om, add2(q.a, f2(1.f)));           // 1 - a^2
+    // 2^k: the low bits of km are k
+    const float2 sc = make_float2(__uint_as_float(__float_as_uint(km.x) * (1u << 23) + 0x3f800000u),
+                                  __uint_as_float(__float_as_uint(km.y) * (1u << 23) + 0x3f800000u));
+    t = mul2(sc, t);
+    q.a = add2(sc, t);
+    float2 om = fma2(t, f2(-1.f), fma2(sc, f2(-1.f), f2(1.f)));  // 1 - a
+    om = mul2(om, add2(q.a, f2(1.f)));                            // 1 - a^2
     om = make_float2(fmaxf(om.x, 1e-37f), fmaxf(om.y, 1e-37f));
     q.rm = make_float2(rsqa(om.x), rsqa(om.y));
     q.m = mul2(om, q.rm);
@@ -114,19 +121,17 @@ __device__ __forceinline__ Gate2 gate2(float2 rg, float2 ig, float2 nl2) {
 struct GsArgs {
     const uint8_t *reset;
     const int32_t *lens;
-    long long T, chunks;
-    int B, D, n_cw;  // n_cw: groups of 16 channels
+    const float *rate;  // -c softplus(lam) log2 e
+    int T, B, D;
+    int tw, n_cw, chunks;  // warps of a block in time; groups of 16 channels (whole blocks); block chunks
     float c;
 };
 
-__device__ __forceinline__ long long seq_len(const GsArgs &g, int b) {
-    if (g.lens == nullptr) return g.T;
-    const long long n = g.lens[b];
-    return n < 0 ? 0 : (n > g.T ? g.T : n);
+__device__ __forceinline__ int seq_len(const GsArgs &g, int b) {
+    return g.lens == nullptr ? g.T : min(max(__ldg(g.lens + b), 0), g.T);
 }
 
-// Four adjacent elements as they lie in memory; VEC: with one access, else one by one (rows that
-// are not aligned), those below `n` only.
+// Four adjacent elements as they lie in memory.
 template <typename E>
 struct Raw4 {
     uint2 w;
@@ -135,16 +140,17 @@ template <>
 struct Raw4<float> {
     float4 w;
 };
+// VEC: with one access, else one by one (rows that are not aligned), those below `n` only.
 template <typename E, bool VEC>
 __device__ __forceinline__ Raw4<E> ld4(const E *p, int n) {
     Raw4<E> r;
     if constexpr (VEC) {
         r.w = __ldcs(reinterpret_cast<const decltype(r.w) *>(p));
     } else if constexpr (sizeof(E) == 4) {
-        r.w = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+        r.w = make_float4(n > 0 ? __ldg(p) : 0.f, n > 1 ? __ldg(p + 1) : 0.f, n > 2 ? __ldg(p + 2) : 0.f, n > 3 ? __ldg(p + 3) : 0.f);
     } else {
         const unsigned short *s = reinterpret_cast<const unsigned short *>(p);
-        const unsigned int a = n > 0 ? s[0] : 0, b = n > 1 ? s[1] : 0, c = n > 2 ? s[2] : 0, d = n > 3 ? s[3] : 0;
+        const unsigned int a = n > 0 ? __ldg(s) : 0, b = n > 1 ? __ldg(s + 1) : 0, c = n > 2 ? __ldg(s + 2) : 0, d = n > 3 ? __ldg(s + 3) : 0;
         r.w = make_uint2(a | b << 16, c | d << 16);
     }
     return r;
@@ -259,11 +265,18 @@ __device__ __forceinline__ bool peek4(const unsigned int *p, float2 (&v)[2]) {
     v[1] = make_float2(__uint_as_float(c), __uint_as_float(d));
     return a != 0u && b != 0u && c != 0u && d != 0u;
 }
-// Polls until the four words are there, a bounded number of times; then records the timeout and
-// carries on with what it saw.
-__device__ __forceinline__ void wait4(const unsigned int *p, float2 (&v)[2], WsHeader *hdr, unsigned int where) {
+// Polls until the words that a lane asks for are there (p: a pair, q: a state; either may be NULL),
+// a bounded number of times; then records the timeout and carries on with what it saw.
+__device__ __forceinline__ void wait_words(const unsigned int *p, float2 (&a)[2], float2 (&b)[2], const unsigned int *q,
+                                           float2 (&s)[2], WsHeader *hdr, unsigned int where) {
     for (unsigned int it = 0; it < kSpinLimit; ++it) {
-        if (peek4(p, v)) return;
+        bool ok = true;
+        if (p != nullptr) {
+            const bool x = peek4(p, a), y = peek4(p + 4, b);
+            ok = x && y;
+        }
+        if (q != nullptr) ok = peek4(q, s) && ok;
+        if (ok) return;
         if (it >= 8) __nanosleep(64);
     }
     atomicOr(&hdr->error, kErrTimeout);
@@ -272,42 +285,31 @@ __device__ __forceinline__ void wait4(const unsigned int *p, float2 (&v)[2], WsH
 
 struct GsWords {
     WsHeader *hdr;
-    unsigned int *pairs;   // [chunk][b][cw][cg][A, B][4], chunks in the scan's order
+    unsigned int *pairs;   // [block chunk][b][cw][cg][A, B][4], chunks in the scan's order
     unsigned int *states;  // [group][b][cw][cg][4]
 };
 
-// The state entering chunk `idx` (of `per` units a chunk; this warp's is `rem`): the pairs of
-// the group's chunks before it, eight lanes folding contiguous shares and then each other's, on
-// the state at the end of the group before, or `s0`.  Publishes this chunk's pair (held by the
-// lanes with `pubs`) and, at the end of a group, the state behind it.
+// By one warp: publishes the pair (A, B) of block chunk `idx` for 16 channels (`rem` of the `per`
+// groups of them; every lane holds its cg's), and returns the state entering it: the pairs of the
+// group's chunks before it, one a sub, on the
+// state at the end of the group before, or `s0`.  The last chunk of a group publishes the state
+// behind it.
 template <bool RST>
-__device__ __forceinline__ void carry_in(const GsWords &w, long long idx, long long chunks, long long per, long long rem,
-                                         int sub, int cg, bool pubs, const float2 (&A)[2], const float2 (&B)[2],
-                                         const float2 (&s0)[2], float2 (&s)[2], unsigned int where) {
-    const int n = (int)(idx % kGsGroup);
-    const long long first = idx - n;
-    const bool last_of_group = n == kGsGroup - 1;
-    if (pubs && !last_of_group && idx + 1 < chunks) {
-        unsigned int *p = w.pairs + ((idx * per + rem) * 4 + cg) * 8;
+__device__ __forceinline__ void carry_in(const GsWords &w, int idx, int chunks, int per, int rem, const float2 (&A)[2],
+                                         const float2 (&B)[2], const float2 (&s0)[2], float2 (&s)[2], unsigned int where) {
+    const int lane = threadIdx.x & 31, sub = lane >> 2, cg = lane & 3;
+    const int n = idx % kGsGroup, first = idx - n;
+    const bool last_of_group = n == kGsGroup - 1, more = idx + 1 < chunks && sub == 0;
+    if (more && !last_of_group) {
+        unsigned int *p = w.pairs + (((size_t)idx * per + rem) * 4 + cg) * 8;
         publish4(p, A);
         publish4(p + 4, B);
     }
-    float2 PA[2] = {f2(1.f), f2(1.f)}, PB[2] = {f2(0.f), f2(0.f)};
+    float2 PA[2] = {f2(1.f), f2(1.f)}, PB[2] = {f2(0.f), f2(0.f)}, S[2] = {s0[0], s0[1]};
+    wait_words(sub < n ? w.pairs + (((size_t)(first + sub) * per + rem) * 4 + cg) * 8 : nullptr, PA, PB,
+               first > 0 ? w.states + (((size_t)(first / kGsGroup - 1) * per + rem) * 4 + cg) * 4 : nullptr, S, w.hdr, where);
+    __syncwarp();
     if (n > 0) {
-        const int share = (n + 7) / 8, k0 = sub * share, k1 = k0 + share < n ? k0 + share : n;
-        for (int k = k0; k < k1; ++k) {
-            const unsigned int *p = w.pairs + (((first + k) * per + rem) * 4 + cg) * 8;
-            float2 a[2], b[2];
-            wait4(p, a, w.hdr, where);
-            wait4(p + 4, b, w.hdr, where);
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                after<RST>(a[v], b[v], PA[v], PB[v]);
-                PA[v] = a[v];
-                PB[v] = b[v];
-            }
-        }
-        __syncwarp();
         scan_runs<RST, false>(PA, PB, sub);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
@@ -315,83 +317,159 @@ __device__ __forceinline__ void carry_in(const GsWords &w, long long idx, long l
             PB[v] = shfl2(PB[v], 28 + cg);
         }
     }
-    float2 S[2] = {s0[0], s0[1]};
-    if (first > 0) {
-        wait4(w.states + (((first / kGsGroup - 1) * per + rem) * 4 + cg) * 4, S, w.hdr, where + 1);
-        __syncwarp();
-    }
 #pragma unroll
     for (int v = 0; v < 2; ++v) s[v] = apply<RST>(PA[v], S[v], PB[v]);
-    if (pubs && last_of_group && idx + 1 < chunks) {
+    if (more && last_of_group) {
         const float2 e[2] = {apply<RST>(A[0], s[0], B[0]), apply<RST>(A[1], s[1], B[1])};
-        publish4(w.states + ((idx / kGsGroup * per + rem) * 4 + cg) * 4, e);
+        publish4(w.states + (((size_t)(idx / kGsGroup) * per + rem) * 4 + cg) * 4, e);
     }
 }
 
-// Blocks take their units in the order in which they start, so that every unit a warp waits for
-// belongs to a warp that runs already.
-__device__ __forceinline__ long long take_unit(WsHeader *hdr, int which) {
-    __shared__ unsigned int ticket;
-    if (threadIdx.x == 0) ticket = atomicAdd(&hdr->ticket[which], 1u);
+// What the warps of a block exchange: each warp's pair, the state entering the block's steps for
+// each group of channels, the block's unit.
+template <int NW>
+struct Exchange {
+    float4 pair[NW][4][2];
+    float4 in[NW][4];
+    unsigned int ticket;
+    __device__ __forceinline__ static float4 pack(const float2 (&v)[2]) { return make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
+    __device__ __forceinline__ static void unpack(float4 r, float2 (&v)[2]) {
+        v[0] = make_float2(r.x, r.y);
+        v[1] = make_float2(r.z, r.w);
+    }
+};
+
+// The block's part of the scan.  A, B: this warp's whole pair, in the lanes of `holder` (the sub
+// whose run is last in the scan's order).  Returns the state entering this warp's steps.
+template <bool RST, int NW>
+__device__ __forceinline__ void block_carry(Exchange<NW> &ex, const GsArgs &g, const GsWords &w, int idx, int per, int rem,
+                                            int holder, const float2 (&A)[2], const float2 (&B)[2], const float2 (&s0)[2],
+                                            float2 (&s)[2], unsigned int where) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane >> 2, cg = lane & 3;
+    const int cb = NW / g.tw, wt = warp / cb, wc = warp - wt * cb;
+    if (sub == holder) {
+        ex.pair[warp][cg][0] = ex.pack(A);
+        ex.pair[warp][cg][1] = ex.pack(B);
+    }
     __syncthreads();
-    return (long long)ticket * kGsWarps + (threadIdx.x >> 5);
+    // the pairs of the warps before this one; the first warp: of all of them
+    float2 PA[2] = {f2(1.f), f2(1.f)}, PB[2] = {f2(0.f), f2(0.f)};
+    for (int k = 0; k < (wt == 0 ? g.tw : wt); ++k) {
+        float2 a[2], b[2];
+        ex.unpack(ex.pair[k * cb + wc][cg][0], a);
+        ex.unpack(ex.pair[k * cb + wc][cg][1], b);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            after<RST>(a[v], b[v], PA[v], PB[v]);
+            PA[v] = a[v];
+            PB[v] = b[v];
+        }
+    }
+    if (wt == 0) {
+        carry_in<RST>(w, idx, g.chunks, per, rem, PA, PB, s0, s, where);
+        if (sub == 0) ex.in[wc][cg] = ex.pack(s);
+    }
+    __syncthreads();
+    if (wt > 0) {
+        ex.unpack(ex.in[wc][cg], s);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) s[v] = apply<RST>(PA[v], s[v], PB[v]);
+    }
+}
+
+// Blocks take units from a counter, in the order in which they start: every unit that a block waits
+// for was taken by a block that runs already, whatever else the GPU does.
+template <int NW>
+__device__ __forceinline__ int take_unit(Exchange<NW> &ex, WsHeader *hdr, int which) {
+    if (threadIdx.x == 0) ex.ticket = atomicAdd(&hdr->ticket[which], 1u);
+    __syncthreads();
+    return (int)ex.ticket;
+}
+
+// What a unit is: block chunk, sequence, channels, and this lane's run of steps in it.
+struct Unit {
+    int idx, rem, chunk, t0, b, c0, nv, n, rows;  // channels from c0 (nv of them exist); n: steps of the run in the sequence, rows: in T
+    size_t at;
+    template <int L, int NW, bool REV>
+    static __device__ __forceinline__ Unit make(const GsArgs &g, int unit) {
+        const int warp = threadIdx.x >> 5, sub = (threadIdx.x >> 2) & 7, cg = threadIdx.x & 3;
+        const int cb = NW / g.tw, wt = warp / cb, cbs = g.n_cw / cb, per = g.B * cbs;
+        Unit u;
+        u.idx = unit / per;
+        const int r = unit - u.idx * per;
+        u.b = r / cbs;
+        const int cw = (r - u.b * cbs) * cb + warp - wt * cb;
+        u.rem = u.b * g.n_cw + cw;
+        u.chunk = REV ? (g.chunks - u.idx) * g.tw - 1 - wt : u.idx * g.tw + wt;  // of 8 L steps
+        u.c0 = cw * 16 + cg * 4;
+        u.nv = g.D - u.c0;
+        u.t0 = u.chunk * (8 * L) + sub * L;
+        u.n = u.nv <= 0 ? 0 : min(max(seq_len(g, u.b) - u.t0, 0), L);
+        u.rows = u.nv <= 0 ? 0 : min(max(g.T - u.t0, 0), L);
+        u.at = ((size_t)u.b * g.T + u.t0) * g.D + u.c0;
+        return u;
+    }
+};
+
+// Clears the words that are waited for, and the header, and forms the channels' rates
+// -c softplus(lam) log2 e (padded to whole units): once here instead of in every unit, where they
+// cost 5 instructions a step and channel.
+__global__ void gated_setup_kernel(uint4 *ws, long long words, float *rate, const float *__restrict__ lam, int D, int padded, float c) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    for (long long k = i; k < words; k += (long long)gridDim.x * blockDim.x) ws[k] = make_uint4(0u, 0u, 0u, 0u);
+    for (long long k = i; k < padded; k += (long long)gridDim.x * blockDim.x) rate[k] = k < D ? -c * softplus(lam[k]) * kLog2e : 0.f;
+}
+__device__ __forceinline__ void load_rate(const float *rate, int c0, float2 (&v)[2]) {
+    const float4 r = __ldg(reinterpret_cast<const float4 *>(rate + c0));
+    v[0] = make_float2(r.x, r.y);
+    v[1] = make_float2(r.z, r.w);
 }
 
 // ------------------------------------------------------------------ forward
-// L = 8 steps a lane for 2-byte elements, 4 for fp32 (the raw inputs of a run are held in
-// registers until they are used).  h may be NULL: only the checkpoint is written then.
+// L = 8 steps a lane for 2-byte elements, 4 for fp32.  h may be NULL: only the checkpoint is
+// written then.
 template <typename E, bool VEC, bool RST, int L>
-__global__ void __launch_bounds__(kGsWarps * 32, 4)
-gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__restrict__ ig, const float *__restrict__ lam,
+__global__ void __launch_bounds__(kFwdWarps * 32, kFwdBlocks)
+gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__restrict__ ig,
                  const float *__restrict__ h0, E *__restrict__ h, float *__restrict__ hT, float *__restrict__ ckpt, GsArgs g,
                  GsWords w) {
-    const long long per = (long long)g.B * g.n_cw, unit = take_unit(w.hdr, 0);
-    const long long chunk = unit / per, rem = unit - chunk * per;
-    if (chunk >= g.chunks) return;
-    const int b = (int)(rem / g.n_cw), lane = threadIdx.x & 31, sub = lane >> 2, cg = lane & 3;
-    const int c0 = (int)(rem % g.n_cw) * 16 + cg * 4, nv = g.D - c0;
-    const long long n = nv > 0 ? seq_len(g, b) : 0, t0 = chunk * (8 * L) + sub * L;
-    const size_t at0 = ((size_t)b * g.T + t0) * g.D + c0;
-
+    __shared__ Exchange<kFwdWarps> ex;
+    const Unit q = Unit::make<L, kFwdWarps, false>(g, take_unit(ex, w.hdr, 0));
+    const int sub = (threadIdx.x >> 2) & 7;
     Raw4<E> rx[L], rr[L], ri[L];
     bool rs[L];
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (t0 + j < n) {
-            const size_t at = at0 + (size_t)j * g.D;
-            rr[j] = ld4<E, VEC>(rg + at, nv);
-            ri[j] = ld4<E, VEC>(ig + at, nv);
-            rx[j] = ld4<E, VEC>(x + at, nv);
-            if constexpr (RST) rs[j] = g.reset[(size_t)b * g.T + t0 + j] != 0;
+    for (int j = 0; j < L; ++j)
+        if (j < q.n) {
+            const size_t at = q.at + (size_t)j * g.D;
+            rr[j] = ld4<E, VEC>(rg + at, q.nv);
+            ri[j] = ld4<E, VEC>(ig + at, q.nv);
+            rx[j] = ld4<E, VEC>(x + at, q.nv);
+            if constexpr (RST) rs[j] = g.reset[(size_t)q.b * g.T + q.t0 + j] != 0;
         }
-    }
     float2 nl2[2], s0[2] = {f2(0.f), f2(0.f)};
-    ldf4(lam + (nv > 0 ? c0 : 0), nl2, nv);
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-        nl2[v] = make_float2(-g.c * softplus(nl2[v].x) * kLog2e, -g.c * softplus(nl2[v].y) * kLog2e);
-    if (h0 != nullptr && nv > 0) ldf4(h0 + (size_t)b * g.D + c0, s0, nv);
+    load_rate(g.rate, q.c0, nl2);
+    if (h0 != nullptr && q.nv > 0) ldf4(h0 + (size_t)q.b * g.D + q.c0, s0, q.nv);
+    const bool full = __all_sync(~0u, q.n == L);
 
     float2 a[L][2], u[L][2], A[2] = {f2(1.f), f2(1.f)}, B[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-        const bool on = t0 + j < n;
         float2 xv[2], rv[2], iv[2];
-        cvt4<E>(rx[j], xv);
         cvt4<E>(rr[j], rv);
         cvt4<E>(ri[j], iv);
+        cvt4<E>(rx[j], xv);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            if (on) {
-                const Gate2 q = gate2(rv[v], iv[v], nl2[v]);
-                a[j][v] = q.a;
-                u[j][v] = mul2(mul2(q.m, q.i), xv[v]);
-                if constexpr (RST)
-                    if (rs[j]) {
-                        a[j][v] = f2(0.f);
-                        u[j][v] = mul2(q.i, xv[v]);
-                    }
-            } else {
+            const Gate2 e = gate2(rv[v], iv[v], nl2[v]);
+            a[j][v] = e.a;
+            u[j][v] = mul2(mul2(e.m, e.i), xv[v]);
+            if constexpr (RST)
+                if (j < q.n && rs[j]) {
+                    a[j][v] = f2(0.f);
+                    u[j][v] = mul2(e.i, xv[v]);
+                }
+            if (!full && j >= q.n) {  // behind the sequence
                 a[j][v] = f2(1.f);
                 u[j][v] = f2(0.f);
             }
@@ -409,25 +487,24 @@ gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
         Bx[v] = shfl_up2(B[v], 4);
         if (sub == 0) Ax[v] = f2(1.f), Bx[v] = f2(0.f);
     }
-    carry_in<RST>(w, chunk, g.chunks, per, rem, sub, cg, sub == 7, A, B, s0, s, 11u);
-    if (nv <= 0) return;
+    block_carry<RST, kFwdWarps>(ex, g, w, q.idx, g.B * g.n_cw, q.rem, 7, A, B, s0, s, 11u);
+    if (q.nv <= 0) return;
 #pragma unroll
     for (int v = 0; v < 2; ++v) s[v] = apply<RST>(Ax[v], s[v], Bx[v]);
-    if (ckpt != nullptr && (sub * L) % kGsCkpt == 0 && t0 < g.T)
-        stf4(ckpt + ((size_t)b * ((g.T + kGsCkpt - 1) / kGsCkpt) + t0 / kGsCkpt) * g.D + c0, s, nv);
+    if (ckpt != nullptr && (sub * L) % kGsCkpt == 0 && q.rows > 0)
+        stf4(ckpt + ((size_t)q.b * ((g.T + kGsCkpt - 1) / kGsCkpt) + q.t0 / kGsCkpt) * g.D + q.c0, s, q.nv);
 #pragma unroll
     for (int j = 0; j < L; ++j) {
 #pragma unroll
         for (int v = 0; v < 2; ++v) s[v] = apply<RST>(a[j][v], s[v], u[j][v]);
-        if (t0 + j < g.T) {
-            if (h != nullptr) {
-                const bool on = t0 + j < n;
-                const float2 z[2] = {on ? s[0] : f2(0.f), on ? s[1] : f2(0.f)};
-                st4<E, VEC>(h + at0 + (size_t)j * g.D, z, nv);
-            }
-            if (hT != nullptr && t0 + j == g.T - 1) stf4(hT + (size_t)b * g.D + c0, s, nv);
+        if (j < q.rows && h != nullptr) {
+            float2 z[2] = {s[0], s[1]};
+            if (!full && j >= q.n) z[0] = z[1] = f2(0.f);
+            st4<E, VEC>(h + q.at + (size_t)j * g.D, z, q.nv);
         }
     }
+    // the steps behind T keep the state, so the run's last one is T's
+    if (hT != nullptr && q.rows > 0 && q.t0 + q.rows == g.T) stf4(hT + (size_t)q.b * g.D + q.c0, s, q.nv);
 }
 
 // ------------------------------------------------------------------ backward
@@ -436,71 +513,61 @@ gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
 // scanned as the forward's state is, and every gradient is written once.  Each chunk leaves its
 // sums of G for dlam in a row of `part`.
 template <typename E, bool VEC, bool RST>
-__global__ void __launch_bounds__(kGsWarps * 32, 3)
-gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__restrict__ ig, const float *__restrict__ lam,
+__global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocks)
+gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__restrict__ ig,
                  const float *__restrict__ ckpt, const E *__restrict__ dh, const float *__restrict__ dhT,
                  E *__restrict__ dx, E *__restrict__ drg, E *__restrict__ dig, float *__restrict__ part,
                  float *__restrict__ dh0, GsArgs g, GsWords w) {
     constexpr int L = 4;
-    static_assert(8 * L == kGsCkpt, "a chunk of the backward starts at a checkpoint");
-    const long long per = (long long)g.B * g.n_cw, unit = take_unit(w.hdr, 1);
-    const long long idx = unit / per, rem = unit - idx * per, chunk = g.chunks - 1 - idx;
-    if (chunk < 0) return;
-    const int b = (int)(rem / g.n_cw), lane = threadIdx.x & 31, sub = lane >> 2, cg = lane & 3;
-    const int c0 = (int)(rem % g.n_cw) * 16 + cg * 4, nv = g.D - c0;
-    const long long n = nv > 0 ? seq_len(g, b) : 0, t0 = chunk * (8 * L) + sub * L;
-    const size_t at0 = ((size_t)b * g.T + t0) * g.D + c0;
-
+    static_assert(8 * L == kGsCkpt, "a warp's steps start at a checkpoint");
+    __shared__ Exchange<kBwdWarps> ex;
+    const Unit q = Unit::make<L, kBwdWarps, true>(g, take_unit(ex, w.hdr, 1));
+    const int sub = (threadIdx.x >> 2) & 7, ckpts = (g.T + kGsCkpt - 1) / kGsCkpt;
     Raw4<E> rx[L], rr[L], ri[L], rd[L];
     bool rs[L];
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (t0 + j < n) {
-            const size_t at = at0 + (size_t)j * g.D;
-            rr[j] = ld4<E, VEC>(rg + at, nv);
-            ri[j] = ld4<E, VEC>(ig + at, nv);
-            rx[j] = ld4<E, VEC>(x + at, nv);
-            rd[j] = ld4<E, VEC>(dh + at, nv);
-            if constexpr (RST) rs[j] = g.reset[(size_t)b * g.T + t0 + j] != 0;
+    for (int j = 0; j < L; ++j)
+        if (j < q.n) {
+            const size_t at = q.at + (size_t)j * g.D;
+            rr[j] = ld4<E, VEC>(rg + at, q.nv);
+            ri[j] = ld4<E, VEC>(ig + at, q.nv);
+            rx[j] = ld4<E, VEC>(x + at, q.nv);
+            rd[j] = ld4<E, VEC>(dh + at, q.nv);
+            if constexpr (RST) rs[j] = g.reset[(size_t)q.b * g.T + q.t0 + j] != 0;
         }
-    }
     float2 nl2[2], s0[2] = {f2(0.f), f2(0.f)}, hs[2] = {f2(0.f), f2(0.f)};
-    ldf4(lam + (nv > 0 ? c0 : 0), nl2, nv);
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-        nl2[v] = make_float2(-g.c * softplus(nl2[v].x) * kLog2e, -g.c * softplus(nl2[v].y) * kLog2e);
-    if (nv > 0) {
-        if (dhT != nullptr) ldf4(dhT + (size_t)b * g.D + c0, s0, nv);
-        ldf4(ckpt + ((size_t)b * g.chunks + chunk) * g.D + c0, hs, nv);
+    load_rate(g.rate, q.c0, nl2);
+    if (q.nv > 0) {
+        if (dhT != nullptr) ldf4(dhT + (size_t)q.b * g.D + q.c0, s0, q.nv);
+        if (q.chunk < ckpts) ldf4(ckpt + ((size_t)q.b * ckpts + q.chunk) * g.D + q.c0, hs, q.nv);
     }
+    const bool full = __all_sync(~0u, q.n == L);
 
-    // per step: a, L a, 1 - r, a u / m, m i, x (1 - i), dh, and b = m i x, then h_{t-1}
-    float2 a[L][2], La[L][2], r1[L][2], w2[L][2], mi[L][2], xi[L][2], gd[L][2], hp[L][2];
+    // per step: a, L a, 1 - r, a u / m, m i, x (1 - i), and b = m i x, then h_{t-1}
+    float2 a[L][2], La[L][2], r1[L][2], w2[L][2], mi[L][2], xi[L][2], hp[L][2];
     float2 A[2] = {f2(1.f), f2(1.f)}, B[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-        const bool on = t0 + j < n;
         float2 xv[2], rv[2], iv[2];
-        cvt4<E>(rx[j], xv);
         cvt4<E>(rr[j], rv);
         cvt4<E>(ri[j], iv);
-        cvt4<E>(rd[j], gd[j]);
+        cvt4<E>(rx[j], xv);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            if (on) {
-                const Gate2 q = gate2(rv[v], iv[v], nl2[v]);
-                a[j][v] = q.a;
-                La[j][v] = mul2(mul2(q.y, f2(kLn2)), q.a);
-                r1[j][v] = q.r1;
-                w2[j][v] = mul2(mul2(q.a, q.rm), mul2(q.i, xv[v]));
-                mi[j][v] = mul2(q.m, q.i);
-                if constexpr (RST)
-                    if (rs[j]) a[j][v] = La[j][v] = w2[j][v] = f2(0.f), mi[j][v] = q.i;
-                xi[j][v] = mul2(xv[v], q.i1);
-                hp[j][v] = mul2(mi[j][v], xv[v]);
-            } else {
+            const Gate2 e = gate2(rv[v], iv[v], nl2[v]);
+            a[j][v] = e.a;
+            La[j][v] = mul2(mul2(e.y, f2(kLn2)), e.a);
+            r1[j][v] = e.r1;
+            w2[j][v] = mul2(mul2(e.a, e.rm), mul2(e.i, xv[v]));
+            mi[j][v] = mul2(e.m, e.i);
+            if constexpr (RST)
+                if (j < q.n && rs[j])
+                    a[j][v] = La[j][v] = w2[j][v] = f2(0.f), mi[j][v] = e.i;
+            xi[j][v] = mul2(xv[v], e.i1);
+            hp[j][v] = mul2(mi[j][v], xv[v]);
+            if (!full && j >= q.n) {
                 a[j][v] = f2(1.f);
-                La[j][v] = r1[j][v] = w2[j][v] = mi[j][v] = xi[j][v] = hp[j][v] = gd[j][v] = f2(0.f);
+                La[j][v] = r1[j][v] = w2[j][v] = mi[j][v] = xi[j][v] = hp[j][v] = f2(0.f);
             }
             const float2 pa = A[v], pb = B[v];
             A[v] = a[j][v];
@@ -509,6 +576,10 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
         }
     }
     scan_runs<RST, false>(A, B, sub);
+    auto grad = [&](int j, float2 (&v)[2]) {  // dh_t of the run's step j
+        cvt4<E>(rd[j], v);
+        if (!full && j >= q.n) v[0] = v[1] = f2(0.f);
+    };
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
         const float2 pa = shfl_up2(A[v], 4), pb = shfl_up2(B[v], 4);
@@ -521,11 +592,16 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
         }
         A[v] = f2(1.f);
         B[v] = f2(0.f);
+    }
 #pragma unroll
-        for (int j = L - 1; j >= 0; --j) {
+    for (int j = L - 1; j >= 0; --j) {
+        float2 gd[2];
+        grad(j, gd);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
             const float2 pa = A[v], pb = B[v];
             A[v] = a[j][v];
-            B[v] = apply<RST>(a[j][v], gd[j][v], f2(0.f));
+            B[v] = apply<RST>(a[j][v], gd[v], f2(0.f));
             after<RST>(A[v], B[v], pa, pb);
         }
     }
@@ -537,44 +613,41 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
         Bx[v] = shfl_down2(B[v], 4);
         if (sub == 7) Ax[v] = f2(1.f), Bx[v] = f2(0.f);
     }
-    carry_in<RST>(w, idx, g.chunks, per, rem, sub, cg, sub == 0, A, B, s0, s, 13u);
+    block_carry<RST, kBwdWarps>(ex, g, w, q.idx, g.B * g.n_cw, q.rem, 0, A, B, s0, s, 13u);
     float2 sum[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-        s[v] = apply<RST>(Ax[v], s[v], Bx[v]);
+    for (int v = 0; v < 2; ++v) s[v] = apply<RST>(Ax[v], s[v], Bx[v]);
 #pragma unroll
-        for (int j = L - 1; j >= 0; --j) {
-            const float2 hb = add2(gd[j][v], s[v]);
+    for (int j = L - 1; j >= 0; --j) {
+        float2 gd[2], ox[2], oi[2], orr[2];
+        grad(j, gd);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const float2 hb = add2(gd[v], s[v]);
             s[v] = apply<RST>(a[j][v], hb, f2(0.f));
             float2 before = hp[j][v];
-            if constexpr (RST) {
-                if (a[j][v].x == 0.f) before = f2(0.f);
-            }
+            if constexpr (RST)
+                if (a[j][v].x == 0.f) before = f2(0.f);  // a reset is one of all channels
             const float2 G = mul2(mul2(hb, La[j][v]), fma2(w2[j][v], f2(-1.f), before));
             sum[v] = add2(sum[v], G);
-            const float2 ox = mul2(hb, mi[j][v]);
-            mi[j][v] = ox;
-            xi[j][v] = mul2(ox, xi[j][v]);
-            r1[j][v] = mul2(G, r1[j][v]);
+            ox[v] = mul2(hb, mi[j][v]);
+            oi[v] = mul2(ox[v], xi[j][v]);
+            orr[v] = mul2(G, r1[j][v]);
+        }
+        if (j < q.rows) {
+            const size_t at = q.at + (size_t)j * g.D;
+            st4<E, VEC>(dx + at, ox, q.nv);
+            st4<E, VEC>(dig + at, oi, q.nv);
+            st4<E, VEC>(drg + at, orr, q.nv);
         }
     }
-    if (nv > 0) {
-#pragma unroll
-        for (int j = 0; j < L; ++j)
-            if (t0 + j < g.T) {
-                const size_t at = at0 + (size_t)j * g.D;
-                st4<E, VEC>(dx + at, mi[j], nv);
-                st4<E, VEC>(dig + at, xi[j], nv);
-                st4<E, VEC>(drg + at, r1[j], nv);
-            }
-        if (dh0 != nullptr && chunk == 0 && sub == 0) stf4(dh0 + (size_t)b * g.D + c0, s, nv);
-    }
+    if (q.nv > 0 && dh0 != nullptr && q.chunk == 0 && sub == 0) stf4(dh0 + (size_t)q.b * g.D + q.c0, s, q.nv);
 #pragma unroll
     for (int v = 0; v < 2; ++v)
 #pragma unroll
         for (int off = 16; off >= 4; off >>= 1)
             sum[v] = add2(sum[v], make_float2(__shfl_xor_sync(~0u, sum[v].x, off), __shfl_xor_sync(~0u, sum[v].y, off)));
-    if (nv > 0 && sub == 0) stf4(part + ((size_t)chunk * g.B + b) * g.D + c0, sum, nv);
+    if (q.nv > 0 && sub == 0 && q.chunk < ckpts) stf4(part + ((size_t)q.chunk * g.B + q.b) * g.D + q.c0, sum, q.nv);
 }
 
 // Sums of rows: block (x, y) adds its share of the rows of 32 channels, in a fixed order, into
@@ -624,41 +697,48 @@ __global__ void gated_step_kernel(const E *x, const E *rg, const E *ig, const fl
 }
 
 // ------------------------------------------------------------------ host side
+// 10^12 elements, rounded up to whole units, are fewer than 2^31 units of 32 steps x 16 channels.
+bool gs_sizes_ok(int64_t B, int64_t T, int64_t D) {
+    return B >= 0 && T >= 0 && D >= 0 && T <= kMaxTokens && product_below({B, D}, 2147483648.0) &&
+           product_below({B, T + 511, D / 128 + 1, 128}, 1e12);
+}
+
 int gs_check(const char *fn, int64_t B, int64_t T, int64_t D, int dtype, float c) {
     if (B < 0 || T < 0 || D < 0) return fail(CLA_ERR_INVALID_ARG, "%s: negative size", fn);
     if (!(c > 0.f) || !isfinite(c)) return fail(CLA_ERR_INVALID_ARG, "%s: c must be positive and finite", fn);
     if (dtype_bytes(dtype) == 0) return fail(CLA_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
-    if (!product_below({B, D}, 2147483648.0) || !product_below({B, T, D}, 1e12) || T > kMaxTokens)
-        return fail(CLA_ERR_UNSUPPORTED, "%s: B * D must be below 2^31, B * T * D below 10^12, T at most 2^31 - 512", fn);
+    if (!gs_sizes_ok(B, T, D))
+        return fail(CLA_ERR_UNSUPPORTED, "%s: B * D must be below 2^31, B * T * (D rounded up to 16) below 10^12, T at most 2^31 - 512", fn);
     return CLA_OK;
 }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// The workspace: header, the words of the published pairs and states (sized for the backward's
-// chunks of 32 steps, twice the forward's at most), the rebuilt checkpoint, the rows of dlam's
+// The workspace: header, the words of the published pairs and states (sized for blocks of 32
+// steps, the fewest that one covers), the rebuilt checkpoint, the rows of dlam's
 // sums and the rows that these are reduced to.
 struct GsLayout {
-    size_t words, clear, states, ckpt, part, part2, total;
+    size_t words, clear, states, rate, ckpt, part, part2, total;
 };
 constexpr long long kDlamRows = 1024;  // above these many rows, dlam's sums go in two steps
 constexpr int kDlamShares = 64;
 
+// Groups of 16 channels, in whole blocks whatever their shape.
+int64_t gs_groups(int64_t D) { return ceil_div(D, 16 * kFwdWarps) * kFwdWarps; }
+static_assert(kFwdWarps >= kBwdWarps, "groups in whole blocks");
+
 GsLayout gs_layout(int64_t B, int64_t T, int64_t D) {
     GsLayout l;
-    const size_t units = (size_t)B * ceil_div(D, 16), ch = (size_t)ceil_div(T, kGsCkpt);
+    const size_t units = (size_t)B * gs_groups(D), ch = (size_t)ceil_div(T, kGsCkpt);
     l.words = sizeof(WsHeader);
     l.states = l.words + ch * units * 4 * 8 * 4;
     l.clear = l.states + (size_t)ceil_div(ch, kGsGroup) * units * 4 * 4 * 4;
-    l.ckpt = l.clear;
+    l.rate = l.clear;
+    l.ckpt = l.rate + (size_t)gs_groups(D) * 64;
     l.part = l.ckpt + align_up(ch * (size_t)B * D * 4, 16);
     l.part2 = l.part + align_up(ch * (size_t)B * D * 4, 16);
     l.total = l.part2 + (ch * B > (size_t)kDlamRows ? align_up((size_t)kDlamShares * D * 4, 16) : 0);
     return l;
-}
-
-bool gs_sizes_ok(int64_t B, int64_t T, int64_t D) {
-    return B >= 0 && T >= 0 && D >= 0 && T <= kMaxTokens && product_below({B, D}, 2147483648.0) && product_below({B, T, D}, 1e12);
 }
 
 template <typename E>
@@ -672,28 +752,56 @@ GsWords gs_words(void *ws, const GsLayout &l) {
                    reinterpret_cast<unsigned int *>(p + l.states)};
 }
 
-// Clears the header and the words, which lie one behind the other from the start of `ws`.
-int gs_clear(const char *fn, void *ws, const GsLayout &l, cudaStream_t s) {
-    CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, l.clear, s), fn);
-    return CLA_OK;
+// The header and the words lie one behind the other from the start of `ws`; `from`: the first byte
+// that is cleared.
+int gs_setup(const char *fn, void *ws, const GsLayout &l, size_t from, const float *lam, int64_t D, float c, cudaStream_t s) {
+    char *p = static_cast<char *>(ws);
+    const long long words = (long long)((l.clear - from) / 16), padded = gs_groups(D) * 16, most = words > padded ? words : padded;
+    const long long blocks = ceil_div(most, 256);
+    gated_setup_kernel<<<(unsigned)(blocks < 608 ? blocks : 608), 256, 0, s>>>(
+        reinterpret_cast<uint4 *>(p + from), words, reinterpret_cast<float *>(p + l.rate), lam, (int)D, (int)padded, c);
+    return check_launch(fn);
+}
+
+// A block's warps lie one behind the other in time, as far as T fills them (a power of two), and
+// the rest of them side by side in the channels.
+template <int NW>
+unsigned gs_grid(GsArgs &g, int steps) {
+    g.tw = 1;
+    while (g.tw < NW && (long long)g.tw * steps < g.T) g.tw *= 2;
+    g.chunks = (int)ceil_div(g.T, (long long)steps * g.tw);
+    const int cb = NW / g.tw;
+    g.n_cw = (int)(ceil_div(ceil_div(g.D, 16), cb) * cb);
+    return (unsigned)(g.chunks * g.B * (g.n_cw / cb));
+}
+
+template <typename E, bool V, bool R>
+int gs_fwd_launch(const char *fn, const void *x, const void *rg, const void *ig, const float *h0, void *h,
+                  float *hT, float *ckpt, GsArgs g, const GsWords &w, cudaStream_t s) {
+    constexpr int L = sizeof(E) == 2 ? 8 : 4;
+    const unsigned blocks = gs_grid<kFwdWarps>(g, 8 * L);
+    gated_fwd_kernel<E, V, R, L><<<blocks, kFwdWarps * 32, 0, s>>>((const E *)x, (const E *)rg, (const E *)ig, h0, (E *)h, hT, ckpt, g, w);
+    return check_launch(fn);
 }
 
 template <typename E>
-int gs_fwd(const char *fn, const void *x, const void *rg, const void *ig, const float *lam, const float *h0, void *h,
-           float *hT, float *ckpt, GsArgs g, void *ws, const GsLayout &l, cudaStream_t s) {
-    constexpr int L = sizeof(E) == 2 ? 8 : 4;
-    g.chunks = ceil_div(g.T, 8 * L);
-    const long long blocks = ceil_div(g.chunks * g.B * g.n_cw, kGsWarps);
+int gs_fwd(const char *fn, const void *x, const void *rg, const void *ig, const float *h0, void *h,
+           float *hT, float *ckpt, const GsArgs &g, void *ws, const GsLayout &l, cudaStream_t s) {
     const bool vec = vec_ok<E>(g.D, {x, rg, ig, h});
     const GsWords w = gs_words(ws, l);
-#define CLA_GS_FWD(V, R)                                                                                             \
-    gated_fwd_kernel<E, V, R, L><<<(unsigned)blocks, kGsWarps * 32, 0, s>>>((const E *)x, (const E *)rg, (const E *)ig, \
-                                                                            lam, h0, (E *)h, hT, ckpt, g, w)
-    if (vec && g.reset == nullptr) CLA_GS_FWD(true, false);
-    else if (vec) CLA_GS_FWD(true, true);
-    else if (g.reset == nullptr) CLA_GS_FWD(false, false);
-    else CLA_GS_FWD(false, true);
-#undef CLA_GS_FWD
+    if (vec && g.reset == nullptr) return gs_fwd_launch<E, true, false>(fn, x, rg, ig, h0, h, hT, ckpt, g, w, s);
+    if (vec) return gs_fwd_launch<E, true, true>(fn, x, rg, ig, h0, h, hT, ckpt, g, w, s);
+    if (g.reset == nullptr) return gs_fwd_launch<E, false, false>(fn, x, rg, ig, h0, h, hT, ckpt, g, w, s);
+    return gs_fwd_launch<E, false, true>(fn, x, rg, ig, h0, h, hT, ckpt, g, w, s);
+}
+
+template <typename E, bool V, bool R>
+int gs_bwd_launch(const char *fn, const void *x, const void *rg, const void *ig, const float *ckpt,
+                  const void *dh, const float *dhT, void *dx, void *drg, void *dig, float *part, float *dh0, GsArgs g,
+                  const GsWords &w, cudaStream_t s) {
+    const unsigned blocks = gs_grid<kBwdWarps>(g, 32);
+    gated_bwd_kernel<E, V, R><<<blocks, kBwdWarps * 32, 0, s>>>((const E *)x, (const E *)rg, (const E *)ig, ckpt, (const E *)dh, dhT,
+                                                                  (E *)dx, (E *)drg, (E *)dig, part, dh0, g, w);
     return check_launch(fn);
 }
 
@@ -702,31 +810,26 @@ int gs_bwd(const char *fn, const void *x, const void *rg, const void *ig, const 
            const float *ckpt, const void *dh, const float *dhT, void *dx, void *drg, void *dig, float *dlam, float *dh0,
            GsArgs g, void *ws, const GsLayout &l, cudaStream_t s) {
     char *p = static_cast<char *>(ws);
-    if (int st = gs_clear(fn, ws, l, s)) return st;
+    g.rate = reinterpret_cast<const float *>(p + l.rate);
+    if (int st = gs_setup(fn, ws, l, 0, lam, g.D, g.c, s)) return st;
     if (ckpt == nullptr) {
         float *states = reinterpret_cast<float *>(p + l.ckpt);
-        if (int st = gs_fwd<E>(fn, x, rg, ig, lam, h0, nullptr, nullptr, states, g, ws, l, s)) return st;
+        if (int st = gs_fwd<E>(fn, x, rg, ig, h0, nullptr, nullptr, states, g, ws, l, s)) return st;
         // the words again, but not the header, which holds the scan's status
-        CLA_CUDA_TRY(cudaMemsetAsync(p + l.words, 0, l.clear - l.words, s), fn);
+        if (int st = gs_setup(fn, ws, l, l.words, lam, g.D, g.c, s)) return st;
         ckpt = states;
     }
-    g.chunks = ceil_div(g.T, kGsCkpt);
-    const long long blocks = ceil_div(g.chunks * g.B * g.n_cw, kGsWarps);
     const bool vec = vec_ok<E>(g.D, {x, rg, ig, dh, dx, drg, dig});
     const GsWords w = gs_words(ws, l);
     float *part = reinterpret_cast<float *>(p + l.part);
-#define CLA_GS_BWD(V, R)                                                                                              \
-    gated_bwd_kernel<E, V, R><<<(unsigned)blocks, kGsWarps * 32, 0, s>>>((const E *)x, (const E *)rg, (const E *)ig, lam, \
-                                                                         ckpt, (const E *)dh, dhT, (E *)dx, (E *)drg,   \
-                                                                         (E *)dig, part, dh0, g, w)
-    if (vec && g.reset == nullptr) CLA_GS_BWD(true, false);
-    else if (vec) CLA_GS_BWD(true, true);
-    else if (g.reset == nullptr) CLA_GS_BWD(false, false);
-    else CLA_GS_BWD(false, true);
-#undef CLA_GS_BWD
-    if (int st = check_launch(fn)) return st;
+    int st;
+    if (vec && g.reset == nullptr) st = gs_bwd_launch<E, true, false>(fn, x, rg, ig, ckpt, dh, dhT, dx, drg, dig, part, dh0, g, w, s);
+    else if (vec) st = gs_bwd_launch<E, true, true>(fn, x, rg, ig, ckpt, dh, dhT, dx, drg, dig, part, dh0, g, w, s);
+    else if (g.reset == nullptr) st = gs_bwd_launch<E, false, false>(fn, x, rg, ig, ckpt, dh, dhT, dx, drg, dig, part, dh0, g, w, s);
+    else st = gs_bwd_launch<E, false, true>(fn, x, rg, ig, ckpt, dh, dhT, dx, drg, dig, part, dh0, g, w, s);
+    if (st) return st;
     if (dlam != nullptr) {
-        long long rows = g.chunks * g.B;
+        long long rows = ceil_div(g.T, kGsCkpt) * g.B;
         if (rows > kDlamRows) {
             float *part2 = reinterpret_cast<float *>(p + l.part2);
             gated_dlam_kernel<<<dim3((unsigned)ceil_div(g.D, 32), kDlamShares), 1024, 0, s>>>(part, lam, part2, rows, g.D);
@@ -767,19 +870,19 @@ extern "C" int cla_gated_scan_fwd(const void *x, const void *rgate, const void *
     if (ws == nullptr || !aligned16(ws) || ws_bytes < cla_gated_scan_workspace_size(B, T, D))
         return fail(CLA_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes,
                     cla_gated_scan_workspace_size(B, T, D));
-    const GsArgs g{reset, lens, T, 0, (int)B, (int)D, (int)ceil_div(D, 16), c};
     const GsLayout l = gs_layout(B, T, D);
+    const GsArgs g{reset, lens, reinterpret_cast<const float *>(static_cast<char *>(ws) + l.rate), (int)T, (int)B, (int)D, 1, 0, 0, c};
     cudaStream_t s = (cudaStream_t)stream;
-    if (int st = gs_clear(fn, ws, l, s)) return st;
+    if (int st = gs_setup(fn, ws, l, 0, lam, D, c, s)) return st;
     if (T == 0) {
         if (hT == nullptr) return CLA_OK;
         if (h0 != nullptr) CLA_CUDA_TRY(cudaMemcpyAsync(hT, h0, (size_t)(B * D) * 4, cudaMemcpyDeviceToDevice, s), fn);
         else CLA_CUDA_TRY(cudaMemsetAsync(hT, 0, (size_t)(B * D) * 4, s), fn);
         return CLA_OK;
     }
-    if (dtype == CLA_F32) return gs_fwd<float>(fn, x, rgate, igate, lam, h0, h, hT, ckpt, g, ws, l, s);
-    if (dtype == CLA_BF16) return gs_fwd<__nv_bfloat16>(fn, x, rgate, igate, lam, h0, h, hT, ckpt, g, ws, l, s);
-    return gs_fwd<__half>(fn, x, rgate, igate, lam, h0, h, hT, ckpt, g, ws, l, s);
+    if (dtype == CLA_F32) return gs_fwd<float>(fn, x, rgate, igate, h0, h, hT, ckpt, g, ws, l, s);
+    if (dtype == CLA_BF16) return gs_fwd<__nv_bfloat16>(fn, x, rgate, igate, h0, h, hT, ckpt, g, ws, l, s);
+    return gs_fwd<__half>(fn, x, rgate, igate, h0, h, hT, ckpt, g, ws, l, s);
 }
 
 extern "C" int cla_gated_scan_bwd(const void *x, const void *rgate, const void *igate, const float *lam, const float *h0,
@@ -799,7 +902,7 @@ extern "C" int cla_gated_scan_bwd(const void *x, const void *rgate, const void *
     if (ws == nullptr || !aligned16(ws) || ws_bytes < cla_gated_scan_workspace_size(B, T, D))
         return fail(CLA_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes,
                     cla_gated_scan_workspace_size(B, T, D));
-    const GsArgs g{reset, lens, T, 0, (int)B, (int)D, (int)ceil_div(D, 16), c};
+    const GsArgs g{reset, lens, nullptr, (int)T, (int)B, (int)D, 1, 0, 0, c};
     const GsLayout l = gs_layout(B, T, D);
     cudaStream_t s = (cudaStream_t)stream;
     if (B * T == 0) {
@@ -808,7 +911,8 @@ extern "C" int cla_gated_scan_bwd(const void *x, const void *rgate, const void *
             if (dhT != nullptr) CLA_CUDA_TRY(cudaMemcpyAsync(dh0, dhT, (size_t)(B * D) * 4, cudaMemcpyDeviceToDevice, s), fn);
             else CLA_CUDA_TRY(cudaMemsetAsync(dh0, 0, (size_t)(B * D) * 4, s), fn);
         }
-        return gs_clear(fn, ws, l, s);
+        CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(WsHeader), s), fn);
+        return CLA_OK;
     }
     if (dtype == CLA_F32)
         return gs_bwd<float>(fn, x, rgate, igate, lam, h0, ckpt, dh, dhT, dx, drgate, digate, dlam, dh0, g, ws, l, s);

@@ -70,16 +70,9 @@ int wa_strides(const char *fn, const int64_t *strides, const char *const *names,
     return CLA_OK;
 }
 
-// Multiprocessors of the current device, asked for once per device.
 int wa_blocks(const char *fn, long long items, unsigned *blocks) {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    CLA_CUDA_TRY(cudaGetDevice(&dev), fn);
-    if (dev < 64) n = known[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        CLA_CUDA_TRY(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev), fn);
-        if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-    }
+    int n = 0;
+    if (int st = multiprocessors(fn, &n)) return st;
     *blocks = (unsigned)(items < n ? items : n);
     return CLA_OK;
 }

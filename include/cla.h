@@ -616,7 +616,7 @@ size_t cla_gated_scan_workspace_size(int64_t B, int64_t T, int64_t D);
  *          chunk, for the backward
  *   c      a positive finite number; the decay of a fully open gate is
  *          exp(-c softplus(lam)); decays below 2^-126 count as 2^-126
- * B * D must be below 2^31, B * T * D below 10^12. */
+ * B * D must be below 2^31, B * T * D (D rounded up to 16) below 10^12. */
 int cla_gated_scan_fwd(const void *x, const void *rgate, const void *igate,
                        const float *lam, const float *h0, const uint8_t *reset,
                        const int32_t *lens, void *h, float *hT, float *ckpt,
