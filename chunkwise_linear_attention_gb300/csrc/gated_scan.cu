@@ -54,6 +54,11 @@ __device__ __forceinline__ float rsqa(float v) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
     return y;
 }
+__device__ __forceinline__ float sqra(float v) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+    return y;
+}
 __device__ __forceinline__ float2 f2(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
@@ -81,18 +86,24 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // with no digits lost, where 1 - a^2 from a rounded a would keep only those above
 // 2^-24 / (1 - a).  The polynomial is a least-maximum-error fit of 2^f on [-1/2, 1/2] with
 // p(0) = 1 (Lawson's reweighted least squares, degree 6, 2e-9).  NaN passes through.
+//
+// BWD: with the factors that the gradients need (rm, r1, i1); without them nothing has to be held
+// in range for 1 - sigmoid(g), and m is one square root.
+template <bool BWD>
 __device__ __forceinline__ Gate2 gate2(float2 rg, float2 ig, float2 nl2) {
     constexpr float kP1 = 6.931471825e-01f, kP2 = 2.402264774e-01f, kP3 = 5.550332367e-02f, kP4 = 9.618437849e-03f,
                     kP5 = 1.339887269e-03f, kP6 = 1.535334159e-04f, kMagic = 12582912.0f;
     Gate2 q;
     const float2 pr = mul2(rg, f2(-kLog2e)), pi = mul2(ig, f2(-kLog2e));
-    const float2 er = make_float2(ex2a(min_nan(pr.x, 126.f)), ex2a(min_nan(pr.y, 126.f)));
-    const float2 ei = make_float2(ex2a(min_nan(pi.x, 126.f)), ex2a(min_nan(pi.y, 126.f)));
+    const float2 er = BWD ? make_float2(ex2a(min_nan(pr.x, 126.f)), ex2a(min_nan(pr.y, 126.f))) : make_float2(ex2a(pr.x), ex2a(pr.y));
+    const float2 ei = BWD ? make_float2(ex2a(min_nan(pi.x, 126.f)), ex2a(min_nan(pi.y, 126.f))) : make_float2(ex2a(pi.x), ex2a(pi.y));
     const float2 br = add2(er, f2(1.f)), bi = add2(ei, f2(1.f));
     const float2 r = make_float2(rcpa(br.x), rcpa(br.y));
     q.i = make_float2(rcpa(bi.x), rcpa(bi.y));
-    q.r1 = mul2(er, r);
-    q.i1 = mul2(ei, q.i);
+    if constexpr (BWD) {
+        q.r1 = mul2(er, r);
+        q.i1 = mul2(ei, q.i);
+    }
     float2 y = mul2(nl2, r);
     y = make_float2(max_nan(y.x, -126.f), max_nan(y.y, -126.f));
     q.y = y;
@@ -112,9 +123,13 @@ __device__ __forceinline__ Gate2 gate2(float2 rg, float2 ig, float2 nl2) {
     q.a = add2(sc, t);
     float2 om = fma2(t, f2(-1.f), fma2(sc, f2(-1.f), f2(1.f)));  // 1 - a
     om = mul2(om, add2(q.a, f2(1.f)));                            // 1 - a^2
-    om = make_float2(fmaxf(om.x, 1e-37f), fmaxf(om.y, 1e-37f));
-    q.rm = make_float2(rsqa(om.x), rsqa(om.y));
-    q.m = mul2(om, q.rm);
+    if constexpr (BWD) {
+        om = make_float2(fmaxf(om.x, 1e-37f), fmaxf(om.y, 1e-37f));
+        q.rm = make_float2(rsqa(om.x), rsqa(om.y));
+        q.m = mul2(om, q.rm);
+    } else {
+        q.m = make_float2(sqra(om.x), sqra(om.y));
+    }
     return q;
 }
 
@@ -461,7 +476,7 @@ gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
         cvt4<E>(rx[j], xv);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            const Gate2 e = gate2(rv[v], iv[v], nl2[v]);
+            const Gate2 e = gate2<false>(rv[v], iv[v], nl2[v]);
             a[j][v] = e.a;
             u[j][v] = mul2(mul2(e.m, e.i), xv[v]);
             if constexpr (RST)
@@ -469,16 +484,22 @@ gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
                     a[j][v] = f2(0.f);
                     u[j][v] = mul2(e.i, xv[v]);
                 }
-            if (!full && j >= q.n) {  // behind the sequence
-                a[j][v] = f2(1.f);
-                u[j][v] = f2(0.f);
-            }
+        }
+    }
+    if (!full) {  // behind the sequence
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            if (j >= q.n) a[j][0] = a[j][1] = f2(1.f), u[j][0] = u[j][1] = f2(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
             const float2 pa = A[v], pb = B[v];
             A[v] = a[j][v];
             B[v] = u[j][v];
             after<RST>(A[v], B[v], pa, pb);
         }
-    }
     scan_runs<RST, false>(A, B, sub);
     float2 Ax[2], Bx[2], s[2];
 #pragma unroll
@@ -554,7 +575,7 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
         cvt4<E>(rx[j], xv);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            const Gate2 e = gate2(rv[v], iv[v], nl2[v]);
+            const Gate2 e = gate2<true>(rv[v], iv[v], nl2[v]);
             a[j][v] = e.a;
             La[j][v] = mul2(mul2(e.y, f2(kLn2)), e.a);
             r1[j][v] = e.r1;
@@ -565,16 +586,27 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
                     a[j][v] = La[j][v] = w2[j][v] = f2(0.f), mi[j][v] = e.i;
             xi[j][v] = mul2(xv[v], e.i1);
             hp[j][v] = mul2(mi[j][v], xv[v]);
-            if (!full && j >= q.n) {
-                a[j][v] = f2(1.f);
-                La[j][v] = r1[j][v] = w2[j][v] = mi[j][v] = xi[j][v] = hp[j][v] = f2(0.f);
-            }
+        }
+    }
+    if (!full) {  // behind the sequence
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            if (j >= q.n)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    a[j][v] = f2(1.f);
+                    La[j][v] = r1[j][v] = w2[j][v] = mi[j][v] = xi[j][v] = hp[j][v] = f2(0.f);
+                }
+    }
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
             const float2 pa = A[v], pb = B[v];
             A[v] = a[j][v];
             B[v] = hp[j][v];
             after<RST>(A[v], B[v], pa, pb);
         }
-    }
     scan_runs<RST, false>(A, B, sub);
     auto grad = [&](int j, float2 (&v)[2]) {  // dh_t of the run's step j
         cvt4<E>(rd[j], v);
@@ -689,7 +721,7 @@ __global__ void gated_step_kernel(const E *x, const E *rg, const E *ig, const fl
     const long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (u >= (long long)B * D) return;
     const int b = (int)(u / D), d = (int)(u % D);
-    const Gate2 q = gate2(f2(to_f32(rg[u])), f2(to_f32(ig[u])), f2(-c * softplus(lam[d]) * kLog2e));
+    const Gate2 q = gate2<false>(f2(to_f32(rg[u])), f2(to_f32(ig[u])), f2(-c * softplus(lam[d]) * kLog2e));
     const float w = q.i.x * to_f32(x[u]);
     const float s = (reset != nullptr && reset[b]) ? w : fmaf(q.a.x, h[u], q.m.x * w);
     h[u] = s;
