@@ -105,7 +105,7 @@ long long wa_dkv_blocks(int64_t B, int64_t H, int64_t T, int64_t window, int64_t
 }
 
 template <int D, bool BF>
-int wa_bwd(const char *fn, const WaMaps &m, const void *o, const void *dO, const float *lse, void *dq, void *dk, void *dv,
+int wa_bwd(const char *fn, const WaMaps &m, const WaMaps &mkv, const void *o, const void *dO, const float *lse, void *dq, void *dk, void *dv,
            const Str3 *r, const WaArgs &g, void *ws, cudaStream_t s) {
     static std::atomic<unsigned long long> done_q{0}, done_kv{0};
     constexpr int smem_q = DqCfg<D>::SMEM > kMinSmem ? DqCfg<D>::SMEM : kMinSmem;
@@ -123,7 +123,7 @@ int wa_bwd(const char *fn, const WaMaps &m, const void *o, const void *dO, const
     if (int st = check_launch(fn)) return st;
     if (int st = wa_blocks(fn, wa_dkv_blocks(g.B, g.H, g.T, g.window, g.sinks), &blocks)) return st;
     CutList *cuts = reinterpret_cast<CutList *>(parts + (size_t)wa_dkv_blocks(g.B, g.H, g.T, g.window, g.sinks) * 4 * kWT * D);
-    wa_dkv_kernel<D, BF><<<blocks, DkvCfg<D>::THREADS, smem_kv, s>>>(m, lse, delta, dk, dv, parts, cuts, r[6], r[7], g, hdr);
+    wa_dkv_kernel<D, BF><<<blocks, DkvCfg<D>::THREADS, smem_kv, s>>>(mkv, lse, delta, dk, dv, parts, cuts, r[6], r[7], g, hdr);
     if (int st = check_launch(fn)) return st;
     if (blocks > 1) {
         wa_join_kernel<D, BF><<<dim3(blocks - 1, kJoinY), 256, 0, s>>>(parts, cuts, dk, dv, r[6], r[7], g.T, (int)blocks);
@@ -163,9 +163,10 @@ extern "C" int cla_window_attn_fwd(const void *q, const void *k, const void *v, 
     const bool bf = dtype == CLA_BF16;
     WaMaps m;
     if (!make_map_bht(&m.q, q, bf, d, T, H, B, r[0]) || !make_map_bht(&m.k, k, bf, d, T, Hkv, B, r[1]) ||
-        !make_map_bht(&m.v, v, bf, d, T, Hkv, B, r[2]))
+        !make_map_bht(&m.v, v, bf, d, T, Hkv, B, r[2]) || !make_map_bht(&m.x, o, bf, d, T, H, B, r[3]))
         return fail(CLA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
     m.g = m.q;
+    m.y = m.q;
     if (d == 128) return bf ? wa_fwd<128, true>(fn, m, o, lse, r[3], g, hdr, s) : wa_fwd<128, false>(fn, m, o, lse, r[3], g, hdr, s);
     return bf ? wa_fwd<64, true>(fn, m, o, lse, r[3], g, hdr, s) : wa_fwd<64, false>(fn, m, o, lse, r[3], g, hdr, s);
 }
@@ -207,13 +208,18 @@ extern "C" int cla_window_attn_bwd(const void *q, const void *k, const void *v, 
     const bool bf = dtype == CLA_BF16;
     WaMaps m;
     if (!make_map_bht(&m.q, q, bf, d, T, H, B, r[0]) || !make_map_bht(&m.k, k, bf, d, T, Hkv, B, r[1]) ||
-        !make_map_bht(&m.v, v, bf, d, T, Hkv, B, r[2]) || !make_map_bht(&m.g, dO, bf, d, T, H, B, r[4]))
+        !make_map_bht(&m.v, v, bf, d, T, Hkv, B, r[2]) || !make_map_bht(&m.g, dO, bf, d, T, H, B, r[4]) ||
+        !make_map_bht(&m.x, dq, bf, d, T, H, B, r[5]))
+        return fail(CLA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
+    m.y = m.x;
+    WaMaps mkv = m;
+    if (!make_map_bht(&mkv.x, dk, bf, d, T, Hkv, B, r[6]) || !make_map_bht(&mkv.y, dv, bf, d, T, Hkv, B, r[7]))
         return fail(CLA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
     if (d == 128)
-        return bf ? wa_bwd<128, true>(fn, m, o, dO, lse, dq, dk, dv, r, g, ws, s)
-                  : wa_bwd<128, false>(fn, m, o, dO, lse, dq, dk, dv, r, g, ws, s);
-    return bf ? wa_bwd<64, true>(fn, m, o, dO, lse, dq, dk, dv, r, g, ws, s)
-              : wa_bwd<64, false>(fn, m, o, dO, lse, dq, dk, dv, r, g, ws, s);
+        return bf ? wa_bwd<128, true>(fn, m, mkv, o, dO, lse, dq, dk, dv, r, g, ws, s)
+                  : wa_bwd<128, false>(fn, m, mkv, o, dO, lse, dq, dk, dv, r, g, ws, s);
+    return bf ? wa_bwd<64, true>(fn, m, mkv, o, dO, lse, dq, dk, dv, r, g, ws, s)
+              : wa_bwd<64, false>(fn, m, mkv, o, dO, lse, dq, dk, dv, r, g, ws, s);
 }
 
 extern "C" int cla_window_cache_write(const void *k, const void *v, const int32_t *lens, void *kcache, void *vcache,

@@ -37,8 +37,9 @@ struct WaArgs {
     int T, window, sinks, B, H, Hkv;
 };
 
+// Of the inputs q, k, v, dO, and of the outputs: o, dq in `x`, dk in `x`, dv in `y`.
 struct WaMaps {
-    CUtensorMap q, k, v, g;
+    CUtensorMap q, k, v, g, x, y;
 };
 
 __device__ __forceinline__ int wa_len(const WaArgs &g, int b) {
@@ -50,6 +51,43 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
         "[%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, int x, int y, int z, int w, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
+                 : "memory");
+}
+// A value that is the same in all lanes, in a form that the compiler knows to be.  The warp that
+// issues the products keeps its loops' bounds and operands so: descriptors that it takes for
+// divergent are moved into uniform registers before each product, which took 75 cycles each.
+__device__ __forceinline__ int uni(int v) { return __shfl_sync(~0u, v, 0); }
+// The lane that issues them, chosen once.
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n .reg .b32 r;\n elect.sync r|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 e, %0, 0;\n setp.ne.b32 p, %5, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n}" ::"r"(lead),
+        "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 e, %0, 0;\n setp.ne.b32 p, %5, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n}" ::"r"(lead),
+        "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.b32 e, %0, 0;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}" ::"r"(lead),
+        "r"(bar)
         : "memory");
 }
 // kind::f16 instruction descriptor, fp32 accumulate, A and B both bf16 or both fp16.
@@ -138,21 +176,21 @@ struct Tile {
 // kNegateA for -A B^T.
 constexpr uint32_t kNegateA = 1u << 13;
 template <int D, bool BF>
-__device__ __forceinline__ void mma_scores(uint32_t acc, uint32_t a, uint32_t b, uint32_t negate = 0u) {
+__device__ __forceinline__ void mma_scores(uint32_t lead, uint32_t acc, uint32_t a, uint32_t b, uint32_t negate = 0u) {
     const uint64_t da = Tile<D>::kmajor(a), db = Tile<D>::kmajor(b);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss_w(acc, da + Tile<D>::kstep(kk), db + Tile<D>::kstep(kk), idesc16<BF>(kWT, 0) | negate, kk ? 1u : 0u);
+        mma_ss(lead, acc, da + Tile<D>::kstep(kk), db + Tile<D>::kstep(kk), idesc16<BF>(kWT, 0) | negate, kk ? 1u : 0u);
 }
 // acc (+)= P X: P [128 x 128] in tensor memory, X a tile [128 tokens][D].  P lies packed over the
 // scores it came from in pieces of C columns, each at the start of its C score columns: a thread
 // then writes only where it has read itself, and the threads of a row need not wait for another.
 template <int D, bool BF, int C>
-__device__ __forceinline__ void mma_apply(uint32_t acc, uint32_t p, uint32_t x, bool add) {
+__device__ __forceinline__ void mma_apply(uint32_t lead, uint32_t acc, uint32_t p, uint32_t x, bool add) {
     const uint64_t dx = Tile<D>::nmajor(x);
 #pragma unroll
     for (int kk = 0; kk < kWT / 16; ++kk)
-        mma_ts_w(acc, p + (kk / (C / 16)) * C + (kk % (C / 16)) * 8, dx + Tile<D>::nstep(kk), idesc16<BF>(D, 1),
+        mma_ts(lead, acc, p + (kk / (C / 16)) * C + (kk % (C / 16)) * 8, dx + Tile<D>::nstep(kk), idesc16<BF>(D, 1),
                  (add || kk) ? 1u : 0u);
 }
 
@@ -178,9 +216,9 @@ __device__ __forceinline__ void tmem_free_all(uint32_t tmem) {
 // that did not is reported, not used.
 constexpr int kSmall = 2560;
 struct Small {
-    uint64_t bars[32];
+    uint64_t bars[40];
     uint32_t tmem, dead;
-    uint32_t pad[62];
+    uint32_t pad[46];
     float f[512];
 };
 static_assert(sizeof(Small) == kSmall, "layout behind the tiles");
@@ -222,28 +260,36 @@ __device__ __forceinline__ uint32_t query_bits(const WaArgs &g, int t0, int s) {
     return ~bits_below(s - t0) & (s < g.sinks ? ~0u : bits_below(s - t0 + g.window));
 }
 
-// One row of o, dq, dk or dv (D columns of an accumulator, times f) to memory.
-template <int D, bool BF>
-__device__ __forceinline__ void store_row(uint32_t taddr, void *out, long long at, float f, bool write, bool zero) {
+// Columns [col, col + N) of a row of an accumulator, times f, into a tile in shared memory, from
+// where one store takes the tile out.  (Rows stored by their own threads are 32 lines an
+// instruction; that took 4000 cycles a tile.)
+template <int N, bool BF>
+__device__ __forceinline__ void stage_row(uint32_t taddr, uint32_t tile, int row, int col, float f, bool zero) {
 #pragma unroll
-    for (int c = 0; c < D; c += 16) {
+    for (int c = 0; c < N; c += 16) {
         uint32_t r[16];
         tmem_ld16(taddr + c, r);
         tmem_ld_wait();
-        if (write) {
-            uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at + c);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t w[4];
+        for (int k = 0; k < 2; ++k) {
+            uint32_t w[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = zero ? 0u
-                                : pack16<BF>(make_float2(__uint_as_float(r[k * 8 + 2 * j]) * f,
-                                                         __uint_as_float(r[k * 8 + 2 * j + 1]) * f));
-                p[k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int j = 0; j < 4; ++j)
+                w[j] = zero ? 0u
+                            : pack16<BF>(make_float2(__uint_as_float(r[k * 8 + 2 * j]) * f, __uint_as_float(r[k * 8 + 2 * j + 1]) * f));
+            const int x = col + c + 8 * k;
+            st_shared_v4(tile + (x >> 6) * (kWT * 128) + row * 128 + ((((x >> 3) ^ row) & 7) << 4), __uint_as_float(w[0]),
+                         __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
         }
     }
+    fence_async_smem();
+}
+// By one thread, when the tile is staged.
+template <int D>
+__device__ __forceinline__ void store_tile(const CUtensorMap *m, uint32_t tile, int t, int h, int b) {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) tma_store_4d(m, c * 64, t, h, b, tile + c * (kWT * 128));
+    tma_store_commit();
 }
 template <int D>
 __device__ __forceinline__ void zero_row(void *out, long long at) {
@@ -265,7 +311,7 @@ template <int D>
 struct FwdCfg {
     static constexpr int STAGES = D == 128 ? 3 : 8;  // of keys and values, beside two pairs of query tiles
     static constexpr int SMEM = (4 + STAGES) * Tile<D>::BYTES + kSmall;
-    static constexpr int THREADS = 576;  // 16 math warps, products, loads
+    static constexpr int THREADS = 608;  // 16 math warps, products, loads, stores
 };
 
 struct FwdItem {
@@ -306,17 +352,16 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sq = smem_u32(smem_raw), skv = sq + 4 * TB;
     Small &sm = *reinterpret_cast<Small *>(smem_raw + (4 + ST) * TB);
-    static_assert(2 * ST + 10 <= 32, "barriers");
+    static_assert(2 * ST + 14 <= 40, "barriers");
     float(*s_row)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [tile][half][row]: maxima, in the end sums
     if (misplaced(sq, hdr)) return;
     const int warp = threadIdx.x >> 5, tiles = (g.T + kWT - 1) / kWT;
     const uint32_t b0 = smem_u32(sm.bars);
-    const uint32_t q_full = b0, q_empty = b0 + 16, o_full = b0 + 32, s_full = b0 + 48, p_ready = b0 + 64;  // two each
-    const uint32_t kv_full = b0 + 80, kv_empty = kv_full + 8 * ST;
+    const uint32_t q_full = b0, q_empty = b0 + 16, o_full = b0 + 32, s_full = b0 + 48, p_ready = b0 + 64, staged = b0 + 80;  // two each; of staged four, [tile][parity]
+    const uint32_t kv_full = b0 + 112, kv_empty = kv_full + 8 * ST;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 8; ++i) mbar_init(b0 + 8 * i, 1);
-        mbar_init(p_ready, 8);
-        mbar_init(p_ready + 8, 8);
+        for (int i = 0; i < 6; ++i) mbar_init(p_ready + 8 * i, 8);  // and staged
         for (int i = 0; i < 2 * ST; ++i) mbar_init(kv_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = 0u;
@@ -358,6 +403,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
         // One stream of steps over all items: for each of the two tiles the output of the step
         // before, then the scores of this one, so that a tile begins the next item while the other
         // still ends the last.
+        const uint32_t lead = elect();
         uint32_t j = 0, it = 0, np[2] = {0, 0};  // steps, items, probabilities taken
         const uint32_t negate = g.scale < 0.f ? kNegateA : 0u;
         bool owed[2] = {false, false}, begun[2] = {false, false}, ends[2] = {false, false};
@@ -372,14 +418,14 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
             }
             wait(p_ready + 8 * u, np[u]++, 25);
             tc_fence_after();
-            mma_apply<D, BF, 64>(tO + 128 * u, tS + 128 * u, skv + s * TB, begun[u]);
+            mma_apply<D, BF, 64>(lead, tO + 128 * u, tS + 128 * u, skv + s * TB, begun[u]);
             begun[u] = !ends[u];
-            if (ends[u]) mma_commit_w(o_full + 8 * u);
+            if (ends[u]) mma_commit(lead, o_full + 8 * u);
             owed[u] = false;
         };
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             const FwdItem w = fwd_item(g, item, tiles);
-            const int len = wa_len(g, w.b);
+            const int len = uni(wa_len(g, w.b));
             const FwdTiles kt(g, w, len);
             if (kt.count == 0) continue;
             const uint32_t qb = it & 1;
@@ -396,21 +442,41 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
                     if (!got_k) wait(kv_full + 8 * s, 2 * j / ST, 26);
                     got_k = true;
                     tc_fence_after();
-                    mma_scores<D, BF>(tS + 128 * u, sq + (2 * qb + u) * TB, skv + s * TB, negate);
-                    mma_commit_w(s_full + 8 * u);
+                    mma_scores<D, BF>(lead, tS + 128 * u, sq + (2 * qb + u) * TB, skv + s * TB, negate);
+                    mma_commit(lead, s_full + 8 * u);
                     owed[u] = true;
                     ends[u] = tile == mine.hi;
                 }
-                if (j > 0) mma_commit_w(kv_empty + 8 * ((2 * j - 1) % ST));
-                mma_commit_w(kv_empty + 8 * s);
+                if (j > 0) mma_commit(lead, kv_empty + 8 * ((2 * j - 1) % ST));
+                mma_commit(lead, kv_empty + 8 * s);
                 rows = len - tile * kWT;
             }
-            mma_commit_w(q_empty + 8 * qb);
             ++it;
         }
         bool got = false;
         settle(0, got);
         settle(1, got);
+    } else if (warp == 18) {
+        // ------------------------------------------------------------ stores, which give the query tiles back
+        if ((threadIdx.x & 31) == 0) {
+            uint32_t it = 0, n[2] = {0, 0};
+            for (int item = blockIdx.x; item < items; item += gridDim.x) {
+                const FwdItem w = fwd_item(g, item, tiles);
+                const FwdTiles kt(g, w, wa_len(g, w.b));
+                if (kt.count == 0) continue;
+                for (int u = 0; u < 2; ++u)
+                    if (u == 0 || kt.b.hi >= kt.b.lo) {
+                        wait(staged + 16 * u + 8 * (n[u] & 1), n[u] >> 1, 29);
+                        ++n[u];
+                        if (*wait.dead == 0u)
+                            store_tile<D>(&maps.x, sq + (2 * (it & 1) + u) * TB, w.t0 + u * w.step_t, w.h + u * w.step_h, w.b);
+                    }
+                tma_store_wait_read();
+                mbar_arrive(q_empty + 8 * (it & 1));
+                ++it;
+            }
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ probabilities and output
         const int u = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + (threadIdx.x & 31);
@@ -419,7 +485,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
         // the scores of a negative factor come negated, and a factor of 0 must leave masked scores at -inf
         const float c = fmaxf(fabsf(g.scale) * 1.4426950408889634f, 1e-30f);
         float *own = &s_row[u][half][row], *other = &s_row[u][half ^ 1][row];
-        uint32_t ns = 0, no = 0;
+        uint32_t ns = 0, no = 0, it = 0;
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             const FwdItem w = fwd_item(g, item, tiles);
             const int len = wa_len(g, w.b), t0 = w.t0 + u * w.step_t, t = t0 + row;
@@ -501,21 +567,27 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
             }
             if (t0 < g.T) {  // the same for the whole tile
                 const int h = w.h + u * w.step_h;
-                const long long at = w.b * so.b + h * so.h + t * so.t + half * (D / 2);
                 const bool dead = t >= len;
                 if (first) {
-                    if (t < g.T) zero_row<D / 2>(o, at);
+                    if (t < g.T) zero_row<D / 2>(o, w.b * so.b + h * so.h + t * so.t + half * (D / 2));
                 } else {
                     *own = l;
                     quarter_sync<2>(id);
                     l += *other;
-                    store_row<D / 2, BF>(to, o, at, 1.f / l, t < g.T, dead);
-                    quarter_sync<2>(id);  // *other has been read
+                    // into the query tile, whose last product is done
+                    stage_row<D / 2, BF>(to, sq + (2 * (it & 1) + u) * TB, row, half * (D / 2), 1.f / l, dead);
                 }
                 if (half == 0 && t < g.T)
                     lse[((long long)w.b * g.H + h) * g.T + t] = dead ? -INFINITY : m * 0.6931471805599453f + logf(l);
             }
             tc_fence_before();
+            if (!first) {
+                warp_arrive(staged + 16 * u + 8 * ((no - 1) & 1));
+                quarter_sync<2>(id);  // *other has been read
+                ++it;
+            } else if (kt.count > 0) {
+                ++it;
+            }
         }
     }
     tmem_free_all(tmem);
@@ -531,7 +603,7 @@ struct DqCfg {
     // pairs of q and dO tiles: two where they fit, so that an item begins while the last one ends
     static constexpr int QST = D == 128 ? 1 : 2, KST = D == 128 ? 3 : 5, VST = D == 128 ? 2 : 4;
     static constexpr int SMEM = (2 * QST + KST + VST) * Tile<D>::BYTES + kSmall;
-    static constexpr int THREADS = 640;  // 16 math warps, products, loads, two for the rows' statistics
+    static constexpr int THREADS = 640;  // 16 math warps, products, loads, the rows' statistics, stores
 };
 
 template <int D, bool BF>
@@ -543,18 +615,20 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sq = smem_u32(smem_raw), sk = sq + 2 * QST * TB, sv = sk + KST * TB;  // q, dO in turn
     Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 * QST + KST + VST) * TB);
-    static_assert(13 + 2 * (KST + VST) <= 32, "barriers");
+    static_assert(15 + 2 * (KST + VST) <= 40, "barriers");
     float(*s_stat)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [item's parity][delta, lse log2 e][row]
     if (misplaced(sq, hdr)) return;
     const int warp = threadIdx.x >> 5, tiles = (g.T + kWT - 1) / kWT, G = g.H / g.Hkv;
     const uint32_t b0 = smem_u32(sm.bars);
     const uint32_t q_full = b0, q_empty = b0 + 16, acc_full = b0 + 32, dp_full = b0 + 40, s_full = b0 + 48, ds_ready = b0 + 64;
     const uint32_t st_full = b0 + 72, st_empty = b0 + 88;  // two each, by the item's parity
-    const uint32_t k_full = b0 + 104, k_empty = k_full + 8 * KST, v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST;
+    const uint32_t staged = b0 + 104, k_full = b0 + 120, k_empty = k_full + 8 * KST, v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 8; ++i) mbar_init(b0 + 8 * i, 1);
         mbar_init(ds_ready, 16);
         for (int i = 0; i < 2; ++i) mbar_init(st_full + 8 * i, 2), mbar_init(st_empty + 8 * i, 16);
+        mbar_init(staged, 16);
+        mbar_init(staged + 8, 16);
         for (int i = 0; i < 2 * (KST + VST); ++i) mbar_init(k_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = 0u;
@@ -603,11 +677,12 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
         }
         __syncwarp();
     } else if (warp == 16) {
+        const uint32_t lead = elect();
         uint32_t n = 0, it = 0;
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             int b, h, hk, t0;
             place(item, b, h, hk, t0);
-            const int len = wa_len(g, b);
+            const int len = uni(wa_len(g, b));
             const KeyTiles kt = key_tiles(g, t0, len);
             if (kt.hi < kt.lo) continue;
             const int ns = min(kt.sinks, kt.lo), count = kt.hi - kt.lo + 1 + ns;
@@ -617,15 +692,15 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 const int left = len - (i < ns ? i : kt.lo + i - ns) * kWT;
                 if (g.lens != nullptr && left < kWT) Tile<D>::zero_rows(sk + (j % KST) * TB, left);
                 tc_fence_after();
-                mma_scores<D, BF>(tS + 128 * (j & 1), sq + 2 * qb * TB, sk + (j % KST) * TB);
-                mma_commit_w(s_full + 8 * (j & 1));
+                mma_scores<D, BF>(lead, tS + 128 * (j & 1), sq + 2 * qb * TB, sk + (j % KST) * TB);
+                mma_commit(lead, s_full + 8 * (j & 1));
             };
             auto grads = [&](uint32_t j) {
                 wait(v_full + 8 * (j % VST), j / VST, 35);
                 tc_fence_after();
-                mma_scores<D, BF>(tP, sq + (2 * qb + 1) * TB, sv + (j % VST) * TB);
-                mma_commit_w(dp_full);
-                mma_commit_w(v_empty + 8 * (j % VST));
+                mma_scores<D, BF>(lead, tP, sq + (2 * qb + 1) * TB, sv + (j % VST) * TB);
+                mma_commit(lead, dp_full);
+                mma_commit(lead, v_empty + 8 * (j % VST));
             };
             wait(q_full + 8 * qb, it / QST, 36);
             scores(n, 0);
@@ -635,16 +710,31 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 wait(ds_ready, n, 37);
                 tc_fence_after();
                 if (i + 1 < count) grads(n + 1);
-                if (i + 1 == count) mma_commit_w(q_empty + 8 * qb);
-                mma_apply<D, BF, 32>(tA, tS + 128 * (n & 1), sk + (n % KST) * TB, i > 0);
-                mma_commit_w(k_empty + 8 * (n % KST));
+                mma_apply<D, BF, 32>(lead, tA, tS + 128 * (n & 1), sk + (n % KST) * TB, i > 0);
+                mma_commit(lead, k_empty + 8 * (n % KST));
             }
-            mma_commit_w(acc_full);
+            mma_commit(lead, acc_full);
             ++it;
         }
     } else if (warp >= 18) {
         // ------------------------------------------------------------ delta = dO . o and lse of the next item's rows
-        // A warp takes 64 rows, D / 8 lanes a row (16 bytes each), eight rows in flight a lane.
+        // A warp takes 64 rows, D / 8 lanes a row (16 bytes each), eight rows in flight a lane.  The
+        // second of them also stores dq, of the item before the one whose statistics it has formed.
+        uint32_t it = 0;
+        auto store = [&](int item) {
+            int b, h, hk, t0;
+            place(item, b, h, hk, t0);
+            const KeyTiles kt = key_tiles(g, t0, wa_len(g, b));
+            if (kt.hi < kt.lo) return;
+            if ((threadIdx.x & 31) == 0) {
+                wait(staged + 8 * (it & 1), it >> 1, 43);
+                if (*wait.dead == 0u) store_tile<D>(&maps.x, sq + 2 * (it % QST) * TB, t0, h, b);
+                tma_store_wait_read();
+                mbar_arrive(q_empty + 8 * (it % QST));
+            }
+            __syncwarp();
+            ++it;
+        };
         constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an access
         const int lane = threadIdx.x & 31, first = (warp - 18) * 64 + lane / LPR, col = lane % LPR * 8;
         uint32_t all = 0;
@@ -689,7 +779,9 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 dst2[row] = t < len ? __ldg(lse + at + t) * 1.4426950408889634f : INFINITY;
             }
             warp_arrive(st_full + 8 * (all & 1));
+            if (warp == 19 && all > 0) store(item - gridDim.x);
         }
+        if (warp == 19 && all > 0) store(blockIdx.x + (all - 1) * gridDim.x);
     } else {
         const int part = warp >> 2, quarter = warp & 3, row = quarter * 32 + (threadIdx.x & 31);  // columns 32 part ..
         const uint32_t lanes = (uint32_t)quarter << 21;
@@ -740,15 +832,17 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 tc_fence_before();
                 warp_arrive(ds_ready);
             }
-            const long long out = b * sdq.b + h * sdq.h + t * sdq.t + part * (D / 4);
             if (count > 0) {
-                wait(acc_full, it++, 40);
+                wait(acc_full, it, 40);
                 tc_fence_after();
-                store_row<D / 4, BF>(tA + lanes + part * (D / 4), dq, out, g.scale, t < g.T, !live);
+                const uint32_t tile = sq + 2 * (it % QST) * TB;  // q's, whose last product is done
+                stage_row<D / 4, BF>(tA + lanes + part * (D / 4), tile, row, part * (D / 4), g.scale, !live);
+                tc_fence_before();
+                warp_arrive(staged + 8 * (it & 1));
+                ++it;
             } else if (t < g.T) {
-                zero_row<D / 4>(dq, out);
+                zero_row<D / 4>(dq, b * sdq.b + h * sdq.h + t * sdq.t + part * (D / 4));
             }
-            tc_fence_before();
         }
     }
     tmem_free_all(tmem);
@@ -772,7 +866,7 @@ struct DkvCfg {
     // begins while the last one ends
     static constexpr int ST = D == 128 ? 2 : 4, KVST = D == 128 ? 1 : 2;
     static constexpr int SMEM = (2 * KVST + 2 * ST) * Tile<D>::BYTES + kSmall;
-    static constexpr int THREADS = 608;  // 16 math warps, products, loads, statistics
+    static constexpr int THREADS = 640;  // 16 math warps, products, loads, statistics, stores
 };
 
 // The lists of a sequence of n tiles: tile k is seen by n - k query tiles if it has sinks (k < st),
@@ -908,14 +1002,15 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sk = smem_u32(smem_raw), sq = sk + 2 * KVST * TB, sg = sq + ST * TB;  // k, v in turn
     Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 * KVST + 2 * ST) * TB);
-    static_assert(10 + 4 * ST + 4 <= 32, "barriers");
+    static_assert(13 + 4 * ST + 4 <= 40, "barriers");
     float(*s_stat)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [slot][lse log2 e, delta][query]
     if (misplaced(sk, hdr)) return;
     const int warp = threadIdx.x >> 5, G = g.H / g.Hkv;
     const uint32_t b0 = smem_u32(sm.bars);
     const uint32_t kv_full = b0, kv_empty = b0 + 16, acc_full = b0 + 32, s_full = b0 + 40, dp_full = b0 + 48;
     const uint32_t p_ready = b0 + 56, ds_ready = b0 + 64;
-    const uint32_t q_full = b0 + 80, q_empty = q_full + 8 * ST, g_full = q_empty + 8 * ST, g_empty = g_full + 8 * ST;
+    const uint32_t staged = b0 + 72;  // [dk, dv][parity of the list]
+    const uint32_t q_full = b0 + 104, q_empty = q_full + 8 * ST, g_full = q_empty + 8 * ST, g_empty = g_full + 8 * ST;
     const uint32_t st_full = g_empty + 8 * ST, st_empty = st_full + 16;
     if (warp == 1) {  // this block's share of the chain
         const long long total = chain_length(g), p0 = total * blockIdx.x / gridDim.x, p1 = total * (blockIdx.x + 1) / gridDim.x;
@@ -930,6 +1025,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
         for (int i = 0; i < 7; ++i) mbar_init(b0 + 8 * i, 1);
         mbar_init(p_ready, 16);
         mbar_init(ds_ready, 16);
+        for (int i = 0; i < 4; ++i) mbar_init(staged + 8 * i, 8);
         for (int i = 0; i < 4 * ST; ++i) mbar_init(q_full + 8 * i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(st_full + 8 * i, 1), mbar_init(st_empty + 8 * i, 16);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -943,7 +1039,10 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
     struct Step {
         int h, qt;
     };
-    auto first_step = [&]() { return Step{w.p.hk * G + w.i0 / w.f, w.p.tile + w.i0 % w.f}; };
+    auto first_step = [&]() {
+        if (w.i0 == 0) return Step{w.p.hk * G, w.p.tile};
+        return Step{w.p.hk * G + w.i0 / w.f, w.p.tile + w.i0 % w.f};
+    };
     auto advance = [&](Step &s) {
         if (++s.qt == w.p.tile + w.f) s.qt = w.p.tile, ++s.h;
     };
@@ -1005,46 +1104,63 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
             }
         }
         if (lane == 0) cuts[blockIdx.x] = cut;
+    } else if (warp == 19) {
+        // ------------------------------------------------------------ stores, which give the key tiles back
+        if ((threadIdx.x & 31) == 0) {
+            uint32_t it = 0;
+            while (w.next()) {
+                for (int which = 0; which < 2; ++which) {
+                    wait(staged + 16 * which + 8 * (it & 1), it >> 1, 54);
+                    if (w.i0 == 0 && w.i1 == w.list && *wait.dead == 0u)
+                        store_tile<D>(which == 0 ? &maps.x : &maps.y, sk + (2 * (it % KVST) + which) * TB, w.p.tile * kWT, w.p.hk, w.p.b);
+                }
+                tma_store_wait_read();
+                mbar_arrive(kv_empty + 8 * (it % KVST));
+                ++it;
+            }
+        }
+        __syncwarp();
     } else if (warp == 16) {
+        const uint32_t lead = elect();
         uint32_t n = 0, it = 0;
         while (w.next()) {
+            const int i0 = uni(w.i0), i1 = uni(w.i1), len = uni(w.len), tile = uni(w.p.tile), f = uni(w.f);
             const uint32_t kb = it % KVST, kt = sk + 2 * kb * TB;
             auto scores = [&](uint32_t j, int qt) {
                 const uint32_t s = j % ST;
                 wait(q_full + 8 * s, j / ST, 45);
-                if (g.lens != nullptr && w.len - qt * kWT < kWT) Tile<D>::zero_rows(sq + s * TB, w.len - qt * kWT);
+                if (g.lens != nullptr && len - qt * kWT < kWT) Tile<D>::zero_rows(sq + s * TB, len - qt * kWT);
                 tc_fence_after();
-                mma_scores<D, BF>(tS, kt, sq + s * TB);
-                mma_commit_w(s_full);
+                mma_scores<D, BF>(lead, tS, kt, sq + s * TB);
+                mma_commit(lead, s_full);
             };
             auto grads = [&](uint32_t j, int qt) {
                 const uint32_t s = j % ST;
                 wait(g_full + 8 * s, j / ST, 46);
-                if (g.lens != nullptr && w.len - qt * kWT < kWT) Tile<D>::zero_rows(sg + s * TB, w.len - qt * kWT);
+                if (g.lens != nullptr && len - qt * kWT < kWT) Tile<D>::zero_rows(sg + s * TB, len - qt * kWT);
                 tc_fence_after();
-                mma_scores<D, BF>(tP, kt + TB, sg + s * TB);
-                mma_commit_w(dp_full);
+                mma_scores<D, BF>(lead, tP, kt + TB, sg + s * TB);
+                mma_commit(lead, dp_full);
             };
-            Step x = first_step();
+            int qt = tile + uni(i0 == 0 ? 0 : i0 % f);
             wait(kv_full + 8 * kb, it / KVST, 47);
-            scores(n, x.qt);
-            grads(n, x.qt);
-            for (int i = w.i0; i < w.i1; ++i, ++n) {
+            scores(n, qt);
+            grads(n, qt);
+            for (int i = i0; i < i1; ++i, ++n) {
                 const uint32_t s = n % ST;
-                advance(x);  // to step i + 1
+                if (++qt == tile + f) qt = tile;  // of step i + 1
                 wait(p_ready, n, 48);
                 tc_fence_after();
-                mma_apply<D, BF, 32>(tV, tS, sg + s * TB, i > w.i0);
-                mma_commit_w(g_empty + 8 * s);
-                if (i + 1 < w.i1) scores(n + 1, x.qt);
+                mma_apply<D, BF, 32>(lead, tV, tS, sg + s * TB, i > i0);
+                mma_commit(lead, g_empty + 8 * s);
+                if (i + 1 < i1) scores(n + 1, qt);
                 wait(ds_ready, n, 49);
                 tc_fence_after();
-                mma_apply<D, BF, 32>(tK, tP, sq + s * TB, i > w.i0);
-                mma_commit_w(q_empty + 8 * s);
-                if (i + 1 < w.i1) grads(n + 1, x.qt);
+                mma_apply<D, BF, 32>(lead, tK, tP, sq + s * TB, i > i0);
+                mma_commit(lead, q_empty + 8 * s);
+                if (i + 1 < i1) grads(n + 1, qt);
             }
-            mma_commit_w(kv_empty + 8 * kb);
-            mma_commit_w(acc_full);
+            mma_commit(lead, acc_full);
             ++it;
         }
     } else {
@@ -1106,18 +1222,18 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                 warp_arrive(ds_ready);
                 warp_arrive(st_empty + 8 * sl);
             }
-            const bool write = key < g.T, zero = key >= w.len;
-            wait(acc_full, it++, 53);
+            const bool zero = key >= w.len, whole = w.i0 == 0 && w.i1 == w.list;
+            wait(acc_full, it, 53);
             tc_fence_after();
             const uint32_t acc = (which == 0 ? tK : tV) + lanes + col;
+            const uint32_t tile = sk + (2 * (it % KVST) + which) * TB;  // k's or v's, whose last product is done
             const float f = which == 0 ? g.scale : 1.f;
-            if (w.i0 == 0 && w.i1 == w.list) {
-                const Str3 st = which == 0 ? sdk : sdv;
-                store_row<D / 2, BF>(acc, which == 0 ? dk : dv, w.p.b * st.b + w.p.hk * st.h + key * st.t + col, f, write, zero);
+            if (whole) {
+                stage_row<D / 2, BF>(acc, tile, row, col, f, zero);
             } else {
-                // part 0 of a block: a list it joins after its start; part 1: one it leaves before its end
-                float4 *p = reinterpret_cast<float4 *>(
-                    parts + ((2ll * blockIdx.x + (w.i0 > 0 ? 0 : 1)) * 2 + which) * (kWT * D) + row * D + col);
+                // part 0 of a block: a list it joins after its start; part 1: one it leaves before its end.
+                // Four columns of all rows next to each other.
+                float4 *p = reinterpret_cast<float4 *>(parts + ((2ll * blockIdx.x + (w.i0 > 0 ? 0 : 1)) * 2 + which) * (kWT * D)) + row;
 #pragma unroll
                 for (int k = 0; k < D / 2; k += 16) {
                     uint32_t r[16];
@@ -1125,12 +1241,14 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        p[k / 4 + j] = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                            : make_float4(__uint_as_float(r[4 * j]) * f, __uint_as_float(r[4 * j + 1]) * f,
-                                                          __uint_as_float(r[4 * j + 2]) * f, __uint_as_float(r[4 * j + 3]) * f);
+                        p[((col + k) / 4 + j) * kWT] = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                            : make_float4(__uint_as_float(r[4 * j]) * f, __uint_as_float(r[4 * j + 1]) * f,
+                                                                          __uint_as_float(r[4 * j + 2]) * f, __uint_as_float(r[4 * j + 3]) * f);
                 }
             }
             tc_fence_before();
+            warp_arrive(staged + 16 * which + 8 * (it & 1));
+            ++it;
         }
         // the tiles behind a sequence's length, which are in no list
         if (g.lens != nullptr) {
@@ -1179,7 +1297,7 @@ __global__ void __launch_bounds__(256) wa_join_kernel(const float *__restrict__ 
     }
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        const int i = i0 + k * 256 * kJoinY, col = i % C, row = i / C % kWT, which = i / C / kWT, key = c.tile * kWT + row;
+        const int i = i0 + k * 256 * kJoinY, row = i % kWT, col = i / kWT % C, which = i / C / kWT, key = c.tile * kWT + row;
         if (key >= T) continue;
         const Str3 st = which == 0 ? sdk : sdv;
         uint16_t *out = static_cast<uint16_t *>(which == 0 ? dk : dv) + c.b * st.b + c.hk * st.h + key * st.t + 4 * col;
