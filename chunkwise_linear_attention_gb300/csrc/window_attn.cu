@@ -70,6 +70,15 @@ int wa_strides(const char *fn, const int64_t *strides, const char *const *names,
     return CLA_OK;
 }
 
+// bh: the heads that a tile's items are dealt out over, key heads forward and query heads for dq.
+WaArgs wa_args(const int32_t *lens, float scale, int64_t T, int64_t window, int64_t sinks, int64_t B, int64_t H, int64_t Hkv,
+               int64_t bh) {
+    const int64_t G = Hkv > 0 ? H / Hkv : 1;
+    return WaArgs{lens, scale, (int)T, (int)(window < T ? window : T), (int)(sinks < T ? sinks : T), (int)B, (int)H, (int)Hkv,
+                  Div((uint32_t)(G % 2 == 0 ? G / 2 : G)), Div((uint32_t)bh), Div((uint32_t)Hkv), Div((uint32_t)H),
+                  Div((uint32_t)G)};
+}
+
 int wa_blocks(const char *fn, long long items, unsigned *blocks) {
     int n = 0;
     if (int st = multiprocessors(fn, &n)) return st;
@@ -153,7 +162,7 @@ extern "C" int cla_window_attn_fwd(const void *q, const void *k, const void *v, 
     const int64_t heads[] = {H, Hkv, Hkv, H};
     Str3 r[4];
     if (int st = wa_strides(fn, strides, names, heads, 4, B, T, d, r)) return st;
-    const WaArgs g{lens, scale, (int)T, (int)(window < T ? window : T), (int)(sinks < T ? sinks : T), (int)B, (int)H, (int)Hkv};
+    const WaArgs g = wa_args(lens, scale, T, window, sinks, B, H, Hkv, B * Hkv);
     cudaStream_t s = (cudaStream_t)stream;
     WsHeader *hdr = static_cast<WsHeader *>(ws);
     if (B * H * T == 0) {
@@ -201,7 +210,7 @@ extern "C" int cla_window_attn_bwd(const void *q, const void *k, const void *v, 
     const int64_t heads[] = {H, Hkv, Hkv, H, H, H, Hkv, Hkv};
     Str3 r[8];
     if (int st = wa_strides(fn, strides, names, heads, 8, B, T, d, r)) return st;
-    const WaArgs g{lens, scale, (int)T, (int)(window < T ? window : T), (int)(sinks < T ? sinks : T), (int)B, (int)H, (int)Hkv};
+    const WaArgs g = wa_args(lens, scale, T, window, sinks, B, H, Hkv, B * H);
     cudaStream_t s = (cudaStream_t)stream;
     CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(WsHeader), s), fn);
     if (B * H * T == 0) return CLA_OK;

@@ -30,11 +30,25 @@ struct Str3 {
     long long b, h, t;
 };
 
+// Division of a number below 2^31 by one known on the host (the round-up method of Granlund and
+// Montgomery): items are taken apart in every warp of a block, and a division is a hundred cycles.
+struct Div {
+    uint32_t d, mul, shift;
+    __host__ Div(uint32_t n = 1) : d(n ? n : 1), mul(0), shift(0) {
+        while ((1ull << shift) < d) ++shift;
+        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ int operator()(int x) const {
+        return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift);
+    }
+};
+
 // Token numbers, the window and the sinks (both at most T) fit 32 bits: T is at most 2^31 - 512.
 struct WaArgs {
     const int32_t *lens;
     float scale;
     int T, window, sinks, B, H, Hkv;
+    Div per, bh, hkv, heads, group;  // items of a group, B Hkv, Hkv, H, H / Hkv
 };
 
 // Of the inputs q, k, v, dO, and of the outputs: o, dq in `x`, dk in `x`, dv in `y`.
@@ -321,11 +335,11 @@ struct FwdItem {
 // leave the blocks with almost equal shares.
 __device__ __forceinline__ FwdItem fwd_item(const WaArgs &g, int item, int tiles) {
     FwdItem w;
-    const int G = g.H / g.Hkv, even = (G & 1) == 0, per = even ? G / 2 : G, bh = item / per % (g.B * g.Hkv);
-    const int last = (even ? tiles : (tiles + 1) / 2) - 1, tt = last - item / per / (g.B * g.Hkv);
-    w.b = bh / g.Hkv;
-    w.hk = bh % g.Hkv;
-    w.h = w.hk * G + item % per * (even ? 2 : 1);
+    const int G = g.group.d, even = (G & 1) == 0, per = g.per.d, q = g.per(item), r = g.bh(q), bh = q - r * (int)g.bh.d;
+    const int tt = (even ? tiles : (tiles + 1) / 2) - 1 - r;
+    w.b = g.hkv(bh);
+    w.hk = bh - w.b * g.Hkv;
+    w.h = w.hk * G + (item - q * per) * (even ? 2 : 1);
     w.t0 = tt * (even ? kWT : 2 * kWT);
     w.step_h = even ? 1 : 0;
     w.step_t = even ? 0 : kWT;
@@ -505,10 +519,12 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
                 tmem_ld_wait();
                 if (tile_masked(g, t0, tile * kWT)) {
                     const uint32_t b0 = key_bits(g, t, s0), b1 = key_bits(g, t, s0 + 32);
+                    if (!__all_sync(~0u, (b0 & b1) == ~0u)) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (!(b0 & (1u << k))) r[k] = 0xff800000u;
-                        if (!(b1 & (1u << k))) r[32 + k] = 0xff800000u;
+                        for (int k = 0; k < 32; ++k) {
+                            if (!(b0 & (1u << k))) r[k] = 0xff800000u;
+                            if (!(b1 & (1u << k))) r[32 + k] = 0xff800000u;
+                        }
                     }
                 }
                 float mx[4];
@@ -618,17 +634,17 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
     static_assert(15 + 2 * (KST + VST) <= 40, "barriers");
     float(*s_stat)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [item's parity][delta, lse log2 e][row]
     if (misplaced(sq, hdr)) return;
-    const int warp = threadIdx.x >> 5, tiles = (g.T + kWT - 1) / kWT, G = g.H / g.Hkv;
+    const int warp = threadIdx.x >> 5, tiles = (g.T + kWT - 1) / kWT;
     const uint32_t b0 = smem_u32(sm.bars);
     const uint32_t q_full = b0, q_empty = b0 + 16, acc_full = b0 + 32, dp_full = b0 + 40, s_full = b0 + 48, ds_ready = b0 + 64;
     const uint32_t st_full = b0 + 72, st_empty = b0 + 88;  // two each, by the item's parity
-    const uint32_t staged = b0 + 104, k_full = b0 + 120, k_empty = k_full + 8 * KST, v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST;
+    const uint32_t staged = b0 + 104, x_empty = b0 + 112, k_full = b0 + 120, k_empty = k_full + 8 * KST, v_full = k_empty + 8 * KST, v_empty = v_full + 8 * VST;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 8; ++i) mbar_init(b0 + 8 * i, 1);
         mbar_init(ds_ready, 16);
         for (int i = 0; i < 2; ++i) mbar_init(st_full + 8 * i, 2), mbar_init(st_empty + 8 * i, 16);
         mbar_init(staged, 16);
-        mbar_init(staged + 8, 16);
+        mbar_init(x_empty, 1);
         for (int i = 0; i < 2 * (KST + VST); ++i) mbar_init(k_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = 0u;
@@ -638,11 +654,11 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
     const uint32_t tS = tmem, tP = tmem + 256, tA = tmem + 384;
     // items: all heads of the last tile, then of the one before it (as in the forward)
     auto place = [&](int item, int &b, int &h, int &hk, int &t0) {
-        const int bh = item % (g.B * g.H);
-        t0 = (tiles - 1 - item / (g.B * g.H)) * kWT;
-        b = bh / g.H;
-        h = bh % g.H;
-        hk = h / G;
+        const int r = g.bh(item), bh = item - r * (int)g.bh.d;  // here B H
+        t0 = (tiles - 1 - r) * kWT;
+        b = g.heads(bh);
+        h = bh - b * g.H;
+        hk = g.group(h);
     };
 
     if (warp == 17) {
@@ -710,8 +726,10 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 wait(ds_ready, n, 37);
                 tc_fence_after();
                 if (i + 1 < count) grads(n + 1);
+                else mma_commit(lead, q_empty + 8 * qb);
                 mma_apply<D, BF, 32>(lead, tA, tS + 128 * (n & 1), sk + (n % KST) * TB, i > 0);
-                mma_commit(lead, k_empty + 8 * (n % KST));
+                // an item's last key tile becomes the place of its output
+                if (i + 1 < count) mma_commit(lead, k_empty + 8 * (n % KST));
             }
             mma_commit(lead, acc_full);
             ++it;
@@ -720,17 +738,20 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
         // ------------------------------------------------------------ delta = dO . o and lse of the next item's rows
         // A warp takes 64 rows, D / 8 lanes a row (16 bytes each), eight rows in flight a lane.  The
         // second of them also stores dq, of the item before the one whose statistics it has formed.
-        uint32_t it = 0;
+        uint32_t it = 0, last = 0;
         auto store = [&](int item) {
             int b, h, hk, t0;
             place(item, b, h, hk, t0);
             const KeyTiles kt = key_tiles(g, t0, wa_len(g, b));
             if (kt.hi < kt.lo) return;
+            last += kt.hi - kt.lo + 1 + min(kt.sinks, kt.lo);
+            const uint32_t s = (last - 1) % KST;
             if ((threadIdx.x & 31) == 0) {
-                wait(staged + 8 * (it & 1), it >> 1, 43);
-                if (*wait.dead == 0u) store_tile<D>(&maps.x, sq + 2 * (it % QST) * TB, t0, h, b);
+                wait(staged, it, 43);
+                if (*wait.dead == 0u) store_tile<D>(&maps.x, sk + s * TB, t0, h, b);
                 tma_store_wait_read();
-                mbar_arrive(q_empty + 8 * (it % QST));
+                mbar_arrive(x_empty);
+                mbar_arrive(k_empty + 8 * s);
             }
             __syncwarp();
             ++it;
@@ -821,9 +842,11 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 for (int k = 0; k < 16; ++k) x[k] = __fmul2_rn(x[k], __fadd2_rn(y[k], make_float2(-dl, -dl)));
                 if (tile_masked(g, t0, s0)) {
                     const uint32_t bits = key_bits(g, t, s0 + 32 * part);
+                    if (!__all_sync(~0u, bits == ~0u)) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!(bits & (1u << k))) r[k] = 0u;
+                        for (int k = 0; k < 32; ++k)
+                            if (!(bits & (1u << k))) r[k] = 0u;
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < 16; ++k) ds[k] = pack16<BF>(x[k]);
@@ -833,12 +856,12 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 warp_arrive(ds_ready);
             }
             if (count > 0) {
+                if (it > 0) wait(x_empty, it - 1, 44);  // the item before this one's output has been read
                 wait(acc_full, it, 40);
                 tc_fence_after();
-                const uint32_t tile = sq + 2 * (it % QST) * TB;  // q's, whose last product is done
-                stage_row<D / 4, BF>(tA + lanes + part * (D / 4), tile, row, part * (D / 4), g.scale, !live);
+                stage_row<D / 4, BF>(tA + lanes + part * (D / 4), sk + (n - 1) % KST * TB, row, part * (D / 4), g.scale, !live);
                 tc_fence_before();
-                warp_arrive(staged + 8 * (it & 1));
+                warp_arrive(staged);
                 ++it;
             } else if (t < g.T) {
                 zero_row<D / 4>(dq, b * sdq.b + h * sdq.h + t * sdq.t + part * (D / 4));
@@ -1195,9 +1218,11 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                 }
                 if (tile_masked(g, t0, s0)) {
                     const uint32_t bits = query_bits(g, t0 + 32 * part, key);
+                    if (!__all_sync(~0u, bits == ~0u)) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!(bits & (1u << k))) r[k] = 0u;
+                        for (int k = 0; k < 32; ++k)
+                            if (!(bits & (1u << k))) r[k] = 0u;
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < 16; ++k) p[k] = pack16<BF>(x[k]);
