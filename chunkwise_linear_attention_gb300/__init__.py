@@ -9,7 +9,8 @@ All tensors must be CUDA tensors, contiguous, with the dtype the C ABI names
 (float32, or bfloat16 passed as its bit pattern; float16 too where an entry
 point takes a dtype).  The window_attn_* tensors may be strided over batch,
 heads and tokens.  Outputs and the workspace are allocated with torch when not
-supplied.
+supplied.  `stream` is the stream of the call, the current one by default; what
+another stream has to write first is the caller's to wait for.
 """
 from __future__ import annotations
 
@@ -199,6 +200,12 @@ def _launch(fn, device, args, stream):
             _check_meta(*a)
         for a in tensors:
             _check_place(device, *a)
+    if isinstance(stream, torch.cuda.Stream):
+        # memory that was allocated on another stream (the outputs and the workspace among it) is not
+        # given out again before this stream is done with it; with a raw handle that is the caller's part
+        for a in args:
+            if type(a) is tuple and a[0] is not None:
+                a[0].record_stream(stream)
     call = getattr(_lib or lib(), fn)
     index = device.index
     if index == torch._C._cuda_getDevice():

@@ -20,10 +20,21 @@
 // of them one behind the other in time) in shared memory, and the blocks
 // through pairs that they publish.  The state entering a block's steps is
 // folded from the published pairs of its group's earlier blocks (8 a group,
-// one a sub) and the state at the end of the group before.  That
-// order is fixed by the place in the sequence alone, so the result does not
-// depend on which block came first, and only one wait per 8 blocks is on the
-// serial path.
+// one a sub) and the state at the end of the group before.  That order is
+// fixed by the place in the sequence alone, so the result does not depend on
+// which block came first, and only one wait per 8 blocks is on the serial path.
+//
+// Measured at 8 x 4096 x 1024 bf16 (GB300): forward 93 us (8 bytes a step and
+// channel: 2.9 TB/s, 43% of the measured copy rate), backward 187 us (14
+// bytes: 2.5 TB/s, 37%).  What bounds both is latency at 16 and 12 warps a
+// multiprocessor: 44 and 94 instructions a step and channel issue on 45% of
+// the cycles.  Of a forward block's 12000 cycles the counter takes 2300, the
+// loads and gates 4200, the scan and the block's exchange 1700, the look at
+// the blocks before 1850, the second pass and the stores 1150.  Persistent
+// blocks that ask for their next unit early (335 us for both passes) and five
+// backward blocks a multiprocessor with part of their registers in shared
+// memory (339 us) were slower: the first spills, the second has more blocks
+// than a row of chunks in flight, which then wait for each other.
 #include <math.h>
 
 #include "cla_internal.cuh"
@@ -306,9 +317,8 @@ struct GsWords {
 
 // By one warp: publishes the pair (A, B) of block chunk `idx` for 16 channels (`rem` of the `per`
 // groups of them; every lane holds its cg's), and returns the state entering it: the pairs of the
-// group's chunks before it, one a sub, on the
-// state at the end of the group before, or `s0`.  The last chunk of a group publishes the state
-// behind it.
+// group's chunks before it, one a sub, on the state at the end of the group before, or `s0`.  The
+// last chunk of a group publishes the state behind it.
 template <bool RST>
 __device__ __forceinline__ void carry_in(const GsWords &w, int idx, int chunks, int per, int rem, const float2 (&A)[2],
                                          const float2 (&B)[2], const float2 (&s0)[2], float2 (&s)[2], unsigned int where) {
@@ -441,8 +451,8 @@ __device__ __forceinline__ void load_rate(const float *rate, int c0, float2 (&v)
 }
 
 // ------------------------------------------------------------------ forward
-// L = 8 steps a lane for 2-byte elements, 4 for fp32.  h may be NULL: only the checkpoint is
-// written then.
+// L = 8 steps a lane for 2-byte elements, 4 for fp32 (whose raw rows take twice the registers).
+// h may be NULL: only the checkpoint is written then.
 template <typename E, bool VEC, bool RST, int L>
 __global__ void __launch_bounds__(kFwdWarps * 32, kFwdBlocks)
 gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__restrict__ ig,
@@ -740,19 +750,21 @@ int gs_check(const char *fn, int64_t B, int64_t T, int64_t D, int dtype, float c
     if (!(c > 0.f) || !isfinite(c)) return fail(CLA_ERR_INVALID_ARG, "%s: c must be positive and finite", fn);
     if (dtype_bytes(dtype) == 0) return fail(CLA_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
     if (!gs_sizes_ok(B, T, D))
-        return fail(CLA_ERR_UNSUPPORTED, "%s: B * D must be below 2^31, B * T * (D rounded up to 16) below 10^12, T at most 2^31 - 512", fn);
+        return fail(CLA_ERR_UNSUPPORTED, "%s: B * D must be below 2^31, B * T * D well below 10^12, T at most 2^31 - 512", fn);
     return CLA_OK;
 }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// The workspace: header, the words of the published pairs and states (sized for blocks of 32
-// steps, the fewest that one covers), the rebuilt checkpoint, the rows of dlam's
-// sums and the rows that these are reduced to.
+// The workspace: header, the words of the published pairs and states (blocks that have a
+// successor cover at least 4 warps x 32 steps), the channels' rates, the rebuilt checkpoint, the
+// rows of dlam's sums and the rows that these are reduced to.
 struct GsLayout {
     size_t words, clear, states, rate, ckpt, part, part2, total;
 };
-constexpr long long kDlamRows = 1024;  // above these many rows, dlam's sums go in two steps
+// Above these many rows dlam's sums go in two steps, of enough shares to fill the GPU (1024 rows of
+// 1024 channels: 19 us in one step, 5 us in two).
+constexpr long long kDlamRows = 128;
 constexpr int kDlamShares = 64;
 
 // Groups of 16 channels, in whole blocks whatever their shape.
@@ -762,9 +774,10 @@ static_assert(kFwdWarps >= kBwdWarps, "groups in whole blocks");
 GsLayout gs_layout(int64_t B, int64_t T, int64_t D) {
     GsLayout l;
     const size_t units = (size_t)B * gs_groups(D), ch = (size_t)ceil_div(T, kGsCkpt);
+    const size_t blocks = (size_t)ceil_div(T, kGsCkpt * (kFwdWarps < kBwdWarps ? kFwdWarps : kBwdWarps));
     l.words = sizeof(WsHeader);
-    l.states = l.words + ch * units * 4 * 8 * 4;
-    l.clear = l.states + (size_t)ceil_div(ch, kGsGroup) * units * 4 * 4 * 4;
+    l.states = l.words + blocks * units * 4 * 8 * 4;
+    l.clear = l.states + (size_t)ceil_div(blocks, kGsGroup) * units * 4 * 4 * 4;
     l.rate = l.clear;
     l.ckpt = l.rate + (size_t)gs_groups(D) * 64;
     l.part = l.ckpt + align_up(ch * (size_t)B * D * 4, 16);
@@ -864,10 +877,11 @@ int gs_bwd(const char *fn, const void *x, const void *rg, const void *ig, const 
         long long rows = ceil_div(g.T, kGsCkpt) * g.B;
         if (rows > kDlamRows) {
             float *part2 = reinterpret_cast<float *>(p + l.part2);
-            gated_dlam_kernel<<<dim3((unsigned)ceil_div(g.D, 32), kDlamShares), 1024, 0, s>>>(part, lam, part2, rows, g.D);
+            const long long columns = ceil_div(g.D, 32), want = ceil_div(320, columns), shares = want < kDlamShares ? want : kDlamShares;
+            gated_dlam_kernel<<<dim3((unsigned)columns, (unsigned)(shares > 1 ? shares : 2)), 1024, 0, s>>>(part, lam, part2, rows, g.D);
             if (int st = check_launch(fn)) return st;
             part = part2;
-            rows = kDlamShares;
+            rows = shares > 1 ? shares : 2;
         }
         gated_dlam_kernel<<<dim3((unsigned)ceil_div(g.D, 32), 1), 1024, 0, s>>>(part, lam, dlam, rows, g.D);
         return check_launch(fn);

@@ -1292,27 +1292,34 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
 }
 
 // Adds the parts of a list that was cut, in their order: block (x, y) those of the list that block x
-// of wa_dkv_kernel left, y a share of them.
+// of wa_dkv_kernel left, y an eighth of the columns of dk and dv.  Parts come with the rows next to
+// each other and go out with the columns so, through shared memory.
 constexpr int kJoinY = 8;
 template <int D, bool BF>
 __global__ void __launch_bounds__(256) wa_join_kernel(const float *__restrict__ parts, const CutList *__restrict__ cuts,
                                                       void *__restrict__ dk, void *__restrict__ dv, Str3 sdk, Str3 sdv, int T,
                                                       int blocks) {
+    constexpr int C = D / 4, N = 2 * kWT * C, CY = C / kJoinY, PER = 2 * CY * kWT / 256;  // float4 columns: all, a block's
+    __shared__ uint2 out[2 * kWT][CY + 1];
     const int x0 = blockIdx.x;
     const CutList c = cuts[x0];
     if (c.tile < 0) return;
-    constexpr int C = D / 4, N = 2 * kWT * C, PER = N / (256 * kJoinY);
     const float4 *src = reinterpret_cast<const float4 *>(parts);
-    const int i0 = blockIdx.y * 256 + threadIdx.x;
+    const int row = threadIdx.x % kWT, first = threadIdx.x / kWT;
+    // the k-th of this thread: row `row` of column which * C + blockIdx.y * CY + j
+    auto at = [&](int k) {
+        const int u = first + 2 * k, which = u / CY, j = u % CY;
+        return (which * C + blockIdx.y * CY + j) * kWT + row;
+    };
     float4 s[PER];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) s[k] = src[(2ll * x0 + 1) * N + i0 + k * 256 * kJoinY];
+    for (int k = 0; k < PER; ++k) s[k] = src[(2ll * x0 + 1) * N + at(k)];
     for (int x = x0 + 1; x < blocks; ++x) {
         const int joins = cuts[x].joins;
         if (joins == 0) continue;  // a block without a share
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            const float4 y = src[2ll * x * N + i0 + k * 256 * kJoinY];
+            const float4 y = src[2ll * x * N + at(k)];
             s[k].x += y.x;
             s[k].y += y.y;
             s[k].z += y.z;
@@ -1322,11 +1329,17 @@ __global__ void __launch_bounds__(256) wa_join_kernel(const float *__restrict__ 
     }
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        const int i = i0 + k * 256 * kJoinY, row = i % kWT, col = i / kWT % C, which = i / C / kWT, key = c.tile * kWT + row;
+        const int u = first + 2 * k;
+        out[u / CY * kWT + row][u % CY] = make_uint2(pack16<BF>(make_float2(s[k].x, s[k].y)), pack16<BF>(make_float2(s[k].z, s[k].w)));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int i = threadIdx.x + k * 256, r = i / CY, j = i % CY, which = r / kWT, key = c.tile * kWT + r % kWT;
         if (key >= T) continue;
         const Str3 st = which == 0 ? sdk : sdv;
-        uint16_t *out = static_cast<uint16_t *>(which == 0 ? dk : dv) + c.b * st.b + c.hk * st.h + key * st.t + 4 * col;
-        *reinterpret_cast<uint2 *>(out) = make_uint2(pack16<BF>(make_float2(s[k].x, s[k].y)), pack16<BF>(make_float2(s[k].z, s[k].w)));
+        uint16_t *to = static_cast<uint16_t *>(which == 0 ? dk : dv) + c.b * st.b + c.hk * st.h + key * st.t;
+        *reinterpret_cast<uint2 *>(to + 4 * (blockIdx.y * CY + j)) = out[r][j];
     }
 }
 
