@@ -274,6 +274,10 @@ __device__ __forceinline__ uint32_t query_bits(const WaArgs &g, int t0, int s) {
     return ~bits_below(s - t0) & (s < g.sinks ? ~0u : bits_below(s - t0 + g.window));
 }
 
+// A query that sees one key: its weight is 1 whatever the score, and dS is 0.  It is made so, where
+// dP - delta of two different sums would leave a rounding.
+__device__ __forceinline__ bool sees_one(const WaArgs &g, int t) { return t == 0 || (g.window == 1 && g.sinks == 0); }
+
 // Columns [col, col + N) of a row of an accumulator, times f, into a tile in shared memory, from
 // where one store takes the tile out.  (Rows stored by their own threads are 32 lines an
 // instruction; that took 4000 cycles a tile.)
@@ -797,7 +801,8 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int row = (warp - 18) * 64 + lane + 32 * k, t = t0 + row;
-                dst2[row] = t < len ? __ldg(lse + at + t) * 1.4426950408889634f : INFINITY;
+                // P, and with it dS, of a row without a gradient is 0
+                dst2[row] = t < len && !sees_one(g, t) ? __ldg(lse + at + t) * 1.4426950408889634f : INFINITY;
             }
             warp_arrive(st_full + 8 * (all & 1));
             if (warp == 19 && all > 0) store(item - gridDim.x);
@@ -1240,6 +1245,12 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                     const float4 z = dl[k];
                     p[2 * k] = pack16<BF>(__fmul2_rn(x[2 * k], __fadd2_rn(y[2 * k], make_float2(-z.x, -z.y))));
                     p[2 * k + 1] = pack16<BF>(__fmul2_rn(x[2 * k + 1], __fadd2_rn(y[2 * k + 1], make_float2(-z.z, -z.w))));
+                }
+                if (g.window == 1 && g.sinks == 0) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) p[k] = 0u;
+                } else if (t0 == 0 && part == 0) {
+                    p[0] &= 0xffff0000u;  // query 0
                 }
                 tmem_st16(tP + lanes + 32 * part, p);
                 tmem_st_wait();

@@ -111,6 +111,15 @@ def test_large_logits(cla):
     check(cla, q, k, v, dO, 200, 4)
 
 
+@pytest.mark.parametrize("T,window,sinks", [(1, 1, 0), (1, 50, 4), (200, 1, 0)])
+def test_one_key_has_no_gradient(cla, T, window, sinks):
+    """A query that sees one key gives it all its weight whatever the score: dq and dk are 0, not a rounding."""
+    q, k, v, dO = inputs(2, 4, 2, T, 64, BF16)
+    got = check(cla, q, k, v, dO, window, sinks)
+    assert torch.equal(got["o"], v.repeat_interleave(2, 1))
+    assert float(got["dq"].abs().max()) == 0 and float(got["dk"].abs().max()) == 0
+
+
 def test_strided_views(cla):
     """q, k, v as slices of one projection [B, T, heads, d]; the output and gradients in that layout too."""
     B, H, K, T, d = 2, 4, 2, 150, 64
