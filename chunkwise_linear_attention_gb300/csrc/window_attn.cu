@@ -40,15 +40,20 @@ int wa_check(const char *fn, int64_t B, int64_t H, int64_t Hkv, int64_t T, int64
              int dtype, float scale) {
     if (B < 0 || H < 0 || Hkv < 0 || T < 0) return fail(CLA_ERR_INVALID_ARG, "%s: negative size", fn);
     if (window < 1 || sinks < 0) return fail(CLA_ERR_INVALID_ARG, "%s: window must be at least 1 and sinks 0", fn);
-    if (Hkv == 0 ? H != 0 : H % Hkv != 0)
+    if (H == 0 || Hkv == 0 ? H != Hkv : H % Hkv != 0)
         return fail(CLA_ERR_INVALID_ARG, "%s: the query heads must be a multiple of the key heads", fn);
     if (!isfinite(scale)) return fail(CLA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
     if (dtype != CLA_BF16 && dtype != CLA_F16) return fail(CLA_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
     if (d != 64 && d != 128) return fail(CLA_ERR_UNSUPPORTED, "%s: head dimension %lld", fn, (long long)d);
-    if (!product_below({B, H}, 2147483648.0) || T > kMaxTokens || !product_below({B, H, T, d}, 1e15) ||
-        !product_below({B, H, T}, 128.0 * 2147483648.0) || !product_below({B, Hkv, d, window}, 1e15) ||
-        !product_below({B, Hkv, d, sinks}, 1e15))
+    // tiles are numbered in 32 bits, in strides of a grid
+    if (!product_below({B, H}, 2e9) || T > kMaxTokens || !product_below({B, H, T, d}, 1e15) ||
+        !product_below({B, H, (T + kWT - 1) / kWT}, 2e9))
         return fail(CLA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    return CLA_OK;
+}
+int wa_check_cache(const char *fn, int64_t B, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
+    if (window > kMaxTokens || sinks > kMaxTokens - window || !product_below({B, Hkv, d, sinks + window}, 1e15))
+        return fail(CLA_ERR_UNSUPPORTED, "%s: sinks + window must be at most 2^31 - 512, the cache below 10^15 elements", fn);
     return CLA_OK;
 }
 
@@ -237,6 +242,7 @@ extern "C" int cla_window_cache_write(const void *k, const void *v, const int32_
     const char *fn = "cla_window_cache_write";
     clear_error();
     if (int st = wa_check(fn, B, Hkv, Hkv, T, d, window, sinks, dtype, 1.f)) return st;
+    if (int st = wa_check_cache(fn, B, Hkv, d, window, sinks)) return st;
     if (B * Hkv * T == 0) return CLA_OK;
     if (!k || !v || !kcache || !vcache) return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned_or_null({k, v, kcache, vcache}, 16) || !aligned_or_null({lens}, 4))
@@ -285,8 +291,8 @@ extern "C" int cla_window_attn_step(const void *q, const void *k, const void *v,
     const char *fn = "cla_window_attn_step";
     clear_error();
     if (int st = wa_check(fn, B, H, Hkv, 1, d, window, sinks, dtype, scale)) return st;
-    if (sinks + window > kMaxTokens || !product_below({B, H}, 1 << 27))
-        return fail(CLA_ERR_UNSUPPORTED, "%s: sinks + window must be at most 2^31 - 512, B * H below 2^27", fn);
+    if (int st = wa_check_cache(fn, B, Hkv, d, window, sinks)) return st;
+    if (!product_below({B, H}, 1 << 27)) return fail(CLA_ERR_UNSUPPORTED, "%s: B * H must be below 2^27", fn);
     if (B * H == 0) return CLA_OK;
     if (!q || !k || !v || !kcache || !vcache || !pos || !o)
         return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);

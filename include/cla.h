@@ -616,6 +616,7 @@ size_t cla_gated_scan_workspace_size(int64_t B, int64_t T, int64_t D);
  *          chunk, for the backward
  *   c      a positive finite number; the decay of a fully open gate is
  *          exp(-c softplus(lam)); decays below 2^-126 count as 2^-126
+ * The outputs must not overlap the inputs (hT is not written over h0).
  * B * D must be below 2^31, B * T * D (D rounded up to 16) below 10^12. */
 int cla_gated_scan_fwd(const void *x, const void *rgate, const void *igate,
                        const float *lam, const float *h0, const uint8_t *reset,
@@ -626,7 +627,7 @@ int cla_gated_scan_fwd(const void *x, const void *rgate, const void *igate,
 /* Backward: gradients on everything the forward read, from dh (dtype) and dhT.
  * The states are rebuilt from `ckpt`, or, when it is NULL, from a forward scan
  * into the workspace.
- *   dh     [B, T, D] dtype;  dhT [B, D] fp32 [opt]
+ *   dh     [B, T, D] dtype;  dhT [B, D] fp32 [opt] of the final state
  *   dx, drgate, digate [B, T, D] dtype out, 0 behind a sequence's length
  *   dlam   [D] fp32 [opt] out, summed in a fixed order
  *   dh0    [B, D] fp32 [opt] out
@@ -674,7 +675,8 @@ int cla_gated_scan_step(const void *x, const void *rgate, const void *igate,
  *          logits, natural base (dense)
  *   scale  the logits' factor, a finite number
  *   strides [opt]: of q, k, v, o
- * d in {64, 128}; window >= 1; sinks >= 0. */
+ * d in {64, 128}; window >= 1; sinks >= 0; more than T of either is all of
+ * them.  The weights are rounded to dtype for their product with v. */
 int cla_window_attn_fwd(const void *q, const void *k, const void *v,
                         const int32_t *lens, void *o, float *lse, float scale,
                         int64_t window, int64_t sinks, int dtype, int64_t B,
@@ -694,6 +696,9 @@ size_t cla_window_attn_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv,
 /* Backward: with P = exp(scale q k^T - lse) and dS = P (dO v^T - rowsum(dO o)),
  * dq = scale dS k, dk = scale dS^T q, dv = P^T dO, the gradients of a shared
  * key head summed over its query heads in a fixed order (no float atomics).
+ * P and dS are rounded to dtype for their products: fp16 gradients have to be
+ * scaled so that dS stays within its range, as the tensors' own do.  A query
+ * that sees one key has dq = 0 and adds nothing to dk.
  *   o, lse as the forward returned them;  dO [B, H, T, d] dtype
  *   dq     [B, H, T, d] dtype out;  dk, dv [B, Hkv, T, d] dtype out; all 0
  *          behind a sequence's length

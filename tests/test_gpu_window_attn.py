@@ -120,6 +120,14 @@ def test_one_key_has_no_gradient(cla, T, window, sinks):
     assert float(got["dq"].abs().max()) == 0 and float(got["dk"].abs().max()) == 0
 
 
+def test_window_longer_than_any_sequence(cla):
+    q, k, v, _ = inputs(2, 4, 2, 300, 64, BF16)
+    want = cla.window_attn_fwd(q, k, v, window=300)
+    for w, n in ((2 ** 62, 0), (5, 2 ** 62), (2 ** 31, 2 ** 31)):
+        got = cla.window_attn_fwd(q, k, v, window=w, sinks=n)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_strided_views(cla):
     """q, k, v as slices of one projection [B, T, heads, d]; the output and gradients in that layout too."""
     B, H, K, T, d = 2, 4, 2, 150, 64

@@ -97,6 +97,26 @@ def test_window_refusals(lib, call, kw, status):
     assert lib.cla_last_error_message()
 
 
+@pytest.mark.parametrize("call", [wfwd, wbwd, wstep])
+def test_window_heads_without_queries(lib, call):
+    """Key heads that no query reads: their gradients and cache slots would be nobody's to write."""
+    assert call(lib, H=0, K=2) == 1
+    if call is wstep:  # the others' empty calls clear their workspace on the GPU
+        assert call(lib, H=0, K=0) == 0
+
+
+def test_window_sizes_at_the_limits(lib):
+    # a tile more a head than B H T / 128 counts
+    assert wfwd(lib, B=1 << 15, H=1 << 15, K=1, T=129) == 2 and wbwd(lib, B=1 << 15, H=1 << 15, K=1, T=129) == 2
+    # a window or sinks longer than any sequence are every token
+    assert lib.cla_window_attn_workspace_size(2, 4, 2, 100, 64, (1 << 63) - 1, (1 << 63) - 1) == 256
+    assert (lib.cla_window_attn_bwd_workspace_size(2, 4, 2, 1000, 64, (1 << 63) - 1, 0)
+            == lib.cla_window_attn_bwd_workspace_size(2, 4, 2, 1000, 64, 1000, 0))
+    big = (1 << 63) - 1
+    assert wstep(lib, B=0, window=big, sinks=big) == 2 and wstep(lib, window=(1 << 31) - 512, sinks=1) == 2
+    assert lib.cla_window_cache_write(A, A, None, A, A, big, big, 1, 0, 1, 5, 64, None, None) == 2
+
+
 def test_window_cache_refusals(lib):
     f = lambda k=A, kc=A, w=8, n=1, dtype=1, B=1, K=1, T=5, d=64, s=None: lib.cla_window_cache_write(
         k, A, None, kc, A, w, n, dtype, B, K, T, d, _arr(s), None)
