@@ -22,6 +22,7 @@ namespace cla {
 namespace {
 
 constexpr int kWT = 128;  // tokens of a tile
+constexpr int kHalf = 64 * 128;  // bytes of 64 of its tokens in a block of 64 columns
 // Every block takes all 512 columns of tensor memory, so its shared memory is kept above half of
 // an SM's, which keeps a second block of these kernels off the SM.
 constexpr int kMinSmem = 116 * 1024;
@@ -126,6 +127,23 @@ __device__ __forceinline__ float2 unpack16(uint32_t u) {
     else return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
+// c += A B^T, A [16 x 16], B [8 x 16], by a warp.  The order of the 16 columns is free, so a lane
+// (r = lane / 4, j = lane % 4) may hold any four of them of its rows r, r + 8 and r.
+template <bool BF>
+__device__ __forceinline__ void mma16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    if constexpr (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // The waits of a block: once one has given up none waits long any more.
 struct Waits {
     volatile uint32_t *dead;
@@ -153,6 +171,8 @@ struct Waits {
         atomicExch(&hdr->where, where);
     }
 };
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // After a timeout: the loads that were issued into a ring of S stages (n in all) land before the
 // block leaves.
@@ -189,21 +209,21 @@ struct Tile {
 // acc = A B^T over D columns (both operands K-major): the scores of two tiles.  negate: 0, or
 // kNegateA for -A B^T.
 constexpr uint32_t kNegateA = 1u << 13;
-template <int D, bool BF>
+template <int D, bool BF, int N = kWT>
 __device__ __forceinline__ void mma_scores(uint32_t lead, uint32_t acc, uint32_t a, uint32_t b, uint32_t negate = 0u) {
     const uint64_t da = Tile<D>::kmajor(a), db = Tile<D>::kmajor(b);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss(lead, acc, da + Tile<D>::kstep(kk), db + Tile<D>::kstep(kk), idesc16<BF>(kWT, 0) | negate, kk ? 1u : 0u);
+        mma_ss(lead, acc, da + Tile<D>::kstep(kk), db + Tile<D>::kstep(kk), idesc16<BF>(N, 0) | negate, kk ? 1u : 0u);
 }
-// acc (+)= P X: P [128 x 128] in tensor memory, X a tile [128 tokens][D].  P lies packed over the
-// scores it came from in pieces of C columns, each at the start of its C score columns: a thread
-// then writes only where it has read itself, and the threads of a row need not wait for another.
-template <int D, bool BF, int C>
+// acc (+)= P X: P [128 x K] in tensor memory, X a tile [128 tokens][D] from a token on.  P lies packed
+// over the scores it came from in pieces of C columns, each at the start of its C score columns: a
+// thread then writes only where it has read itself, and the threads of a row need not wait for another.
+template <int D, bool BF, int C, int K = kWT>
 __device__ __forceinline__ void mma_apply(uint32_t lead, uint32_t acc, uint32_t p, uint32_t x, bool add) {
     const uint64_t dx = Tile<D>::nmajor(x);
 #pragma unroll
-    for (int kk = 0; kk < kWT / 16; ++kk)
+    for (int kk = 0; kk < K / 16; ++kk)
         mma_ts(lead, acc, p + (kk / (C / 16)) * C + (kk % (C / 16)) * 8, dx + Tile<D>::nstep(kk), idesc16<BF>(D, 1),
                  (add || kk) ? 1u : 0u);
 }
@@ -623,7 +643,9 @@ struct DqCfg {
     // pairs of q and dO tiles: two where they fit, so that an item begins while the last one ends
     static constexpr int QST = D == 128 ? 1 : 2, KST = D == 128 ? 3 : 5, VST = D == 128 ? 2 : 4;
     static constexpr int SMEM = (2 * QST + KST + VST) * Tile<D>::BYTES + kSmall;
-    static constexpr int THREADS = 640;  // 16 math warps, products, loads, the rows' statistics, stores
+    // 16 math warps, products, loads, two for the rows' statistics, of which one also stores: a warp
+    // more would cost 16 registers a thread
+    static constexpr int THREADS = 640;
 };
 
 template <int D, bool BF>
@@ -740,9 +762,13 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
         }
     } else if (warp >= 18) {
         // ------------------------------------------------------------ delta = dO . o and lse of the next item's rows
-        // A warp takes 64 rows, D / 8 lanes a row (16 bytes each), eight rows in flight a lane.  The
-        // second of them also stores dq, of the item before the one whose statistics it has formed.
-        uint32_t it = 0, last = 0;
+        // A warp takes 64 rows; the second of them also stores dq, of the item before the one whose
+        // statistics it has formed.  delta is the diagonal of dO o^T: 16 rows against 8 and 8, 16 bytes of
+        // them a lane as they come from memory.  (Sums of unpacked products took 11000 cycles of one
+        // warp, more than an item of five key tiles; so did the rows from DRAM, which are therefore
+        // asked for into L2 an item before.)
+        const int lane = threadIdx.x & 31, r = lane >> 2, col = (lane & 3) * 8;
+        uint32_t all = 0, it = 0, last = 0;
         auto store = [&](int item) {
             int b, h, hk, t0;
             place(item, b, h, hk, t0);
@@ -750,7 +776,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
             if (kt.hi < kt.lo) return;
             last += kt.hi - kt.lo + 1 + min(kt.sinks, kt.lo);
             const uint32_t s = (last - 1) % KST;
-            if ((threadIdx.x & 31) == 0) {
+            if (lane == 0) {
                 wait(staged, it, 43);
                 if (*wait.dead == 0u) store_tile<D>(&maps.x, sk + s * TB, t0, h, b);
                 tma_store_wait_read();
@@ -760,9 +786,6 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
             __syncwarp();
             ++it;
         };
-        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an access
-        const int lane = threadIdx.x & 31, first = (warp - 18) * 64 + lane / LPR, col = lane % LPR * 8;
-        uint32_t all = 0;
         for (int item = blockIdx.x; item < items; item += gridDim.x, ++all) {
             int b, h, hk, t0;
             place(item, b, h, hk, t0);
@@ -770,39 +793,65 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
             const uint16_t *x = static_cast<const uint16_t *>(o) + b * so.b + h * so.h + col;
             const uint16_t *y = static_cast<const uint16_t *>(dO) + b * sg.b + h * sg.h + col;
             const long long at = ((long long)b * g.H + h) * g.T;
+            float ls[2];  // P, and with it dS, of a row without a gradient is 0
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int t = t0 + (warp - 18) * 64 + lane + 32 * k;
+                ls[k] = t < len && !sees_one(g, t) ? __ldg(lse + at + t) * 1.4426950408889634f : INFINITY;
+            }
+            if (item < items - (int)gridDim.x) {
+                int b, h, hk, t0;
+                place(item + gridDim.x, b, h, hk, t0);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int t = t0 + (warp - 18) * 64 + lane + 32 * k;
+                    if (t >= wa_len(g, b)) continue;
+#pragma unroll
+                    for (int c = 0; c < D; c += 64) {
+                        prefetch_l2(static_cast<const uint16_t *>(o) + b * so.b + h * so.h + t * so.t + c);
+                        prefetch_l2(static_cast<const uint16_t *>(dO) + b * sg.b + h * sg.h + t * sg.t + c);
+                    }
+                }
+            }
             if (all > 1) wait(st_empty + 8 * (all & 1), all / 2 - 1, 42);
             float *dst = s_stat[all & 1][0], *dst2 = s_stat[all & 1][1];
-            for (int r0 = 0; r0 < 64; r0 += 8 * RPI) {
-                uint4 xv[8], yv[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int t = t0 + first + r0 + k * RPI;
-                    xv[k] = t < len ? __ldg(reinterpret_cast<const uint4 *>(x + t * so.t)) : make_uint4(0u, 0u, 0u, 0u);
-                    yv[k] = t < len ? __ldg(reinterpret_cast<const uint4 *>(y + t * sg.t)) : make_uint4(0u, 0u, 0u, 0u);
-                }
+            for (int k = 0; k < 2; ++k) dst2[(warp - 18) * 64 + lane + 32 * k] = ls[k];
+#pragma unroll 1
+            for (int r0 = (warp - 18) * 64; r0 < (warp - 18) * 64 + 64; r0 += 32) {
+                float acc[4][4];  // rows r0 + 8 k ..
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t aw[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w}, ew[4] = {yv[k].x, yv[k].y, yv[k].z, yv[k].w};
-                    float sum = 0.f;
+                for (int k = 0; k < 4; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 p = unpack16<BF>(aw[j]), q = unpack16<BF>(ew[j]);
-                        sum = fmaf(p.x, q.x, fmaf(p.y, q.y, sum));
+                for (int c = 0; c < D; c += 64) {
+                    uint4 xv[4][2], yv[4][2];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int t = t0 + r0 + 8 * k + r;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            xv[k][e] = t < len ? __ldg(reinterpret_cast<const uint4 *>(x + t * so.t + c + 32 * e)) : make_uint4(0u, 0u, 0u, 0u);
+                            yv[k][e] = t < len ? __ldg(reinterpret_cast<const uint4 *>(y + t * sg.t + c + 32 * e)) : make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
 #pragma unroll
-                    for (int s = LPR / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(~0u, sum, s);
-                    const int row = first + r0 + k * RPI, t = t0 + row;
-                    if (lane % LPR == 0) {
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint4 &a = yv[k & ~1][e], &b = yv[k | 1][e], &o = xv[k][e];
+                            mma16x8<BF>(acc[k], a.x, b.x, a.y, b.y, o.x, o.y);
+                            mma16x8<BF>(acc[k], a.z, b.z, a.w, b.w, o.z, o.w);
+                        }
+                }
+                if ((lane & 3) == r >> 1) {  // the lanes that hold the diagonals
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float sum = (r & 1) ? acc[k][2 * (k & 1) + 1] : acc[k][2 * (k & 1)];
+                        const int row = r0 + 8 * k + r, t = t0 + row;
                         dst[row] = sum;
                         if (t < g.T) delta[at + t] = sum;
                     }
                 }
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int row = (warp - 18) * 64 + lane + 32 * k, t = t0 + row;
-                // P, and with it dS, of a row without a gradient is 0
-                dst2[row] = t < len && !sees_one(g, t) ? __ldg(lse + at + t) * 1.4426950408889634f : INFINITY;
             }
             warp_arrive(st_full + 8 * (all & 1));
             if (warp == 19 && all > 0) store(item - gridDim.x);
@@ -890,10 +939,11 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
 // and lengths alone.
 template <int D>
 struct DkvCfg {
-    // stages of q and dO each, and pairs of k and v tiles: two where they fit, so that a list
-    // begins while the last one ends
-    static constexpr int ST = D == 128 ? 2 : 4, KVST = D == 128 ? 1 : 2;
-    static constexpr int SMEM = (2 * KVST + 2 * ST) * Tile<D>::BYTES + kSmall;
+    // Stages of q and of dO, and pairs of k and v tiles: two where they fit, so that a list begins while
+    // the last one ends.  The scores of step i + 2 are asked for before the last product with q of
+    // step i is: q needs three stages.
+    static constexpr int QST = D == 128 ? 3 : 4, GST = D == 128 ? 2 : 4, KVST = D == 128 ? 1 : 2;
+    static constexpr int SMEM = (2 * KVST + QST + GST) * Tile<D>::BYTES + kSmall;
     static constexpr int THREADS = 640;  // 16 math warps, products, loads, statistics, stores
 };
 
@@ -1026,20 +1076,21 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
 wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse, const float *__restrict__ delta,
               void *__restrict__ dk, void *__restrict__ dv, float *__restrict__ parts, CutList *__restrict__ cuts, Str3 sdk,
               Str3 sdv, WaArgs g, WsHeader *hdr) {
-    constexpr int ST = DkvCfg<D>::ST, KVST = DkvCfg<D>::KVST, TB = Tile<D>::BYTES;
+    constexpr int QST = DkvCfg<D>::QST, GST = DkvCfg<D>::GST, KVST = DkvCfg<D>::KVST, TB = Tile<D>::BYTES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t sk = smem_u32(smem_raw), sq = sk + 2 * KVST * TB, sg = sq + ST * TB;  // k, v in turn
-    Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 * KVST + 2 * ST) * TB);
-    static_assert(13 + 4 * ST + 4 <= 40, "barriers");
+    const uint32_t sk = smem_u32(smem_raw), sq = sk + 2 * KVST * TB, sg = sq + QST * TB;  // k, v in turn
+    Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 * KVST + QST + GST) * TB);
+    static_assert(17 + 2 * (QST + GST) + 4 <= 40, "barriers");
+    static_assert(QST >= 3 && GST >= 2, "stages");
     float(*s_stat)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [slot][lse log2 e, delta][query]
     if (misplaced(sk, hdr)) return;
     const int warp = threadIdx.x >> 5, G = g.H / g.Hkv;
     const uint32_t b0 = smem_u32(sm.bars);
-    const uint32_t kv_full = b0, kv_empty = b0 + 16, acc_full = b0 + 32, s_full = b0 + 40, dp_full = b0 + 48;
-    const uint32_t p_ready = b0 + 56, ds_ready = b0 + 64;
-    const uint32_t staged = b0 + 72;  // [dk, dv][parity of the list]
-    const uint32_t q_full = b0 + 104, q_empty = q_full + 8 * ST, g_full = q_empty + 8 * ST, g_empty = g_full + 8 * ST;
-    const uint32_t st_full = g_empty + 8 * ST, st_empty = st_full + 16;
+    const uint32_t kv_full = b0, kv_empty = b0 + 16, acc_full = b0 + 32;
+    const uint32_t s_full = b0 + 40, dp_full = b0 + 56, p_ready = b0 + 72, ds_ready = b0 + 88;  // of each half
+    const uint32_t staged = b0 + 104;  // [dk, dv][parity of the list]
+    const uint32_t q_full = b0 + 136, q_empty = q_full + 8 * QST, g_full = q_empty + 8 * QST, g_empty = g_full + 8 * GST;
+    const uint32_t st_full = g_empty + 8 * GST, st_empty = st_full + 16;
     if (warp == 1) {  // this block's share of the chain
         const long long total = chain_length(g), p0 = total * blockIdx.x / gridDim.x, p1 = total * (blockIdx.x + 1) / gridDim.x;
         Place p{0, 0, 0, 0};
@@ -1050,11 +1101,9 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
         }
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 7; ++i) mbar_init(b0 + 8 * i, 1);
-        mbar_init(p_ready, 16);
-        mbar_init(ds_ready, 16);
-        for (int i = 0; i < 4; ++i) mbar_init(staged + 8 * i, 8);
-        for (int i = 0; i < 4 * ST; ++i) mbar_init(q_full + 8 * i, 1);
+        for (int i = 0; i < 9; ++i) mbar_init(b0 + 8 * i, 1);
+        for (int i = 0; i < 8; ++i) mbar_init(p_ready + 8 * i, 8);  // ds_ready and staged too
+        for (int i = 0; i < 2 * (QST + GST); ++i) mbar_init(q_full + 8 * i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(st_full + 8 * i, 1), mbar_init(st_empty + 8 * i, 16);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = 0u;
@@ -1087,18 +1136,18 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                 Tile<D>::load(sk + (2 * kb + 1) * TB, &maps.v, w.p.tile * kWT, w.p.hk, w.p.b, kv_full + 8 * kb);
                 Step x = first_step();
                 for (int i = w.i0; i < w.i1; ++i, ++n, advance(x)) {
-                    const uint32_t s = n % ST;
-                    if (n >= ST) wait(q_empty + 8 * s, n / ST - 1, 42);
+                    const uint32_t s = n % QST, r = n % GST;
+                    if (n >= QST) wait(q_empty + 8 * s, n / QST - 1, 42);
                     if (*wait.dead != 0u) break;
                     mbar_expect_tx(q_full + 8 * s, TB);
                     Tile<D>::load(sq + s * TB, &maps.q, x.qt * kWT, x.h, w.p.b, q_full + 8 * s);
-                    if (n >= ST) wait(g_empty + 8 * s, n / ST - 1, 43);
-                    mbar_expect_tx(g_full + 8 * s, TB);
-                    Tile<D>::load(sg + s * TB, &maps.g, x.qt * kWT, x.h, w.p.b, g_full + 8 * s);
+                    if (n >= GST) wait(g_empty + 8 * r, n / GST - 1, 43);
+                    mbar_expect_tx(g_full + 8 * r, TB);
+                    Tile<D>::load(sg + r * TB, &maps.g, x.qt * kWT, x.h, w.p.b, g_full + 8 * r);
                 }
                 ++it;
             }
-            if (*wait.dead != 0u) drain(kv_full, it, KVST), drain(q_full, n, ST), drain(g_full, n, ST);
+            if (*wait.dead != 0u) drain(kv_full, it, KVST), drain(q_full, n, QST), drain(g_full, n, GST);
         }
         __syncwarp();
     } else if (warp == 18) {
@@ -1154,40 +1203,60 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
         while (w.next()) {
             const int i0 = uni(w.i0), i1 = uni(w.i1), len = uni(w.len), tile = uni(w.p.tile), f = uni(w.f);
             const uint32_t kb = it % KVST, kt = sk + 2 * kb * TB;
-            auto scores = [&](uint32_t j, int qt) {
-                const uint32_t s = j % ST;
-                wait(q_full + 8 * s, j / ST, 45);
-                if (g.lens != nullptr && len - qt * kWT < kWT) Tile<D>::zero_rows(sq + s * TB, len - qt * kWT);
+            auto scores = [&](uint32_t j, int qt, int u) {
+                const uint32_t s = j % QST;
+                if (u == 0) {
+                    wait(q_full + 8 * s, j / QST, 45);
+                    if (g.lens != nullptr && len - qt * kWT < kWT) Tile<D>::zero_rows(sq + s * TB, len - qt * kWT);
+                }
                 tc_fence_after();
-                mma_scores<D, BF>(lead, tS, kt, sq + s * TB);
-                mma_commit(lead, s_full);
+                mma_scores<D, BF, 64>(lead, tS + 64 * u, kt, sq + s * TB + u * kHalf);
+                mma_commit(lead, s_full + 8 * u);
             };
-            auto grads = [&](uint32_t j, int qt) {
-                const uint32_t s = j % ST;
-                wait(g_full + 8 * s, j / ST, 46);
-                if (g.lens != nullptr && len - qt * kWT < kWT) Tile<D>::zero_rows(sg + s * TB, len - qt * kWT);
+            auto grads = [&](uint32_t j, int qt, int u) {
+                const uint32_t s = j % GST;
+                if (u == 0) {
+                    wait(g_full + 8 * s, j / GST, 46);
+                    if (g.lens != nullptr && len - qt * kWT < kWT) Tile<D>::zero_rows(sg + s * TB, len - qt * kWT);
+                }
                 tc_fence_after();
-                mma_scores<D, BF>(lead, tP, kt + TB, sg + s * TB);
-                mma_commit(lead, dp_full);
+                mma_scores<D, BF, 64>(lead, tP + 64 * u, kt + TB, sg + s * TB + u * kHalf);
+                mma_commit(lead, dp_full + 8 * u);
+            };
+            // of step j: dv += P^T dO of a half, then the half's next scores; dk += dS^T Q, then its next dP
+            auto values = [&](uint32_t j, int u, bool first, bool last, int next) {
+                const uint32_t s = j % GST;
+                wait(p_ready + 8 * u, j, 48);
+                tc_fence_after();
+                mma_apply<D, BF, 32, 64>(lead, tV, tS + 64 * u, sg + s * TB + u * kHalf, !first || u > 0);
+                if (u == 1) mma_commit(lead, g_empty + 8 * s);
+                if (!last) scores(j + 1, next, u);
+            };
+            auto keys = [&](uint32_t j, int u, bool first, bool last, int next) {
+                const uint32_t s = j % QST;
+                wait(ds_ready + 8 * u, j, 49);
+                tc_fence_after();
+                mma_apply<D, BF, 32, 64>(lead, tK, tP + 64 * u, sq + s * TB + u * kHalf, !first || u > 0);
+                if (u == 1) mma_commit(lead, q_empty + 8 * s);
+                if (!last) grads(j + 1, next, u);
             };
             int qt = tile + uni(i0 == 0 ? 0 : i0 % f);
             wait(kv_full + 8 * kb, it / KVST, 47);
-            scores(n, qt);
-            grads(n, qt);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) scores(n, qt, u), grads(n, qt, u);
             for (int i = i0; i < i1; ++i, ++n) {
-                const uint32_t s = n % ST;
+                const int now = qt;
                 if (++qt == tile + f) qt = tile;  // of step i + 1
-                wait(p_ready, n, 48);
-                tc_fence_after();
-                mma_apply<D, BF, 32>(lead, tV, tS, sg + s * TB, i > i0);
-                mma_commit(lead, g_empty + 8 * s);
-                if (i + 1 < i1) scores(n + 1, qt);
-                wait(ds_ready, n, 49);
-                tc_fence_after();
-                mma_apply<D, BF, 32>(lead, tK, tP, sq + s * TB, i > i0);
-                mma_commit(lead, q_empty + 8 * s);
-                if (i + 1 < i1) grads(n + 1, qt);
+                const bool first = i == i0, last = i + 1 == i1;
+                values(n, 0, first, last, qt);
+                // the second half's gradients of the step before; in a list's first step its values, with
+                // which its warps say that they have read the accumulators of the list before
+                if (first) values(n, 1, first, last, qt);
+                else keys(n - 1, 1, i - 1 == i0, false, now);
+                keys(n, 0, first, last, qt);
+                if (!first) values(n, 1, first, last, qt);
             }
+            keys(n - 1, 1, i1 - 1 == i0, true, 0);
             mma_commit(lead, acc_full);
             ++it;
         }
@@ -1195,8 +1264,9 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
         const int part = warp >> 2, quarter = warp & 3, row = quarter * 32 + (threadIdx.x & 31);  // queries 32 part ..
         const uint32_t lanes = (uint32_t)quarter << 21;
         const float c = g.scale * 1.4426950408889634f;
-        // dk by the first eight warps, dv by the others, half of the columns each
-        const int which = part >> 1, col = (part & 1) * (D / 2);
+        // dv by the first half's warps, dk by the second's: a list's first product for dv follows the
+        // first half's probabilities, its first product for dk those of both
+        const int u = part >> 1, which = u ^ 1, col = (part & 1) * (D / 2);
         uint32_t n = 0, it = 0;
         while (w.next()) {
             const int s0 = w.p.tile * kWT, key = s0 + row;
@@ -1205,7 +1275,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                 const int t0 = st.qt * kWT;
                 const uint32_t sl = n & 1;
                 wait(st_full + 8 * sl, n >> 1, 50);
-                wait(s_full, n, 51);
+                wait(s_full + 8 * u, n, 51);
                 tc_fence_after();
                 uint32_t r[32], e[32], p[16];
                 tmem_ld32(tS + lanes + 32 * part, r);
@@ -1234,8 +1304,8 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                 tmem_st16(tS + lanes + 32 * part, p);
                 tmem_st_wait();
                 tc_fence_before();
-                warp_arrive(p_ready);
-                wait(dp_full, n, 52);
+                warp_arrive(p_ready + 8 * u);
+                wait(dp_full + 8 * u, n, 52);
                 tc_fence_after();
                 tmem_ld32(tP + lanes + 32 * part, e);
                 tmem_ld_wait();
@@ -1255,7 +1325,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                 tmem_st16(tP + lanes + 32 * part, p);
                 tmem_st_wait();
                 tc_fence_before();
-                warp_arrive(ds_ready);
+                warp_arrive(ds_ready + 8 * u);
                 warp_arrive(st_empty + 8 * sl);
             }
             const bool zero = key >= w.len, whole = w.i0 == 0 && w.i1 == w.list;
