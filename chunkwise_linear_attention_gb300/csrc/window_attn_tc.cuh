@@ -303,13 +303,15 @@ __device__ __forceinline__ bool sees_one(const WaArgs &g, int t) { return t == 0
 // instruction; that took 4000 cycles a tile.)
 template <int N, bool BF>
 __device__ __forceinline__ void stage_row(uint32_t taddr, uint32_t tile, int row, int col, float f, bool zero) {
+    constexpr int C = N < 32 ? N : 32;
 #pragma unroll
-    for (int c = 0; c < N; c += 16) {
-        uint32_t r[16];
-        tmem_ld16(taddr + c, r);
+    for (int c = 0; c < N; c += C) {
+        uint32_t r[C];
+        if constexpr (C == 32) tmem_ld32(taddr + c, r);
+        else tmem_ld16(taddr + c, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < C / 8; ++k) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -615,10 +617,10 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
                     quarter_sync<2>(id);
                     l += *other;
                     // into the query tile, whose last product is done
-                    stage_row<D / 2, BF>(to, sq + (2 * (it & 1) + u) * TB, row, half * (D / 2), 1.f / l, dead);
+                    stage_row<D / 2, BF>(to, sq + (2 * (it & 1) + u) * TB, row, half * (D / 2), __fdividef(1.f, l), dead);
                 }
                 if (half == 0 && t < g.T)
-                    lse[((long long)w.b * g.H + h) * g.T + t] = dead ? -INFINITY : m * 0.6931471805599453f + logf(l);
+                    lse[((long long)w.b * g.H + h) * g.T + t] = dead ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
             }
             tc_fence_before();
             if (!first) {
@@ -822,7 +824,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                 float acc[4][4];  // rows r0 + 8 k ..
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D; c += 64) {
                     uint4 xv[4][2], yv[4][2];
 #pragma unroll
