@@ -725,17 +725,51 @@ __global__ void __launch_bounds__(1024) gated_dlam_kernel(const float *__restric
 }
 
 // ------------------------------------------------------------------ one token
-template <typename E>
-__global__ void gated_step_kernel(const E *x, const E *rg, const E *ig, const float *lam, const uint8_t *reset,
-                                  float *h, E *y, int B, int D, float c) {
+// A thread takes 4 adjacent channels (VEC: with one access a tensor): at 512 x 4096 bf16 12 us against
+// 20 us with one channel a thread, at 1024 x 8192 31 (4.4 TB/s, 64% of the measured copy rate) against
+// 61.  Four rows a thread, which share their channels' rates, gave 29 at the latter and nothing below.
+template <typename E, bool VEC>
+__global__ void __launch_bounds__(128) gated_step_kernel(const E *x, const E *rg, const E *ig, const float *lam, const uint8_t *reset,
+                                                         float *h, E *y, int B, int D, float c) {
+    const int quads = (D + 3) / 4;
     const long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (u >= (long long)B * D) return;
-    const int b = (int)(u / D), d = (int)(u % D);
-    const Gate2 q = gate2<false>(f2(to_f32(rg[u])), f2(to_f32(ig[u])), f2(-c * softplus(lam[d]) * kLog2e));
-    const float w = q.i.x * to_f32(x[u]);
-    const float s = (reset != nullptr && reset[b]) ? w : fmaf(q.a.x, h[u], q.m.x * w);
-    h[u] = s;
-    y[u] = from_f32<E>(s);
+    const int b = (int)(u / quads), d = (int)(u % quads) * 4, n = D - d;
+    if (b >= B) return;
+    const size_t at = (size_t)b * D + d;
+    float2 xv[2], rv[2], iv[2], hv[2], l[2], s[2];
+    cvt4<E>(ld4<E, VEC>(rg + at, n), rv);
+    cvt4<E>(ld4<E, VEC>(ig + at, n), iv);
+    cvt4<E>(ld4<E, VEC>(x + at, n), xv);
+    if constexpr (VEC) {
+        const float4 r = *reinterpret_cast<const float4 *>(h + at);
+        hv[0] = make_float2(r.x, r.y);
+        hv[1] = make_float2(r.z, r.w);
+    } else {
+        ldf4(h + at, hv, n);
+    }
+    ldf4(lam + d, l, n);
+    const bool fresh = reset != nullptr && reset[b] != 0;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const Gate2 q = gate2<false>(rv[v], iv[v], make_float2(-c * softplus(l[v].x) * kLog2e, -c * softplus(l[v].y) * kLog2e));
+        const float2 w = mul2(q.i, xv[v]);
+        s[v] = fresh ? w : fma2(q.a, hv[v], mul2(q.m, w));
+    }
+    if constexpr (VEC) *reinterpret_cast<float4 *>(h + at) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+    else stf4(h + at, s, n);
+    st4<E, VEC>(y + at, s, n);
+}
+
+template <typename E>
+int gs_step(const char *fn, const void *x, const void *rg, const void *ig, const float *lam, const uint8_t *reset, float *h, void *y,
+            float c, int64_t B, int64_t D, cudaStream_t s) {
+    const unsigned grid = (unsigned)((B * ((D + 3) / 4) + 127) / 128);
+    auto go = [&](auto kernel) {
+        kernel<<<grid, 128, 0, s>>>((const E *)x, (const E *)rg, (const E *)ig, lam, reset, h, (E *)y, (int)B, (int)D, c);
+    };
+    if (D % 4 == 0 && aligned_or_null({x, rg, ig, y}, 4 * sizeof(E)) && aligned16(h)) go(gated_step_kernel<E, true>);
+    else go(gated_step_kernel<E, false>);
+    return check_launch(fn);
 }
 
 // ------------------------------------------------------------------ host side
@@ -978,12 +1012,7 @@ extern "C" int cla_gated_scan_step(const void *x, const void *rgate, const void 
     if (!aligned_or_null({x, rgate, igate, y}, dtype_bytes(dtype)) || !aligned_or_null({lam, h}, 4))
         return fail(CLA_ERR_INVALID_ARG, "%s: a pointer is misaligned", fn);
     cudaStream_t s = (cudaStream_t)stream;
-    const unsigned grid = (unsigned)((B * D + 127) / 128);
-    if (dtype == CLA_F32)
-        gated_step_kernel<float><<<grid, 128, 0, s>>>((const float *)x, (const float *)rgate, (const float *)igate, lam, reset, h, (float *)y, (int)B, (int)D, c);
-    else if (dtype == CLA_BF16)
-        gated_step_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>((const __nv_bfloat16 *)x, (const __nv_bfloat16 *)rgate, (const __nv_bfloat16 *)igate, lam, reset, h, (__nv_bfloat16 *)y, (int)B, (int)D, c);
-    else
-        gated_step_kernel<__half><<<grid, 128, 0, s>>>((const __half *)x, (const __half *)rgate, (const __half *)igate, lam, reset, h, (__half *)y, (int)B, (int)D, c);
-    return check_launch(fn);
+    if (dtype == CLA_F32) return gs_step<float>(fn, x, rgate, igate, lam, reset, h, y, c, B, D, s);
+    if (dtype == CLA_BF16) return gs_step<__nv_bfloat16>(fn, x, rgate, igate, lam, reset, h, y, c, B, D, s);
+    return gs_step<__half>(fn, x, rgate, igate, lam, reset, h, y, c, B, D, s);
 }

@@ -172,6 +172,25 @@ def test_step(cla, B, D, dtype):
         R.assert_within("h", h, *ref["hT"])
 
 
+def test_step_at_odd_addresses(cla):
+    """Rows that are not aligned for four elements at once; what lies around them stays as it was."""
+    t, _, _ = inputs(5, 1, 64, BF16)
+    ref = R.gated(t["x"], t["rgate"], t["igate"], t["lam"], t["h0"])
+
+    def moved(v):
+        buf = torch.full((v.numel() + 8,), 7.0, dtype=v.dtype, device="cuda")
+        buf[1:1 + v.numel()] = v.reshape(-1)
+        return buf, buf[1:1 + v.numel()].view(v.shape)
+
+    (_, x), (_, r), (_, i) = (moved(t[n][:, 0].contiguous()) for n in ("x", "rgate", "igate"))
+    (hb, h), (yb, y) = moved(t["h0"]), moved(torch.zeros_like(t["x"][:, 0]))
+    assert cla.gated_scan_step(x, r, i, t["lam"], h, y=y) is y
+    R.assert_within("y", y, ref["h"][0][:, 0], ref["h"][1][:, 0])
+    R.assert_within("h", h, *ref["hT"])
+    for buf, n in ((hb, h.numel()), (yb, y.numel())):
+        assert float(buf[0]) == 7 and bool((buf[1 + n:] == 7).all())
+
+
 def test_steps_continue_a_forward(cla):
     t, _, _ = inputs(3, 100, 64, BF16)
     ref = R.gated(t["x"], t["rgate"], t["igate"], t["lam"], t["h0"])
