@@ -19,7 +19,7 @@
 namespace cla {
 namespace {
 
-// One 16-byte piece of a cache slot per thread.
+// One 16-byte piece of a cache slot per thread; it is 5 us of a 32768-token prefill's 528.
 __global__ void wa_write_kernel(const char *k, const char *v, const int32_t *lens, char *kc, char *vc, Str3 sk, Str3 sv, int B,
                                 int Hkv, int T, long long window, long long sinks, int pieces) {
     const long long S = sinks + window;
@@ -90,9 +90,6 @@ int wa_blocks(const char *fn, long long items, unsigned *blocks) {
     *blocks = (unsigned)(items < n ? items : n);
     return CLA_OK;
 }
-
-// The step's blocks are made at least this many by splitting the slots, where there are so many.
-constexpr long long kStepBlocks = 912;
 
 long long wa_tiles(long long T) { return (T + kWT - 1) / kWT; }
 
@@ -260,30 +257,75 @@ extern "C" int cla_window_cache_write(const void *k, const void *v, const int32_
     return check_launch(fn);
 }
 
-template <int D, bool BF, int NG>
-static int wa_step(const char *fn, const void *q, const void *k, const void *v, void *kc, void *vc, const int32_t *pos, void *o,
-                   const Str3 *r, StepArgs g, cudaStream_t s) {
-    const int G = g.H / g.Hkv;
-    g.groups = (G + 8 * NG - 1) / (8 * NG);
-    const long long units = (long long)g.B * g.Hkv * g.groups;
-    const long long tiles = (g.slots + 15) / 16;
-    g.splits = 1;
-    while (g.splits < 8 && units * g.splits < kStepBlocks && tiles > g.splits * kStepWarps) g.splits *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * g.splits));
+namespace cla {
+namespace {
+
+constexpr int kMaxSplits = 16;  // blocks of a cluster; above 8 with the kernel's leave
+
+void step_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &at, long long clusters, int splits, cudaStream_t s) {
+    cfg.gridDim = dim3((unsigned)(clusters * splits));
     cfg.blockDim = dim3(kStepWarps * 32);
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)g.splits;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)splits;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
     cfg.numAttrs = 1;
+}
+
+// Clusters of each size that the current device runs at once (0: none), asked for once per device.
+template <int D, bool BF, int NG>
+int step_resident(const char *fn, int (&n)[kMaxSplits + 1]) {
+    static std::atomic<int> known[64][kMaxSplits + 1];  // the number and 1
+    int dev = 0;
+    CLA_CUDA_TRY(cudaGetDevice(&dev), fn);
+    const bool keep = dev < 64;
+    for (int s = 1; s <= kMaxSplits; ++s) {
+        n[s] = keep ? known[dev][s].load(std::memory_order_relaxed) - 1 : -1;
+        if (n[s] >= 0) continue;
+        if (s > 8)
+            CLA_CUDA_TRY(cudaFuncSetAttribute((const void *)wa_step_kernel<D, BF, NG>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), fn);
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at;
+        step_config(cfg, at, 1, s, nullptr);
+        CLA_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n[s], wa_step_kernel<D, BF, NG>, &cfg), fn);
+        if (keep) known[dev][s].store(n[s] + 1, std::memory_order_relaxed);
+    }
+    return CLA_OK;
+}
+
+// Splits the slots of a (sequence, key head) over as many blocks as give the least rounds of clusters
+// times the 16-slot tiles of a warp; a round's latency and join count as 3 tiles.  Measured (us; 4
+// warps a block, d = 128, key heads in all x slots; 1, 2, 3, 4, 6, 8, 16 blocks a cluster):
+//   8 x 32772   604 307 209 160 111  86  54      256 x 4100  104 124  98 110 110 121 177
+//   64 x 2052    47  31  27  23  23  31  44      512 x 4100  230 202 190 187 194 221 335
+//   128 x 4100   88  57  53  70  59  66  96
+template <int D, bool BF, int NG>
+int wa_step(const char *fn, const void *q, const void *k, const void *v, void *kc, void *vc, const int32_t *pos, void *o,
+            const Str3 *r, StepArgs g, cudaStream_t s) {
+    const int G = g.H / g.Hkv;
+    g.groups = (G + 8 * NG - 1) / (8 * NG);
+    const long long units = (long long)g.B * g.Hkv * g.groups, tiles = (g.slots + 15) / 16;
+    int resident[kMaxSplits + 1];
+    if (int st = step_resident<D, BF, NG>(fn, resident)) return st;
+    g.splits = 1;
+    long long least = -1;
+    for (int n = 1; n <= kMaxSplits && (n - 1) * kStepWarps < tiles; ++n) {
+        if (resident[n] == 0) continue;
+        const long long cost = (units + resident[n] - 1) / resident[n] * ((tiles + n * kStepWarps - 1) / (n * kStepWarps) + 3);
+        if (least < 0 || cost < least) least = cost, g.splits = n;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at;
+    step_config(cfg, at, units, g.splits, s);
     CLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, wa_step_kernel<D, BF, NG>, (const uint16_t *)q, (const uint16_t *)k, (const uint16_t *)v,
                                     (uint16_t *)kc, (uint16_t *)vc, pos, (uint16_t *)o, r[0], r[1], r[2], g),
                  fn);
     return check_launch(fn);
 }
+
+}  // namespace
+}  // namespace cla
 
 extern "C" int cla_window_attn_step(const void *q, const void *k, const void *v, void *kcache, void *vcache,
                                     const int32_t *pos, void *o, float scale, int64_t window, int64_t sinks, int dtype,
@@ -307,6 +349,8 @@ extern "C" int cla_window_attn_step(const void *q, const void *k, const void *v,
     if (int st = wa_strides(fn, strides ? full : nullptr, names, heads, 3, B, 1, d, r)) return st;
     const StepArgs g{scale * 1.4426950408889634f, window, sinks + window, (int)sinks, (int)B, (int)H, (int)Hkv, 1, 1};
     cudaStream_t s = (cudaStream_t)stream;
+    // 16 heads a block read the cache once for up to 16 heads of a group (64 x 2 x 4100 x 128, 16 heads a
+    // group: 64 us against 78 with two blocks of 8) in 240 registers; 8 or fewer take 161
     const bool bf = dtype == CLA_BF16, wide = H / Hkv > 8;
 #define CLA_STEP(D, BF) \
     (wide ? wa_step<D, BF, 2>(fn, q, k, v, kcache, vcache, pos, o, r, g, s) : wa_step<D, BF, 1>(fn, q, k, v, kcache, vcache, pos, o, r, g, s))

@@ -5,11 +5,31 @@
 //
 // Tiles are 128 tokens on both sides.  Every kernel is persistent (a block per
 // SM, items taken in a fixed order) and has its roles in separate warps: 16
-// math warps, one that issues the products, one that issues the loads (and in
-// the dk/dv kernel one that stages the rows' statistics), so that loads and
-// products run ahead of the elementwise work.  A math warp reads the lane
-// quarter of tensor memory that its rank in its group of four allows; the
-// thread's lane is its row.
+// math warps, one that issues the products, one that issues the loads, and one
+// or two that form the rows' statistics and store what the math warps staged,
+// so that loads, products and stores run beside the elementwise work.  A math
+// warp reads the lane quarter of tensor memory that its rank in its group of
+// four allows; the thread's lane is its row.
+//
+// Probabilities P and their gradients dS are rounded to the tensors' type for
+// their products, with fp32 sums: the tensor cores take no fp32 operand, and
+// two 16-bit parts would double the products that bound the kernels at d = 128.
+// Against a form that keeps them in fp32 this adds about as much error to dq
+// and dk as the rounding of the outputs does (bf16: 2.5e-3 against 1.7e-3).
+//
+// Measured on GB300 (B x H / Hkv x T x d, window, sinks; bf16):
+//                                     4 x 16/16 x 8192 x 64   2 x 16/4 x 8192 x 128
+//                                     512, 0                  2048, 16
+//   forward                           118 us, 31% of the      196 us, 64%
+//   dq                                139 us  40% tensor      249 us, 74%
+//   dk, dv                            172 us, 41% pipe's      343 us, 74%
+//   join                              7 us        cycles      10 us
+// At d = 128 the products bound them (all tiles are formed whole, also those
+// that the window or the diagonal cuts: 17 where 16 would do at that window,
+// 5 where 4 would at the other); at d = 64, where a pair of tiles has half the
+// products and the same 16384 exponentials and roundings, the elementwise work:
+// 55-60% of the issue slots, and the exchange and staging at the end of each
+// item, a fifth of its time at five key tiles.
 //
 // Waits are bounded: one that gives up marks the block, which then waits no
 // more, and records the timeout in the workspace header.
@@ -347,6 +367,12 @@ __device__ __forceinline__ void zero_row(void *out, long long at) {
 // probabilities lie over its scores) and two output accumulators.  The running maximum is moved
 // only when a row's grows by more than 8 (in powers of two), so the accumulator is rescaled
 // rarely and by the warps that own it; sums and outputs are fp32.
+//
+// 1 x 32/8 x 32768 x 128, window 1024, sinks 4: 495 us, of 284 us for the products of the visible
+// pairs alone at the measured rate of a library's (10 tiles are formed where 8 would do).
+// Tried and not kept: products of 16 columns for tiles that only sinks are seen of (no gain there,
+// 3% slower without sinks), probabilities in two passes over half rows, a suspend-time hint on the
+// waits (5% slower than spinning).
 template <int D>
 struct FwdCfg {
     static constexpr int STAGES = D == 128 ? 3 : 8;  // of keys and values, beside two pairs of query tiles
@@ -639,7 +665,10 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
 // One query tile at a time; each row's 128 scores and their gradients are shared by four threads
 // (32 columns each).  Tensor memory: two score tiles in turn (dS is written over the scores), one
 // dP tile, the accumulator.  While the math warps work on key tile i, the tensor cores form the
-// scores of i + 1, and when its dS is there, dP of i + 1 and then dq += dS k.
+// scores of i + 1, and when its dS is there, dP of i + 1 and then dq += dS k.  In two groups of 64
+// key columns, as the dk/dv kernel has them, it was slower (64 columns: 454 us for the whole pass at
+// d = 64 against 447; 299 us against 250 at d = 128, where products 64 wide read the row operand
+// twice as often).
 template <int D>
 struct DqCfg {
     // pairs of q and dO tiles: two where they fit, so that an item begins while the last one ends
@@ -930,9 +959,10 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
 // ------------------------------------------------------------------ backward: dk, dv
 // A key tile against the query tiles that see it, head by head of the group.  The scores are
 // transposed (a row is a key), so that P^T and dS^T are A operands from tensor memory: S^T = K Q^T,
-// dP^T = V dO^T, dv += P^T dO, dk += dS^T Q, with P^T over S^T and dS^T over dP^T.  Each half of
-// the elementwise work runs beside two products: forming P beside dk += and the next dP, forming
-// dS beside dv += and the next S.
+// dP^T = V dO^T, dv += P^T dO, dk += dS^T Q, with P^T over S^T and dS^T over dP^T.  The
+// 128 queries of a step are two halves, each with its own eight warps, products and barriers and half
+// a step behind the other, so that one forms P while the other forms dS (347 -> 343 us at d = 128,
+// 176 -> 172 at d = 64 against all 16 warps in step).
 //
 // The lists of the key tiles, one behind the other (sequence, key head, tile), are cut into equal
 // shares, one a block: few tiles with long lists (sinks are seen by every later query) and a
@@ -1376,7 +1406,8 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
 
 // Adds the parts of a list that was cut, in their order: block (x, y) those of the list that block x
 // of wa_dkv_kernel left, y an eighth of the columns of dk and dv.  Parts come with the rows next to
-// each other and go out with the columns so, through shared memory.
+// each other and go out with the columns so, through shared memory.  At 151 cuts of 128 x 128 it reads
+// 40 MB in 10 us (4 TB/s).
 constexpr int kJoinY = 8;
 template <int D, bool BF>
 __global__ void __launch_bounds__(256) wa_join_kernel(const float *__restrict__ parts, const CutList *__restrict__ cuts,

