@@ -27,9 +27,13 @@
 // At d = 128 the products bound them (all tiles are formed whole, also those
 // that the window or the diagonal cuts: 17 where 16 would do at that window,
 // 5 where 4 would at the other); at d = 64, where a pair of tiles has half the
-// products and the same 16384 exponentials and roundings, the elementwise work:
-// 55-60% of the issue slots, and the exchange and staging at the end of each
-// item, a fifth of its time at five key tiles.
+// products and the same 16384 exponentials and roundings, the chain of a warp's
+// elementwise work (load, 2^x, rounding, store, each behind the other; no unit
+// above half of its rate), and the exchange and staging at the end of each item,
+// a fifth of its time at five key tiles.  More overlap did not help there: next
+// scores formed before the probabilities' product, in columns of their own, 452
+// us for the pass against 446; nor cheaper polls of the barriers, 442, or sleep
+// between them, 451.
 //
 // Waits are bounded: one that gives up marks the block, which then waits no
 // more, and records the timeout in the workspace header.
