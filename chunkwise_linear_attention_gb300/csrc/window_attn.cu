@@ -214,8 +214,10 @@ extern "C" int cla_window_attn_bwd(const void *q, const void *k, const void *v, 
     if (int st = wa_strides(fn, strides, names, heads, 8, B, T, d, r)) return st;
     const WaArgs g = wa_args(lens, scale, T, window, sinks, B, H, Hkv, B * H);
     cudaStream_t s = (cudaStream_t)stream;
-    CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(WsHeader), s), fn);
-    if (B * H * T == 0) return CLA_OK;
+    if (B * H * T == 0) {
+        CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(WsHeader), s), fn);
+        return CLA_OK;
+    }
     const bool bf = dtype == CLA_BF16;
     WaMaps m;
     if (!make_map_bht(&m.q, q, bf, d, T, H, B, r[0]) || !make_map_bht(&m.k, k, bf, d, T, Hkv, B, r[1]) ||

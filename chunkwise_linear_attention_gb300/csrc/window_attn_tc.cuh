@@ -709,6 +709,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
         for (int i = 0; i < 2 * (KST + VST); ++i) mbar_init(k_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = 0u;
+        if (blockIdx.x == 0) hdr->error = 0u, hdr->where = 0u;  // of the whole call
     }
     const uint32_t tmem = tmem_alloc_all(&sm.tmem);
     const Waits wait{&sm.dead, hdr};
