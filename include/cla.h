@@ -736,6 +736,7 @@ int cla_window_cache_write(const void *k, const void *v, const int32_t *lens,
  *          cache is left alone.
  *   o      [B, H, d] dtype out, dense
  *   strides [opt]: {batch, head} pairs of q, k, v, under the rules above
+ * The sums are in an order that the sizes and the device model fix.
  * sinks + window is at most 2^31 - 512, B * H below 2^27. */
 int cla_window_attn_step(const void *q, const void *k, const void *v, void *kcache,
                          void *vcache, const int32_t *pos, void *o, float scale,
