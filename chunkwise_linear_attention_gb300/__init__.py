@@ -10,7 +10,10 @@ All tensors must be CUDA tensors, contiguous, with the dtype the C ABI names
 point takes a dtype).  The window_attn_* tensors may be strided over batch,
 heads and tokens.  Outputs and the workspace are allocated with torch when not
 supplied.  `stream` is the stream of the call, the current one by default; what
-another stream has to write first is the caller's to wait for.
+another stream has to write first is the caller's to wait for.  That holds for
+a buffer the caller makes as well, a *_ckpt function's among them: its memory
+is ready for a call on another stream once that stream has waited for the
+current one.  What a call allocates itself needs no such wait.
 """
 from __future__ import annotations
 
@@ -127,6 +130,15 @@ def _stream(stream, device=None):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _stream_object(stream, device):
+    """`stream` (a torch.cuda.Stream or a raw handle) as a torch.cuda.Stream of `device`."""
+    handle = _stream(stream, device).value or 0  # refuses a stream of another device
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # 0 and 1 (cudaStreamLegacy) are the device's default stream
+    return torch.cuda.default_stream(device) if handle < 2 else torch.cuda.ExternalStream(handle, device=device)
+
+
 def _dims(t, n, name):
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
@@ -163,19 +175,32 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
-def _ws(nbytes, device, workspace, minimum=None):
+def _empty(shape, dtype, device, stream, returned):
+    """Memory for a call on `stream`: allocated on that stream, so that what queued work on another one still does with a
+    block that was given back there is not overtaken.  What is `returned` is then used on the current stream, and not
+    given out again before that is done with it either."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_stream_object(stream, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _ws(nbytes, device, workspace, stream, minimum=None):
     """A workspace of nbytes (allocated when not given); a given one needs at least `minimum`
     bytes (default nbytes) -- the entry points that take less than their size query's amount."""
     if workspace is None:
-        workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+        workspace = _empty((max(int(nbytes), 256),), torch.uint8, device, stream, False)
     need = nbytes if minimum is None else minimum
     if _nbytes(workspace) < need:
         raise ValueError(f"workspace of {_nbytes(workspace)} bytes < {need} needed")
     return workspace
 
 
-def _out(t, shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else t
+def _out(t, shape, dtype, device, stream):
+    return _empty(shape, dtype, device, stream, True) if t is None else t
 
 
 def _launch(fn, device, args, stream):
@@ -201,8 +226,9 @@ def _launch(fn, device, args, stream):
         for a in tensors:
             _check_place(device, *a)
     if isinstance(stream, torch.cuda.Stream):
-        # memory that was allocated on another stream (the outputs and the workspace among it) is not
-        # given out again before this stream is done with it; with a raw handle that is the caller's part
+        _stream(stream, device)  # of the same device, or refused
+        # memory that was allocated on another stream is not given out again before this stream is done
+        # with it; with a raw handle that is the caller's part
         for a in args:
             if type(a) is tuple and a[0] is not None:
                 a[0].record_stream(stream)
@@ -239,13 +265,13 @@ def _scan_fwd(fn, a, b, h0, h, hT, workspace, stream, with_ws=True):
     B, T, D = _dims(a, 3, "a")
     dev = a.device
     f32 = torch.float32
-    h = _out(h, (B, T, D), f32, dev)
-    hT = _out(hT, (B, D), f32, dev)
+    h = _out(h, (B, T, D), f32, dev, stream)
+    hT = _out(hT, (B, D), f32, dev, stream)
     bt, bd = (B, T, D), (B, D)
     args = (_T(a, f32, "a", bt), _T(b, f32, "b", bt), _T(h0, f32, "h0", bd),
             _T(h, f32, "h", bt), _T(hT, f32, "hT", bd), B, T, D)
     if with_ws:
-        ws = _ws(scan_diag_workspace_size(B, T, D), dev, workspace)
+        ws = _ws(scan_diag_workspace_size(B, T, D), dev, workspace, stream)
         args += (_T(ws, None, "workspace"), _nbytes(ws))
     _launch(fn, dev, args, stream)
     return h, hT
@@ -282,10 +308,10 @@ def scan_diag_bwd(a, b, h0, h, dh, dhT=None, *, da=None, db=None, dh0=None, work
     B, T, D = _dims(a, 3, "a")
     dev = a.device
     f32 = torch.float32
-    da = _out(da, (B, T, D), f32, dev)
-    db = _out(db, (B, T, D), f32, dev)
-    dh0 = _out(dh0, (B, D), f32, dev)
-    ws = _ws(scan_diag_workspace_size(B, T, D), dev, workspace)
+    da = _out(da, (B, T, D), f32, dev, stream)
+    db = _out(db, (B, T, D), f32, dev, stream)
+    dh0 = _out(dh0, (B, D), f32, dev, stream)
+    ws = _ws(scan_diag_workspace_size(B, T, D), dev, workspace, stream)
     bt, bd = (B, T, D), (B, D)
     _launch("cla_scan_diag_bwd", dev, (
         _T(a, f32, "a", bt), _T(b, f32, "b", bt), _T(h0, f32, "h0", bd), _T(h, f32, "h", bt),
@@ -320,11 +346,11 @@ def selective_scan_fwd(x, delta, A, Bm, Cm, h0=None, *, y=None, hT=None, ckpt=No
     N = _dims(A, 2, "A")[1]
     dev = x.device
     f32, bf16 = torch.float32, torch.bfloat16
-    y = _out(y, (B, T, D), f32, dev)
-    hT = _out(hT, (B, D, N), f32, dev)
+    y = _out(y, (B, T, D), f32, dev, stream)
+    hT = _out(hT, (B, D, N), f32, dev, stream)
     if ckpt is None and want_ckpt:
-        ckpt = torch.empty(selective_scan_ckpt_elems(B, T, D, N), dtype=f32, device=dev)
-    ws = _ws(selective_scan_workspace_size(B, T, D, N), dev, workspace)
+        ckpt = _out(None, (selective_scan_ckpt_elems(B, T, D, N),), f32, dev, stream)
+    ws = _ws(selective_scan_workspace_size(B, T, D, N), dev, workspace, stream)
     btd, btn, bdn = (B, T, D), (B, T, N), (B, D, N)
     _launch("cla_selective_scan_fwd", dev, (
         _T(x, bf16, "x", btd), _T(delta, f32, "delta", btd), _T(A, f32, "A", (D, N)),
@@ -341,13 +367,13 @@ def selective_scan_bwd(x, delta, A, Bm, Cm, h0, ckpt, dy, dhT=None, *, dx=None, 
     N = _dims(A, 2, "A")[1]
     dev = x.device
     f32, bf16 = torch.float32, torch.bfloat16
-    dx = _out(dx, (B, T, D), f32, dev)
-    ddelta = _out(ddelta, (B, T, D), f32, dev)
-    dA = _out(dA, (D, N), f32, dev) if (want_dA or dA is not None) else None
-    dB = _out(dB, (B, T, N), f32, dev)
-    dC = _out(dC, (B, T, N), f32, dev)
-    dh0 = _out(dh0, (B, D, N), f32, dev) if (want_dh0 or dh0 is not None) else None
-    ws = _ws(selective_scan_workspace_size(B, T, D, N), dev, workspace)
+    dx = _out(dx, (B, T, D), f32, dev, stream)
+    ddelta = _out(ddelta, (B, T, D), f32, dev, stream)
+    dA = _out(dA, (D, N), f32, dev, stream) if (want_dA or dA is not None) else None
+    dB = _out(dB, (B, T, N), f32, dev, stream)
+    dC = _out(dC, (B, T, N), f32, dev, stream)
+    dh0 = _out(dh0, (B, D, N), f32, dev, stream) if (want_dh0 or dh0 is not None) else None
+    ws = _ws(selective_scan_workspace_size(B, T, D, N), dev, workspace, stream)
     btd, btn, bdn = (B, T, D), (B, T, N), (B, D, N)
     _launch("cla_selective_scan_bwd", dev, (
         _T(x, bf16, "x", btd), _T(delta, f32, "delta", btd), _T(A, f32, "A", (D, N)),
@@ -393,9 +419,9 @@ def chunk_la_fwd(q, k, v, log_decay, S0=None, *, chunk=64, o=None, ST=None, ckpt
     dv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    o = _out(o, (B, H, T, dv), f32, dev)
-    ST = _out(ST, (B, H, dk, dv), f32, dev)
-    ws = _ws(chunk_la_workspace_size(B, H, T, dk, dv, chunk), dev, workspace)
+    o = _out(o, (B, H, T, dv), f32, dev, stream)
+    ST = _out(ST, (B, H, dk, dv), f32, dev, stream)
+    ws = _ws(chunk_la_workspace_size(B, H, T, dk, dv, chunk), dev, workspace, stream)
     tk, tv, st = (B, H, T, dk), (B, H, T, dv), (B, H, dk, dv)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", (B, H, T)), _T(S0, f32, "S0", st),
@@ -417,12 +443,12 @@ def chunk_la_bwd(q, k, v, log_decay, S0, dO, dST=None, *, chunk=64, dq=None, dk=
     dvv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    dq = _out(dq, (B, H, T, dkk), f32, dev)
-    dk = _out(dk, (B, H, T, dkk), f32, dev)
-    dv = _out(dv, (B, H, T, dvv), f32, dev)
-    dlog_decay = _out(dlog_decay, (B, H, T), f32, dev)
-    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev)
-    ws = _ws(chunk_la_workspace_size(B, H, T, dkk, dvv, chunk), dev, workspace)
+    dq = _out(dq, (B, H, T, dkk), f32, dev, stream)
+    dk = _out(dk, (B, H, T, dkk), f32, dev, stream)
+    dv = _out(dv, (B, H, T, dvv), f32, dev, stream)
+    dlog_decay = _out(dlog_decay, (B, H, T), f32, dev, stream)
+    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev, stream)
+    ws = _ws(chunk_la_workspace_size(B, H, T, dkk, dvv, chunk), dev, workspace, stream)
     tk, tv, st, bht = (B, H, T, dkk), (B, H, T, dvv), (B, H, dkk, dvv), (B, H, T)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", bht), _T(S0, f32, "S0", st),
@@ -470,9 +496,9 @@ def gla_fwd(q, k, v, log_decay, S0=None, *, chunk=64, o=None, ST=None, ckpt=None
     dv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    o = _out(o, (B, H, T, dv), f32, dev)
-    ST = _out(ST, (B, H, dk, dv), f32, dev)
-    ws = _ws(gla_workspace_size(B, H, T, dk, dv, chunk), dev, workspace)
+    o = _out(o, (B, H, T, dv), f32, dev, stream)
+    ST = _out(ST, (B, H, dk, dv), f32, dev, stream)
+    ws = _ws(gla_workspace_size(B, H, T, dk, dv, chunk), dev, workspace, stream)
     tk, tv, st = (B, H, T, dk), (B, H, T, dv), (B, H, dk, dv)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", tk), _T(S0, f32, "S0", st),
@@ -498,12 +524,12 @@ def gla_bwd(q, k, v, log_decay, S0, dO, dST=None, *, chunk=64, dq=None, dk=None,
     dvv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    dq = _out(dq, (B, H, T, dkk), f32, dev)
-    dk = _out(dk, (B, H, T, dkk), f32, dev)
-    dv = _out(dv, (B, H, T, dvv), f32, dev)
-    dlog_decay = _out(dlog_decay, (B, H, T, dkk), f32, dev)
-    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev)
-    ws = _ws(gla_bwd_workspace_size(B, H, T, dkk, dvv, chunk), dev, workspace)
+    dq = _out(dq, (B, H, T, dkk), f32, dev, stream)
+    dk = _out(dk, (B, H, T, dkk), f32, dev, stream)
+    dv = _out(dv, (B, H, T, dvv), f32, dev, stream)
+    dlog_decay = _out(dlog_decay, (B, H, T, dkk), f32, dev, stream)
+    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev, stream)
+    ws = _ws(gla_bwd_workspace_size(B, H, T, dkk, dvv, chunk), dev, workspace, stream)
     tk, tv, st = (B, H, T, dkk), (B, H, T, dvv), (B, H, dkk, dvv)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", tk), _T(S0, f32, "S0", st), _T(dO, bf16, "dO", tv),
@@ -528,7 +554,7 @@ def decay_total(log_decay, *, alpha=None, stream=None):
         B, H, T, A = _dims(log_decay, 4, "log_decay")
         shape = (B, H, A)
     dev = log_decay.device
-    alpha = _out(alpha, shape, torch.float32, dev)
+    alpha = _out(alpha, shape, torch.float32, dev, stream)
     _launch("cla_decay_total", dev, (_T(log_decay, torch.float32, "log_decay", tuple(log_decay.shape)),
                                      _T(alpha, torch.float32, "alpha", shape), B * H, T, A), stream)
     return alpha
@@ -540,7 +566,7 @@ def state_compose(alphas, dSs, edge, first, count, step, *, out=None, stream=Non
     P, B, H, dk, dv = _dims(dSs, 5, "dSs")
     A = 1 if alphas.dim() == 3 else alphas.shape[3]
     dev = dSs.device
-    out = _out(out, (B, H, dk, dv), torch.float32, dev)
+    out = _out(out, (B, H, dk, dv), torch.float32, dev, stream)
     st = (B, H, dk, dv)
     _launch("cla_state_compose", dev, (
         _T(alphas, torch.float32, "alphas", (P, B, H) if A == 1 else (P, B, H, A)),
@@ -583,9 +609,9 @@ def delta_fwd(q, k, v, log_decay, beta, S0=None, *, chunk=64, o=None, ST=None, c
     dv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    o = _out(o, (B, H, T, dv), f32, dev)
-    ST = _out(ST, (B, H, dk, dv), f32, dev)
-    ws = _ws(delta_workspace_size(B, H, T, dk, dv, chunk), dev, workspace, minimum=256)
+    o = _out(o, (B, H, T, dv), f32, dev, stream)
+    ST = _out(ST, (B, H, dk, dv), f32, dev, stream)
+    ws = _ws(delta_workspace_size(B, H, T, dk, dv, chunk), dev, workspace, stream, minimum=256)
     tk, tv, st, bht = (B, H, T, dk), (B, H, T, dv), (B, H, dk, dv), (B, H, T)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", bht), _T(beta, f32, "beta", bht), _T(S0, f32, "S0", st),
@@ -610,16 +636,16 @@ def delta_bwd(q, k, v, log_decay, beta, S0, dO, dST=None, *, chunk=64, dq=None, 
     dvv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    dq = _out(dq, (B, H, T, dkk), f32, dev)
-    dk = _out(dk, (B, H, T, dkk), f32, dev)
-    dv = _out(dv, (B, H, T, dvv), f32, dev)
-    dlog_decay = _out(dlog_decay, (B, H, T), f32, dev)
-    dbeta = _out(dbeta, (B, H, T), f32, dev)
-    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev)
+    dq = _out(dq, (B, H, T, dkk), f32, dev, stream)
+    dk = _out(dk, (B, H, T, dkk), f32, dev, stream)
+    dv = _out(dv, (B, H, T, dvv), f32, dev, stream)
+    dlog_decay = _out(dlog_decay, (B, H, T), f32, dev, stream)
+    dbeta = _out(dbeta, (B, H, T), f32, dev, stream)
+    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev, stream)
     need = delta_bwd_workspace_size(B, H, T, dkk, dvv, chunk)
     if ckpt is not None:  # no states in the workspace: the header and the partials only
         need = max(need - delta_ckpt_size(B, H, T, dkk, dvv, chunk), 256)
-    ws = _ws(need, dev, workspace)
+    ws = _ws(need, dev, workspace, stream)
     tk, tv, st, bht = (B, H, T, dkk), (B, H, T, dvv), (B, H, dkk, dvv), (B, H, T)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", bht), _T(beta, f32, "beta", bht), _T(S0, f32, "S0", st),
@@ -677,9 +703,9 @@ def gated_scan_fwd(x, rgate, igate, lam, h0=None, *, reset=None, lens=None, c=8.
     B, T, D = _dims(x, 3, "x")
     dev, dt, f32 = x.device, x.dtype, torch.float32
     code = _dtype_code(x, "x", _DTYPES)
-    h = _out(h, (B, T, D), dt, dev)
-    hT = _out(hT, (B, D), f32, dev)
-    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace)
+    h = _out(h, (B, T, D), dt, dev, stream)
+    hT = _out(hT, (B, D), f32, dev, stream)
+    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace, stream)
     bt, bd = (B, T, D), (B, D)
     _launch("cla_gated_scan_fwd", dev, (
         _T(x, dt, "x", bt), _T(rgate, dt, "rgate", bt), _T(igate, dt, "igate", bt), _T(lam, f32, "lam", (D,)),
@@ -697,10 +723,10 @@ def gated_scan_bwd(x, rgate, igate, lam, h0, dh, dhT=None, *, reset=None, lens=N
     dev, dt, f32 = x.device, x.dtype, torch.float32
     code = _dtype_code(x, "x", _DTYPES)
     bt, bd = (B, T, D), (B, D)
-    dx, drgate, digate = (_out(t, bt, dt, dev) for t in (dx, drgate, digate))
-    dlam = _out(dlam, (D,), f32, dev)
-    dh0 = _out(dh0, bd, f32, dev)
-    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace)
+    dx, drgate, digate = (_out(t, bt, dt, dev, stream) for t in (dx, drgate, digate))
+    dlam = _out(dlam, (D,), f32, dev, stream)
+    dh0 = _out(dh0, bd, f32, dev, stream)
+    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace, stream)
     _launch("cla_gated_scan_bwd", dev, (
         _T(x, dt, "x", bt), _T(rgate, dt, "rgate", bt), _T(igate, dt, "igate", bt), _T(lam, f32, "lam", (D,)),
         _T(h0, f32, "h0", bd), _reset_arg(reset, (B, T)), _T(lens, torch.int32, "lens", (B,)),
@@ -716,7 +742,7 @@ def gated_scan_step(x, rgate, igate, lam, h, *, reset=None, c=8.0, y=None, strea
     B, D = _dims(x, 2, "x")
     dt, dev, bd = x.dtype, x.device, (B, D)
     code = _dtype_code(x, "x", _DTYPES)
-    y = _out(y, bd, dt, dev)
+    y = _out(y, bd, dt, dev, stream)
     _launch("cla_gated_scan_step", dev, (
         _T(x, dt, "x", bd), _T(rgate, dt, "rgate", bd), _T(igate, dt, "igate", bd), _T(lam, torch.float32, "lam", (D,)),
         _reset_arg(reset, (B,)), _T(h, torch.float32, "h", bd), _T(y, dt, "y", bd), float(c), code, B, D), stream)
@@ -751,9 +777,9 @@ def window_attn_fwd(q, k, v, *, window, sinks=0, lens=None, scale=None, o=None, 
     Hkv = _dims(k, 4, "k")[1]
     dev, dt = q.device, q.dtype
     code = _dtype_code(q, "q", _HALF)
-    o = _out(o, (B, H, T, d), dt, dev)
-    lse = _out(lse, (B, H, T), torch.float32, dev)
-    ws = _ws(window_attn_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace)
+    o = _out(o, (B, H, T, d), dt, dev, stream)
+    lse = _out(lse, (B, H, T), torch.float32, dev, stream)
+    ws = _ws(window_attn_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace, stream)
     hs, ks = (B, H, T, d), (B, Hkv, T, d)
     _launch("cla_window_attn_fwd", dev, (
         _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True),
@@ -775,9 +801,9 @@ def window_attn_bwd(q, k, v, o, lse, dO, *, window, sinks=0, lens=None, scale=No
     dev, dt = q.device, q.dtype
     code = _dtype_code(q, "q", _HALF)
     hs, ks = (B, H, T, d), (B, Hkv, T, d)
-    dq = _out(dq, hs, dt, dev)
-    dk, dv = _out(dk, ks, dt, dev), _out(dv, ks, dt, dev)
-    ws = _ws(window_attn_bwd_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace)
+    dq = _out(dq, hs, dt, dev, stream)
+    dk, dv = _out(dk, ks, dt, dev, stream), _out(dv, ks, dt, dev, stream)
+    ws = _ws(window_attn_bwd_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace, stream)
     _launch("cla_window_attn_bwd", dev, (
         _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True),
         _T(lens, torch.int32, "lens", (B,)), _T(o, dt, "o", hs, True), _T(lse, torch.float32, "lse", (B, H, T)),
@@ -809,7 +835,7 @@ def window_attn_step(q, k, v, kcache, vcache, pos, *, window, sinks=0, scale=Non
     Hkv = _dims(k, 3, "k")[1]
     dev, dt = q.device, q.dtype
     code = _dtype_code(q, "q", _HALF)
-    o = _out(o, (B, H, d), dt, dev)
+    o = _out(o, (B, H, d), dt, dev, stream)
     cs = (B, Hkv, int(sinks) + int(window), d)
     _launch("cla_window_attn_step", dev, (
         _T(q, dt, "q", (B, H, d), True), _T(k, dt, "k", (B, Hkv, d), True), _T(v, dt, "v", (B, Hkv, d), True),
