@@ -36,7 +36,9 @@
 // between them, 451.
 //
 // Waits are bounded: one that gives up marks the block, which then waits no
-// more, and records the timeout in the workspace header.
+// more, and records the timeout in the workspace header.  Most last a step; those
+// for the end of a list or item, which may have any number of steps, give up only
+// when the block's loads have stopped moving too.
 #pragma once
 
 #include "mma_sync.cuh"
@@ -194,6 +196,27 @@ struct Waits {
         atomicOr(&hdr->error, kErrTimeout);
         atomicExch(&hdr->where, where);
     }
+    // For a list's or an item's end, which may be any number of steps away (2^24 polls are 24 s at the
+    // 1.4 us that a poll lasts where nothing wakes the warp): the bound begins anew whenever the loads'
+    // warp, which is a few steps ahead of the products at most, has moved.
+    __device__ __forceinline__ void end(volatile uint32_t *loads, uint32_t bar, uint32_t parity, unsigned int where) const {
+        if (!try_once(bar, parity & 1u)) slow_end(dead, loads, hdr, bar, parity & 1u, where);
+    }
+    // (its members as values: an object whose address is taken would lie in local memory)
+    __device__ __noinline__ static void slow_end(volatile uint32_t *dead, volatile uint32_t *loads, WsHeader *hdr, uint32_t bar,
+                                                 uint32_t parity, unsigned int where) {
+        uint32_t seen = *loads;
+        for (uint32_t it = 0; it < (1u << 24); ++it) {
+            if (try_once(bar, parity)) return;
+            if ((it & 255u) != 255u) continue;
+            if (*dead != 0u) return;
+            const uint32_t now = *loads;
+            if (now != seen) seen = now, it = 0u;
+        }
+        *dead = 1u;
+        atomicOr(&hdr->error, kErrTimeout);
+        atomicExch(&hdr->where, where);
+    }
 };
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -276,7 +299,8 @@ constexpr int kSmall = 2560;
 struct Small {
     uint64_t bars[40];
     uint32_t tmem, dead;
-    uint32_t pad[46];
+    uint32_t pad[45];
+    uint32_t loads;  // issued of the tiles that a step takes, for the long waits
     float f[512];
 };
 static_assert(sizeof(Small) == kSmall, "layout behind the tiles");
@@ -434,11 +458,12 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
         for (int i = 0; i < 6; ++i) mbar_init(p_ready + 8 * i, 8);  // and staged
         for (int i = 0; i < 2 * ST; ++i) mbar_init(kv_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        sm.dead = 0u;
+        sm.dead = sm.loads = 0u;
         if (blockIdx.x == 0) hdr->error = 0u, hdr->where = 0u;
     }
     const uint32_t tmem = tmem_alloc_all(&sm.tmem);
     const Waits wait{&sm.dead, hdr};
+    volatile uint32_t *loads = &sm.loads;
     const uint32_t tS = tmem, tO = tmem + 256;
 
     if (warp == 17) {
@@ -462,6 +487,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
                     if (*wait.dead != 0u) break;
                     mbar_expect_tx(kv_full + 8 * s, TB);
                     Tile<D>::load(skv + s * TB, (i & 1) ? &maps.v : &maps.k, kt.tile(i >> 1) * kWT, w.hk, w.b, kv_full + 8 * s);
+                    *loads = n + 1;
                 }
                 ++it;
             }
@@ -536,7 +562,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
                 if (kt.count == 0) continue;
                 for (int u = 0; u < 2; ++u)
                     if (u == 0 || kt.b.hi >= kt.b.lo) {
-                        wait(staged + 16 * u + 8 * (n[u] & 1), n[u] >> 1, 29);
+                        wait.end(loads, staged + 16 * u + 8 * (n[u] & 1), n[u] >> 1, 29);
                         ++n[u];
                         if (*wait.dead == 0u)
                             store_tile<D>(&maps.x, sq + (2 * (it & 1) + u) * TB, w.t0 + u * w.step_t, w.h + u * w.step_h, w.b);
@@ -708,11 +734,12 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
         mbar_init(x_empty, 1);
         for (int i = 0; i < 2 * (KST + VST); ++i) mbar_init(k_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        sm.dead = 0u;
+        sm.dead = sm.loads = 0u;
         if (blockIdx.x == 0) hdr->error = 0u, hdr->where = 0u;  // of the whole call
     }
     const uint32_t tmem = tmem_alloc_all(&sm.tmem);
     const Waits wait{&sm.dead, hdr};
+    volatile uint32_t *loads = &sm.loads;
     const uint32_t tS = tmem, tP = tmem + 256, tA = tmem + 384;
     // items: all heads of the last tile, then of the one before it (as in the forward)
     auto place = [&](int item, int &b, int &h, int &hk, int &t0) {
@@ -748,6 +775,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                     if (n >= VST) wait(v_empty + 8 * c, n / VST - 1, 33);
                     mbar_expect_tx(v_full + 8 * c, TB);
                     Tile<D>::load(sv + c * TB, &maps.v, s0, hk, b, v_full + 8 * c);
+                    *loads = n + 1;
                 }
                 ++it;
             }
@@ -813,7 +841,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
             last += kt.hi - kt.lo + 1 + min(kt.sinks, kt.lo);
             const uint32_t s = (last - 1) % KST;
             if (lane == 0) {
-                wait(staged, it, 43);
+                wait.end(loads, staged, it, 43);
                 if (*wait.dead == 0u) store_tile<D>(&maps.x, sk + s * TB, t0, h, b);
                 tma_store_wait_read();
                 mbar_arrive(x_empty);
@@ -849,7 +877,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
                     }
                 }
             }
-            if (all > 1) wait(st_empty + 8 * (all & 1), all / 2 - 1, 42);
+            if (all > 1) wait.end(loads, st_empty + 8 * (all & 1), all / 2 - 1, 42);
             float *dst = s_stat[all & 1][0], *dst2 = s_stat[all & 1][1];
 #pragma unroll
             for (int k = 0; k < 2; ++k) dst2[(warp - 18) * 64 + lane + 32 * k] = ls[k];
@@ -1143,10 +1171,11 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
         for (int i = 0; i < 2 * (QST + GST); ++i) mbar_init(q_full + 8 * i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(st_full + 8 * i, 1), mbar_init(st_empty + 8 * i, 16);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        sm.dead = 0u;
+        sm.dead = sm.loads = 0u;
     }
     const uint32_t tmem = tmem_alloc_all(&sm.tmem);
     const Waits wait{&sm.dead, hdr};
+    volatile uint32_t *loads = &sm.loads;
     const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
     Walk w(g, *reinterpret_cast<const Place *>(sm.pad), *reinterpret_cast<const long long *>(sm.pad + 4));
     // the head and the query tile of a step, without a division in the loops
@@ -1181,6 +1210,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
                     if (n >= GST) wait(g_empty + 8 * r, n / GST - 1, 43);
                     mbar_expect_tx(g_full + 8 * r, TB);
                     Tile<D>::load(sg + r * TB, &maps.g, x.qt * kWT, x.h, w.p.b, g_full + 8 * r);
+                    *loads = n + 1;
                 }
                 ++it;
             }
@@ -1224,7 +1254,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
             uint32_t it = 0;
             while (w.next()) {
                 for (int which = 0; which < 2; ++which) {
-                    wait(staged + 16 * which + 8 * (it & 1), it >> 1, 54);
+                    wait.end(loads, staged + 16 * which + 8 * (it & 1), it >> 1, 54);
                     if (w.i0 == 0 && w.i1 == w.list && *wait.dead == 0u)
                         store_tile<D>(which == 0 ? &maps.x : &maps.y, sk + (2 * (it % KVST) + which) * TB, w.p.tile * kWT, w.p.hk, w.p.b);
                 }

@@ -93,3 +93,27 @@ def test_gated_scan(cla):
     for name, y in (("h", h), ("dx", dx), ("drgate", dr), ("digate", di)):
         tail_within(name, y, ref[name], n // 2)
     R.assert_within("hT", hT, *ref["hT"])
+
+
+def test_list_of_a_million_steps(cla):
+    """One key head for 128 query heads: the list of the sinks' tile has 2^20 steps, over all of which its stores wait.
+    Queries, keys and values of 0 leave P = 1 / n_t (n_t: the keys that t sees) and dv_s = sum of dO_t / n_t over the
+    queries that see s."""
+    H, T, d, W = 128, 1 << 20, 64, 12800
+    zeros = torch.zeros(1, H, T, d, dtype=BF16, device="cuda")  # q and o
+    kv = torch.zeros(1, 1, T, d, dtype=BF16, device="cuda")
+    dO = torch.empty(1, H, T, d, dtype=BF16, device="cuda").uniform_(0.5, 1.5, generator=torch.Generator(device="cuda").manual_seed(1))
+    t = torch.arange(T, device="cuda")
+    seen = ((t + 1).clamp(max=W) + (t >= W)).double()
+    lse = seen.log().float().expand(1, H, T).contiguous()
+    ws = torch.empty(cla.window_attn_bwd_workspace_size(1, H, 1, T, d, W, 1), dtype=torch.uint8, device="cuda")
+    dq, dk, dv = cla.window_attn_bwd(zeros, kv, kv, zeros, lse, dO, window=W, sinks=1, workspace=ws)
+    cla.check_status(ws)
+    assert not dq.any() and not dk.any() and torch.isfinite(dv).all()
+    share = torch.stack([dO[0, :, :, c].sum(0, dtype=torch.float64) for c in range(d)], 1) / seen[:, None]
+    run = torch.cat([share.new_zeros(1, d), share.cumsum(0)])
+    want = run[(t + W).clamp(max=T)] - run[t]
+    # P: the log's and the exponential's roundings and half a step of bf16; fp32 sums of 101 x 128 steps of 8 products
+    # each, every one off by at most a step of the sum so far (all terms are positive); dv's own half step
+    bound = want * (1.01 * (2.0 ** -8 + 64 * 2.0 ** -24) + 101 * 128 * 8 * 2.0 ** -23 + 2.0 ** -8)
+    R.assert_within("dv", dv[0, 0, 1:], want[1:], bound[1:])
