@@ -100,6 +100,9 @@ extern "C" int cla_check_status(const void *ws, void *stream) {
     cla::WsHeader hdr;
     CLA_CUDA_TRY(cudaMemcpyAsync(&hdr, ws, sizeof(hdr), cudaMemcpyDeviceToHost, s), "cla_check_status: copy");
     CLA_CUDA_TRY(cudaStreamSynchronize(s), "cla_check_status: synchronize");
+    for (const unsigned char site : hdr.block)
+        if ((hdr.error & cla::kErrInBlocks) && site != 0)
+            return cla::fail(CLA_ERR_TIMEOUT, "a wait inside a block gave up (site %u)", (unsigned)site);
     if (hdr.error & cla::kErrTimeout)
         return cla::fail(CLA_ERR_TIMEOUT, "a cross-block wait gave up (site %u)", hdr.where);
     if (hdr.error & cla::kErrRange)

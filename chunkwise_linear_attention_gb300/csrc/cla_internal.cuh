@@ -49,12 +49,16 @@ inline bool aligned_or_null(std::initializer_list<const void *> ps, uintptr_t n)
 }
 
 // Every workspace starts with this header.  It is cleared (with the flag
-// arrays that follow it) by one cudaMemsetAsync at the start of each call.
+// arrays that follow it) by one cudaMemsetAsync at the start of each call, or
+// its status is written by the call's first kernel, whose blocks then leave
+// their timeouts in an entry of `block` each (kErrInBlocks).
+constexpr int kStatusBlocks = 160;
 struct WsHeader {
     unsigned int ticket[8];   // per-kernel atomic tickets: block order of start
-    unsigned int error;       // nonzero: a bounded wait gave up
+    unsigned int error;       // kErr* bits
     unsigned int where;       // which wait gave up (debug aid)
-    unsigned int pad[54];
+    unsigned int pad[14];
+    unsigned char block[kStatusBlocks];  // nonzero: that block gave up the wait of this number
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
@@ -62,6 +66,8 @@ constexpr unsigned int kErrTimeout = 1u;
 // An input outside what a kernel handles was met on the device (data the host
 // cannot check without a synchronisation); the results are not valid.
 constexpr unsigned int kErrRange = 2u;
+// Not an error: timeouts of this call stand in `block`.
+constexpr unsigned int kErrInBlocks = 4u;
 
 // Bound on polls of one flag (each poll after the first few sleeps ~100 ns):
 // about a second before a block gives up, far beyond any legitimate wait.

@@ -87,6 +87,7 @@ WaArgs wa_args(const int32_t *lens, float scale, int64_t T, int64_t window, int6
 int wa_blocks(const char *fn, long long items, unsigned *blocks) {
     int n = 0;
     if (int st = multiprocessors(fn, &n)) return st;
+    n = n < kStatusBlocks ? n : kStatusBlocks;
     *blocks = (unsigned)(items < n ? items : n);
     return CLA_OK;
 }

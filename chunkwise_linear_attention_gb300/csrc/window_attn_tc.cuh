@@ -36,9 +36,9 @@
 // between them, 451.
 //
 // Waits are bounded: one that gives up marks the block, which then waits no
-// more, and records the timeout in the workspace header.  Most last a step; those
-// for the end of a list or item, which may have any number of steps, give up only
-// when the block's loads have stopped moving too.
+// more, and records the timeout in the block's entry of the workspace header.
+// Most last a step; those for the end of a list or item, which may have any
+// number of steps, give up only when the block's loads have stopped moving too.
 #pragma once
 
 #include "mma_sync.cuh"
@@ -172,8 +172,7 @@ __device__ __forceinline__ void mma16x8(float (&c)[4], uint32_t a0, uint32_t a1,
 
 // The waits of a block: once one has given up none waits long any more.
 struct Waits {
-    volatile uint32_t *dead;
-    WsHeader *hdr;
+    volatile uint32_t *dead;  // 0, or the wait that gave up
     __device__ __forceinline__ static bool try_once(uint32_t bar, uint32_t parity) {
         uint32_t done;
         asm volatile(
@@ -192,18 +191,16 @@ struct Waits {
             if (try_once(bar, parity)) return;
             if ((it & 255u) == 255u && *dead != 0u) return;
         }
-        *dead = 1u;
-        atomicOr(&hdr->error, kErrTimeout);
-        atomicExch(&hdr->where, where);
+        *dead = where;
     }
     // For a list's or an item's end, which may be any number of steps away (2^24 polls are 24 s at the
     // 1.4 us that a poll lasts where nothing wakes the warp): the bound begins anew whenever the loads'
     // warp, which is a few steps ahead of the products at most, has moved.
     __device__ __forceinline__ void end(volatile uint32_t *loads, uint32_t bar, uint32_t parity, unsigned int where) const {
-        if (!try_once(bar, parity & 1u)) slow_end(dead, loads, hdr, bar, parity & 1u, where);
+        if (!try_once(bar, parity & 1u)) slow_end(dead, loads, bar, parity & 1u, where);
     }
     // (its members as values: an object whose address is taken would lie in local memory)
-    __device__ __noinline__ static void slow_end(volatile uint32_t *dead, volatile uint32_t *loads, WsHeader *hdr, uint32_t bar,
+    __device__ __noinline__ static void slow_end(volatile uint32_t *dead, volatile uint32_t *loads, uint32_t bar,
                                                  uint32_t parity, unsigned int where) {
         uint32_t seen = *loads;
         for (uint32_t it = 0; it < (1u << 24); ++it) {
@@ -213,9 +210,7 @@ struct Waits {
             const uint32_t now = *loads;
             if (now != seen) seen = now, it = 0u;
         }
-        *dead = 1u;
-        atomicOr(&hdr->error, kErrTimeout);
-        atomicExch(&hdr->where, where);
+        *dead = where;
     }
 };
 
@@ -306,8 +301,18 @@ struct Small {
 static_assert(sizeof(Small) == kSmall, "layout behind the tiles");
 __device__ __forceinline__ bool misplaced(uint32_t base, WsHeader *hdr) {
     if ((base & 1023u) == 0u) return false;
-    if (threadIdx.x == 0) atomicOr(&hdr->error, kErrTimeout);
+    if (threadIdx.x == 0) hdr->error = kErrTimeout, hdr->where = 1u;  // in every block
     return true;
+}
+// The call's status, by all threads at a kernel's end: each block's entry says which wait gave up (0:
+// none).  The call's first kernel writes every entry, block 0 those that have no block, so that nothing
+// has to be cleared before it; a later kernel adds to them.
+template <bool FIRST>
+__device__ __forceinline__ void leave_status(WsHeader *hdr, const Small &sm) {
+    if (threadIdx.x == 0 && (FIRST || sm.dead != 0u)) hdr->block[blockIdx.x] = (unsigned char)sm.dead;
+    if (!FIRST || blockIdx.x != 0) return;
+    if (threadIdx.x == 0) hdr->error = kErrInBlocks, hdr->where = 0u;
+    if (threadIdx.x >= gridDim.x && threadIdx.x < kStatusBlocks) hdr->block[threadIdx.x] = 0;
 }
 // Between the N warps that share a lane quarter, and so their rows.
 template <int N>
@@ -459,10 +464,9 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
         for (int i = 0; i < 2 * ST; ++i) mbar_init(kv_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = sm.loads = 0u;
-        if (blockIdx.x == 0) hdr->error = 0u, hdr->where = 0u;
     }
     const uint32_t tmem = tmem_alloc_all(&sm.tmem);
-    const Waits wait{&sm.dead, hdr};
+    const Waits wait{&sm.dead};
     volatile uint32_t *loads = &sm.loads;
     const uint32_t tS = tmem, tO = tmem + 256;
 
@@ -689,6 +693,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
         }
     }
     tmem_free_all(tmem);
+    leave_status<true>(hdr, sm);
 }
 
 // ------------------------------------------------------------------ backward: dq (and delta)
@@ -735,10 +740,9 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
         for (int i = 0; i < 2 * (KST + VST); ++i) mbar_init(k_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = sm.loads = 0u;
-        if (blockIdx.x == 0) hdr->error = 0u, hdr->where = 0u;  // of the whole call
     }
     const uint32_t tmem = tmem_alloc_all(&sm.tmem);
-    const Waits wait{&sm.dead, hdr};
+    const Waits wait{&sm.dead};
     volatile uint32_t *loads = &sm.loads;
     const uint32_t tS = tmem, tP = tmem + 256, tA = tmem + 384;
     // items: all heads of the last tile, then of the one before it (as in the forward)
@@ -987,6 +991,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
         }
     }
     tmem_free_all(tmem);
+    leave_status<true>(hdr, sm);
 }
 
 // ------------------------------------------------------------------ backward: dk, dv
@@ -1174,7 +1179,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
         sm.dead = sm.loads = 0u;
     }
     const uint32_t tmem = tmem_alloc_all(&sm.tmem);
-    const Waits wait{&sm.dead, hdr};
+    const Waits wait{&sm.dead};
     volatile uint32_t *loads = &sm.loads;
     const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
     Walk w(g, *reinterpret_cast<const Place *>(sm.pad), *reinterpret_cast<const long long *>(sm.pad + 4));
@@ -1437,6 +1442,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
         }
     }
     tmem_free_all(tmem);
+    leave_status<false>(hdr, sm);
 }
 
 // Adds the parts of a list that was cut, in their order: block (x, y) those of the list that block x

@@ -26,7 +26,7 @@
  *  - Errors: argument and shape errors are detected before anything is
  *    enqueued and return CLA_ERR_INVALID_ARG / CLA_ERR_UNSUPPORTED /
  *    CLA_ERR_WORKSPACE; a failed launch returns CLA_ERR_CUDA.  The kernels
- *    never trap: a cross-block wait that exceeds its iteration bound records
+ *    never trap: a wait that exceeds its iteration bound records
  *    a flag in the workspace and the block carries on; cla_check_status()
  *    reports it as CLA_ERR_TIMEOUT.  cla_last_error_message() gives a
  *    one-line description of the last failure on the calling host thread.
@@ -51,7 +51,7 @@ typedef enum {
     CLA_ERR_INVALID_ARG = 1, /* null required pointer, negative size, misalignment */
     CLA_ERR_UNSUPPORTED = 2, /* a size or head dimension this build has no kernel for */
     CLA_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed */
-    CLA_ERR_TIMEOUT = 4,     /* a bounded cross-block wait gave up (see cla_check_status) */
+    CLA_ERR_TIMEOUT = 4,     /* a bounded wait gave up (see cla_check_status) */
     CLA_ERR_WORKSPACE = 5    /* ws is NULL, unaligned or smaller than required */
 } cla_status;
 
@@ -62,7 +62,7 @@ const char *cla_status_string(int status);
 const char *cla_last_error_message(void);
 
 /* Synchronises `stream`, then reports CLA_ERR_TIMEOUT if a kernel of the last
- * call that used `ws` gave up a cross-block wait, CLA_ERR_UNSUPPORTED if it
+ * call that used `ws` gave up a wait, CLA_ERR_UNSUPPORTED if it
  * met data outside its range (cla_gla_fwd's decay bound), CLA_ERR_CUDA if the
  * stream holds an error, else CLA_OK.  `ws` must be the workspace of that
  * call. */

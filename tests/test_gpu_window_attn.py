@@ -270,3 +270,28 @@ def test_step_in_a_graph(cla):
         pos += 1
         q.copy_(rnd(B, H, d)), k.copy_(rnd(B, K, d)), v.copy_(rnd(B, K, d))
     assert torch.equal(kc, k1) and torch.equal(vc, v1)
+
+
+# ------------------------------------------------------------------ status
+def test_status_of_a_call(cla):
+    """Each block of the attention's kernels records a timeout in an entry of its own behind the header's words: a call
+    clears them all, whatever the workspace held and however few its blocks are, and check_status reads them."""
+    q, k, v, dO = inputs(1, 2, 1, 100, 64, BF16)
+    kw = dict(window=30, sinks=2)
+    n = cla.window_attn_bwd_workspace_size(1, 2, 1, 100, 64, 30, 2)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    o, lse = cla.window_attn_fwd(q, k, v, **kw)
+    for call in (lambda: cla.window_attn_fwd(q, k, v, workspace=ws, **kw),
+                 lambda: cla.window_attn_bwd(q, k, v, o, lse, dO, workspace=ws, **kw)):
+        for at in (96, 97, 96 + 151, 255):  # an entry, of a block that ran or of one that did not
+            ws.fill_(255)
+            call()
+            cla.check_status(ws)
+            ws[at] = 27
+            with pytest.raises(cla.ClaError, match="site 27"):
+                cla.check_status(ws)
+    # calls that record elsewhere do not read what an earlier call's blocks left there
+    a = torch.rand(1, 50, 8, device="cuda")
+    big = torch.full((max(cla.scan_diag_workspace_size(1, 50, 8), 256),), 255, dtype=torch.uint8, device="cuda")
+    cla.scan_diag_fwd(a, a, workspace=big)
+    cla.check_status(big)
