@@ -291,8 +291,9 @@ __device__ __forceinline__ void tmem_free_all(uint32_t tmem) {
 // static shared memory, so that the tiles start on the 1024 bytes that the swizzle needs; a base
 // that did not is reported, not used.
 constexpr int kSmall = 2560;
+constexpr int kLast = 39;  // the barrier of products_done
 struct Small {
-    uint64_t bars[40];
+    uint64_t bars[kLast + 1];
     uint32_t tmem, dead;
     uint32_t pad[45];
     uint32_t loads;  // issued of the tiles that a step takes, for the long waits
@@ -313,6 +314,12 @@ __device__ __forceinline__ void leave_status(WsHeader *hdr, const Small &sm) {
     if (!FIRST || blockIdx.x != 0) return;
     if (threadIdx.x == 0) hdr->error = kErrInBlocks, hdr->where = 0u;
     if (threadIdx.x >= gridDim.x && threadIdx.x < kStatusBlocks) hdr->block[threadIdx.x] = 0;
+}
+// By the warp that issues the products, in the end: none is in flight when tensor memory is given back.
+// (The math warps have waited for the last of them, unless a wait was given up.)
+__device__ __forceinline__ void products_done(uint32_t lead, uint32_t bars) {
+    mma_commit(lead, bars + 8 * kLast);
+    (void)mbar_wait(bars + 8 * kLast, 0u);
 }
 // Between the N warps that share a lane quarter, and so their rows.
 template <int N>
@@ -451,7 +458,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sq = smem_u32(smem_raw), skv = sq + 4 * TB;
     Small &sm = *reinterpret_cast<Small *>(smem_raw + (4 + ST) * TB);
-    static_assert(2 * ST + 14 <= 40, "barriers");
+    static_assert(2 * ST + 14 <= kLast, "barriers");
     float(*s_row)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [tile][half][row]: maxima, in the end sums
     if (misplaced(sq, hdr)) return;
     const int warp = threadIdx.x >> 5, tiles = (g.T + kWT - 1) / kWT;
@@ -462,6 +469,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
         for (int i = 0; i < 8; ++i) mbar_init(b0 + 8 * i, 1);
         for (int i = 0; i < 6; ++i) mbar_init(p_ready + 8 * i, 8);  // and staged
         for (int i = 0; i < 2 * ST; ++i) mbar_init(kv_full + 8 * i, 1);
+        mbar_init(b0 + 8 * kLast, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = sm.loads = 0u;
     }
@@ -556,6 +564,7 @@ wa_fwd_kernel(const __grid_constant__ WaMaps maps, void *__restrict__ o, float *
         bool got = false;
         settle(0, got);
         settle(1, got);
+        products_done(lead, b0);
     } else if (warp == 18) {
         // ------------------------------------------------------------ stores, which give the query tiles back
         if ((threadIdx.x & 31) == 0) {
@@ -723,7 +732,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sq = smem_u32(smem_raw), sk = sq + 2 * QST * TB, sv = sk + KST * TB;  // q, dO in turn
     Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 * QST + KST + VST) * TB);
-    static_assert(15 + 2 * (KST + VST) <= 40, "barriers");
+    static_assert(15 + 2 * (KST + VST) <= kLast, "barriers");
     float(*s_stat)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [item's parity][delta, lse log2 e][row]
     if (misplaced(sq, hdr)) return;
     const int warp = threadIdx.x >> 5, tiles = (g.T + kWT - 1) / kWT;
@@ -738,6 +747,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
         mbar_init(staged, 16);
         mbar_init(x_empty, 1);
         for (int i = 0; i < 2 * (KST + VST); ++i) mbar_init(k_full + 8 * i, 1);
+        mbar_init(b0 + 8 * kLast, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = sm.loads = 0u;
     }
@@ -828,6 +838,7 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
             mma_commit(lead, acc_full);
             ++it;
         }
+        products_done(lead, b0);
     } else if (warp >= 18) {
         // ------------------------------------------------------------ delta = dO . o and lse of the next item's rows
         // A warp takes 64 rows; the second of them also stores dq, of the item before the one whose
@@ -1150,7 +1161,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sk = smem_u32(smem_raw), sq = sk + 2 * KVST * TB, sg = sq + QST * TB;  // k, v in turn
     Small &sm = *reinterpret_cast<Small *>(smem_raw + (2 * KVST + QST + GST) * TB);
-    static_assert(17 + 2 * (QST + GST) + 4 <= 40, "barriers");
+    static_assert(17 + 2 * (QST + GST) + 4 <= kLast, "barriers");
     static_assert(QST >= 3 && GST >= 2, "stages");
     float(*s_stat)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [slot][lse log2 e, delta][query]
     if (misplaced(sk, hdr)) return;
@@ -1175,6 +1186,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
         for (int i = 0; i < 8; ++i) mbar_init(p_ready + 8 * i, 8);  // ds_ready and staged too
         for (int i = 0; i < 2 * (QST + GST); ++i) mbar_init(q_full + 8 * i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(st_full + 8 * i, 1), mbar_init(st_empty + 8 * i, 16);
+        mbar_init(b0 + 8 * kLast, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.dead = sm.loads = 0u;
     }
@@ -1332,6 +1344,7 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
             mma_commit(lead, acc_full);
             ++it;
         }
+        products_done(lead, b0);
     } else {
         const int part = warp >> 2, quarter = warp & 3, row = quarter * 32 + (threadIdx.x & 31);  // queries 32 part ..
         const uint32_t lanes = (uint32_t)quarter << 21;
