@@ -230,22 +230,29 @@ __device__ __forceinline__ void stf4(float *p, const float2 (&v)[2], int n) {
     if (n > 3) p[3] = v[1].y;
 }
 
-// (A, B) after (pa, pb): B <- A pb + B, A <- A pa.  RST: a decay of exactly 0 (a reset; no other
-// decay is below 2^-126) drops what came before, NaN and infinity included.
-template <bool RST>
+// A reset's decay is -0: no other is negative, so a product of decays is -0 where a reset is among
+// them (two of them are kept apart below) and +0 only where decays ran out of range.
+// One step's decay (ONE) is at least 2^-126 otherwise, and a plain comparison tells.
+template <bool ONE>
+__device__ __forceinline__ bool is_reset(float a) { return ONE ? a == 0.f : __float_as_uint(a) == 0x80000000u; }
+constexpr float kReset = -0.0f;
+
+// (A, B) after (pa, pb): B <- A pb + B, A <- A pa.  RST: behind a reset, what came before it is
+// dropped, NaN and infinity included; a product that only underflowed drops neither.
+template <bool RST, bool ONE = false>
 __device__ __forceinline__ void after(float2 &A, float2 &B, float2 pa, float2 pb) {
     if constexpr (RST) {
-        if (A.x == 0.f) pa.x = pb.x = 0.f;
-        if (A.y == 0.f) pa.y = pb.y = 0.f;
+        if (is_reset<ONE>(A.x)) pa.x = pb.x = 0.f;
+        if (is_reset<ONE>(A.y)) pa.y = pb.y = 0.f;
     }
     B = fma2(A, pb, B);
     A = mul2(A, pa);
 }
-template <bool RST>
+template <bool RST, bool ONE = false>
 __device__ __forceinline__ float2 apply(float2 A, float2 s, float2 B) {
     if constexpr (RST) {
-        if (A.x == 0.f) s.x = 0.f;
-        if (A.y == 0.f) s.y = 0.f;
+        if (is_reset<ONE>(A.x)) s.x = 0.f;
+        if (is_reset<ONE>(A.y)) s.y = 0.f;
     }
     return fma2(A, s, B);
 }
@@ -273,15 +280,18 @@ __device__ __forceinline__ void scan_runs(float2 (&A)[2], float2 (&B)[2], int su
 }
 
 // Published values: 32-bit words, 0 until written (the launch clears them); +0.0 goes out as
-// -0.0.  Each element of a 16-byte relaxed access is single-copy atomic: a reader that sees a
+// -0.0, of a decay, where that is a reset, as the smallest number.  Each element of a 16-byte relaxed access is single-copy atomic: a reader that sees a
 // nonzero word sees the value, without fences.
 __device__ __forceinline__ unsigned int pub(float v) {
     const unsigned int b = __float_as_uint(v);
     return b != 0u ? b : 0x80000000u;
 }
+__device__ __forceinline__ unsigned int pub_decay(float v) { return max(__float_as_uint(v), 1u); }
+template <bool DECAY>
 __device__ __forceinline__ void publish4(unsigned int *p, const float2 (&v)[2]) {
-    asm volatile("st.relaxed.gpu.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(pub(v[0].x)), "r"(pub(v[0].y)),
-                 "r"(pub(v[1].x)), "r"(pub(v[1].y))
+    auto word = [](float x) { return DECAY ? pub_decay(x) : pub(x); };
+    asm volatile("st.relaxed.gpu.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(word(v[0].x)), "r"(word(v[0].y)),
+                 "r"(word(v[1].x)), "r"(word(v[1].y))
                  : "memory");
 }
 __device__ __forceinline__ bool peek4(const unsigned int *p, float2 (&v)[2]) {
@@ -327,8 +337,8 @@ __device__ __forceinline__ void carry_in(const GsWords &w, int idx, int chunks, 
     const bool last_of_group = n == kGsGroup - 1, more = idx + 1 < chunks && sub == 0;
     if (more && !last_of_group) {
         unsigned int *p = w.pairs + (((size_t)idx * per + rem) * 4 + cg) * 8;
-        publish4(p, A);
-        publish4(p + 4, B);
+        publish4<true>(p, A);
+        publish4<false>(p + 4, B);
     }
     float2 PA[2] = {f2(1.f), f2(1.f)}, PB[2] = {f2(0.f), f2(0.f)}, S[2] = {s0[0], s0[1]};
     wait_words(sub < n ? w.pairs + (((size_t)(first + sub) * per + rem) * 4 + cg) * 8 : nullptr, PA, PB,
@@ -346,7 +356,7 @@ __device__ __forceinline__ void carry_in(const GsWords &w, int idx, int chunks, 
     for (int v = 0; v < 2; ++v) s[v] = apply<RST>(PA[v], S[v], PB[v]);
     if (more && last_of_group) {
         const float2 e[2] = {apply<RST>(A[0], s[0], B[0]), apply<RST>(A[1], s[1], B[1])};
-        publish4(w.states + (((size_t)(idx / kGsGroup) * per + rem) * 4 + cg) * 4, e);
+        publish4<false>(w.states + (((size_t)(idx / kGsGroup) * per + rem) * 4 + cg) * 4, e);
     }
 }
 
@@ -491,7 +501,7 @@ gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
             u[j][v] = mul2(mul2(e.m, e.i), xv[v]);
             if constexpr (RST)
                 if (j < q.n && rs[j]) {
-                    a[j][v] = f2(0.f);
+                    a[j][v] = f2(kReset);
                     u[j][v] = mul2(e.i, xv[v]);
                 }
         }
@@ -508,7 +518,7 @@ gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
             const float2 pa = A[v], pb = B[v];
             A[v] = a[j][v];
             B[v] = u[j][v];
-            after<RST>(A[v], B[v], pa, pb);
+            after<RST, true>(A[v], B[v], pa, pb);
         }
     scan_runs<RST, false>(A, B, sub);
     float2 Ax[2], Bx[2], s[2];
@@ -527,7 +537,7 @@ gated_fwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
 #pragma unroll
     for (int j = 0; j < L; ++j) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) s[v] = apply<RST>(a[j][v], s[v], u[j][v]);
+        for (int v = 0; v < 2; ++v) s[v] = apply<RST, true>(a[j][v], s[v], u[j][v]);
         if (j < q.rows && h != nullptr) {
             float2 z[2] = {s[0], s[1]};
             if (!full && j >= q.n) z[0] = z[1] = f2(0.f);
@@ -593,7 +603,7 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
             mi[j][v] = mul2(e.m, e.i);
             if constexpr (RST)
                 if (j < q.n && rs[j])
-                    a[j][v] = La[j][v] = w2[j][v] = f2(0.f), mi[j][v] = e.i;
+                    a[j][v] = f2(kReset), La[j][v] = w2[j][v] = f2(0.f), mi[j][v] = e.i;
             xi[j][v] = mul2(xv[v], e.i1);
             hp[j][v] = mul2(mi[j][v], xv[v]);
         }
@@ -615,7 +625,7 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
             const float2 pa = A[v], pb = B[v];
             A[v] = a[j][v];
             B[v] = hp[j][v];
-            after<RST>(A[v], B[v], pa, pb);
+            after<RST, true>(A[v], B[v], pa, pb);
         }
     scan_runs<RST, false>(A, B, sub);
     auto grad = [&](int j, float2 (&v)[2]) {  // dh_t of the run's step j
@@ -628,7 +638,7 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
         if (sub > 0) hs[v] = apply<RST>(pa, hs[v], pb);
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            const float2 next = apply<RST>(a[j][v], hs[v], hp[j][v]);
+            const float2 next = apply<RST, true>(a[j][v], hs[v], hp[j][v]);
             hp[j][v] = hs[v];
             hs[v] = next;
         }
@@ -643,8 +653,8 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
         for (int v = 0; v < 2; ++v) {
             const float2 pa = A[v], pb = B[v];
             A[v] = a[j][v];
-            B[v] = apply<RST>(a[j][v], gd[v], f2(0.f));
-            after<RST>(A[v], B[v], pa, pb);
+            B[v] = apply<RST, true>(a[j][v], gd[v], f2(0.f));
+            after<RST, true>(A[v], B[v], pa, pb);
         }
     }
     scan_runs<RST, true>(A, B, sub);
@@ -666,10 +676,10 @@ gated_bwd_kernel(const E *__restrict__ x, const E *__restrict__ rg, const E *__r
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
             const float2 hb = add2(gd[v], s[v]);
-            s[v] = apply<RST>(a[j][v], hb, f2(0.f));
+            s[v] = apply<RST, true>(a[j][v], hb, f2(0.f));
             float2 before = hp[j][v];
             if constexpr (RST)
-                if (a[j][v].x == 0.f) before = f2(0.f);  // a reset is one of all channels
+                if (is_reset<true>(a[j][v].x)) before = f2(0.f);  // a reset is one of all channels
             const float2 G = mul2(mul2(hb, La[j][v]), fma2(w2[j][v], f2(-1.f), before));
             sum[v] = add2(sum[v], G);
             ox[v] = mul2(hb, mi[j][v]);

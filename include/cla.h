@@ -606,6 +606,8 @@ size_t cla_gated_scan_workspace_size(int64_t B, int64_t T, int64_t D);
  *   reset  [B, T] bytes [opt]: nonzero starts afresh there, h_t = i_t x_t (the
  *          first token of each document of a packed sequence).  Nothing before
  *          it reaches the states from it on, infinities and NaN included.
+ *          Without one, a state that is not finite stays so (an infinity may
+ *          become NaN).
  *   lens   [B]    int32 [opt]: tokens of each sequence of a right-padded batch
  *          (clamped to [0, T]); behind them h is 0, the state is kept and the
  *          inputs are not used

@@ -233,3 +233,29 @@ def test_in_a_graph_and_on_a_stream(cla):
         want = cla.gated_scan_fwd(*(t2[n] for n in names)) + cla.gated_scan_bwd(*(t2[n] for n in names), dh, dhT)
         for x, y in zip(outs[0] + outs[1], want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_only_a_reset_drops_what_is_not_finite(cla, dtype):
+    """Decays whose product underflows carry a NaN or an infinity on, with a reset mask as without one, as far as the next
+    reset and no further; in the gradients' direction too."""
+    t, dh, dhT = inputs(2, 700, 16, dtype)
+    t["lam"] = torch.zeros(16, device="cuda")  # open gates leave e^-5.5 a step: 20 steps are below the smallest float
+    t["rgate"] = t["rgate"] + 2
+    names = ("x", "rgate", "igate", "lam", "h0")
+    reset = torch.zeros(2, 700, dtype=torch.bool)
+    reset[0, 500] = True
+    bad = dict(t, x=t["x"].clone())
+    bad["x"][:, 5, ::2], bad["x"][:, 5, 1::2] = float("nan"), float("inf")
+    good = cla.gated_scan_fwd(*(t[n] for n in names), reset=reset.cuda())
+    h, hT = cla.gated_scan_fwd(*(bad[n] for n in names), reset=reset.cuda())
+    assert not torch.isfinite(h[0, 5:500]).any() and not torch.isfinite(h[1, 5:]).any() and not torch.isfinite(hT[1]).any()
+    assert torch.equal(h[0, 500:], good[0][0, 500:]) and torch.equal(hT[0], good[1][0]) and torch.equal(h[:, :5], good[0][:, :5])
+    bdh = dh.clone()
+    bdh[:, 690, ::2], bdh[:, 690, 1::2] = float("nan"), float("inf")
+    want = cla.gated_scan_bwd(*(t[n] for n in names), dh, dhT, reset=reset.cuda())
+    got = cla.gated_scan_bwd(*(t[n] for n in names), bdh, dhT, reset=reset.cuda())
+    assert not torch.isfinite(got[0][0, 500:691]).any() and not torch.isfinite(got[0][1, :691]).any()
+    assert not torch.isfinite(got[4][1]).any() and torch.equal(got[4][0], want[4][0])
+    for x, y in zip(got[:3], want[:3]):
+        assert torch.equal(x[0, :500], y[0, :500]) and torch.equal(x[:, 691:], y[:, 691:])
