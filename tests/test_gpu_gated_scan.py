@@ -259,3 +259,47 @@ def test_only_a_reset_drops_what_is_not_finite(cla, dtype):
     assert not torch.isfinite(got[4][1]).any() and torch.equal(got[4][0], want[4][0])
     for x, y in zip(got[:3], want[:3]):
         assert torch.equal(x[0, :500], y[0, :500]) and torch.equal(x[:, 691:], y[:, 691:])
+
+
+@pytest.mark.parametrize("B,D", [(97, 40), (120, 33), (128, 64), (306, 5120), (700, 5120), (300, 3000)])
+def test_rows_of_dlam(cla, B, D):
+    """Every sequence of two steps leaves a row for dlam: up to 128 are added in one step, more in shares whose rows are
+    taken 128 at a time (5120 channels: two shares, 153 and 350 rows; 3000: four, of 75)."""
+    t, dh, dhT = inputs(B, 2, D, F32)
+    ref = R.gated(t["x"], t["rgate"], t["igate"], t["lam"], t["h0"], None, None, 8.0, dh, dhT)
+    got = cla.gated_scan_bwd(t["x"], t["rgate"], t["igate"], t["lam"], t["h0"], dh, dhT)
+    R.assert_within("dlam", got[3], *ref["dlam"])
+    R.assert_within("dh0", got[4], *ref["dh0"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("which", ["inputs", "outputs", "all"])
+def test_odd_addresses(cla, dtype, off, which):
+    """Rows of a multiple of four channels at addresses that are not one of four elements; what lies around the outputs
+    stays as it was."""
+    B, T, D = 2, 150, 36
+    t, dh, dhT = inputs(B, T, D, dtype)
+    bufs = []
+
+    def moved(v, now):
+        buf = torch.full((v.numel() + 16,), 7.0, dtype=v.dtype, device="cuda")
+        at = off if now else 8
+        view = buf[at:at + v.numel()].view(v.shape)
+        view.copy_(v)
+        bufs.append((buf, at, v.numel()))
+        return view
+
+    x, r, i, g = (moved(v, which != "outputs") for v in (t["x"], t["rgate"], t["igate"], dh))
+    h, dx, dr, di = (moved(torch.zeros_like(t["x"]), which != "inputs") for _ in range(4))
+    ck = cla.gated_scan_ckpt(x)
+    reset = torch.zeros(B, T, dtype=torch.bool)
+    reset[1, 70] = True
+    for rs in (None, reset.cuda()):
+        ref = R.gated(t["x"], t["rgate"], t["igate"], t["lam"], t["h0"], rs, None, 8.0, dh, dhT)
+        _, hT = cla.gated_scan_fwd(x, r, i, t["lam"], t["h0"], reset=rs, h=h, ckpt=ck)
+        _, _, _, dlam, dh0 = cla.gated_scan_bwd(x, r, i, t["lam"], t["h0"], g, dhT, reset=rs, dx=dx, drgate=dr, digate=di, ckpt=ck)
+        for n, v in dict(h=h, hT=hT, dx=dx, drgate=dr, digate=di, dlam=dlam, dh0=dh0).items():
+            R.assert_within(n, v, *ref[n])
+        for buf, at, n in bufs:
+            assert bool((buf[:at] == 7).all()) and bool((buf[at + n:] == 7).all())

@@ -117,3 +117,31 @@ def test_list_of_a_million_steps(cla):
     # each, every one off by at most a step of the sum so far (all terms are positive); dv's own half step
     bound = want * (1.01 * (2.0 ** -8 + 64 * 2.0 ** -24) + 101 * 128 * 8 * 2.0 ** -23 + 2.0 ** -8)
     R.assert_within("dv", dv[0, 0, 1:], want[1:], bound[1:])
+
+
+def test_gated_scan_sums(cla):
+    """dlam, whose terms come from more than 2^31 elements, and dh0: resets every 1024 tokens make the documents
+    independent, so that the 64-bit form takes four channels of them as a batch."""
+    T, D, n, C = (1 << 20) + 77, 2048, 1024, 4
+    x, r, i, dh = rnd(1, 1, T, D), rnd(2, 1, T, D, std=1.5), rnd(3, 1, T, D, std=1.5), rnd(4, 1, T, D)
+    lam = torch.linspace(-8, 0, D, device="cuda").roll(D // 2 - 2)
+    h0 = torch.ones(1, D, device="cuda")
+    reset = torch.zeros(1, T, dtype=torch.bool, device="cuda")
+    reset[:, n::n] = True
+    at = D // 2 - 4  # channels at the ends and the middle of lam's range
+    _, _, _, dlam, dh0 = cla.gated_scan_bwd(x, r, i, lam, h0, dh, reset=reset)
+    docs = (T + n - 1) // n
+
+    def cut(v):
+        v = torch.nn.functional.pad(v[0, :, at:at + C], (0, 0, 0, docs * n - T))
+        return v.reshape(docs, n, C).contiguous()
+
+    first = torch.zeros(docs, n, dtype=torch.bool)
+    first[1:, 0] = True
+    h = torch.zeros(docs, C)
+    h[0] = 1.0
+    lens = torch.full((docs,), n)
+    lens[-1] = T - (docs - 1) * n
+    ref = R.gated(cut(x), cut(r), cut(i), lam[at:at + C], h, first, lens, dh=cut(dh))
+    R.assert_within("dlam", dlam[at:at + C], *ref["dlam"])
+    R.assert_within("dh0", dh0[0, at:at + C], ref["dh0"][0][0], ref["dh0"][1][0])

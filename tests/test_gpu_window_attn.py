@@ -295,3 +295,37 @@ def test_status_of_a_call(cla):
     big = torch.full((max(cla.scan_diag_workspace_size(1, 50, 8), 256),), 255, dtype=torch.uint8, device="cuda")
     cla.scan_diag_fwd(a, a, workspace=big)
     cla.check_status(big)
+
+
+# ------------------------------------------------------------------ more items than blocks
+@pytest.mark.parametrize("dtype,ragged,H,K,d", [(BF16, False, 8, 2, 128), (F16, True, 8, 2, 128), (BF16, True, 6, 2, 128),
+                                                (F16, False, 8, 2, 64)])
+def test_more_items_than_blocks(cla, dtype, ragged, H, K, d):
+    """Blocks that take several items and lists one after the other (stages and parities in use again), every output
+    compared: 4 sequences of 11 tiles."""
+    lens = torch.tensor([1300, 700, 0, 1291], dtype=torch.int32).cuda() if ragged else None
+    check(cla, *inputs(4, H, K, 1300, d, dtype, 7), 300, 5, lens)
+
+
+def test_lse_against_differences(cla):
+    """Central differences of the kernel's own lse along q: with v = k, o is sum P k, and d lse = scale o . dq."""
+    q, k, _, _ = inputs(1, 4, 2, 200, 64, F16)
+    w = torch.randn(q.shape, generator=torch.Generator().manual_seed(5)).cuda()
+    up, down = (q + s * w for s in (0.03125, -0.03125))
+    up, down = up.half(), down.half()
+    kw = dict(window=90, sinks=3)
+    o, _ = cla.window_attn_fwd(q, k, k, **kw)
+    num = (cla.window_attn_fwd(up, k, k, **kw)[1].double() - cla.window_attn_fwd(down, k, k, **kw)[1].double()).cpu()
+    q, k, o, up, down = (x.cpu().double() for x in (q, k, o, up, down))
+    step = up - down
+    ana = (o * step).sum(3) / 8
+    mid = (up + down) / 2 - q
+    # the logits of a row move by up to `reach` either way: a third derivative, the third moment of what moves by that,
+    # is below its cube, of which the difference has a third (2 is allowed); up and down are rounded, so their middle is
+    # off q by `mid`, which moves logits by `shift` and the derivative by the second moment, 2 reach shift; o and the P
+    # in it are rounded by half a step of fp16 each; each lse is off by some 300 roundings of fp32 in its sums
+    kk = k.repeat_interleave(2, 1)
+    reach = (step / 2 @ kk.transpose(2, 3)).abs().amax(3) / 8
+    shift = (mid @ kk.transpose(2, 3)).abs().amax(3) / 8
+    bound = 2 * reach ** 3 + 2 * reach * shift + 2.1 * 2.0 ** -11 * (step.abs().sum(3) * kk.abs().amax((2, 3))[..., None]) / 8 + 300 * 2.0 ** -22
+    assert bool(((num - ana).abs() <= bound).all()), float(((num - ana).abs() / bound).max())
