@@ -1,5 +1,5 @@
 // elem_io.cuh -- the element types of the entry points that take a cla_dtype
-// (fp32, bf16, fp16): loads to and stores from fp32 registers.
+// (fp32, bf16, fp16): stores from fp32 registers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -9,9 +9,6 @@
 namespace cla {
 namespace {
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 template <typename E>
 __device__ __forceinline__ E from_f32(float v);
 template <>

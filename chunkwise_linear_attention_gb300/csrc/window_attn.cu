@@ -97,7 +97,8 @@ long long wa_tiles(long long T) { return (T + kWT - 1) / kWT; }
 template <int D, bool BF>
 int wa_fwd(const char *fn, const WaMaps &m, void *o, float *lse, const Str3 &so, const WaArgs &g, WsHeader *hdr, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
-    constexpr int smem = FwdCfg<D>::SMEM > kMinSmem ? FwdCfg<D>::SMEM : kMinSmem;
+    constexpr int smem = FwdCfg<D>::SMEM;
+    static_assert(smem >= kMinSmem, "one block a multiprocessor");
     const long long G = g.H / g.Hkv, tiles = wa_tiles(g.T);
     const long long items = (long long)g.B * g.Hkv * (G % 2 == 0 ? G / 2 * tiles : G * ((tiles + 1) / 2));
     unsigned blocks;
@@ -120,8 +121,8 @@ template <int D, bool BF>
 int wa_bwd(const char *fn, const WaMaps &m, const WaMaps &mkv, const void *o, const void *dO, const float *lse, void *dq, void *dk, void *dv,
            const Str3 *r, const WaArgs &g, void *ws, cudaStream_t s) {
     static std::atomic<unsigned long long> done_q{0}, done_kv{0};
-    constexpr int smem_q = DqCfg<D>::SMEM > kMinSmem ? DqCfg<D>::SMEM : kMinSmem;
-    constexpr int smem_kv = DkvCfg<D>::SMEM > kMinSmem ? DkvCfg<D>::SMEM : kMinSmem;
+    constexpr int smem_q = DqCfg<D>::SMEM, smem_kv = DkvCfg<D>::SMEM;
+    static_assert(smem_q >= kMinSmem && smem_kv >= kMinSmem, "one block a multiprocessor");
     char *p = static_cast<char *>(ws);
     WsHeader *hdr = reinterpret_cast<WsHeader *>(p);
     float *delta = reinterpret_cast<float *>(p + sizeof(WsHeader));
