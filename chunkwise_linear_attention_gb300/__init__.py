@@ -761,18 +761,27 @@ def _strides(*tensors):
     return (ctypes.c_int64 * len(flat))(*flat)
 
 
+def _counts(window, sinks):
+    """Window and sinks as the C ABI's 64 bits hold them (ctypes would cut longer ones)."""
+    out = int(window), int(sinks)
+    if out != (window, sinks) or not -2 ** 63 <= min(out) <= max(out) < 2 ** 63:
+        raise ValueError(f"window and sinks must be a whole number of 64 bits each, got {window} and {sinks}")
+    return out
+
+
 def _scale(scale, d):
     return float(d) ** -0.5 if scale is None else float(scale)
 
 
 def window_attn_workspace_size(B, H, Hkv, T, d, window, sinks=0) -> int:
-    return int(lib().cla_window_attn_workspace_size(B, H, Hkv, T, d, int(window), int(sinks)))
+    return int(lib().cla_window_attn_workspace_size(B, H, Hkv, T, d, *_counts(window, sinks)))
 
 
 def window_attn_fwd(q, k, v, *, window, sinks=0, lens=None, scale=None, o=None, lse=None, workspace=None, stream=None):
     """Softmax attention of token t over s <= t with t - s < window or s < sinks: q [B, H, T, d], k and v
     [B, Hkv, T, d] (bf16 or fp16, d 64 or 128, H a multiple of Hkv; strided views are taken as they are).  lens [B]
     int32: lengths of a right-padded batch.  scale: d ** -0.5 when None.  Returns (o, lse [B, H, T] fp32)."""
+    window, sinks = _counts(window, sinks)
     B, H, T, d = _dims(q, 4, "q")
     Hkv = _dims(k, 4, "k")[1]
     dev, dt = q.device, q.dtype
@@ -784,18 +793,19 @@ def window_attn_fwd(q, k, v, *, window, sinks=0, lens=None, scale=None, o=None, 
     _launch("cla_window_attn_fwd", dev, (
         _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True),
         _T(lens, torch.int32, "lens", (B,)), _T(o, dt, "o", hs, True), _T(lse, torch.float32, "lse", (B, H, T)),
-        _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, T, d, _strides(q, k, v, o),
+        _scale(scale, d), window, sinks, code, B, H, Hkv, T, d, _strides(q, k, v, o),
         _T(ws, None, "workspace"), _nbytes(ws)), stream)
     return o, lse
 
 
 def window_attn_bwd_workspace_size(B, H, Hkv, T, d, window, sinks=0) -> int:
-    return int(lib().cla_window_attn_bwd_workspace_size(B, H, Hkv, T, d, int(window), int(sinks)))
+    return int(lib().cla_window_attn_bwd_workspace_size(B, H, Hkv, T, d, *_counts(window, sinks)))
 
 
 def window_attn_bwd(q, k, v, o, lse, dO, *, window, sinks=0, lens=None, scale=None, dq=None, dk=None, dv=None,
                     workspace=None, stream=None):
     """Adjoint of window_attn_fwd from its outputs (o, lse) and dO; returns (dq, dk, dv)."""
+    window, sinks = _counts(window, sinks)
     B, H, T, d = _dims(q, 4, "q")
     Hkv = _dims(k, 4, "k")[1]
     dev, dt = q.device, q.dtype
@@ -808,7 +818,7 @@ def window_attn_bwd(q, k, v, o, lse, dO, *, window, sinks=0, lens=None, scale=No
         _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True),
         _T(lens, torch.int32, "lens", (B,)), _T(o, dt, "o", hs, True), _T(lse, torch.float32, "lse", (B, H, T)),
         _T(dO, dt, "dO", hs, True), _T(dq, dt, "dq", hs, True), _T(dk, dt, "dk", ks, True), _T(dv, dt, "dv", ks, True),
-        _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, T, d, _strides(q, k, v, o, dO, dq, dk, dv),
+        _scale(scale, d), window, sinks, code, B, H, Hkv, T, d, _strides(q, k, v, o, dO, dq, dk, dv),
         _T(ws, None, "workspace"), _nbytes(ws)), stream)
     return dq, dk, dv
 
@@ -817,13 +827,14 @@ def window_cache_write(k, v, kcache, vcache, *, window, sinks=0, lens=None, stre
     """Writes the prompts' keys and values ([B, Hkv, T, d], from position 0) into the rolling cache
     [B, Hkv, sinks + window, d] that window_attn_step reads: token p in slot p while p < sinks, else in slot
     sinks + (p - sinks) % window, the last one that falls on a slot; slots without one stay as they were."""
+    window, sinks = _counts(window, sinks)
     B, Hkv, T, d = _dims(k, 4, "k")
     dev, dt = k.device, k.dtype
     code = _dtype_code(k, "k", _HALF)
-    ks, cs = (B, Hkv, T, d), (B, Hkv, int(sinks) + int(window), d)
+    ks, cs = (B, Hkv, T, d), (B, Hkv, sinks + window, d)
     _launch("cla_window_cache_write", dev, (
         _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True), _T(lens, torch.int32, "lens", (B,)),
-        _T(kcache, dt, "kcache", cs), _T(vcache, dt, "vcache", cs), int(window), int(sinks), code, B, Hkv, T, d,
+        _T(kcache, dt, "kcache", cs), _T(vcache, dt, "vcache", cs), window, sinks, code, B, Hkv, T, d,
         _strides(k, v)), stream)
 
 
@@ -831,14 +842,15 @@ def window_attn_step(q, k, v, kcache, vcache, pos, *, window, sinks=0, scale=Non
     """One token for each of B sequences: writes k and v [B, Hkv, d] into the rolling cache (see window_cache_write) and
     returns the attention of q [B, H, d] over what it then holds.  pos [B] int32: tokens before this one; negative: a
     row without a sequence (o is 0, its cache is left alone)."""
+    window, sinks = _counts(window, sinks)
     B, H, d = _dims(q, 3, "q")
     Hkv = _dims(k, 3, "k")[1]
     dev, dt = q.device, q.dtype
     code = _dtype_code(q, "q", _HALF)
     o = _out(o, (B, H, d), dt, dev, stream)
-    cs = (B, Hkv, int(sinks) + int(window), d)
+    cs = (B, Hkv, sinks + window, d)
     _launch("cla_window_attn_step", dev, (
         _T(q, dt, "q", (B, H, d), True), _T(k, dt, "k", (B, Hkv, d), True), _T(v, dt, "v", (B, Hkv, d), True),
         _T(kcache, dt, "kcache", cs), _T(vcache, dt, "vcache", cs), _T(pos, torch.int32, "pos", (B,)),
-        _T(o, dt, "o", (B, H, d)), _scale(scale, d), int(window), int(sinks), code, B, H, Hkv, d, _strides(q, k, v)), stream)
+        _T(o, dt, "o", (B, H, d)), _scale(scale, d), window, sinks, code, B, H, Hkv, d, _strides(q, k, v)), stream)
     return o

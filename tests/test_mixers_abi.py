@@ -203,3 +203,20 @@ def test_window_form_against_autograd():
     ref = R.window(q, k, v, 7, 2, lens, None, dO)
     for n, x in zip(("o", "dq", "dk", "dv"), (o,) + grads):
         torch.testing.assert_close(ref[n][0], x.detach(), rtol=1e-9, atol=1e-11)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 64 + 5, 0), (4.5, 0), (8, 2 ** 63), (8, 0.25), (-2 ** 63 - 1, 0)])
+def test_binding_counts(lib, window, sinks):
+    """Windows and sinks that 64 bits cannot hold, or that are not whole, are not cut to some other number."""
+    import chunkwise_linear_attention_gb300 as cla
+
+    q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    for call in (lambda: cla.window_attn_workspace_size(1, 2, 2, 4, 64, window, sinks),
+                 lambda: cla.window_attn_bwd_workspace_size(1, 2, 2, 4, 64, window, sinks),
+                 lambda: cla.window_attn_fwd(q, q, q, window=window, sinks=sinks),
+                 lambda: cla.window_cache_write(q, q, q, q, window=window, sinks=sinks),
+                 lambda: cla.window_attn_step(q[:, :, 0], q[:, :, 0], q[:, :, 0], q, q, torch.zeros(1, dtype=torch.int32),
+                                              window=window, sinks=sinks)):
+        with pytest.raises(ValueError, match="a whole number"):
+            call()
+    assert cla.window_attn_workspace_size(1, 2, 2, 4, 64, 8.0, 2 ** 63 - 1) == 256
