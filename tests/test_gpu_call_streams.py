@@ -1,5 +1,9 @@
 """Calls that name a stream other than the current one: what the binding allocates for them (outputs, workspaces) shares
 no memory with work that is still queued on either stream."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -92,3 +96,67 @@ def test_default_stream_by_its_handles(cla):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_calls_on_a_stream_that_a_capture_forks_to(cla):
+    """Named streams inside a capture: outputs and workspaces come from the graph's own memory, and replays on new inputs
+    give what calls outside give."""
+    t, t2 = inputs(4), inputs(5)
+    static = tuple(x.clone() for x in t)
+    work(cla, static, None)
+    s, fork = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        fork.wait_stream(s)
+        got = work(cla, static, fork)
+        s.wait_stream(fork)
+    for now in (t2, t):
+        want = work(cla, now, None)
+        for a, b in zip(static, now):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+FIRST_CALLS = """
+import torch
+import chunkwise_linear_attention_gb300 as cla
+g = torch.Generator().manual_seed(0)
+rnd = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()
+x, r, i, dh = (rnd(2, 300, 64) for _ in range(4))
+lam, state = torch.full((64,), -5.0, device="cuda"), torch.zeros(2, 64, device="cuda")
+q, k, v, dO = rnd(2, 4, 300, 128), rnd(2, 2, 300, 128), rnd(2, 2, 300, 128), rnd(2, 4, 300, 128)
+kc, vc = (torch.zeros(2, 2, 104, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+pos = torch.tensor([300, 300], dtype=torch.int32, device="cuda")
+kw = dict(window=100, sinks=4)
+
+def work():
+    o, lse = cla.window_attn_fwd(q, k, v, **kw)
+    cla.window_cache_write(k, v, kc, vc, **kw)
+    state.zero_()
+    return (cla.gated_scan_fwd(x, r, i, lam) + cla.gated_scan_bwd(x, r, i, lam, None, dh) + (o, lse)
+            + cla.window_attn_bwd(q, k, v, o, lse, dO, **kw)
+            + (cla.window_attn_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], kc, vc, pos, **kw),
+               cla.gated_scan_step(x[:, 0].contiguous(), r[:, 0].contiguous(), i[:, 0].contiguous(), lam, state)))
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = work()
+graph.replay()
+torch.cuda.synchronize()
+got = [y.clone() for y in got]
+for a, b in zip(got, work()):
+    assert torch.equal(a, b)
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_are_captured(cla):
+    """No entry point needs a call outside a capture before one inside."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
