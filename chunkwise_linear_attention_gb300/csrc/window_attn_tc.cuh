@@ -14,17 +14,22 @@
 // Probabilities P and their gradients dS are rounded to the tensors' type for
 // their products, with fp32 sums: the tensor cores take no fp32 operand, and
 // two 16-bit parts would double the products that bound the kernels at d = 128.
-// Against a form that keeps them in fp32 this adds about as much error to dq
-// and dk as the rounding of the outputs does (bf16: 2.5e-3 against 1.7e-3).
+// delta is the sum of dO o with the o that the backward is given, which is
+// rounded too; a sum of P dP would need both formed once more.  Against a form
+// that keeps all three in fp32 this adds about as much error to dq and dk as
+// the rounding of the outputs does (bf16: 2.5e-3 against 1.7e-3 at a window of
+// 512, of which dS is 1.7e-3 and delta 1.1e-3; delta's share grows as a query
+// sees fewer keys, to twice the outputs' rounding at two).
 //
 // Measured on GB300 (B x H / Hkv x T x d, window, sinks; bf16):
 //                                     4 x 16/16 x 8192 x 64   2 x 16/4 x 8192 x 128
 //                                     512, 0                  2048, 16
-//   forward                           118 us, 31% of the      196 us, 64%
-//   dq                                139 us  40% tensor      249 us, 74%
-//   dk, dv                            172 us, 41% pipe's      343 us, 74%
-//   join                              7 us        cycles      10 us
-// At d = 128 the products bound them (all tiles are formed whole, also those
+//   forward                           117 us, 31% of the      198 us, 64%
+//   dq                                141 us  40% tensor      252 us, 74%
+//   dk, dv                            173 us, 41% pipe's      342 us, 74%
+//   join                              6 us        cycles      8 us
+// At d = 128 the products bound them (of the backward's seven, two are S and dP
+// formed a second time, for rows of keys; all tiles are formed whole, also those
 // that the window or the diagonal cuts: 17 where 16 would do at that window,
 // 5 where 4 would at the other); at d = 64, where a pair of tiles has half the
 // products and the same 16384 exponentials and roundings, the chain of a warp's
@@ -1016,8 +1021,8 @@ wa_dq_kernel(const __grid_constant__ WaMaps maps, const void *__restrict__ o, co
 // The lists of the key tiles, one behind the other (sequence, key head, tile), are cut into equal
 // shares, one a block: few tiles with long lists (sinks are seen by every later query) and a
 // number of tiles that the blocks do not divide cost nothing.  A list that is cut leaves fp32
-// partial sums, which wa_join_kernel adds in their order; where the cuts are depends on the sizes
-// and lengths alone.
+// partial sums, which wa_join_kernel adds in their order; where the cuts are depends on the sizes, the
+// lengths and the device's multiprocessors.
 template <int D>
 struct DkvCfg {
     // Stages of q and of dO, and pairs of k and v tiles: two where they fit, so that a list begins while

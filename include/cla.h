@@ -700,7 +700,8 @@ size_t cla_window_attn_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv,
  * key head summed over its query heads in a fixed order (no float atomics).
  * P and dS are rounded to dtype for their products: fp16 gradients have to be
  * scaled so that dS stays within its range, as the tensors' own do.  A query
- * that sees one key has dq = 0 and adds nothing to dk.
+ * that sees one key has dq = 0 and adds nothing to dk.  The order of the sums
+ * is fixed by the sizes, the lengths and the device model.
  *   o, lse as the forward returned them;  dO [B, H, T, d] dtype
  *   dq     [B, H, T, d] dtype out;  dk, dv [B, Hkv, T, d] dtype out; all 0
  *          behind a sequence's length
