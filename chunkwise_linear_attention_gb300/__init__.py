@@ -18,6 +18,7 @@ current one.  What a call allocates itself needs no such wait.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -130,13 +131,16 @@ def _stream(stream, device=None):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _stream_object(stream, device):
-    """`stream` (a torch.cuda.Stream or a raw handle) as a torch.cuda.Stream of `device`."""
+def _other_stream(stream, device):
+    """`stream` (a torch.cuda.Stream or a raw handle) as a torch.cuda.Stream of `device`; None if it is the current one."""
     handle = _stream(stream, device).value or 0  # refuses a stream of another device
+    if handle == 1:  # cudaStreamLegacy: the device's default stream, as 0 is
+        handle = 0
+    if handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return None
     if isinstance(stream, torch.cuda.Stream):
         return stream
-    # 0 and 1 (cudaStreamLegacy) are the device's default stream
-    return torch.cuda.default_stream(device) if handle < 2 else torch.cuda.ExternalStream(handle, device=device)
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
 
 
 def _dims(t, n, name):
@@ -175,32 +179,43 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
-def _empty(shape, dtype, device, stream, returned):
-    """Memory for a call on `stream`: allocated on that stream, so that what queued work on another one still does with a
-    block that was given back there is not overtaken.  What is `returned` is then used on the current stream, and not
-    given out again before that is done with it either."""
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(_stream_object(stream, device)):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if returned:
-        t.record_stream(torch.cuda.current_stream(device))
-    return t
-
-
-def _ws(nbytes, device, workspace, stream, minimum=None):
+def _ws(nbytes, device, workspace, minimum=None):
     """A workspace of nbytes (allocated when not given); a given one needs at least `minimum`
     bytes (default nbytes) -- the entry points that take less than their size query's amount."""
     if workspace is None:
-        workspace = _empty((max(int(nbytes), 256),), torch.uint8, device, stream, False)
+        workspace = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
     need = nbytes if minimum is None else minimum
     if _nbytes(workspace) < need:
         raise ValueError(f"workspace of {_nbytes(workspace)} bytes < {need} needed")
     return workspace
 
 
-def _out(t, shape, dtype, device, stream):
-    return _empty(shape, dtype, device, stream, True) if t is None else t
+def _out(t, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else t
+
+
+def _own_memory(call):
+    """An entry point that allocates.  Where its stream is named and not the current one, it allocates on that stream, so
+    that it cannot be given a block that was freed while queued work of the current stream still uses it; what it
+    returns is used on the current stream, and not given out again before that is done with it either."""
+    @functools.wraps(call)
+    def entry(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        device = next((a.device for a in (*args, *kw.values()) if isinstance(a, torch.Tensor)), None)
+        if device is None or device.type != "cuda":
+            return call(*args, stream=stream, **kw)
+        on = _other_stream(stream, device)
+        if on is None:
+            return call(*args, stream=stream, **kw)
+        current = torch.cuda.current_stream(device)
+        with torch.cuda.stream(on):
+            out = call(*args, stream=stream, **kw)
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(current)
+        return out
+    return entry
 
 
 def _launch(fn, device, args, stream):
@@ -225,8 +240,8 @@ def _launch(fn, device, args, stream):
             _check_meta(*a)
         for a in tensors:
             _check_place(device, *a)
+    handle = None if stream is None else _stream(stream, device)  # refuses a stream of another device
     if isinstance(stream, torch.cuda.Stream):
-        _stream(stream, device)  # of the same device, or refused
         # memory that was allocated on another stream is not given out again before this stream is done
         # with it; with a raw handle that is the caller's part
         for a in args:
@@ -236,10 +251,10 @@ def _launch(fn, device, args, stream):
     index = device.index
     if index == torch._C._cuda_getDevice():
         # the current stream's handle, without the Stream object around it
-        status = call(*cargs, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, device))
+        status = call(*cargs, torch._C._cuda_getCurrentRawStream(index) if handle is None else handle)
     else:
         with torch.cuda.device(device):
-            status = call(*cargs, _stream(stream, device))
+            status = call(*cargs, _stream(None, device) if handle is None else handle)
     if status != CLA_OK:
         _check(fn, status)
 
@@ -265,29 +280,32 @@ def _scan_fwd(fn, a, b, h0, h, hT, workspace, stream, with_ws=True):
     B, T, D = _dims(a, 3, "a")
     dev = a.device
     f32 = torch.float32
-    h = _out(h, (B, T, D), f32, dev, stream)
-    hT = _out(hT, (B, D), f32, dev, stream)
+    h = _out(h, (B, T, D), f32, dev)
+    hT = _out(hT, (B, D), f32, dev)
     bt, bd = (B, T, D), (B, D)
     args = (_T(a, f32, "a", bt), _T(b, f32, "b", bt), _T(h0, f32, "h0", bd),
             _T(h, f32, "h", bt), _T(hT, f32, "hT", bd), B, T, D)
     if with_ws:
-        ws = _ws(scan_diag_workspace_size(B, T, D), dev, workspace, stream)
+        ws = _ws(scan_diag_workspace_size(B, T, D), dev, workspace)
         args += (_T(ws, None, "workspace"), _nbytes(ws))
     _launch(fn, dev, args, stream)
     return h, hT
 
 
+@_own_memory
 def scan_diag_fwd(a, b, h0=None, *, h=None, hT=None, workspace=None, stream=None):
     """h_t = a_t h_{t-1} + b_t over axis 1 of [B, T, D] (fp32); returns (h, hT)."""
     return _scan_fwd("cla_scan_diag_fwd", a, b, h0, h, hT, workspace, stream)
 
 
+@_own_memory
 def scan_diag_fwd_blelloch(a, b, h0=None, *, h=None, hT=None, workspace=None, stream=None):
     """scan_diag_fwd with a Blelloch tree across the runs of a chunk (a measured
     alternative to Hillis-Steele); returns (h, hT)."""
     return _scan_fwd("cla_scan_diag_fwd_blelloch", a, b, h0, h, hT, workspace, stream)
 
 
+@_own_memory
 def scan_diag_fwd_noalloc(a, b, h0=None, *, h=None, hT=None, stream=None):
     """scan_diag_fwd without a workspace: the library's static scratch array
     is used (limited size; overlapping calls race).  Returns (h, hT)."""
@@ -302,16 +320,17 @@ def scan_diag_noalloc_check_status(stream=None, device=None) -> None:
                lib().cla_scan_diag_noalloc_check_status(_stream(stream, dev)))
 
 
+@_own_memory
 def scan_diag_bwd(a, b, h0, h, dh, dhT=None, *, da=None, db=None, dh0=None, workspace=None, stream=None):
     """Adjoint of scan_diag_fwd; returns (da, db, dh0).  h: the forward's states, or None to
     recompute them from (a, b, h0) (then b is required; b may be None when h is given)."""
     B, T, D = _dims(a, 3, "a")
     dev = a.device
     f32 = torch.float32
-    da = _out(da, (B, T, D), f32, dev, stream)
-    db = _out(db, (B, T, D), f32, dev, stream)
-    dh0 = _out(dh0, (B, D), f32, dev, stream)
-    ws = _ws(scan_diag_workspace_size(B, T, D), dev, workspace, stream)
+    da = _out(da, (B, T, D), f32, dev)
+    db = _out(db, (B, T, D), f32, dev)
+    dh0 = _out(dh0, (B, D), f32, dev)
+    ws = _ws(scan_diag_workspace_size(B, T, D), dev, workspace)
     bt, bd = (B, T, D), (B, D)
     _launch("cla_scan_diag_bwd", dev, (
         _T(a, f32, "a", bt), _T(b, f32, "b", bt), _T(h0, f32, "h0", bd), _T(h, f32, "h", bt),
@@ -339,6 +358,7 @@ def _sel_ckpt_arg(ckpt, B, T, D, N):
     return _T(ckpt, torch.float32, "ckpt")
 
 
+@_own_memory
 def selective_scan_fwd(x, delta, A, Bm, Cm, h0=None, *, y=None, hT=None, ckpt=None, want_ckpt=True,
                        workspace=None, stream=None):
     """Selective scan forward; returns (y, hT, ckpt)."""
@@ -346,11 +366,11 @@ def selective_scan_fwd(x, delta, A, Bm, Cm, h0=None, *, y=None, hT=None, ckpt=No
     N = _dims(A, 2, "A")[1]
     dev = x.device
     f32, bf16 = torch.float32, torch.bfloat16
-    y = _out(y, (B, T, D), f32, dev, stream)
-    hT = _out(hT, (B, D, N), f32, dev, stream)
+    y = _out(y, (B, T, D), f32, dev)
+    hT = _out(hT, (B, D, N), f32, dev)
     if ckpt is None and want_ckpt:
-        ckpt = _out(None, (selective_scan_ckpt_elems(B, T, D, N),), f32, dev, stream)
-    ws = _ws(selective_scan_workspace_size(B, T, D, N), dev, workspace, stream)
+        ckpt = torch.empty(selective_scan_ckpt_elems(B, T, D, N), dtype=f32, device=dev)
+    ws = _ws(selective_scan_workspace_size(B, T, D, N), dev, workspace)
     btd, btn, bdn = (B, T, D), (B, T, N), (B, D, N)
     _launch("cla_selective_scan_fwd", dev, (
         _T(x, bf16, "x", btd), _T(delta, f32, "delta", btd), _T(A, f32, "A", (D, N)),
@@ -360,6 +380,7 @@ def selective_scan_fwd(x, delta, A, Bm, Cm, h0=None, *, y=None, hT=None, ckpt=No
     return y, hT, ckpt
 
 
+@_own_memory
 def selective_scan_bwd(x, delta, A, Bm, Cm, h0, ckpt, dy, dhT=None, *, dx=None, ddelta=None, dA=None,
                        dB=None, dC=None, dh0=None, want_dA=True, want_dh0=True, workspace=None, stream=None):
     """Selective scan backward; returns (dx, ddelta, dA, dB, dC, dh0)."""
@@ -367,13 +388,13 @@ def selective_scan_bwd(x, delta, A, Bm, Cm, h0, ckpt, dy, dhT=None, *, dx=None, 
     N = _dims(A, 2, "A")[1]
     dev = x.device
     f32, bf16 = torch.float32, torch.bfloat16
-    dx = _out(dx, (B, T, D), f32, dev, stream)
-    ddelta = _out(ddelta, (B, T, D), f32, dev, stream)
-    dA = _out(dA, (D, N), f32, dev, stream) if (want_dA or dA is not None) else None
-    dB = _out(dB, (B, T, N), f32, dev, stream)
-    dC = _out(dC, (B, T, N), f32, dev, stream)
-    dh0 = _out(dh0, (B, D, N), f32, dev, stream) if (want_dh0 or dh0 is not None) else None
-    ws = _ws(selective_scan_workspace_size(B, T, D, N), dev, workspace, stream)
+    dx = _out(dx, (B, T, D), f32, dev)
+    ddelta = _out(ddelta, (B, T, D), f32, dev)
+    dA = _out(dA, (D, N), f32, dev) if (want_dA or dA is not None) else None
+    dB = _out(dB, (B, T, N), f32, dev)
+    dC = _out(dC, (B, T, N), f32, dev)
+    dh0 = _out(dh0, (B, D, N), f32, dev) if (want_dh0 or dh0 is not None) else None
+    ws = _ws(selective_scan_workspace_size(B, T, D, N), dev, workspace)
     btd, btn, bdn = (B, T, D), (B, T, N), (B, D, N)
     _launch("cla_selective_scan_bwd", dev, (
         _T(x, bf16, "x", btd), _T(delta, f32, "delta", btd), _T(A, f32, "A", (D, N)),
@@ -411,6 +432,7 @@ def _ckpt_arg(ckpt, B, H, T, dk, dv, chunk):
     return _T(ckpt, torch.float32, "ckpt")
 
 
+@_own_memory
 def chunk_la_fwd(q, k, v, log_decay, S0=None, *, chunk=64, o=None, ST=None, ckpt=None, workspace=None,
                  stream=None):
     """Chunkwise decayed linear attention forward; returns (o, ST).  With ckpt (see
@@ -419,9 +441,9 @@ def chunk_la_fwd(q, k, v, log_decay, S0=None, *, chunk=64, o=None, ST=None, ckpt
     dv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    o = _out(o, (B, H, T, dv), f32, dev, stream)
-    ST = _out(ST, (B, H, dk, dv), f32, dev, stream)
-    ws = _ws(chunk_la_workspace_size(B, H, T, dk, dv, chunk), dev, workspace, stream)
+    o = _out(o, (B, H, T, dv), f32, dev)
+    ST = _out(ST, (B, H, dk, dv), f32, dev)
+    ws = _ws(chunk_la_workspace_size(B, H, T, dk, dv, chunk), dev, workspace)
     tk, tv, st = (B, H, T, dk), (B, H, T, dv), (B, H, dk, dv)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", (B, H, T)), _T(S0, f32, "S0", st),
@@ -435,6 +457,7 @@ def chunk_la_fwd(q, k, v, log_decay, S0=None, *, chunk=64, o=None, ST=None, ckpt
     return o, ST
 
 
+@_own_memory
 def chunk_la_bwd(q, k, v, log_decay, S0, dO, dST=None, *, chunk=64, dq=None, dk=None, dv=None,
                  dlog_decay=None, dS0=None, ckpt=None, workspace=None, stream=None):
     """Chunkwise decayed linear attention backward; returns (dq, dk, dv, dlog_decay, dS0).  ckpt:
@@ -443,12 +466,12 @@ def chunk_la_bwd(q, k, v, log_decay, S0, dO, dST=None, *, chunk=64, dq=None, dk=
     dvv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    dq = _out(dq, (B, H, T, dkk), f32, dev, stream)
-    dk = _out(dk, (B, H, T, dkk), f32, dev, stream)
-    dv = _out(dv, (B, H, T, dvv), f32, dev, stream)
-    dlog_decay = _out(dlog_decay, (B, H, T), f32, dev, stream)
-    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev, stream)
-    ws = _ws(chunk_la_workspace_size(B, H, T, dkk, dvv, chunk), dev, workspace, stream)
+    dq = _out(dq, (B, H, T, dkk), f32, dev)
+    dk = _out(dk, (B, H, T, dkk), f32, dev)
+    dv = _out(dv, (B, H, T, dvv), f32, dev)
+    dlog_decay = _out(dlog_decay, (B, H, T), f32, dev)
+    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev)
+    ws = _ws(chunk_la_workspace_size(B, H, T, dkk, dvv, chunk), dev, workspace)
     tk, tv, st, bht = (B, H, T, dkk), (B, H, T, dvv), (B, H, dkk, dvv), (B, H, T)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", bht), _T(S0, f32, "S0", st),
@@ -488,6 +511,7 @@ def _gla_ckpt_arg(ckpt, B, H, T, dk, dv, chunk):
     return _T(ckpt, torch.float32, "ckpt")
 
 
+@_own_memory
 def gla_fwd(q, k, v, log_decay, S0=None, *, chunk=64, o=None, ST=None, ckpt=None, workspace=None, stream=None):
     """Gated linear attention forward (one decay per key dimension: log_decay [B, H, T, dk]);
     returns (o, ST).  check_status(workspace) reports decays outside the kernel's range.  With
@@ -496,9 +520,9 @@ def gla_fwd(q, k, v, log_decay, S0=None, *, chunk=64, o=None, ST=None, ckpt=None
     dv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    o = _out(o, (B, H, T, dv), f32, dev, stream)
-    ST = _out(ST, (B, H, dk, dv), f32, dev, stream)
-    ws = _ws(gla_workspace_size(B, H, T, dk, dv, chunk), dev, workspace, stream)
+    o = _out(o, (B, H, T, dv), f32, dev)
+    ST = _out(ST, (B, H, dk, dv), f32, dev)
+    ws = _ws(gla_workspace_size(B, H, T, dk, dv, chunk), dev, workspace)
     tk, tv, st = (B, H, T, dk), (B, H, T, dv), (B, H, dk, dv)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", tk), _T(S0, f32, "S0", st),
@@ -515,6 +539,7 @@ def gla_bwd_workspace_size(B, H, T, dim_k, dim_v, chunk=64) -> int:
     return int(lib().cla_gla_bwd_workspace_size(B, H, T, dim_k, dim_v, int(chunk)))
 
 
+@_own_memory
 def gla_bwd(q, k, v, log_decay, S0, dO, dST=None, *, chunk=64, dq=None, dk=None, dv=None, dlog_decay=None,
             dS0=None, ckpt=None, workspace=None, stream=None):
     """Gated linear attention backward; returns (dq, dk, dv, dlog_decay [B, H, T, dk], dS0).  ckpt:
@@ -524,12 +549,12 @@ def gla_bwd(q, k, v, log_decay, S0, dO, dST=None, *, chunk=64, dq=None, dk=None,
     dvv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    dq = _out(dq, (B, H, T, dkk), f32, dev, stream)
-    dk = _out(dk, (B, H, T, dkk), f32, dev, stream)
-    dv = _out(dv, (B, H, T, dvv), f32, dev, stream)
-    dlog_decay = _out(dlog_decay, (B, H, T, dkk), f32, dev, stream)
-    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev, stream)
-    ws = _ws(gla_bwd_workspace_size(B, H, T, dkk, dvv, chunk), dev, workspace, stream)
+    dq = _out(dq, (B, H, T, dkk), f32, dev)
+    dk = _out(dk, (B, H, T, dkk), f32, dev)
+    dv = _out(dv, (B, H, T, dvv), f32, dev)
+    dlog_decay = _out(dlog_decay, (B, H, T, dkk), f32, dev)
+    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev)
+    ws = _ws(gla_bwd_workspace_size(B, H, T, dkk, dvv, chunk), dev, workspace)
     tk, tv, st = (B, H, T, dkk), (B, H, T, dvv), (B, H, dkk, dvv)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", tk), _T(S0, f32, "S0", st), _T(dO, bf16, "dO", tv),
@@ -544,6 +569,7 @@ def gla_bwd(q, k, v, log_decay, S0, dO, dST=None, *, chunk=64, dq=None, dk=None,
 
 
 # ---------------------------------------------------------------- state passing between slices
+@_own_memory
 def decay_total(log_decay, *, alpha=None, stream=None):
     """exp of the sum over the slice of log_decay: [B, H, T] -> [B, H] (one decay per head) or
     [B, H, T, dk] -> [B, H, dk] (gated)."""
@@ -554,19 +580,20 @@ def decay_total(log_decay, *, alpha=None, stream=None):
         B, H, T, A = _dims(log_decay, 4, "log_decay")
         shape = (B, H, A)
     dev = log_decay.device
-    alpha = _out(alpha, shape, torch.float32, dev, stream)
+    alpha = _out(alpha, shape, torch.float32, dev)
     _launch("cla_decay_total", dev, (_T(log_decay, torch.float32, "log_decay", tuple(log_decay.shape)),
                                      _T(alpha, torch.float32, "alpha", shape), B * H, T, A), stream)
     return alpha
 
 
+@_own_memory
 def state_compose(alphas, dSs, edge, first, count, step, *, out=None, stream=None):
     """Fold acc <- diag(alpha_j) acc + dS_j over j = first + c * step (c < count) from edge.
     alphas [P, B, H] or [P, B, H, dk]; dSs [P, B, H, dk, dv]; edge [B, H, dk, dv] or None."""
     P, B, H, dk, dv = _dims(dSs, 5, "dSs")
     A = 1 if alphas.dim() == 3 else alphas.shape[3]
     dev = dSs.device
-    out = _out(out, (B, H, dk, dv), torch.float32, dev, stream)
+    out = _out(out, (B, H, dk, dv), torch.float32, dev)
     st = (B, H, dk, dv)
     _launch("cla_state_compose", dev, (
         _T(alphas, torch.float32, "alphas", (P, B, H) if A == 1 else (P, B, H, A)),
@@ -599,6 +626,7 @@ def _delta_ckpt_arg(ckpt, B, H, T, dk, dv, chunk):
     return _T(ckpt, torch.float32, "ckpt")
 
 
+@_own_memory
 def delta_fwd(q, k, v, log_decay, beta, S0=None, *, chunk=64, o=None, ST=None, ckpt=None, workspace=None,
               stream=None):
     """Delta rule with a decay per head: S_t = a_t (I - beta_t k_t^T k_t) S_{t-1} + beta_t k_t^T v_t,
@@ -609,9 +637,9 @@ def delta_fwd(q, k, v, log_decay, beta, S0=None, *, chunk=64, o=None, ST=None, c
     dv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    o = _out(o, (B, H, T, dv), f32, dev, stream)
-    ST = _out(ST, (B, H, dk, dv), f32, dev, stream)
-    ws = _ws(delta_workspace_size(B, H, T, dk, dv, chunk), dev, workspace, stream, minimum=256)
+    o = _out(o, (B, H, T, dv), f32, dev)
+    ST = _out(ST, (B, H, dk, dv), f32, dev)
+    ws = _ws(delta_workspace_size(B, H, T, dk, dv, chunk), dev, workspace, minimum=256)
     tk, tv, st, bht = (B, H, T, dk), (B, H, T, dv), (B, H, dk, dv), (B, H, T)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", bht), _T(beta, f32, "beta", bht), _T(S0, f32, "S0", st),
@@ -628,6 +656,7 @@ def delta_bwd_workspace_size(B, H, T, dim_k, dim_v, chunk=64) -> int:
     return int(lib().cla_delta_bwd_workspace_size(B, H, T, dim_k, dim_v, int(chunk)))
 
 
+@_own_memory
 def delta_bwd(q, k, v, log_decay, beta, S0, dO, dST=None, *, chunk=64, dq=None, dk=None, dv=None,
               dlog_decay=None, dbeta=None, dS0=None, ckpt=None, workspace=None, stream=None):
     """Adjoint of delta_fwd (dO bf16 [B, H, T, dv]); returns (dq, dk, dv, dlog_decay, dbeta, dS0).  ckpt:
@@ -636,16 +665,16 @@ def delta_bwd(q, k, v, log_decay, beta, S0, dO, dST=None, *, chunk=64, dq=None, 
     dvv = _dims(v, 4, "v")[3]
     dev = q.device
     f32, bf16 = torch.float32, torch.bfloat16
-    dq = _out(dq, (B, H, T, dkk), f32, dev, stream)
-    dk = _out(dk, (B, H, T, dkk), f32, dev, stream)
-    dv = _out(dv, (B, H, T, dvv), f32, dev, stream)
-    dlog_decay = _out(dlog_decay, (B, H, T), f32, dev, stream)
-    dbeta = _out(dbeta, (B, H, T), f32, dev, stream)
-    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev, stream)
+    dq = _out(dq, (B, H, T, dkk), f32, dev)
+    dk = _out(dk, (B, H, T, dkk), f32, dev)
+    dv = _out(dv, (B, H, T, dvv), f32, dev)
+    dlog_decay = _out(dlog_decay, (B, H, T), f32, dev)
+    dbeta = _out(dbeta, (B, H, T), f32, dev)
+    dS0 = _out(dS0, (B, H, dkk, dvv), f32, dev)
     need = delta_bwd_workspace_size(B, H, T, dkk, dvv, chunk)
     if ckpt is not None:  # no states in the workspace: the header and the partials only
         need = max(need - delta_ckpt_size(B, H, T, dkk, dvv, chunk), 256)
-    ws = _ws(need, dev, workspace, stream)
+    ws = _ws(need, dev, workspace)
     tk, tv, st, bht = (B, H, T, dkk), (B, H, T, dvv), (B, H, dkk, dvv), (B, H, T)
     args = (_T(q, bf16, "q", tk), _T(k, bf16, "k", tk), _T(v, bf16, "v", tv),
             _T(log_decay, f32, "log_decay", bht), _T(beta, f32, "beta", bht), _T(S0, f32, "S0", st),
@@ -695,6 +724,7 @@ def _gated_ckpt_arg(ckpt, B, T, D):
     return _T(ckpt, torch.float32, "ckpt")
 
 
+@_own_memory
 def gated_scan_fwd(x, rgate, igate, lam, h0=None, *, reset=None, lens=None, c=8.0, h=None, hT=None, ckpt=None,
                    workspace=None, stream=None):
     """h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(igate_t) x_t with a = exp(-c softplus(lam) sigmoid(rgate)) over axis 1
@@ -703,9 +733,9 @@ def gated_scan_fwd(x, rgate, igate, lam, h0=None, *, reset=None, lens=None, c=8.
     B, T, D = _dims(x, 3, "x")
     dev, dt, f32 = x.device, x.dtype, torch.float32
     code = _dtype_code(x, "x", _DTYPES)
-    h = _out(h, (B, T, D), dt, dev, stream)
-    hT = _out(hT, (B, D), f32, dev, stream)
-    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace, stream)
+    h = _out(h, (B, T, D), dt, dev)
+    hT = _out(hT, (B, D), f32, dev)
+    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace)
     bt, bd = (B, T, D), (B, D)
     _launch("cla_gated_scan_fwd", dev, (
         _T(x, dt, "x", bt), _T(rgate, dt, "rgate", bt), _T(igate, dt, "igate", bt), _T(lam, f32, "lam", (D,)),
@@ -715,6 +745,7 @@ def gated_scan_fwd(x, rgate, igate, lam, h0=None, *, reset=None, lens=None, c=8.
     return h, hT
 
 
+@_own_memory
 def gated_scan_bwd(x, rgate, igate, lam, h0, dh, dhT=None, *, reset=None, lens=None, c=8.0, dx=None, drgate=None,
                    digate=None, dlam=None, dh0=None, ckpt=None, workspace=None, stream=None):
     """Adjoint of gated_scan_fwd; returns (dx, drgate, digate, dlam, dh0).  ckpt: what a gated_scan_fwd on the same
@@ -723,10 +754,10 @@ def gated_scan_bwd(x, rgate, igate, lam, h0, dh, dhT=None, *, reset=None, lens=N
     dev, dt, f32 = x.device, x.dtype, torch.float32
     code = _dtype_code(x, "x", _DTYPES)
     bt, bd = (B, T, D), (B, D)
-    dx, drgate, digate = (_out(t, bt, dt, dev, stream) for t in (dx, drgate, digate))
-    dlam = _out(dlam, (D,), f32, dev, stream)
-    dh0 = _out(dh0, bd, f32, dev, stream)
-    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace, stream)
+    dx, drgate, digate = (_out(t, bt, dt, dev) for t in (dx, drgate, digate))
+    dlam = _out(dlam, (D,), f32, dev)
+    dh0 = _out(dh0, bd, f32, dev)
+    ws = _ws(gated_scan_workspace_size(B, T, D), dev, workspace)
     _launch("cla_gated_scan_bwd", dev, (
         _T(x, dt, "x", bt), _T(rgate, dt, "rgate", bt), _T(igate, dt, "igate", bt), _T(lam, f32, "lam", (D,)),
         _T(h0, f32, "h0", bd), _reset_arg(reset, (B, T)), _T(lens, torch.int32, "lens", (B,)),
@@ -736,13 +767,14 @@ def gated_scan_bwd(x, rgate, igate, lam, h0, dh, dhT=None, *, reset=None, lens=N
     return dx, drgate, digate, dlam, dh0
 
 
+@_own_memory
 def gated_scan_step(x, rgate, igate, lam, h, *, reset=None, c=8.0, y=None, stream=None):
     """One token of gated_scan_fwd for each of B sequences ([B, D]); updates the state h [B, D] fp32 in place and
     returns it rounded to x's dtype."""
     B, D = _dims(x, 2, "x")
     dt, dev, bd = x.dtype, x.device, (B, D)
     code = _dtype_code(x, "x", _DTYPES)
-    y = _out(y, bd, dt, dev, stream)
+    y = _out(y, bd, dt, dev)
     _launch("cla_gated_scan_step", dev, (
         _T(x, dt, "x", bd), _T(rgate, dt, "rgate", bd), _T(igate, dt, "igate", bd), _T(lam, torch.float32, "lam", (D,)),
         _reset_arg(reset, (B,)), _T(h, torch.float32, "h", bd), _T(y, dt, "y", bd), float(c), code, B, D), stream)
@@ -777,6 +809,7 @@ def window_attn_workspace_size(B, H, Hkv, T, d, window, sinks=0) -> int:
     return int(lib().cla_window_attn_workspace_size(B, H, Hkv, T, d, *_counts(window, sinks)))
 
 
+@_own_memory
 def window_attn_fwd(q, k, v, *, window, sinks=0, lens=None, scale=None, o=None, lse=None, workspace=None, stream=None):
     """Softmax attention of token t over s <= t with t - s < window or s < sinks: q [B, H, T, d], k and v
     [B, Hkv, T, d] (bf16 or fp16, d 64 or 128, H a multiple of Hkv; strided views are taken as they are).  lens [B]
@@ -786,9 +819,9 @@ def window_attn_fwd(q, k, v, *, window, sinks=0, lens=None, scale=None, o=None, 
     Hkv = _dims(k, 4, "k")[1]
     dev, dt = q.device, q.dtype
     code = _dtype_code(q, "q", _HALF)
-    o = _out(o, (B, H, T, d), dt, dev, stream)
-    lse = _out(lse, (B, H, T), torch.float32, dev, stream)
-    ws = _ws(window_attn_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace, stream)
+    o = _out(o, (B, H, T, d), dt, dev)
+    lse = _out(lse, (B, H, T), torch.float32, dev)
+    ws = _ws(window_attn_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace)
     hs, ks = (B, H, T, d), (B, Hkv, T, d)
     _launch("cla_window_attn_fwd", dev, (
         _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True),
@@ -802,6 +835,7 @@ def window_attn_bwd_workspace_size(B, H, Hkv, T, d, window, sinks=0) -> int:
     return int(lib().cla_window_attn_bwd_workspace_size(B, H, Hkv, T, d, *_counts(window, sinks)))
 
 
+@_own_memory
 def window_attn_bwd(q, k, v, o, lse, dO, *, window, sinks=0, lens=None, scale=None, dq=None, dk=None, dv=None,
                     workspace=None, stream=None):
     """Adjoint of window_attn_fwd from its outputs (o, lse) and dO; returns (dq, dk, dv)."""
@@ -811,9 +845,9 @@ def window_attn_bwd(q, k, v, o, lse, dO, *, window, sinks=0, lens=None, scale=No
     dev, dt = q.device, q.dtype
     code = _dtype_code(q, "q", _HALF)
     hs, ks = (B, H, T, d), (B, Hkv, T, d)
-    dq = _out(dq, hs, dt, dev, stream)
-    dk, dv = _out(dk, ks, dt, dev, stream), _out(dv, ks, dt, dev, stream)
-    ws = _ws(window_attn_bwd_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace, stream)
+    dq = _out(dq, hs, dt, dev)
+    dk, dv = _out(dk, ks, dt, dev), _out(dv, ks, dt, dev)
+    ws = _ws(window_attn_bwd_workspace_size(B, H, Hkv, T, d, window, sinks), dev, workspace)
     _launch("cla_window_attn_bwd", dev, (
         _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True),
         _T(lens, torch.int32, "lens", (B,)), _T(o, dt, "o", hs, True), _T(lse, torch.float32, "lse", (B, H, T)),
@@ -838,6 +872,7 @@ def window_cache_write(k, v, kcache, vcache, *, window, sinks=0, lens=None, stre
         _strides(k, v)), stream)
 
 
+@_own_memory
 def window_attn_step(q, k, v, kcache, vcache, pos, *, window, sinks=0, scale=None, o=None, stream=None):
     """One token for each of B sequences: writes k and v [B, Hkv, d] into the rolling cache (see window_cache_write) and
     returns the attention of q [B, H, d] over what it then holds.  pos [B] int32: tokens before this one; negative: a
@@ -847,7 +882,7 @@ def window_attn_step(q, k, v, kcache, vcache, pos, *, window, sinks=0, scale=Non
     Hkv = _dims(k, 3, "k")[1]
     dev, dt = q.device, q.dtype
     code = _dtype_code(q, "q", _HALF)
-    o = _out(o, (B, H, d), dt, dev, stream)
+    o = _out(o, (B, H, d), dt, dev)
     cs = (B, Hkv, sinks + window, d)
     _launch("cla_window_attn_step", dev, (
         _T(q, dt, "q", (B, H, d), True), _T(k, dt, "k", (B, Hkv, d), True), _T(v, dt, "v", (B, Hkv, d), True),
