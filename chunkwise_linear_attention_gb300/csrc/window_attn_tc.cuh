@@ -1169,7 +1169,10 @@ wa_dkv_kernel(const __grid_constant__ WaMaps maps, const float *__restrict__ lse
     static_assert(17 + 2 * (QST + GST) + 4 <= kLast, "barriers");
     static_assert(QST >= 3 && GST >= 2, "stages");
     float(*s_stat)[2][kWT] = reinterpret_cast<float(*)[2][kWT]>(sm.f);  // [slot][lse log2 e, delta][query]
-    if (misplaced(sk, hdr)) return;
+    if (misplaced(sk, hdr)) {
+        if (threadIdx.x == 0) cuts[blockIdx.x] = CutList{0, 0, -1, 0};  // nothing to join
+        return;
+    }
     const int warp = threadIdx.x >> 5, G = g.H / g.Hkv;
     const uint32_t b0 = smem_u32(sm.bars);
     const uint32_t kv_full = b0, kv_empty = b0 + 16, acc_full = b0 + 32;
