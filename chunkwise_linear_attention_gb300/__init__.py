@@ -99,6 +99,12 @@ def lib():
                 "cla_window_attn_bwd": ([P] * 10 + [F, I64, I64, INT] + [I64] * 5 + [P, P, SZ, P], INT),
                 "cla_window_cache_write": ([P] * 5 + [I64, I64, INT] + [I64] * 4 + [P, P], INT),
                 "cla_window_attn_step": ([P] * 7 + [F, I64, I64, INT] + [I64] * 4 + [P, P], INT),
+                "cla_window_cache8_write": ([P] * 7 + [I64, I64, INT] + [I64] * 4 + [P, P], INT),
+                "cla_window_attn_step8": ([P] * 9 + [F, I64, I64, INT] + [I64] * 4 + [P, P], INT),
+                "cla_qk_norm_rope_fwd": ([P] * 9 + [F, I64, INT, INT] + [I64] * 5 + [P, P], INT),
+                "cla_qk_norm_rope_bwd_workspace_size": ([I64] * 5, SZ),
+                "cla_qk_norm_rope_bwd": ([P] * 13 + [F, I64, INT, INT] + [I64] * 5 + [P, P, SZ, P], INT),
+                "cla_delta_step": ([P] * 8 + [INT] + [I64] * 6 + [P, P], INT),
             }
             for name, (args, res) in sig.items():
                 f = getattr(L, name)
@@ -149,9 +155,13 @@ def _dims(t, n, name):
     return tuple(t.shape)
 
 
+_ALL = "all"
+
+
 def _T(t, dtype, name, shape=None, strided=False):
     """A tensor argument of an entry point (None stays NULL), checked by _launch for what the
     C ABI cannot check: dtype and shape (the sizes the call passes), then device and layout.
+    strided: the entry point takes the outer strides; _ALL: the last dimension's too.
     A plain tuple: a call makes up to fifteen of them."""
     return (t, dtype, name, shape, strided)
 
@@ -169,7 +179,7 @@ def _check_place(device, t, dtype, name, shape, strided):
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's first tensor on {device}")
     if strided:  # the entry point takes the outer strides
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+        if t.shape[-1] > 1 and t.stride(-1) != 1 and strided is not _ALL:
             raise ValueError(f"{name} must be contiguous in its last dimension")
     elif not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -230,7 +240,7 @@ def _launch(fn, device, args, stream):
                 a = None
             else:
                 if ((t.dtype is not dtype and dtype is not None) or (shape is not None and t.shape != shape)
-                        or t.device != device or not (t.is_contiguous() or strided and t.stride(-1) == 1)):
+                        or t.device != device or not (t.is_contiguous() or strided and (t.stride(-1) == 1 or strided is _ALL))):
                     good = False
                 a = t.data_ptr()
         cargs.append(a)
@@ -888,4 +898,142 @@ def window_attn_step(q, k, v, kcache, vcache, pos, *, window, sinks=0, scale=Non
         _T(q, dt, "q", (B, H, d), True), _T(k, dt, "k", (B, Hkv, d), True), _T(v, dt, "v", (B, Hkv, d), True),
         _T(kcache, dt, "kcache", cs), _T(vcache, dt, "vcache", cs), _T(pos, torch.int32, "pos", (B,)),
         _T(o, dt, "o", (B, H, d)), _scale(scale, d), window, sinks, code, B, H, Hkv, d, _strides(q, k, v)), stream)
+    return o
+
+
+# ---------------------------------------------------------------- the window's cache in 8 bits
+WINDOW_CACHE8_BLOCK = 64
+
+
+def _cache8_args(kcache, vcache, kscale, vscale, B, Hkv, d, window, sinks):
+    S = sinks + window
+    cs, ss = (B, Hkv, S, d), (B, Hkv, -(-S // WINDOW_CACHE8_BLOCK))
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    return (_T(kcache, e4m3, "kcache", cs), _T(vcache, e4m3, "vcache", cs), _T(kscale, f32, "kscale", ss),
+            _T(vscale, f32, "vscale", ss))
+
+
+def window_cache8(B, Hkv, d, *, window, sinks=0, device="cuda"):
+    """An empty cache of window_cache8_write and window_attn_step8: (kcache, vcache, kscale, vscale)."""
+    window, sinks = _counts(window, sinks)
+    S = sinks + window
+    cache = (torch.zeros(B, Hkv, S, d, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+    return (*cache, *(torch.zeros(B, Hkv, -(-S // WINDOW_CACHE8_BLOCK), dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def window_cache8_write(k, v, kcache, vcache, kscale, vscale, *, window, sinks=0, lens=None, stream=None):
+    """window_cache_write into a cache of 8 bits: kcache and vcache [B, Hkv, sinks + window, d] float8_e4m3fn, whose numbers
+    stand for themselves times a power of two for every 64 slots of a key head, kscale and vscale [B, Hkv,
+    ceil((sinks + window) / 64)] fp32."""
+    window, sinks = _counts(window, sinks)
+    B, Hkv, T, d = _dims(k, 4, "k")
+    dev, dt = k.device, k.dtype
+    code = _dtype_code(k, "k", _HALF)
+    ks = (B, Hkv, T, d)
+    _launch("cla_window_cache8_write", dev, (
+        _T(k, dt, "k", ks, True), _T(v, dt, "v", ks, True), _T(lens, torch.int32, "lens", (B,)),
+        *_cache8_args(kcache, vcache, kscale, vscale, B, Hkv, d, window, sinks), window, sinks, code, B, Hkv, T, d,
+        _strides(k, v)), stream)
+
+
+@_own_memory
+def window_attn_step8(q, k, v, kcache, vcache, kscale, vscale, pos, *, window, sinks=0, scale=None, o=None, stream=None):
+    """window_attn_step over a cache of 8 bits (see window_cache8_write): k and v go into their slot, the factors of its
+    block become those of what the block then holds, and q attends over what the cache then holds."""
+    window, sinks = _counts(window, sinks)
+    B, H, d = _dims(q, 3, "q")
+    Hkv = _dims(k, 3, "k")[1]
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q, "q", _HALF)
+    o = _out(o, (B, H, d), dt, dev)
+    _launch("cla_window_attn_step8", dev, (
+        _T(q, dt, "q", (B, H, d), True), _T(k, dt, "k", (B, Hkv, d), True), _T(v, dt, "v", (B, Hkv, d), True),
+        *_cache8_args(kcache, vcache, kscale, vscale, B, Hkv, d, window, sinks), _T(pos, torch.int32, "pos", (B,)),
+        _T(o, dt, "o", (B, H, d)), _scale(scale, d), window, sinks, code, B, H, Hkv, d, _strides(q, k, v)), stream)
+    return o
+
+
+# ---------------------------------------------------------------- norm and rotation of queries and keys
+def _rot(freq):
+    return 0 if freq is None else 2 * _dims(freq, 1, "freq")[0]
+
+
+@_own_memory
+def qk_norm_rope_fwd(q, k, wq=None, wk=None, freq=None, *, pos=None, lens=None, eps=1e-6, interleaved=False, qo=None, ko=None,
+                     stream=None):
+    """Norm and rotation of every query and key head: x / sqrt(mean(x^2) + eps) times the weights (wq, wk [d] fp32; ones when
+    None), with the first 2 len(freq) values turned by pos freq (freq [rot / 2] fp32 radians; pairs (i, i + rot / 2), or
+    (2i, 2i + 1) when interleaved; None turns nothing).  q [B, H, T, d], k [B, Hkv, T, d] (fp32, bf16 or fp16; strided views
+    are taken as they are); pos [B, T] int32, 0, 1, ... when None; lens [B] int32: lengths of a right-padded batch.
+    Returns (qo, ko); q and k themselves may be given for them."""
+    B, H, T, d = _dims(q, 4, "q")
+    Hkv = _dims(k, 4, "k")[1]
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    code = _dtype_code(q, "q", _DTYPES)
+    hs, ks, rot = (B, H, T, d), (B, Hkv, T, d), _rot(freq)
+    qo, ko = _out(qo, hs, dt, dev), _out(ko, ks, dt, dev)
+    _launch("cla_qk_norm_rope_fwd", dev, (
+        _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(wq, f32, "wq", (d,)), _T(wk, f32, "wk", (d,)),
+        _T(freq, f32, "freq", (rot // 2,)), _T(pos, torch.int32, "pos", (B, T)), _T(lens, torch.int32, "lens", (B,)),
+        _T(qo, dt, "qo", hs, True), _T(ko, dt, "ko", ks, True), float(eps), rot, int(bool(interleaved)), code, B, H, Hkv, T, d,
+        _strides(q, k, qo, ko)), stream)
+    return qo, ko
+
+
+def qk_norm_rope_step(q, k, wq, wk, freq, pos, *, eps=1e-6, interleaved=False, qo=None, ko=None, stream=None):
+    """qk_norm_rope_fwd for one token of each of B sequences: q [B, H, d], k [B, Hkv, d], pos [B] int32 (what
+    window_attn_step takes)."""
+    _dims(q, 3, "q"), _dims(k, 3, "k")
+    given = tuple(None if t is None else t.unsqueeze(2) for t in (qo, ko))
+    a, b = qk_norm_rope_fwd(q.unsqueeze(2), k.unsqueeze(2), wq, wk, freq, pos=None if pos is None else pos.unsqueeze(-1), eps=eps,
+                            interleaved=interleaved, qo=given[0], ko=given[1], stream=stream)
+    return a.squeeze(2) if qo is None else qo, b.squeeze(2) if ko is None else ko
+
+
+def qk_norm_rope_bwd_workspace_size(B, H, Hkv, T, d) -> int:
+    return int(lib().cla_qk_norm_rope_bwd_workspace_size(B, H, Hkv, T, d))
+
+
+@_own_memory
+def qk_norm_rope_bwd(q, k, wq, wk, freq, dqo, dko, *, pos=None, lens=None, eps=1e-6, interleaved=False, dq=None, dk=None,
+                     dwq=None, dwk=None, workspace=None, stream=None):
+    """Adjoint of qk_norm_rope_fwd from its inputs; returns (dq, dk, dwq, dwk), dwq and dwk [d] fp32 (None for weights that
+    are None)."""
+    B, H, T, d = _dims(q, 4, "q")
+    Hkv = _dims(k, 4, "k")[1]
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    code = _dtype_code(q, "q", _DTYPES)
+    hs, ks, rot = (B, H, T, d), (B, Hkv, T, d), _rot(freq)
+    dq, dk = _out(dq, hs, dt, dev), _out(dk, ks, dt, dev)
+    dwq = _out(dwq, (d,), f32, dev) if wq is not None else dwq
+    dwk = _out(dwk, (d,), f32, dev) if wk is not None else dwk
+    ws = _ws(qk_norm_rope_bwd_workspace_size(B, H, Hkv, T, d), dev, workspace)
+    _launch("cla_qk_norm_rope_bwd", dev, (
+        _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(wq, f32, "wq", (d,)), _T(wk, f32, "wk", (d,)),
+        _T(freq, f32, "freq", (rot // 2,)), _T(pos, torch.int32, "pos", (B, T)), _T(lens, torch.int32, "lens", (B,)),
+        _T(dqo, dt, "dqo", hs, True), _T(dko, dt, "dko", ks, True), _T(dq, dt, "dq", hs, True), _T(dk, dt, "dk", ks, True),
+        _T(dwq, f32, "dwq", (d,)), _T(dwk, f32, "dwk", (d,)), float(eps), rot, int(bool(interleaved)), code, B, H, Hkv, T, d,
+        _strides(q, k, dqo, dko, dq, dk), _T(ws, None, "workspace"), _nbytes(ws)), stream)
+    return dq, dk, dwq, dwk
+
+
+# ---------------------------------------------------------------- the delta rule token by token
+@_own_memory
+def delta_step(q, k, v, log_decay, beta, S, *, lens=None, o=None, stream=None):
+    """The recurrence of delta_fwd for a few tokens of each of B sequences, on the states S [B, H, dk, dv] fp32, which it
+    updates in place: q, k [B, Hk, T, dk], v [B, H, T, dv] (fp32, bf16 or fp16; H a multiple of Hk), log_decay, beta [B, H, T]
+    fp32; strided views are taken as they are.  lens [B] int32: tokens of each sequence.  Returns o [B, H, T, dv] fp32."""
+    B, Hk, T, dk = _dims(q, 4, "q")
+    H, dv = _dims(v, 4, "v")[1::2]
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    code = _dtype_code(q, "q", _DTYPES)
+    o = _out(o, (B, H, T, dv), f32, dev)
+    ks, gs = (B, Hk, T, dk), (B, H, T)
+    strides = None
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and log_decay.is_contiguous() and beta.is_contiguous()):
+        strides = (ctypes.c_int64 * 15)(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *log_decay.stride(), *beta.stride())
+    _launch("cla_delta_step", dev, (
+        _T(q, dt, "q", ks, True), _T(k, dt, "k", ks, True), _T(v, dt, "v", (B, H, T, dv), True),
+        _T(log_decay, f32, "log_decay", gs, _ALL), _T(beta, f32, "beta", gs, _ALL), _T(lens, torch.int32, "lens", (B,)),
+        _T(S, f32, "S", (B, H, dk, dv)), _T(o, f32, "o", (B, H, T, dv)), code, B, H, Hk, T, dk, dv, strides), stream)
     return o

@@ -747,6 +747,123 @@ int cla_window_attn_step(const void *q, const void *k, const void *v, void *kcac
                          int64_t H, int64_t Hkv, int64_t d, const int64_t *strides,
                          void *stream);
 
+/* The same cache in 8 bits, half the bytes of a step.  Its slots go in blocks
+ * of CLA_WINDOW_CACHE8_BLOCK (the last block may be shorter); a key head's
+ * numbers of a block are e4m3 (1 sign, 4 exponent, 3 mantissa bits, largest
+ * 448) times the block's factor: the smallest power of two, 2^-64 at least,
+ * under which the largest of them stays within 448.  Numbers are rounded to
+ * nearest, ties to even.
+ *   kcache, vcache [B, Hkv, sinks + window, d] bytes, e4m3, dense, in and out
+ *   kscale, vscale [B, Hkv, ceil((sinks + window) / 64)] fp32, in and out: the
+ *              factors; those of blocks that hold no token are not used */
+#define CLA_WINDOW_CACHE8_BLOCK 64
+
+/* cla_window_cache_write into that cache.  Bytes of slots and factors of blocks
+ * that no token reaches are left as they were.  An infinity is held as the
+ * largest number, a NaN stays one and does not count for the factor. */
+int cla_window_cache8_write(const void *k, const void *v, const int32_t *lens,
+                            void *kcache, void *vcache, float *kscale,
+                            float *vscale, int64_t window, int64_t sinks,
+                            int dtype, int64_t B, int64_t Hkv, int64_t T,
+                            int64_t d, const int64_t *strides, void *stream);
+
+/* cla_window_attn_step over that cache: the token's key and value go into their
+ * slot, the factors of its block become those of what the block then holds (its
+ * other numbers are rounded anew where a factor changes: exactly, but for those
+ * that fall below e4m3's normal range), and the attention is over what the cache
+ * then holds, the token's own key and value included.  Other blocks are read
+ * only.  The weights are rounded to 11 bits for their product with the cache's
+ * numbers.
+ * The arguments are cla_window_attn_step's, with the caches above. */
+int cla_window_attn_step8(const void *q, const void *k, const void *v, void *kcache,
+                          void *vcache, float *kscale, float *vscale,
+                          const int32_t *pos, void *o, float scale, int64_t window,
+                          int64_t sinks, int dtype, int64_t B, int64_t H,
+                          int64_t Hkv, int64_t d, const int64_t *strides,
+                          void *stream);
+
+/* ======================================================================== */
+/* Norm and rotation of queries and keys                                    */
+/* ======================================================================== */
+
+/* Before the attention or the delta rule: each head's query and key x (d values)
+ * is brought to a root mean square of 1, weighted, and turned by its position:
+ *   n = x / sqrt(mean(x^2) + eps),  y = w n,
+ *   o = y with the pairs (y_i, y_i+rot/2), i < rot / 2, turned by the angle
+ *       pos freq_i:  (a, b) -> (a cos - b sin, b cos + a sin);
+ *       interleaved != 0: the pairs are (y_2i, y_2i+1)
+ * rot = 0 turns nothing: with w = d^-1/2 that is the L2 norm that keys of the
+ * delta rule take.
+ *   q, qo  [B, H, T, d] dtype;  k, ko [B, Hkv, T, d] dtype; any H and Hkv
+ *   wq, wk [d] fp32 [opt]: NULL = ones
+ *   freq   [rot / 2] fp32: angle per position, in radians, finite (NULL for
+ *          rot = 0)
+ *   pos    [B, T] int32 [opt]: each token's position; NULL: 0, 1, ... T - 1
+ *   lens   [B] int32 [opt]: tokens of each sequence of a right-padded batch;
+ *          behind them the outputs are 0 and the inputs are not used
+ *   strides [opt]: {batch, head, token} triples of q, k, qo, ko as for the window
+ *          attention (of 16-byte multiples)
+ * qo may be q and ko may be k, with the same strides; the tensors overlap in no
+ * other way.  Angles are exact to 2^-31 (1 + |freq|) of a turn for every position.
+ * A row's sum of squares has to stay within fp32.  Sums and angles are fp32, the
+ * result is rounded once.
+ * d and rot are multiples of 16, rot <= d <= 256; eps is positive and finite;
+ * B * T below 2^31, H + Hkv below 2^20, B * T * (H + Hkv) at most 2^36. */
+int cla_qk_norm_rope_fwd(const void *q, const void *k, const float *wq,
+                         const float *wk, const float *freq, const int32_t *pos,
+                         const int32_t *lens, void *qo, void *ko, float eps,
+                         int64_t rot, int interleaved, int dtype, int64_t B,
+                         int64_t H, int64_t Hkv, int64_t T, int64_t d,
+                         const int64_t *strides, void *stream);
+
+/* Bytes of workspace for cla_qk_norm_rope_bwd; 0 for what the call refuses. */
+size_t cla_qk_norm_rope_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv,
+                                           int64_t T, int64_t d);
+
+/* Backward: with g the gradient on o turned back,
+ *   dw = sum over rows of g n,  dx = r (g w - n mean(g w n)),  r = n / x.
+ *   dqo, dko  gradients on qo and ko, dtype;  dq, dk dtype out, 0 behind a
+ *             sequence's length
+ *   dwq, dwk  [d] fp32 [opt] out, summed in an order that the sizes fix
+ *   strides [opt]: of q, k, dqo, dko, dq, dk
+ * dq may be q or dqo, with the same strides, and so for dk.  The other arguments
+ * are the forward's. */
+int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq,
+                         const float *wk, const float *freq, const int32_t *pos,
+                         const int32_t *lens, const void *dqo, const void *dko,
+                         void *dq, void *dk, float *dwq, float *dwk, float eps,
+                         int64_t rot, int interleaved, int dtype, int64_t B,
+                         int64_t H, int64_t Hkv, int64_t T, int64_t d,
+                         const int64_t *strides, void *ws, size_t ws_bytes,
+                         void *stream);
+
+/* ======================================================================== */
+/* The delta rule token by token                                            */
+/* ======================================================================== */
+
+/* The recurrence of cla_delta_fwd for a few tokens of each of B sequences, on
+ * states that are updated in place (those that cla_delta_fwd leaves, S_T):
+ *   S_t = a_t (I - beta_t k_t^T k_t) S_{t-1} + beta_t k_t^T v_t,  o_t = q_t S_t
+ * The state is read and written once, however many tokens there are; prompts are
+ * cla_delta_fwd's.
+ *   q, k   [B, Hk, T, dim_k] dtype (any cla_dtype);  v [B, H, T, dim_v] dtype.
+ *          H is a multiple of Hk: value head h takes query and key head
+ *          h / (H / Hk).  Keys are used as given.
+ *   log_decay, beta [B, H, T] fp32; a log decay of -inf drops the state, whatever
+ *          it holds
+ *   lens   [B] int32 [opt]: tokens of each sequence (clamped to [0, T]); behind
+ *          them o is 0, the state is kept and the inputs are not used
+ *   S      [B, H, dim_k, dim_v] fp32, dense, in and out
+ *   o      [B, H, T, dim_v] fp32 out, dense
+ *   strides [opt]: {batch, head, token} triples of q, k, v, log_decay, beta, any
+ *          positive number of elements below 2^39
+ * dim_k 64 or 128, dim_v a multiple of 4; B * H * ceil(dim_v / 32) below 2^31. */
+int cla_delta_step(const void *q, const void *k, const void *v,
+                   const float *log_decay, const float *beta, const int32_t *lens,
+                   float *S, float *o, int dtype, int64_t B, int64_t H, int64_t Hk,
+                   int64_t T, int64_t dim_k, int64_t dim_v, const int64_t *strides,
+                   void *stream);
+
 #ifdef __cplusplus
 }
 #endif
