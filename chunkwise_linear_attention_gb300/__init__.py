@@ -100,7 +100,8 @@ def lib():
                 "cla_window_cache_write": ([P] * 5 + [I64, I64, INT] + [I64] * 4 + [P, P], INT),
                 "cla_window_attn_step": ([P] * 7 + [F, I64, I64, INT] + [I64] * 4 + [P, P], INT),
                 "cla_window_cache8_write": ([P] * 7 + [I64, I64, INT] + [I64] * 4 + [P, P], INT),
-                "cla_window_attn_step8": ([P] * 9 + [F, I64, I64, INT] + [I64] * 4 + [P, P], INT),
+                "cla_window_attn_step8": ([P] * 9 + [F, I64, I64, INT] + [I64] * 4 + [P, P, SZ, P], INT),
+                "cla_window_attn_step8_workspace_size": ([I64] * 6, SZ),
                 "cla_qk_norm_rope_fwd": ([P] * 9 + [F, I64, INT, INT] + [I64] * 5 + [P, P], INT),
                 "cla_qk_norm_rope_bwd_workspace_size": ([I64] * 5, SZ),
                 "cla_qk_norm_rope_bwd": ([P] * 13 + [F, I64, INT, INT] + [I64] * 5 + [P, P, SZ, P], INT),
@@ -936,8 +937,13 @@ def window_cache8_write(k, v, kcache, vcache, kscale, vscale, *, window, sinks=0
         _strides(k, v)), stream)
 
 
+def window_attn_step8_workspace_size(B, H, Hkv, d, window, sinks=0) -> int:
+    return int(lib().cla_window_attn_step8_workspace_size(B, H, Hkv, d, *_counts(window, sinks)))
+
+
 @_own_memory
-def window_attn_step8(q, k, v, kcache, vcache, kscale, vscale, pos, *, window, sinks=0, scale=None, o=None, stream=None):
+def window_attn_step8(q, k, v, kcache, vcache, kscale, vscale, pos, *, window, sinks=0, scale=None, o=None, workspace=None,
+                      stream=None):
     """window_attn_step over a cache of 8 bits (see window_cache8_write): k and v go into their slot, the factors of its
     block become those of what the block then holds, and q attends over what the cache then holds."""
     window, sinks = _counts(window, sinks)
@@ -946,10 +952,12 @@ def window_attn_step8(q, k, v, kcache, vcache, kscale, vscale, pos, *, window, s
     dev, dt = q.device, q.dtype
     code = _dtype_code(q, "q", _HALF)
     o = _out(o, (B, H, d), dt, dev)
+    ws = _ws(window_attn_step8_workspace_size(B, H, Hkv, d, window, sinks), dev, workspace)
     _launch("cla_window_attn_step8", dev, (
         _T(q, dt, "q", (B, H, d), True), _T(k, dt, "k", (B, Hkv, d), True), _T(v, dt, "v", (B, Hkv, d), True),
         *_cache8_args(kcache, vcache, kscale, vscale, B, Hkv, d, window, sinks), _T(pos, torch.int32, "pos", (B,)),
-        _T(o, dt, "o", (B, H, d)), _scale(scale, d), window, sinks, code, B, H, Hkv, d, _strides(q, k, v)), stream)
+        _T(o, dt, "o", (B, H, d)), _scale(scale, d), window, sinks, code, B, H, Hkv, d, _strides(q, k, v),
+        _T(ws, None, "workspace"), _nbytes(ws)), stream)
     return o
 
 

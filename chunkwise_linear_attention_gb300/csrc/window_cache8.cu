@@ -133,271 +133,459 @@ __global__ void __launch_bounds__(128) c8_write_kernel(const E *k, const E *v, c
 }
 
 // ------------------------------------------------------------------ one token
+// A thread block's share of the work is an equal piece of the list of all blocks of slots that hold tokens, (sequence,
+// key head, block) in this order: segments of (sequence, key head) pairs, of which at most the first and the last are cut.
+constexpr int kC8MaxBlocks = 608;  // thread blocks of the step at most: 4 for each of 152 multiprocessors
+
 struct Step8Args {
     const int32_t *pos;
     float c;  // scale log2 e
     long long window, sinks, slots;
-    int H, Hkv, splits, blocks;  // blocks: of slots, of a sequence and key head
+    int B, H, Hkv, blocks;  // blocks: of slots, of a sequence and key head
     Triple sq, sk, sv;
 };
 
-// The token's values into slot `mine` of its block (of n held slots in all), by all threads; what comes
-// after a barrier sees it.
-template <typename E, int D>
-__device__ __forceinline__ void put_token(uint8_t *cache, float *factor, const E *x, long long first, long long mine, long long n,
-                                          float *s_top) {
-    constexpr int P = D / 16, N = kC8Block * P / 128;
-    uint4 code[N];
-    uint32_t most = 0u;
-    float val[16], top = 0.f;
-    int own = -1;
+// What the join has to do for a thread block's last segment: add to its part those of the blocks up to `last`.
+struct Cut8 {
+    int unit, slot, last, all;  // unit: sequence Hkv + key head, or -1: nothing to do; all: blocks of slots in the list
+};
+__device__ __forceinline__ long long share_of(long long all, unsigned block) { return all * block / gridDim.x; }
+
+__device__ __forceinline__ long long held_slots(const Step8Args &g, int b) { return max(0ll, min((long long)g.pos[b] + 1, g.slots)); }
+__device__ __forceinline__ int held_blocks(const Step8Args &g, int b) { return (int)((held_slots(g, b) + kC8Block - 1) / kC8Block); }
+
+// Sum over a block's threads, and what the threads before this one add to it.
+__device__ __forceinline__ long long block_scan(long long v, long long &before, long long *s_sum) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    long long up = v;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int at = threadIdx.x + 128 * i;
-        const long long slot = first + at / P;
-        code[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (slot == mine) {
-            own = i;
-            load16(x + 16 * (at % P), val);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(val[j]));
-        } else if (slot < n) {
-            code[i] = reinterpret_cast<const uint4 *>(cache + first * D)[at];
-        }
-        most = __vmaxu4(most, __vmaxu4(__vmaxu4(code[i].x & 0x7f7f7f7fu, code[i].y & 0x7f7f7f7fu),
-                                       __vmaxu4(code[i].z & 0x7f7f7f7fu, code[i].w & 0x7f7f7f7fu)));
+    for (int x = 1; x < 32; x <<= 1) {
+        const long long y = __shfl_up_sync(~0u, up, x);
+        if (lane >= x) up += y;
     }
-    most = __vmaxu4(most, most >> 16);
-    most = min(max(most & 0xffu, most >> 8 & 0xffu), 0x7eu);  // a NaN counts as the largest number
-    const float old = *factor;
-    if (most != 0u) top = fmaxf(top, unpack16<false>(f16x2_of(most)).x * old);
-#pragma unroll
-    for (int w = 1; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-    if (threadIdx.x % 32 == 0) s_top[threadIdx.x / 32] = top;
     __syncthreads();
-    const float f = factor_of(fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]))), by = inverse(f);
+    if (lane == 31) s_sum[warp] = up;
+    __syncthreads();
+    long long all = 0;
+    before = up - v;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int at = threadIdx.x + 128 * i;
-        const long long slot = first + at / P;
-        uint4 *to = reinterpret_cast<uint4 *>(cache + first * D) + at;
-        if (i == own) {
-            *to = code16(val, by);
-        } else if (slot < n && f != old) {
-            float y[16];
-            decode16(code[i], y);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] *= old;
-            *to = code16(y, by);
-        }
+    for (int w = 0; w < kStepWarps; ++w) {
+        if (w < warp) before += s_sum[w];
+        all += s_sum[w];
     }
-    __syncthreads();  // the old factor has been read, and s_top is free
-    if (threadIdx.x == 0) *factor = f;
+    return all;
+}
+
+// Where 16-byte piece c of slot s lies in a warp's tile.  K's reads take pieces j (or 4 + j) of slots 2i, 2i + 1 at
+// once, V's piece r of four even (or odd) slots: the exclusive or with these keeps either apart in the banks.
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(int s, int c) {
+    return D == 128 ? s * 128 + ((c ^ (s & 6) ^ ((s & 1) << 2)) << 4) : s * 64 + ((c ^ (s >> 1 & 3)) << 4);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+// The token into the block of slots that the warps' tiles (K's 16 slots, then V's) hold, and into the caches: `row` of this
+// warp's 16 slots is its own, where that is one of them, and the first n of them hold tokens.  All threads of the block
+// call it together.  kfac, vfac: the block's factors, before and after.
+template <typename E, int D>
+__device__ __forceinline__ void put_token(uint32_t tile, uint8_t *kc, uint8_t *vc, float *kf, float *vf, const E (*s_new)[D], int row,
+                                          int n, float &kfac, float &vfac, float (*s_top)[kStepWarps]) {
+    constexpr int P = D / 16, R = 32 / P;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = lane % P;
+    __syncthreads();  // s_new is there
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        uint32_t most = 0u;
+#pragma unroll
+        for (int x = 0; x < 16 / R; ++x) {
+            const int s = lane / P + R * x;
+            const uint4 w = lds16(tile + which * 16 * D + tile_at<D>(s, c));
+            const uint32_t a = __vmaxu4(w.x & 0x7f7f7f7fu, w.y & 0x7f7f7f7fu), e = __vmaxu4(w.z & 0x7f7f7f7fu, w.w & 0x7f7f7f7fu);
+            if (s != row) most = __vmaxu4(most, __vmaxu4(a, e));
+        }
+        most = __vmaxu4(most, most >> 16);
+        most = min(max(most & 0xffu, most >> 8 & 0xffu), 0x7eu);  // a NaN counts as the largest number
+        float val[16], top = 0.f;
+        load16(s_new[which] + 16 * c, val);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(val[j]));
+        if (most != 0u) top = fmaxf(top, unpack16<false>(f16x2_of(most)).x * (which == 0 ? kfac : vfac));
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+        if (lane == 0) s_top[which][warp] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const float *tops = s_top[which];
+        const float old = which == 0 ? kfac : vfac, f = factor_of(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]))), by = inverse(f);
+        uint8_t *to = which == 0 ? kc : vc;
+#pragma unroll 1
+        for (int s = lane / P; s < 16; s += R) {
+            if (s != row && (s >= n || f == old)) continue;
+            float val[16];
+            if (s == row) {
+                load16(s_new[which] + 16 * c, val);
+            } else {
+                decode16(lds16(tile + which * 16 * D + tile_at<D>(s, c)), val);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) val[j] *= old;
+            }
+            const uint4 code = code16(val, by);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile + which * 16 * D + tile_at<D>(s, c)), "r"(code.x), "r"(code.y),
+                         "r"(code.z), "r"(code.w)
+                         : "memory");
+            *reinterpret_cast<uint4 *>(to + s * D + 16 * c) = code;
+        }
+        if (threadIdx.x == 0) *(which == 0 ? kf : vf) = f;
+        (which == 0 ? kfac : vfac) = f;
+    }
+    __syncwarp();
+}
+
+constexpr int kC8Stages = 5;  // tiles of a warp on their way
+
+template <int D, int NG>
+constexpr int c8_smem() {
+    const int ring = kStepWarps * kC8Stages * 32 * D, parts = kStepWarps * 8 * NG * (D + 2) * 4;
+    return ring > parts ? ring : parts;
+}
+template <int D>
+constexpr size_t c8_part(size_t G) {  // floats of a part: G heads' sums, their maxima and totals
+    return G * (D + 2);
 }
 
 template <typename E, int D, int NG>
-__global__ void __launch_bounds__(128) c8_step_kernel(const E *__restrict__ q, const E *__restrict__ k, const E *__restrict__ v,
-                                                      uint8_t *kc, uint8_t *vc, float *kf, float *vf, E *__restrict__ o, Step8Args g) {
-    constexpr int NH = 8 * NG, KC = D / 64, M = D / 16;  // 64-column pieces; products of 16 columns of o
+__global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q, const E *__restrict__ k,
+                                                                       const E *__restrict__ v, uint8_t *kc, uint8_t *vc, float *kf,
+                                                                       float *vf, E *__restrict__ o, float *__restrict__ parts,
+                                                                       Cut8 *__restrict__ cuts, Step8Args g) {
+    constexpr int NH = 8 * NG, KC = D / 64, M = D / 16, P = D / 16;  // 64-column pieces; products of 16 columns of o; pieces of a slot
     constexpr bool BF = std::is_same<E, __nv_bfloat16>::value;
-    __shared__ float s_o[kStepWarps][NH][D], s_m[kStepWarps][NH], s_l[kStepWarps][NH], s_top[4];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
-    const int split = blockIdx.x % g.splits;
-    const long long unit = blockIdx.x / g.splits;
-    const int hk = (int)(unit % g.Hkv), b = (int)(unit / g.Hkv), G = g.H / g.Hkv;
-    E *ob = o + ((long long)b * g.H + hk * G) * D;
-    const long long p = g.pos[b];
-    if (p < 0) {  // the whole cluster leaves
-        if (split == 0)
-            for (int i = threadIdx.x; i < G * D / 2; i += blockDim.x) reinterpret_cast<uint32_t *>(ob)[i] = 0u;
-        return;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ __align__(16) E s_new[2][D];
+    __shared__ float s_top[2][kStepWarps];
+    __shared__ long long s_sum[kStepWarps], s_at[2];
+    // the ring of tiles, and after the slots the parts of the result
+    float(*s_o)[NH][D] = reinterpret_cast<float(*)[NH][D]>(smem);
+    float(*s_m)[NH] = reinterpret_cast<float(*)[NH]>(smem + kStepWarps * NH * D * 4);
+    float(*s_l)[NH] = s_m + kStepWarps;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3, G = g.H / g.Hkv;
+
+    // this block's share
+    long long all = 0, before;
+    for (int b0 = 0; b0 < g.B; b0 += 128) all += block_scan(b0 + (int)threadIdx.x < g.B ? held_blocks(g, b0 + threadIdx.x) : 0, before, s_sum);
+    all *= g.Hkv;
+    long long at = share_of(all, blockIdx.x);
+    const long long start = at, end = share_of(all, blockIdx.x + 1);
+    if (threadIdx.x == 0) cuts[blockIdx.x].unit = -1;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits for this grid's end
+    long long seen = 0;
+    for (int b0 = 0; b0 < g.B && at < end && seen <= at; b0 += 128) {
+        const int mine = b0 + (int)threadIdx.x < g.B ? held_blocks(g, b0 + threadIdx.x) : 0;
+        const long long more = block_scan((long long)mine * g.Hkv, before, s_sum);
+        before += seen;
+        if (before <= at && at < before + (long long)mine * g.Hkv) s_at[0] = b0 + threadIdx.x, s_at[1] = at - before;
+        seen += more;
     }
-    const long long mine = p < g.sinks ? p : g.sinks + (p - g.sinks) % g.window, n = min(p + 1, g.slots);
-    uint8_t *kb = kc + unit * g.slots * D, *vb = vc + unit * g.slots * D;
-    float *kfb = kf + unit * g.blocks, *vfb = vf + unit * g.blocks;
-    const long long used = (n + kC8Block - 1) / kC8Block, share = (used + g.splits - 1) / g.splits;
-    const long long first = split * share, end = min(used, first + share);
-    if (mine / kC8Block >= first && mine / kC8Block < end) {
-        const long long at = mine / kC8Block;
-        put_token<E, D>(kb, kfb + at, k + b * g.sk.b + hk * g.sk.h, at * kC8Block, mine, n, s_top);
-        put_token<E, D>(vb, vfb + at, v + b * g.sv.b + hk * g.sv.h, at * kC8Block, mine, n, s_top);
-        __syncthreads();
-    }
-    for (int h0 = 0; h0 < G; h0 += NH) {  // 16 heads at most, or the cache again (from L2)
-        const int nh = min(NH, G - h0);
-        uint32_t qf[NG][KC][8];
-        float fac[NG][2];
+    __syncthreads();
+    int b = 0, used = 1, hk = 0, first = 0;
+    if (at < end) b = (int)s_at[0], used = held_blocks(g, b), hk = (int)(s_at[1] / used), first = (int)(s_at[1] % used);
+
+    const uint32_t ring = smem_u32(smem) + warp * (kC8Stages * 32 * D), ring_end = ring + kC8Stages * 32 * D;
+    // where this lane's pieces go in a tile: the x-th 512 x bytes on, with the keys of tile_at the same for every other x
+    uint32_t at_lane[2] = {tile_at<D>(lane / P, lane % P), tile_at<D>(lane / P + 32 / P, lane % P) - 512u};
+    while (at < end) {
+        const long long unit = (long long)b * g.Hkv + hk, p = g.pos[b];
+        const int mine = (int)(p < g.sinks ? p : g.sinks + (p - g.sinks) % g.window), n = (int)min(p + 1, g.slots);
+        const int cnt = (int)min((long long)(used - first), end - at);
+        const bool whole = cnt == used;
+        uint8_t *kb = kc + unit * g.slots * D, *vb = vc + unit * g.slots * D;
+        float *kfb = kf + unit * g.blocks + first, *vfb = vf + unit * g.blocks + first;
+        const int own = mine / kC8Block - first;  // the token's block, where that is of this segment
+        // the warp's 16 slots of block i, which lie one behind the other; zeros behind the last that holds a token
+        const uint8_t *kl = kb + ((long long)first * kC8Block + 16 * warp) * D + 16 * lane;
+        const uint8_t *vl = vb + ((long long)first * kC8Block + 16 * warp) * D + 16 * lane;
+        auto fetch = [&](int i, uint32_t to) {
+            constexpr int R = 32 / P;
+            const int s0 = (first + i) * kC8Block + 16 * warp;
+            const long long from = (long long)i * (kC8Block * D);
+            if (s0 + 16 <= n) {
 #pragma unroll
-        for (int a = 0; a < NG; ++a) {
-            float x[KC][16], top = 0.f;
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[c][i] = 0.f;
-                if (8 * a + r < nh) load16(q + b * g.sq.b + (hk * G + h0 + 8 * a + r) * g.sq.h + 64 * c + 16 * j, x[c]);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[c][i]));
-            }
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);  // 2^(e - 127) <= top
-            const float up = __uint_as_float(e << 23), down = __uint_as_float((254u - e) << 23);
-#pragma unroll
-            for (int c = 0; c < KC; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) qf[a][c][i] = pack16<false>(make_float2(x[c][2 * i] * down, x[c][2 * i + 1] * down));
-            fac[a][0] = __shfl_sync(~0u, up, 8 * j) * g.c;  // of heads 2j, 2j + 1
-            fac[a][1] = __shfl_sync(~0u, up, 8 * j + 4) * g.c;
-        }
-        float acc[NG][M][4], m[NG][2], l[NG][2];
-#pragma unroll
-        for (int a = 0; a < NG; ++a) {
-            m[a][0] = m[a][1] = -INFINITY;
-            l[a][0] = l[a][1] = 0.f;
-#pragma unroll
-            for (int y = 0; y < M; ++y) acc[a][y][0] = acc[a][y][1] = acc[a][y][2] = acc[a][y][3] = 0.f;
-        }
-        uint4 kx[2][KC];
-        uint32_t vx[4][D / 32];
-        float kfac = 0.f, vfac = 0.f;
-        auto load = [&](long long blk) {
-            const long long s0 = blk * kC8Block + 16 * warp;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const long long s = s0 + r + 8 * i;
-                    kx[i][c] = s < n ? __ldcs(reinterpret_cast<const uint4 *>(kb + s * D + 64 * c + 16 * j)) : make_uint4(0u, 0u, 0u, 0u);
+                for (int x = 0; x < 16 / R; ++x) {
+                    cp_async16(to + at_lane[x & 1] + 512 * x, kl + from + 512 * x, 16u);
+                    cp_async16(to + 16 * D + at_lane[x & 1] + 512 * x, vl + from + 512 * x, 16u);
                 }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const long long s = s0 + 2 * j + (i & 1) + 8 * (i >> 1);
-                if constexpr (D == 128) {
-                    const uint4 w = s < n ? __ldcs(reinterpret_cast<const uint4 *>(vb + s * D + 16 * r)) : make_uint4(0u, 0u, 0u, 0u);
-                    vx[i][0] = w.x, vx[i][1] = w.y, vx[i][2] = w.z, vx[i][3] = w.w;
-                } else {
-                    const uint2 w = s < n ? __ldcs(reinterpret_cast<const uint2 *>(vb + s * D + 8 * r)) : make_uint2(0u, 0u);
-                    vx[i][0] = w.x, vx[i][1] = w.y;
+            } else {
+#pragma unroll 1
+                for (int x = 0; x < 16 / R; ++x) {
+                    const bool in = s0 + lane / P + R * x < n;
+                    cp_async16(to + at_lane[x & 1] + 512 * x, in ? kl + from + 512 * x : kb, in ? 16u : 0u);
+                    cp_async16(to + 16 * D + at_lane[x & 1] + 512 * x, in ? vl + from + 512 * x : vb, in ? 16u : 0u);
                 }
             }
-            kfac = kfb[blk], vfac = fmaxf(vfb[blk], 0x1p-64f);
         };
-        if (first < end) load(first);
-        for (long long blk = first; blk < end; ++blk) {
-            const long long s0 = blk * kC8Block + 16 * warp;
-            const bool in0 = s0 + r < n, in1 = s0 + r + 8 < n;
-            const float lift = __log2f(vfac), less = __frcp_rn(vfac);
-            uint32_t pw[NG][2];
+        for (int h0 = 0; h0 < G; h0 += NH) {  // 16 heads at most, or the segment again (from L2)
+            const int nh = min(NH, G - h0);
+#pragma unroll 1
+            for (int i = 0; i < kC8Stages; ++i) {
+                if (i < cnt) fetch(i, ring + i * (32 * D));
+                cp_async_commit();
+            }
+            if (h0 == 0 && threadIdx.x < 2 * P * 2) {  // the token's key and value
+                const int which = threadIdx.x / (2 * P), c = threadIdx.x % (2 * P);
+                const E *x = which == 0 ? k + b * g.sk.b + hk * g.sk.h : v + b * g.sv.b + hk * g.sv.h;
+                reinterpret_cast<uint4 *>(s_new[which])[c] = reinterpret_cast<const uint4 *>(x)[c];
+            }
+            uint32_t qf[NG][KC][8];
+            float fac[NG][2];
 #pragma unroll
             for (int a = 0; a < NG; ++a) {
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
+                float x[KC][16], top = 0.f;
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
-                    const uint32_t w0[4] = {kx[0][c].x, kx[0][c].y, kx[0][c].z, kx[0][c].w};
-                    const uint32_t w1[4] = {kx[1][c].x, kx[1][c].y, kx[1][c].z, kx[1][c].w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma16x8<false>(s, f16x2_of(w0[i]), f16x2_of(w1[i]), f16x2_of(w0[i] >> 16), f16x2_of(w1[i] >> 16), qf[a][c][2 * i],
-                                       qf[a][c][2 * i + 1]);
+                    for (int i = 0; i < 16; ++i) x[c][i] = 0.f;
+                    if (8 * a + r < nh) load16(q + b * g.sq.b + (hk * G + h0 + 8 * a + r) * g.sq.h + 64 * c + 16 * j, x[c]);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[c][i]));
                 }
-                // s: (slot r, heads 2j, 2j + 1), (slot r + 8, the same heads)
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);  // 2^(e - 127) <= top
+                const float up = __uint_as_float(e << 23), down = __uint_as_float((254u - e) << 23);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = (i < 2 ? in0 : in1) ? fmaf(s[i], fac[a][i & 1] * kfac, lift) : -INFINITY;
-                float top[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
-                if (__any_sync(~0u, top[0] > m[a][0] + 8.f || top[1] > m[a][1] + 8.f)) {
+                for (int c = 0; c < KC; ++c)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int i = 0; i < 8; ++i) qf[a][c][i] = pack16<false>(make_float2(x[c][2 * i] * down, x[c][2 * i + 1] * down));
+                fac[a][0] = __shfl_sync(~0u, up, 8 * j) * g.c;  // of heads 2j, 2j + 1
+                fac[a][1] = __shfl_sync(~0u, up, 8 * j + 4) * g.c;
+            }
+            // per head: the exponent's offset (the maximum less 7; infinity before there is one) and the total
+            float acc[NG][M][4], mu[NG][2], l[NG][2];
 #pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(~0u, top[e], x));
-                        const float mn = fmaxf(m[a][e], top[e]), f = mn == -INFINITY ? 1.f : ex2(m[a][e] - mn);
-                        m[a][e] = mn;
-                        l[a][e] *= f;
+            for (int a = 0; a < NG; ++a) {
+                mu[a][0] = mu[a][1] = -INFINITY;
+                l[a][0] = l[a][1] = 0.f;
 #pragma unroll
-                        for (int y = 0; y < M; ++y) acc[a][y][e] *= f, acc[a][y][2 + e] *= f;
+                for (int y = 0; y < M; ++y) acc[a][y][0] = acc[a][y][1] = acc[a][y][2] = acc[a][y][3] = 0.f;
+            }
+            float kfs = 0.f, vfs = 0.f, lifts = 0.f, lesses = 0.f;  // the factors of 32 blocks, one in each lane
+            uint32_t tile = ring;
+#pragma unroll 1
+            for (int i = 0; i < cnt; ++i) {
+                if (i % 32 == 0 && i + lane < cnt) {
+                    kfs = __ldcg(kfb + i + lane), vfs = __ldcg(vfb + i + lane);
+                    lifts = __log2f(fmaxf(vfs, 0x1p-64f)), lesses = __frcp_rn(fmaxf(vfs, 0x1p-64f));
+                }
+                float kfac = __shfl_sync(~0u, kfs, i % 32), lift = __shfl_sync(~0u, lifts, i % 32), less = __shfl_sync(~0u, lesses, i % 32);
+                cp_async_wait<kC8Stages - 1>();
+                __syncwarp();
+                const int left = n - (first + i) * kC8Block - 16 * warp;  // slots from the warp's first that hold a token
+                if (h0 == 0 && i == own) {
+                    float vfac = __shfl_sync(~0u, vfs, i % 32);
+                    const int s0 = n - left;
+                    put_token<E, D>(tile, kb + (long long)s0 * D, vb + (long long)s0 * D, kfb + i, vfb + i, s_new, mine - s0, left, kfac,
+                                    vfac, s_top);
+                    lift = __log2f(vfac), less = inverse(vfac);
+                }
+                uint4 kx[2][KC];
+                uint32_t vx[4][D / 32];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) kx[x][c] = lds16(tile + tile_at<D>(r, 4 * c + j) + 8 * x * D);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if constexpr (D == 128) {
+                        const uint4 w = lds16(tile + 16 * D + tile_at<D>(2 * j + (x & 1), r) + 8 * (x >> 1) * D);
+                        vx[x][0] = w.x, vx[x][1] = w.y, vx[x][2] = w.z, vx[x][3] = w.w;
+                    } else {
+                        const uint2 w = lds8(tile + 16 * D + tile_at<D>(2 * j + (x & 1), r >> 1) + 8 * (r & 1) + 8 * (x >> 1) * D);
+                        vx[x][0] = w.x, vx[x][1] = w.y;
                     }
                 }
-                const float mu[2] = {m[a][0] == -INFINITY ? 0.f : m[a][0] - 7.f, m[a][1] == -INFINITY ? 0.f : m[a][1] - 7.f};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 e = make_float2(ex2(s[2 * i] - mu[0]), ex2(s[2 * i + 1] - mu[1]));
-                    l[a][0] = fmaf(e.x, less, l[a][0]);
-                    l[a][1] = fmaf(e.y, less, l[a][1]);
-                    pw[a][i] = transpose8x8(pack16<false>(e));
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < D / 32; ++y) {
-                // two columns of d a product: 4 y + 0, 1 and 4 y + 2, 3 of this lane's
-                const uint32_t a0 = __byte_perm(vx[0][y], vx[1][y], 0x5140), a1 = __byte_perm(vx[0][y], vx[1][y], 0x7362);
-                const uint32_t b0 = __byte_perm(vx[2][y], vx[3][y], 0x5140), b1 = __byte_perm(vx[2][y], vx[3][y], 0x7362);
-                const uint32_t f0 = f16x2_of(a0), f1 = f16x2_of(a0 >> 16), f2 = f16x2_of(b0), f3 = f16x2_of(b0 >> 16);
-                const uint32_t h0_ = f16x2_of(a1), h1 = f16x2_of(a1 >> 16), h2 = f16x2_of(b1), h3 = f16x2_of(b1 >> 16);
+                __syncwarp();
+                if (i + kC8Stages < cnt) fetch(i + kC8Stages, tile);
+                cp_async_commit();
+                tile = tile + 32 * D == ring_end ? ring : tile + 32 * D;
+                uint32_t pw[NG][2], pl[NG][2];
 #pragma unroll
                 for (int a = 0; a < NG; ++a) {
-                    mma16x8<false>(acc[a][2 * y], f0, f1, f2, f3, pw[a][0], pw[a][1]);
-                    mma16x8<false>(acc[a][2 * y + 1], h0_, h1, h2, h3, pw[a][0], pw[a][1]);
+                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) {
+                        const uint32_t w0[4] = {kx[0][c].x, kx[0][c].y, kx[0][c].z, kx[0][c].w};
+                        const uint32_t w1[4] = {kx[1][c].x, kx[1][c].y, kx[1][c].z, kx[1][c].w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mma16x8<false>(s, f16x2_of(w0[x]), f16x2_of(w1[x]), f16x2_of(w0[x] >> 16), f16x2_of(w1[x] >> 16),
+                                           qf[a][c][2 * x], qf[a][c][2 * x + 1]);
+                    }
+                    // s: (slot r, heads 2j, 2j + 1), (slot r + 8, the same heads); z: the weights' exponents
+                    const float f0 = fac[a][0] * kfac, f1 = fac[a][1] * kfac;
+                    float z[4];
+                    auto exponents = [&](float by0, float by1) {
+                        z[0] = fmaf(s[0], f0, by0), z[1] = fmaf(s[1], f1, by1), z[2] = fmaf(s[2], f0, by0), z[3] = fmaf(s[3], f1, by1);
+                        if (left < 16) {
+                            if (r >= left) z[0] = z[1] = -INFINITY;
+                            if (r + 8 >= left) z[2] = z[3] = -INFINITY;
+                        }
+                    };
+                    exponents(lift - mu[a][0], lift - mu[a][1]);
+                    if (__any_sync(~0u, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > 15.f)) {
+                        exponents(lift, lift);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float top = fmaxf(z[e], z[2 + e]);
+#pragma unroll
+                            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+                            const float mn = fmaxf(mu[a][e], top - 7.f), f = mn == -INFINITY ? 1.f : ex2(mu[a][e] - mn);
+                            mu[a][e] = mn;
+                            l[a][e] *= f;
+#pragma unroll
+                            for (int y = 0; y < M; ++y) acc[a][y][e] *= f, acc[a][y][2 + e] *= f;
+                        }
+                        exponents(lift - mu[a][0], lift - mu[a][1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) z[x] = ex2(z[x]);
+                    l[a][0] = fmaf(z[0] + z[2], less, l[a][0]);
+                    l[a][1] = fmaf(z[1] + z[3], less, l[a][1]);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t h = pack16<false>(make_float2(z[2 * x], z[2 * x + 1]));
+                        pw[a][x] = transpose8x8(h);
+                        if constexpr (!BF) {
+                            const float2 e = unpack16<false>(h);
+                            pl[a][x] = transpose8x8(pack16<false>(make_float2(z[2 * x] - e.x, z[2 * x + 1] - e.y)));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) {
+                    // two columns of d a product: 4 y + 0, 1 and 4 y + 2, 3 of this lane's
+                    const uint32_t a0 = __byte_perm(vx[0][y], vx[1][y], 0x5140), a1 = __byte_perm(vx[0][y], vx[1][y], 0x7362);
+                    const uint32_t b0 = __byte_perm(vx[2][y], vx[3][y], 0x5140), b1 = __byte_perm(vx[2][y], vx[3][y], 0x7362);
+                    const uint32_t f0 = f16x2_of(a0), f1 = f16x2_of(a0 >> 16), f2 = f16x2_of(b0), f3 = f16x2_of(b0 >> 16);
+                    const uint32_t f4 = f16x2_of(a1), f5 = f16x2_of(a1 >> 16), f6 = f16x2_of(b1), f7 = f16x2_of(b1 >> 16);
+#pragma unroll
+                    for (int a = 0; a < NG; ++a) {
+                        mma16x8<false>(acc[a][2 * y], f0, f1, f2, f3, pw[a][0], pw[a][1]);
+                        mma16x8<false>(acc[a][2 * y + 1], f4, f5, f6, f7, pw[a][0], pw[a][1]);
+                        if constexpr (!BF) {
+                            mma16x8<false>(acc[a][2 * y], f0, f1, f2, f3, pl[a][0], pl[a][1]);
+                            mma16x8<false>(acc[a][2 * y + 1], f4, f5, f6, f7, pl[a][0], pl[a][1]);
+                        }
+                    }
                 }
             }
-            if (blk + 1 < end) load(blk + 1);
-        }
-        // product y, row r: column (D / 8) r + 2 y, row r + 8: the next one
+            __syncthreads();  // the last tiles have been read: the parts take the ring's place
+            // product y, row r: column (D / 8) r + 2 y, row r + 8: the next one
 #pragma unroll
-        for (int a = 0; a < NG; ++a)
+            for (int a = 0; a < NG; ++a)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) l[a][e] += __shfl_xor_sync(~0u, l[a][e], x);
-                const int h = 8 * a + 2 * j + e;
-                if (r == 0) s_m[warp][h] = m[a][e], s_l[warp][h] = l[a][e];
+                    for (int x = 4; x < 32; x <<= 1) l[a][e] += __shfl_xor_sync(~0u, l[a][e], x);
+                    const int h = 8 * a + 2 * j + e;
+                    if (r == 0) s_m[warp][h] = mu[a][e], s_l[warp][h] = l[a][e];
 #pragma unroll
-                for (int y = 0; y < M; ++y)
-                    *reinterpret_cast<float2 *>(&s_o[warp][h][D / 8 * r + 2 * y]) = make_float2(acc[a][y][e], acc[a][y][2 + e]);
+                    for (int y = 0; y < M; ++y)
+                        *reinterpret_cast<float2 *>(&s_o[warp][h][D / 8 * r + 2 * y]) = make_float2(acc[a][y][e], acc[a][y][2 + e]);
+                }
+            __syncthreads();
+            // the warps' parts together: the outputs of a whole segment, or a part for the join
+            const int slot = 2 * blockIdx.x + (at != start);
+            float *part = parts + slot * c8_part<D>(G);
+            for (int i = threadIdx.x; i < nh * D / 2; i += blockDim.x) {
+                const int h = i / (D / 2), d = i % (D / 2) * 2;
+                float mm = s_m[0][h];
+#pragma unroll
+                for (int w = 1; w < kStepWarps; ++w) mm = fmaxf(mm, s_m[w][h]);
+                float lt = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+                for (int w = 0; w < kStepWarps; ++w) {
+                    const float f = ex2(s_m[w][h] - mm);
+                    const float2 e = *reinterpret_cast<const float2 *>(&s_o[w][h][d]);
+                    lt = fmaf(f, s_l[w][h], lt), x = fmaf(f, e.x, x), y = fmaf(f, e.y, y);
+                }
+                if (whole) {
+                    reinterpret_cast<uint32_t *>(o + (unit * G + h0) * D)[i] = pack16<BF>(make_float2(x / lt, y / lt));
+                } else {
+                    reinterpret_cast<float2 *>(part + h0 * D)[i] = make_float2(x, y);
+                    if (d == 0) reinterpret_cast<float2 *>(part + G * D)[h0 + h] = make_float2(mm, lt);
+                }
             }
-        __syncthreads();
-        // the warps' parts into the first's
-        for (int i = threadIdx.x; i < NH * D; i += blockDim.x) {
-            const int h = i / D, d = i % D;
-            float mm = s_m[0][h];
-#pragma unroll
-            for (int w = 1; w < kStepWarps; ++w) mm = fmaxf(mm, s_m[w][h]);
-            const float mu = mm == -INFINITY ? 0.f : mm;
-            float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < kStepWarps; ++w) s += s_o[w][h][d] * ex2(s_m[w][h] - mu);
-            s_o[0][h][d] = s;
+            __syncthreads();  // the ring is free again
         }
-        __syncthreads();
-        if (threadIdx.x < NH) {
-            const int h = threadIdx.x;
-            float mm = s_m[0][h], s = 0.f;
-#pragma unroll
-            for (int w = 1; w < kStepWarps; ++w) mm = fmaxf(mm, s_m[w][h]);
-            const float mu = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-            for (int w = 0; w < kStepWarps; ++w) s += s_l[w][h] * ex2(s_m[w][h] - mu);
-            s_m[0][h] = mm;
-            s_l[0][h] = s;
+        if (!whole && first == 0 && threadIdx.x == 0) {
+            // the thread block that has the pair's last block of slots: the least c with share_of(c + 1) >= at + used
+            const long long x = at + used;
+            cuts[blockIdx.x] = Cut8{(int)unit, 2 * (int)blockIdx.x + (at != start), (int)((x * gridDim.x + all - 1) / all) - 1, (int)all};
         }
-        if (g.splits > 1) cluster_sync();
-        else __syncthreads();
-        // each block of the cluster finishes its share of the outputs
-        const uint32_t ao = smem_u32(&s_o[0][0][0]), am = smem_u32(&s_m[0][0]), al = smem_u32(&s_l[0][0]);
-        for (int i = split * blockDim.x + threadIdx.x; i < nh * D / 2; i += g.splits * blockDim.x) {
-            const int h = i / (D / 2), d = i % (D / 2) * 2;
-            float mm = -INFINITY;
-            for (int w = 0; w < g.splits; ++w) mm = fmaxf(mm, ld_cluster(map_rank(am + 4 * h, w)));
-            float lt = 0.f, x = 0.f, y = 0.f;
-            for (int w = 0; w < g.splits; ++w) {
-                const float f = ex2(ld_cluster(map_rank(am + 4 * h, w)) - mm);
-                const uint32_t at = map_rank(ao + 4 * (h * D + d), w);
-                lt += f * ld_cluster(map_rank(al + 4 * h, w));
-                x += f * ld_cluster(at);
-                y += f * ld_cluster(at + 4);
-            }
-            reinterpret_cast<uint32_t *>(ob + (long long)h0 * D)[i] = pack16<BF>(make_float2(x / lt, y / lt));
+        at += cnt;
+        first = 0;
+        if (at < end && ++hk == g.Hkv) {
+            hk = 0;
+            do used = held_blocks(g, ++b);
+            while (used == 0);
         }
-        if (g.splits > 1) cluster_sync();  // no block leaves, or starts anew, while its part is being read
-        else __syncthreads();
+    }
+    // rows without a sequence
+    for (b = blockIdx.x; b < g.B; b += gridDim.x)
+        if (g.pos[b] < 0)
+            for (int i = threadIdx.x; i < g.H * D / 2; i += blockDim.x)
+                reinterpret_cast<uint32_t *>(o + (long long)b * g.H * D)[i] = 0u;
+}
+
+// Adds the parts of a cut (sequence, key head), for a query head of the group: warps take every eighth part, which meet
+// in a fixed order.
+template <typename E, int D>
+__global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ parts, const Cut8 *__restrict__ cuts, E *__restrict__ o, int G) {
+    constexpr int W = 8, N = D / 32;
+    __shared__ float s_o[W][D], s_m[W], s_l[W];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Cut8 cut = cuts[blockIdx.x];
+    if (cut.unit < 0) return;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.y, n = cut.last - (int)blockIdx.x + 1;
+    float m = -INFINITY, l = 0.f, x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = 0.f;
+    for (int i = warp; i < n; i += W) {
+        const unsigned c = blockIdx.x + i;
+        if (share_of(cut.all, c) == share_of(cut.all, c + 1)) continue;  // more thread blocks than blocks of slots
+        const float *part = parts + (i == 0 ? cut.slot : 2 * (int)c) * c8_part<D>(G);
+        const float2 ml = reinterpret_cast<const float2 *>(part + G * D)[h];
+        const float mn = fmaxf(m, ml.x), a = mn == -INFINITY ? 0.f : ex2(m - mn), f = mn == -INFINITY ? 0.f : ex2(ml.x - mn);
+        m = mn;
+        l = l * a + ml.y * f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = x[e] * a + part[h * D + 32 * e + lane] * f;
+    }
+    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+#pragma unroll
+    for (int e = 0; e < N; ++e) s_o[warp][32 * e + lane] = x[e];
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += 256) {
+        float mm = s_m[0], lt = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 1; w < W; ++w) mm = fmaxf(mm, s_m[w]);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float f = ex2(s_m[w] - mm);
+            lt += f * s_l[w], y += f * s_o[w][d];
+        }
+        o[((long long)cut.unit * G + h) * D + d] = from_f32<E>(y / lt);
     }
 }
 
@@ -418,61 +606,47 @@ int c8_check(const char *fn, int64_t B, int64_t H, int64_t Hkv, int64_t T, int64
     return CLA_OK;
 }
 
-constexpr int kC8Splits = 16;  // blocks of a cluster; above 8 with the kernel's leave
-
-void c8_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &at, long long clusters, int splits, cudaStream_t s) {
-    cfg.gridDim = dim3((unsigned)(clusters * splits));
-    cfg.blockDim = dim3(kStepWarps * 32);
-    cfg.stream = s;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)splits;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-}
-
-// Clusters of each size that the current device runs at once (0: none), asked for once per device.
+// Blocks of the step that the current device runs at once, asked for once per device.
 template <typename E, int D, int NG>
-int c8_resident(const char *fn, int (&n)[kC8Splits + 1]) {
-    static std::atomic<int> known[64][kC8Splits + 1];  // the number and 1
-    int dev = 0;
+int c8_resident(const char *fn, int *n) {
+    static std::atomic<int> known[64];
+    static std::atomic<unsigned long long> done{0};
+    constexpr int smem = c8_smem<D, NG>();
+    int dev = 0, sms = 0;
     CLA_CUDA_TRY(cudaGetDevice(&dev), fn);
-    const bool keep = dev < 64;
-    for (int s = 1; s <= kC8Splits; ++s) {
-        n[s] = keep ? known[dev][s].load(std::memory_order_relaxed) - 1 : -1;
-        if (n[s] >= 0) continue;
-        if (s > 8)
-            CLA_CUDA_TRY(cudaFuncSetAttribute((const void *)c8_step_kernel<E, D, NG>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), fn);
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute at;
-        c8_config(cfg, at, 1, s, nullptr);
-        CLA_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n[s], c8_step_kernel<E, D, NG>, &cfg), fn);
-        if (keep) known[dev][s].store(n[s] + 1, std::memory_order_relaxed);
-    }
+    *n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*n != 0) return CLA_OK;
+    if (int st = set_max_dynamic_smem(done, (const void *)c8_step_kernel<E, D, NG>, smem)) return st;
+    if (int st = multiprocessors(fn, &sms)) return st;
+    CLA_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, c8_step_kernel<E, D, NG>, kStepWarps * 32, smem), fn);
+    *n = *n * sms < kC8MaxBlocks ? *n * sms : kC8MaxBlocks;
+    if (dev < 64) known[dev].store(*n, std::memory_order_relaxed);
     return CLA_OK;
 }
 
-// Splits the slots of a (sequence, key head) over as many blocks as give the least rounds of clusters times the blocks
-// of slots of each; a round's latency and join count as 4.
 template <typename E, int D, int NG>
-int c8_step(const char *fn, const void *q, const void *k, const void *v, void *kc, void *vc, float *kf, float *vf, void *o, int64_t B,
-            Step8Args g, cudaStream_t s) {
-    int resident[kC8Splits + 1];
-    if (int st = c8_resident<E, D, NG>(fn, resident)) return st;
-    const long long units = B * g.Hkv;
-    g.splits = 1;
-    long long least = -1;
-    for (int n = 1; n <= kC8Splits && n <= g.blocks; ++n) {
-        if (resident[n] == 0 || units * n >= 2147483648ll) continue;
-        const long long cost = (units + resident[n] - 1) / resident[n] * ((g.blocks + n - 1) / n + 4);
-        if (least < 0 || cost < least) least = cost, g.splits = n;
-    }
+int c8_step(const char *fn, const void *q, const void *k, const void *v, void *kc, void *vc, float *kf, float *vf, void *o,
+            const Step8Args &g, void *ws, cudaStream_t s) {
+    int n = 0;
+    if (int st = c8_resident<E, D, NG>(fn, &n)) return st;
+    const long long most = (long long)g.B * g.Hkv * g.blocks;
+    const unsigned grid = (unsigned)(most < n ? most : n);
+    Cut8 *cuts = static_cast<Cut8 *>(ws);
+    float *parts = reinterpret_cast<float *>(cuts + kC8MaxBlocks);
+    c8_step_kernel<E, D, NG><<<grid, kStepWarps * 32, c8_smem<D, NG>(), s>>>(
+        (const E *)q, (const E *)k, (const E *)v, (uint8_t *)kc, (uint8_t *)vc, kf, vf, (E *)o, parts, cuts, g);
+    if (int st = check_launch(fn)) return st;
+    // the join's launch goes beside the step's end
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at;
-    c8_config(cfg, at, units, g.splits, s);
-    CLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, c8_step_kernel<E, D, NG>, (const E *)q, (const E *)k, (const E *)v, (uint8_t *)kc, (uint8_t *)vc, kf,
-                                    vf, (E *)o, g),
-                 fn);
+    cfg.gridDim = dim3(grid, (unsigned)(g.H / g.Hkv));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    CLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, c8_join_kernel<E, D>, (const float *)parts, (const Cut8 *)cuts, (E *)o, g.H / g.Hkv), fn);
     return check_launch(fn);
 }
 
@@ -512,17 +686,28 @@ extern "C" int cla_window_cache8_write(const void *k, const void *v, const int32
     return check_launch(fn);
 }
 
+extern "C" size_t cla_window_attn_step8_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
+    if (c8_check("cla_window_attn_step8_workspace_size", B, H, Hkv, 1, d, window, sinks, CLA_BF16, 1.f) != CLA_OK) return 0;
+    const int64_t most = B * Hkv * ((sinks + window + kC8Block - 1) / kC8Block);  // a thread block has one block of slots at least
+    return sizeof(Cut8) * kC8MaxBlocks + (size_t)(2 * (most < kC8MaxBlocks ? most : kC8MaxBlocks) * (Hkv ? H / Hkv : 0) * (d + 2) * 4);
+}
+
 extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v, void *kcache, void *vcache, float *kscale,
                                      float *vscale, const int32_t *pos, void *o, float scale, int64_t window, int64_t sinks, int dtype,
-                                     int64_t B, int64_t H, int64_t Hkv, int64_t d, const int64_t *strides, void *stream) {
+                                     int64_t B, int64_t H, int64_t Hkv, int64_t d, const int64_t *strides, void *ws, size_t ws_bytes,
+                                     void *stream) {
     const char *fn = "cla_window_attn_step8";
     clear_error();
     if (int st = c8_check(fn, B, H, Hkv, 1, d, window, sinks, dtype, scale)) return st;
     if (B * H == 0) return CLA_OK;
+    if (H / Hkv > 65535) return fail(CLA_ERR_UNSUPPORTED, "%s: %lld query heads of a key head", fn, (long long)(H / Hkv));
     if (!q || !k || !v || !kcache || !vcache || !kscale || !vscale || !pos || !o)
         return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned_or_null({q, k, v, kcache, vcache, o}, 16) || !aligned_or_null({pos, kscale, vscale}, 4))
         return fail(CLA_ERR_INVALID_ARG, "%s: a pointer is misaligned", fn);
+    const size_t need = cla_window_attn_step8_workspace_size(B, H, Hkv, d, window, sinks);
+    if (ws == nullptr || !aligned16(ws) || ws_bytes < need)
+        return fail(CLA_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
     static const char *const names[] = {"q", "k", "v"};
     const int64_t heads[] = {H, Hkv, Hkv}, ds[] = {d, d, d};
     Triple r[3];
@@ -530,13 +715,13 @@ extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v
     if (strides != nullptr)
         for (int i = 0; i < 3; ++i) full[3 * i] = strides[2 * i], full[3 * i + 1] = strides[2 * i + 1], full[3 * i + 2] = d;
     if (int st = view_strides(fn, strides ? full : nullptr, names, heads, ds, 3, B, 1, 8, r)) return st;
-    const Step8Args g{pos,    scale * 1.4426950408889634f, window, sinks, sinks + window, (int)H, (int)Hkv, 1,
+    const Step8Args g{pos,      scale * 1.4426950408889634f, window, sinks, sinks + window, (int)B, (int)H, (int)Hkv,
                       (int)((sinks + window + kC8Block - 1) / kC8Block), r[0], r[1], r[2]};
     cudaStream_t s = (cudaStream_t)stream;
     const bool bf = dtype == CLA_BF16, wide = H / Hkv > 8;
-#define CLA_STEP8(E, D)                                                                             \
-    (wide ? c8_step<E, D, 2>(fn, q, k, v, kcache, vcache, kscale, vscale, o, B, g, s) \
-          : c8_step<E, D, 1>(fn, q, k, v, kcache, vcache, kscale, vscale, o, B, g, s))
+#define CLA_STEP8(E, D)                                                                                \
+    (wide ? c8_step<E, D, 2>(fn, q, k, v, kcache, vcache, kscale, vscale, o, g, ws, s) \
+          : c8_step<E, D, 1>(fn, q, k, v, kcache, vcache, kscale, vscale, o, g, ws, s))
     if (d == 128) return bf ? CLA_STEP8(__nv_bfloat16, 128) : CLA_STEP8(__half, 128);
     return bf ? CLA_STEP8(__nv_bfloat16, 64) : CLA_STEP8(__half, 64);
 #undef CLA_STEP8

@@ -774,13 +774,20 @@ int cla_window_cache8_write(const void *k, const void *v, const int32_t *lens,
  * then holds, the token's own key and value included.  Other blocks are read
  * only.  The weights are rounded to 11 bits for their product with the cache's
  * numbers.
- * The arguments are cla_window_attn_step's, with the caches above. */
+ * The arguments are cla_window_attn_step's, with the caches above; the order of
+ * the sums is fixed by the sizes, the positions and the device model.
+ * B * Hkv * ceil((sinks + window) / 64) is below 2^31, H / Hkv below 2^16. */
 int cla_window_attn_step8(const void *q, const void *k, const void *v, void *kcache,
                           void *vcache, float *kscale, float *vscale,
                           const int32_t *pos, void *o, float scale, int64_t window,
                           int64_t sinks, int dtype, int64_t B, int64_t H,
-                          int64_t Hkv, int64_t d, const int64_t *strides,
-                          void *stream);
+                          int64_t Hkv, int64_t d, const int64_t *strides, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* Bytes of workspace for cla_window_attn_step8; 0 for what the call refuses. */
+size_t cla_window_attn_step8_workspace_size(int64_t B, int64_t H, int64_t Hkv,
+                                            int64_t d, int64_t window,
+                                            int64_t sinks);
 
 /* ======================================================================== */
 /* Norm and rotation of queries and keys                                    */

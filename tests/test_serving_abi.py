@@ -69,9 +69,11 @@ def cwrite(lib, q=A, kc=A, ks=A, lens=None, pos=None, o=None, scale=None, window
     return lib.cla_window_cache8_write(q, A, lens, kc, A, ks, A, window, sinks, dtype, B, K, T, d, _arr(s), None)
 
 
-def cstep(lib, q=A, kc=A, ks=A, lens=A, o=A, scale=0.1, window=100, sinks=2, dtype=1, B=2, H=4, K=2, T=1, d=64, s=None):
+def cstep(lib, q=A, kc=A, ks=A, lens=A, o=A, scale=0.1, window=100, sinks=2, dtype=1, B=2, H=4, K=2, T=1, d=64, s=None,
+          ws=WS, nbytes=BIG):
     s = None if s is None else [x for x in s[:2]] * 3
-    return lib.cla_window_attn_step8(q, A, A, kc, A, ks, A, lens, o, scale, window, sinks, dtype, B, H, K, d, _arr(s), None)
+    return lib.cla_window_attn_step8(q, A, A, kc, A, ks, A, lens, o, scale, window, sinks, dtype, B, H, K, d, _arr(s), ws, nbytes,
+                                     None)
 
 
 @pytest.mark.parametrize("call", [cwrite, cstep])
@@ -90,6 +92,9 @@ def test_cache8_calls(lib):
     for kw in (dict(H=5), dict(H=0), dict(K=0), dict(H=-4), dict(scale=float("nan")), dict(scale=float("inf")), dict(o=None),
                dict(lens=None), dict(o=ODD)):
         assert cstep(lib, **kw) == 1, kw
+    assert cstep(lib, ws=None) == 5 and cstep(lib, ws=ODD) == 5 and cstep(lib, nbytes=1000) == 5 and cstep(lib, H=1 << 17, K=1) == 2
+    assert lib.cla_window_attn_step8_workspace_size(2, 4, 2, 64, 100, 2) > 8 * 2 * 66 * 4
+    assert lib.cla_window_attn_step8_workspace_size(2, 4, 3, 64, 100, 2) == 0
     assert cwrite(lib, T=-1) == 1 and cwrite(lib, T=1 << 31) == 2
     assert cwrite(lib, B=0) == 0 and cwrite(lib, T=0) == 0 and cstep(lib, B=0) == 0 and cstep(lib, H=0, K=0) == 0
 
