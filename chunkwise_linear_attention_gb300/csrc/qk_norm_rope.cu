@@ -29,15 +29,16 @@
 namespace cla {
 namespace {
 
-constexpr int kQnThreads = 256;
-constexpr int kQnBlocks = 456;  // of the backward: 3 for each of 152 multiprocessors
+// Persistent blocks, for 152 multiprocessors: forward 2 for each, backward one (its lanes hold 16 sums of dw as well, 170
+// registers; with 128 they went to local memory and the backward took 100 us where it takes 70).
+constexpr int kFwdThreads = 256, kFwdBlocks = 304, kBwdThreads = 384, kBwdBlocks = 152;
 
 struct QnArgs {
     const float *w[2], *freq;  // of queries and keys
     const int32_t *pos, *lens;
     float eps, inv_d;
-    int B, T, heads[2], d, rot, span, spans;  // span: heads that a group of lanes walks over
-    long long items;
+    int T, heads[2], d, rot;
+    long long tokens, tiles;  // tiles: of as many tokens as a warp has groups of lanes
 };
 
 // freq / 2 pi as a signed fraction of a turn in 64 bits
@@ -52,95 +53,101 @@ __device__ __forceinline__ unsigned long long turns(float f) {
     else t = e > -128 ? hi >> (-e - 64) : 0ull;
     return f < 0.f ? 0ull - t : t;
 }
-__device__ __forceinline__ void sincos_at(float f, int pos, float &s, float &c) {
-    const unsigned long long phase = turns(f) * (unsigned long long)(long long)pos;
+__device__ __forceinline__ void sincos_at(unsigned long long turn, int pos, float &s, float &c) {
+    const unsigned long long phase = turn * (unsigned long long)(long long)pos;
     sincospif((float)(int)(unsigned int)(phase >> 32) * 0x1p-31f, &s, &c);
 }
 
-// 8 values as they lie in memory
-template <typename E>
-struct Piece {
-    uint4 v;
-};
-template <>
-struct Piece<float> {
-    uint4 v, w;
-};
-template <typename E>
-__device__ __forceinline__ Piece<E> load_piece(const E *p) {
-    Piece<E> r;
-    r.v = __ldcs(reinterpret_cast<const uint4 *>(p));
-    if constexpr (sizeof(E) == 4) r.w = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
-    return r;
-}
-__device__ __forceinline__ float2 pair_f32(uint32_t u, __nv_bfloat16) { return __bfloat1622float2(reinterpret_cast<__nv_bfloat162 &>(u)); }
+__device__ __forceinline__ float2 pair_f32(uint32_t u, float) { return make_float2(0.f, 0.f); }
+__device__ __forceinline__ float2 pair_f32(uint32_t u, __nv_bfloat16) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
 __device__ __forceinline__ float2 pair_f32(uint32_t u, __half) { return __half22float2(reinterpret_cast<__half2 &>(u)); }
-__device__ __forceinline__ uint32_t pair_of(float a, float b, __nv_bfloat16) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return reinterpret_cast<uint32_t &>(v);
+__device__ __forceinline__ uint32_t pair_of(float2 v, float) { return 0u; }
+__device__ __forceinline__ uint32_t pair_of(float2 v, __nv_bfloat16) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    return reinterpret_cast<const uint32_t &>(h);
 }
-__device__ __forceinline__ uint32_t pair_of(float a, float b, __half) {
-    __half2 v = __floats2half2_rn(a, b);
-    return reinterpret_cast<uint32_t &>(v);
-}
-template <typename E>
-__device__ __forceinline__ void unpack(const Piece<E> &p, float *x) {
-    if constexpr (sizeof(E) == 4) {
-        const uint32_t u[8] = {p.v.x, p.v.y, p.v.z, p.v.w, p.w.x, p.w.y, p.w.z, p.w.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
-    } else {
-        const uint32_t u[4] = {p.v.x, p.v.y, p.v.z, p.v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = pair_f32(u[i], E());
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
-        }
-    }
-}
-template <typename E>
-__device__ __forceinline__ void store_piece(E *p, const float *x) {
-    if constexpr (sizeof(E) == 4) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pair_of(x[0], x[1], E()), pair_of(x[2], x[3], E()), pair_of(x[4], x[5], E()),
-                                                   pair_of(x[6], x[7], E()));
-    }
+__device__ __forceinline__ uint32_t pair_of(float2 v, __half) {
+    const __half2 h = __float22half2_rn(v);
+    return reinterpret_cast<const uint32_t &>(h);
 }
 
-// What a lane has of a row: values 8 c0.. and 8 c1.., x[0..7] and x[8..15]; the 8 frequencies from 8 sub on.
+// A lane's 16 values of a row: the two that turn into one another are a[i] and b[i], in either half of the rotated values
+// or, interleaved, side by side.  v[0 ..]: 16-byte pieces as they lie in memory, the half of them from c0 on, then from c1.
+template <typename E, bool IL>
+struct Row {
+    static constexpr int N = sizeof(E);  // pieces
+    float2 a[4], b[4];
+    __device__ __forceinline__ void unpack(const uint4 *v) {
+        float x[16];
+        if constexpr (N == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[4 * i] = __uint_as_float(v[i].x), x[4 * i + 1] = __uint_as_float(v[i].y);
+                x[4 * i + 2] = __uint_as_float(v[i].z), x[4 * i + 3] = __uint_as_float(v[i].w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = pair_f32(u[j], E());
+                    x[8 * i + 2 * j] = f.x, x[8 * i + 2 * j + 1] = f.y;
+                }
+            }
+        }
+        set(x);
+    }
+    __device__ __forceinline__ void set(const float *x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = IL ? make_float2(x[4 * i], x[4 * i + 2]) : make_float2(x[2 * i], x[2 * i + 1]);
+            b[i] = IL ? make_float2(x[4 * i + 1], x[4 * i + 3]) : make_float2(x[8 + 2 * i], x[9 + 2 * i]);
+        }
+    }
+    __device__ __forceinline__ void get(float *x) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            (IL ? x[4 * i] : x[2 * i]) = a[i].x, (IL ? x[4 * i + 2] : x[2 * i + 1]) = a[i].y;
+            (IL ? x[4 * i + 1] : x[8 + 2 * i]) = b[i].x, (IL ? x[4 * i + 3] : x[9 + 2 * i]) = b[i].y;
+        }
+    }
+    __device__ __forceinline__ void store(E *p, int apart) const {  // from c0 on; c1 = c0 + apart
+        float x[16];
+        get(x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint4 v;
+            if constexpr (N == 4) {
+                v = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]));
+            } else {
+                const float *y = x + 8 * i;
+                v = make_uint4(pair_of(make_float2(y[0], y[1]), E()), pair_of(make_float2(y[2], y[3]), E()),
+                               pair_of(make_float2(y[4], y[5]), E()), pair_of(make_float2(y[6], y[7]), E()));
+            }
+            *reinterpret_cast<uint4 *>(p + (i < N / 2 ? 0 : apart) + (N == 4 && i % 2 ? 4 : 0)) = v;
+        }
+    }
+};
+
+// What a lane has of a row, and its frequencies: the 8 from 8 sub on.
 template <int G, bool IL>
 struct Lane {
-    int sub, c0, c1;
+    int sub, c0, apart;
     bool in, turned;
     __device__ Lane(const QnArgs &g) {
         sub = threadIdx.x % G;
         in = 16 * sub < g.d;
         turned = 16 * sub < g.rot;
         c0 = turned && !IL ? 8 * sub : 16 * sub;
-        c1 = turned && !IL ? 8 * sub + g.rot / 2 : 16 * sub + 8;
+        apart = turned && !IL ? g.rot / 2 : 8;
     }
-    __device__ void angles(const QnArgs &g, int pos, float *s, float *c) const {
+    template <typename E>
+    __device__ __forceinline__ void weights(const float *w, Row<E, IL> &x) const {
+        float y[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            s[i] = 0.f, c[i] = 1.f;
-            if (turned) sincos_at(g.freq[8 * sub + i], pos, s[i], c[i]);
-        }
-    }
-    __device__ void weights(const float *w, float *x) const {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = w != nullptr && in ? w[i < 8 ? c0 + i : c1 + i - 8] : 1.f;
-    }
-    // the 16 values turned by (s, c)
-    static __device__ __forceinline__ void turn(float *x, const float *s, const float *c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float &a = x[IL ? 2 * i : i], &b = x[IL ? 2 * i + 1 : 8 + i];
-            const float t = a * c[i] - b * s[i];
-            b = b * c[i] + a * s[i];
-            a = t;
-        }
+        for (int i = 0; i < 16; ++i) y[i] = w != nullptr && in ? w[c0 + (i < 8 ? i : apart + i - 8)] : 1.f;
+        x.set(y);
     }
 };
 
@@ -151,62 +158,176 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+// Where a lane is in its warp's list of rows: token (b, t), head.  The list has the tiles of 32 / G neighbouring tokens
+// one after the other, and in each its heads.
+template <int G>
+struct At {
+    long long tile;
+    int head, b, t;
+    bool on, live;  // there is such a token; it is of its sequence
+    __device__ void token(const QnArgs &g) {
+        const long long n = tile * (32 / G) + threadIdx.x % 32 / G;
+        on = n < g.tokens;
+        const unsigned i = on ? (unsigned)n : 0u;
+        b = (int)(i / (unsigned)g.T), t = (int)(i % (unsigned)g.T);
+        live = on && (g.lens == nullptr || t < g.lens[b]);
+    }
+    __device__ At(const QnArgs &g, long long unit, int heads) : tile(unit / heads), head((int)(unit % heads)) { token(g); }
+    // to the next row: true where that is of another tile
+    __device__ __forceinline__ bool next(const QnArgs &g, int heads) {
+        if (++head < heads) return false;
+        head = 0, ++tile;
+        token(g);
+        return true;
+    }
+};
+
+// Rows on their way to a lane: 16-byte pieces in shared memory, in the lane's own column of a stage.
+template <int THREADS, int STAGES, int PIECES>
+struct Queue {
+    static constexpr int BYTES = STAGES * PIECES * THREADS * 16;
+    uint32_t base;
+    __device__ __forceinline__ Queue(const void *smem) : base((uint32_t)__cvta_generic_to_shared(smem) + 16 * threadIdx.x) {}
+    __device__ __forceinline__ uint32_t at(int stage, int piece) const { return base + (stage * PIECES + piece) * (THREADS * 16); }
+    template <typename E>
+    __device__ __forceinline__ void put(int stage, int first, const E *p, int apart) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(E); ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(stage, first + i)),
+                         "l"(p + (i < (int)sizeof(E) / 2 ? 0 : apart) + (sizeof(E) == 4 && i % 2 ? 4 : 0))
+                         : "memory");
+    }
+    __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory"); }
+    __device__ __forceinline__ uint4 get(int stage, int piece) const {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at(stage, piece)) : "memory");
+        return v;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ T pick(const T (&a)[2], int which) { return which == 0 ? a[0] : a[1]; }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 minus(float2 a) { return make_float2(-a.x, -a.y); }
+
+// Sines and cosines of the lane's 8 angles at its token.
+template <int G, bool IL>
+__device__ __forceinline__ void angles(const QnArgs &g, const Lane<G, IL> &l, const At<G> &a, const unsigned long long *s_turn, float2 *s, float2 *c) {
+    const int pos = !a.live ? 0 : g.pos != nullptr ? g.pos[(long long)a.b * g.T + a.t] : a.t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s[i] = both(0.f), c[i] = both(1.f);
+        if (l.turned) {
+            sincos_at(s_turn[8 * l.sub + 2 * i], pos, s[i].x, c[i].x);
+            sincos_at(s_turn[8 * l.sub + 2 * i + 1], pos, s[i].y, c[i].y);
+        }
+    }
+}
+
+// The warp's equal share of the list of all rows, queries before keys.
+struct Share {
+    long long at, end;
+    __device__ Share(long long all) {
+        const long long w = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, n = (long long)gridDim.x * (blockDim.x / 32);
+        at = all / n * w + (all % n) * w / n;
+        end = all / n * (w + 1) + (all % n) * (w + 1) / n;
+    }
+};
+
 struct QnFwd {
     const void *x[2];
     void *o[2];
     Triple sx[2], so[2];
 };
 
-// Every lane stays for the shuffles; `on` says whether its group has a token.
+template <typename E>
+constexpr int qn_fwd_stages() { return sizeof(E) == 4 ? 4 : 8; }
+template <typename E>
+constexpr int qn_bwd_stages() { return sizeof(E) == 4 ? 2 : 4; }
+
 template <typename E, int G, bool IL>
-__global__ void __launch_bounds__(kQnThreads) qn_fwd_kernel(QnFwd p, QnArgs g) {
-    constexpr int U = 4;  // rows in flight
+__global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs g) {
+    constexpr int S = qn_fwd_stages<E>(), N = Row<E, IL>::N;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ unsigned long long s_turn[128];
+    const Queue<kFwdThreads, S, N> queue(smem);
     const Lane<G, IL> l(g);
-    const long long item = (long long)blockIdx.x * (kQnThreads / G) + threadIdx.x / G;
-    const bool on = item < g.items;
-    const long long token = on ? item / g.spans : 0;
-    const int b = (int)(token / g.T), t = (int)(token % g.T), first = on ? (int)(item % g.spans) * g.span : 0;
-    const bool live = on && (g.lens == nullptr || t < g.lens[b]);
-    float s[8], c[8], w[16];
-    l.angles(g, live ? (g.pos != nullptr ? g.pos[token] : t) : 0, s, c);
-    const int all = g.heads[0] + g.heads[1];
+    for (int i = threadIdx.x; i < g.rot / 2; i += kFwdThreads) s_turn[i] = turns(g.freq[i]);
+    __syncthreads();
+    const Share share(g.tiles * (g.heads[0] + g.heads[1]));
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
-        const int base = which == 0 ? 0 : g.heads[0];
-        const int lo = max(first, base), hi = min(min(first + g.span, base + g.heads[which]), all);
-        const E *x = static_cast<const E *>(p.x[which]) + b * p.sx[which].b + t * p.sx[which].t;
-        E *o = static_cast<E *>(p.o[which]) + b * p.so[which].b + t * p.so[which].t;
-        l.weights(g.w[which], w);
-        const int n = on ? hi - lo : 0;
-        for (int h = 0; __any_sync(~0u, h < n); h += U) {
-            Piece<E> a[U], z[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                a[u] = z[u] = Piece<E>{};
-                if (h + u < n && live && l.in) {
-                    const E *row = x + (lo - base + h + u) * p.sx[which].h;
-                    a[u] = load_piece(row + l.c0);
-                    z[u] = load_piece(row + l.c1);
-                }
+        const int heads = pick(g.heads, which);
+        const long long base = which == 0 ? 0 : g.tiles * g.heads[0], lo = max(share.at, base), hi = min(share.end, base + g.tiles * heads);
+        if (lo >= hi) continue;
+        const Triple sx = pick(p.sx, which), so = pick(p.so, which);
+        const E *x = static_cast<const E *>(pick(p.x, which)) + l.c0;
+        E *o = static_cast<E *>(pick(p.o, which)) + l.c0;
+        At<G> f(g, lo - base, heads), c = f;
+        const E *xf = x + f.b * sx.b + f.t * sx.t + f.head * sx.h;
+        E *oc = o + c.b * so.b + c.t * so.t + c.head * so.h;
+        long long fetched = lo;
+        auto fetch = [&](int stage) {
+            if (fetched < hi) {
+                if (f.live && l.in) queue.put(stage, 0, xf, l.apart);
+                ++fetched;
+                xf += sx.h;
+                if (fetched < hi && f.next(g, heads)) xf = x + f.b * sx.b + f.t * sx.t;
             }
+            queue.commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < S; ++i) fetch(i);
+        // w_a cos, w_b sin, w_b cos, w_a sin
+        float2 wac[4], wbs[4], wbc[4], was[4];
+        auto coefficients = [&]() {
+            Row<E, IL> w;
+            l.weights(pick(g.w, which), w);
+            angles(g, l, c, s_turn, was, wac);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float v[16], q = 0.f;
-                unpack(a[u], v);
-                unpack(z[u], v + 8);
+            for (int i = 0; i < 4; ++i) {
+                wbs[i] = mul2(w.b[i], minus(was[i])), wbc[i] = mul2(w.b[i], wac[i]);
+                was[i] = mul2(w.a[i], was[i]), wac[i] = mul2(w.a[i], wac[i]);
+            }
+        };
+        coefficients();
+        int stage = 0;
+#pragma unroll 1
+        for (long long at = lo; at < hi; ++at) {
+            queue.wait();
+            uint4 v[N];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) q = fmaf(v[i], v[i], q);
-                const float r = rsqrtf(row_sum<G>(q) * g.inv_d + g.eps);
+            for (int i = 0; i < N; ++i) v[i] = queue.get(stage, i);
+            fetch(stage);
+            stage = stage + 1 == S ? 0 : stage + 1;
+            Row<E, IL> y;
+            y.unpack(v);
+            if (!l.in) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = v[i] * r * w[i];
-                if (l.turned) l.turn(v, s, c);
-                if (h + u < n && l.in) {
-                    E *row = o + (lo - base + h + u) * p.so[which].h;
-                    if (!live)
+                for (int i = 0; i < 4; ++i) y.a[i] = y.b[i] = both(0.f);
+            }
+            float2 q = both(0.f);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0.f;
-                    store_piece(row + l.c0, v);
-                    store_piece(row + l.c1, v + 8);
-                }
+            for (int i = 0; i < 4; ++i) q = fma2(y.a[i], y.a[i], q), q = fma2(y.b[i], y.b[i], q);
+            const float r = c.live ? rsqrtf(row_sum<G>(q.x + q.y) * g.inv_d + g.eps) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = mul2(y.a[i], both(r)), b = mul2(y.b[i], both(r));
+                y.a[i] = fma2(a, wac[i], mul2(b, wbs[i]));
+                y.b[i] = fma2(b, wbc[i], mul2(a, was[i]));
+            }
+            if (!c.live) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y.a[i] = y.b[i] = both(0.f);
+            }
+            if (c.on && l.in) y.store(oc, l.apart);
+            oc += so.h;
+            if (at + 1 < hi && c.next(g, heads)) {
+                oc = o + c.b * so.b + c.t * so.t;
+                coefficients();
             }
         }
     }
@@ -218,81 +339,104 @@ struct QnBwd {
     Triple sx[2], sg[2], sdx[2];
 };
 
-// A persistent block leaves its rows' sums of dw in parts[block][2][d].
+// A block leaves its rows' sums of dw in parts[block][2][d].
 template <typename E, int G, bool IL>
-__global__ void __launch_bounds__(kQnThreads) qn_bwd_kernel(QnBwd p, QnArgs g, float *parts) {
-    __shared__ float s_w[kQnThreads / 32][2][G * 16];
+__global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs g, float *parts) {
+    constexpr int S = qn_bwd_stages<E>(), N = Row<E, IL>::N, W = kBwdThreads / 32;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ unsigned long long s_turn[128];
+    __shared__ float s_w[W][2][G * 16];
+    const Queue<kBwdThreads, S, 2 * N> queue(smem);
     const Lane<G, IL> l(g);
-    float acc[2][16];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int i = threadIdx.x; i < g.rot / 2; i += kBwdThreads) s_turn[i] = turns(g.freq[i]);
+    __syncthreads();
+    const Share share(g.tiles * (g.heads[0] + g.heads[1]));
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const int heads = pick(g.heads, which);
+        const long long base = which == 0 ? 0 : g.tiles * g.heads[0], lo = max(share.at, base), hi = min(share.end, base + g.tiles * heads);
+        Row<E, IL> acc;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
-    for (long long at = (long long)blockIdx.x * (kQnThreads / G); at < g.items; at += (long long)gridDim.x * (kQnThreads / G)) {
-        const long long item = at + threadIdx.x / G;
-        const bool on = item < g.items;
-        const long long token = on ? item / g.spans : 0;
-        const int b = (int)(token / g.T), t = (int)(token % g.T), first = on ? (int)(item % g.spans) * g.span : 0;
-        const bool live = on && (g.lens == nullptr || t < g.lens[b]);
-        float s[8], c[8];
-        l.angles(g, live ? (g.pos != nullptr ? g.pos[token] : t) : 0, s, c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = -s[i];
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const int base = which == 0 ? 0 : g.heads[0];
-            const int lo = max(first, base), hi = min(first + g.span, base + g.heads[which]);
-            const E *x = static_cast<const E *>(p.x[which]) + b * p.sx[which].b + t * p.sx[which].t;
-            const E *y = static_cast<const E *>(p.g[which]) + b * p.sg[which].b + t * p.sg[which].t;
-            E *dx = static_cast<E *>(p.dx[which]) + b * p.sdx[which].b + t * p.sdx[which].t;
-            float w[16];
-            l.weights(g.w[which], w);
-            const int n = on ? hi - lo : 0;
-            for (int h = 0; __any_sync(~0u, h < n); ++h) {
-                const long long row = lo - base + h;
-                const bool here = h < n && live && l.in;
-                float v[16], u[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = u[i] = 0.f;
-                if (here) {
-                    unpack(load_piece(x + row * p.sx[which].h + l.c0), v);
-                    unpack(load_piece(x + row * p.sx[which].h + l.c1), v + 8);
-                    unpack(load_piece(y + row * p.sg[which].h + l.c0), u);
-                    unpack(load_piece(y + row * p.sg[which].h + l.c1), u + 8);
+        for (int i = 0; i < 4; ++i) acc.a[i] = acc.b[i] = both(0.f);
+        if (lo < hi) {
+            const Triple sx = pick(p.sx, which), sg = pick(p.sg, which), sd = pick(p.sdx, which);
+            const E *x = static_cast<const E *>(pick(p.x, which)) + l.c0, *y = static_cast<const E *>(pick(p.g, which)) + l.c0;
+            E *d = static_cast<E *>(pick(p.dx, which)) + l.c0;
+            At<G> f(g, lo - base, heads), c = f;
+            const E *xf = x + f.b * sx.b + f.t * sx.t + f.head * sx.h, *yf = y + f.b * sg.b + f.t * sg.t + f.head * sg.h;
+            E *dc = d + c.b * sd.b + c.t * sd.t + c.head * sd.h;
+            long long fetched = lo;
+            auto fetch = [&](int stage) {
+                if (fetched < hi) {
+                    if (f.live && l.in) queue.put(stage, 0, xf, l.apart), queue.put(stage, N, yf, l.apart);
+                    ++fetched;
+                    xf += sx.h, yf += sg.h;
+                    if (fetched < hi && f.next(g, heads)) xf = x + f.b * sx.b + f.t * sx.t, yf = y + f.b * sg.b + f.t * sg.t;
                 }
-                if (l.turned) l.turn(u, s, c);
-                float q = 0.f, m = 0.f;
+                queue.commit();
+            };
+#pragma unroll 1
+            for (int i = 0; i < S; ++i) fetch(i);
+            Row<E, IL> w;
+            l.weights(pick(g.w, which), w);
+            float2 sn[4], cs[4];
+            angles(g, l, c, s_turn, sn, cs);
+            int stage = 0;
+#pragma unroll 1
+            for (long long at = lo; at < hi; ++at) {
+                queue.wait();
+                uint4 v[N], u[N];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) q = fmaf(v[i], v[i], q), m = fmaf(u[i] * w[i], v[i], m);
-                q = row_sum<G>(q);
-                m = row_sum<G>(m);
-                const float r = rsqrtf(q * g.inv_d + g.eps), k = m * g.inv_d * r * r;
+                for (int i = 0; i < N; ++i) v[i] = queue.get(stage, i), u[i] = queue.get(stage, N + i);
+                fetch(stage);
+                stage = stage + 1 == S ? 0 : stage + 1;
+                Row<E, IL> z, e;
+                z.unpack(v);
+                e.unpack(u);
+                if (!(c.live && l.in)) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    acc[which][i] = fmaf(u[i] * r, v[i], acc[which][i]);
-                    v[i] = r * (u[i] * w[i] - v[i] * k);
+                    for (int i = 0; i < 4; ++i) z.a[i] = z.b[i] = e.a[i] = e.b[i] = both(0.f);
                 }
-                if (h < n && l.in) {
-                    E *to = dx + row * p.sdx[which].h;
-                    store_piece(to + l.c0, v);
-                    store_piece(to + l.c1, v + 8);
+                float2 q = both(0.f), m = both(0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 t = e.a[i];  // turned back
+                    e.a[i] = fma2(t, cs[i], mul2(e.b[i], sn[i]));
+                    e.b[i] = fma2(e.b[i], cs[i], mul2(t, minus(sn[i])));
+                    q = fma2(z.a[i], z.a[i], q), q = fma2(z.b[i], z.b[i], q);
+                    m = fma2(mul2(e.a[i], w.a[i]), z.a[i], m), m = fma2(mul2(e.b[i], w.b[i]), z.b[i], m);
+                }
+                const float r = rsqrtf(row_sum<G>(q.x + q.y) * g.inv_d + g.eps), k = row_sum<G>(m.x + m.y) * g.inv_d * r * r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc.a[i] = fma2(mul2(e.a[i], both(r)), z.a[i], acc.a[i]);
+                    acc.b[i] = fma2(mul2(e.b[i], both(r)), z.b[i], acc.b[i]);
+                    z.a[i] = mul2(both(r), fma2(z.a[i], both(-k), mul2(e.a[i], w.a[i])));
+                    z.b[i] = mul2(both(r), fma2(z.b[i], both(-k), mul2(e.b[i], w.b[i])));
+                }
+                if (c.on && l.in) z.store(dc, l.apart);
+                dc += sd.h;
+                if (at + 1 < hi && c.next(g, heads)) {
+                    dc = d + c.b * sd.b + c.t * sd.t;
+                    angles(g, l, c, s_turn, sn, cs);
                 }
             }
         }
-    }
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-#pragma unroll
-    for (int which = 0; which < 2; ++which)
+        float v[16];
+        acc.get(v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float v = acc[which][i];
 #pragma unroll
-            for (int x = G; x < 32; x <<= 1) v += __shfl_xor_sync(~0u, v, x);
-            if (lane < G && l.in) s_w[warp][which][i < 8 ? l.c0 + i : l.c1 + i - 8] = v;
+            for (int x = G; x < 32; x <<= 1) v[i] += __shfl_xor_sync(~0u, v[i], x);
+            if (lane < G && l.in) s_w[warp][which][l.c0 + (i < 8 ? i : l.apart + i - 8)] = v[i];
         }
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * g.d; i += kQnThreads) {
+    for (int i = threadIdx.x; i < 2 * g.d; i += kBwdThreads) {
         float v = 0.f;
 #pragma unroll
-        for (int x = 0; x < kQnThreads / 32; ++x) v += s_w[x][i / g.d][i % g.d];
+        for (int x = 0; x < W; ++x) v += s_w[x][i / g.d][i % g.d];
         parts[(long long)blockIdx.x * 2 * g.d + i] = v;
     }
 }
@@ -334,54 +478,65 @@ int qn_lanes(int64_t d) {
     return n;
 }
 
-// Heads that a group of lanes walks over: all, or as few as it takes to have 8 groups of lanes for every thread slot
-// of 64 multiprocessors.
 QnArgs qn_args(const float *wq, const float *wk, const float *freq, const int32_t *pos, const int32_t *lens, float eps, int64_t rot,
                int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d) {
     QnArgs g = {};
     g.w[0] = wq, g.w[1] = wk, g.freq = freq, g.pos = pos, g.lens = lens;
     g.eps = eps, g.inv_d = 1.f / (float)d;
-    g.B = (int)B, g.T = (int)T, g.heads[0] = (int)H, g.heads[1] = (int)Hkv, g.d = (int)d, g.rot = (int)rot;
-    g.span = (int)(H + Hkv);
-    const long long enough = 152ll * 1024 / qn_lanes(d);
-    while (g.span > 1 && B * T * ((H + Hkv + g.span - 1) / g.span) < enough) g.span = (g.span + 1) / 2;
-    g.spans = (int)((H + Hkv + g.span - 1) / g.span);
-    g.items = B * T * g.spans;
+    g.T = (int)T, g.heads[0] = (int)H, g.heads[1] = (int)Hkv, g.d = (int)d, g.rot = (int)rot;
+    g.tokens = B * T;
+    const long long per = 32 / qn_lanes(d);
+    g.tiles = (g.tokens + per - 1) / per;
     return g;
+}
+
+// Blocks of the persistent kernels: a warp has one row at least.
+unsigned qn_blocks(const QnArgs &g, int threads, int most) {
+    const long long rows = g.tiles * (g.heads[0] + g.heads[1]), n = (rows + threads / 32 - 1) / (threads / 32);
+    return (unsigned)(n < most ? n : most);
+}
+
+template <typename E, int G, bool IL>
+int qn_fwd_g(const char *fn, const QnFwd &p, const QnArgs &g, cudaStream_t s) {
+    static std::atomic<unsigned long long> done{0};
+    constexpr int smem = Queue<kFwdThreads, qn_fwd_stages<E>(), Row<E, IL>::N>::BYTES;
+    if (int st = set_max_dynamic_smem(done, (const void *)qn_fwd_kernel<E, G, IL>, smem)) return st;
+    qn_fwd_kernel<E, G, IL><<<qn_blocks(g, kFwdThreads, kFwdBlocks), kFwdThreads, smem, s>>>(p, g);
+    return check_launch(fn);
 }
 
 template <typename E, bool IL>
 int qn_fwd(const char *fn, const QnFwd &p, const QnArgs &g, cudaStream_t s) {
-    const int G = qn_lanes(g.d), per = kQnThreads / G;
-    const unsigned grid = (unsigned)((g.items + per - 1) / per);
-    switch (G) {
-        case 1: qn_fwd_kernel<E, 1, IL><<<grid, kQnThreads, 0, s>>>(p, g); break;
-        case 2: qn_fwd_kernel<E, 2, IL><<<grid, kQnThreads, 0, s>>>(p, g); break;
-        case 4: qn_fwd_kernel<E, 4, IL><<<grid, kQnThreads, 0, s>>>(p, g); break;
-        case 8: qn_fwd_kernel<E, 8, IL><<<grid, kQnThreads, 0, s>>>(p, g); break;
-        default: qn_fwd_kernel<E, 16, IL><<<grid, kQnThreads, 0, s>>>(p, g);
+    switch (qn_lanes(g.d)) {
+        case 1: return qn_fwd_g<E, 1, IL>(fn, p, g, s);
+        case 2: return qn_fwd_g<E, 2, IL>(fn, p, g, s);
+        case 4: return qn_fwd_g<E, 4, IL>(fn, p, g, s);
+        case 8: return qn_fwd_g<E, 8, IL>(fn, p, g, s);
+        default: return qn_fwd_g<E, 16, IL>(fn, p, g, s);
     }
-    return check_launch(fn);
 }
 
-unsigned qn_bwd_blocks(const QnArgs &g) {
-    const long long per = kQnThreads / qn_lanes(g.d), n = (g.items + per - 1) / per;
-    return (unsigned)(n < kQnBlocks ? n : kQnBlocks);
+template <typename E, int G, bool IL>
+int qn_bwd_g(const char *fn, const QnBwd &p, const QnArgs &g, float *parts, cudaStream_t s) {
+    static std::atomic<unsigned long long> done{0};
+    constexpr int smem = Queue<kBwdThreads, qn_bwd_stages<E>(), 2 * Row<E, IL>::N>::BYTES;
+    if (int st = set_max_dynamic_smem(done, (const void *)qn_bwd_kernel<E, G, IL>, smem)) return st;
+    qn_bwd_kernel<E, G, IL><<<qn_blocks(g, kBwdThreads, kBwdBlocks), kBwdThreads, smem, s>>>(p, g, parts);
+    return check_launch(fn);
 }
 
 template <typename E, bool IL>
 int qn_bwd(const char *fn, const QnBwd &p, const QnArgs &g, float *dwq, float *dwk, float *parts, cudaStream_t s) {
-    const unsigned grid = qn_bwd_blocks(g);
+    int st;
     switch (qn_lanes(g.d)) {
-        case 1: qn_bwd_kernel<E, 1, IL><<<grid, kQnThreads, 0, s>>>(p, g, parts); break;
-        case 2: qn_bwd_kernel<E, 2, IL><<<grid, kQnThreads, 0, s>>>(p, g, parts); break;
-        case 4: qn_bwd_kernel<E, 4, IL><<<grid, kQnThreads, 0, s>>>(p, g, parts); break;
-        case 8: qn_bwd_kernel<E, 8, IL><<<grid, kQnThreads, 0, s>>>(p, g, parts); break;
-        default: qn_bwd_kernel<E, 16, IL><<<grid, kQnThreads, 0, s>>>(p, g, parts);
+        case 1: st = qn_bwd_g<E, 1, IL>(fn, p, g, parts, s); break;
+        case 2: st = qn_bwd_g<E, 2, IL>(fn, p, g, parts, s); break;
+        case 4: st = qn_bwd_g<E, 4, IL>(fn, p, g, parts, s); break;
+        case 8: st = qn_bwd_g<E, 8, IL>(fn, p, g, parts, s); break;
+        default: st = qn_bwd_g<E, 16, IL>(fn, p, g, parts, s);
     }
-    if (int st = check_launch(fn)) return st;
-    if (dwq == nullptr && dwk == nullptr) return CLA_OK;
-    qn_join_kernel<<<(unsigned)((2 * g.d + 31) / 32), 256, 0, s>>>(parts, dwq, dwk, g.d, (int)grid);
+    if (st != CLA_OK || (dwq == nullptr && dwk == nullptr)) return st;
+    qn_join_kernel<<<(unsigned)((2 * g.d + 31) / 32), 256, 0, s>>>(parts, dwq, dwk, g.d, (int)qn_blocks(g, kBwdThreads, kBwdBlocks));
     return check_launch(fn);
 }
 
@@ -417,7 +572,7 @@ extern "C" int cla_qk_norm_rope_fwd(const void *q, const void *k, const float *w
 
 extern "C" size_t cla_qk_norm_rope_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d) {
     if (qn_check("cla_qk_norm_rope_bwd_workspace_size", B, H, Hkv, T, d, 0, 1.f, CLA_F32) != CLA_OK) return 0;
-    return (size_t)kQnBlocks * 2 * d * 4;
+    return (size_t)kBwdBlocks * 2 * d * 4;
 }
 
 extern "C" int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const float *wk, const float *freq,

@@ -90,44 +90,70 @@ __device__ __forceinline__ void decode16(const uint4 &c, float (&x)[16]) {
 }
 
 // ------------------------------------------------------------------ prompts
-// A block of threads per block of slots, of k or of v; every thread 16 values at a time.
+// A block of threads per block of slots, of k or of v, its values in registers as they come: 8 pieces a thread on their way.
+template <bool BF>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+    if constexpr (BF) {
+        const __nv_bfloat162 m = __hmax2(reinterpret_cast<__nv_bfloat162 &>(a), __habs2(reinterpret_cast<__nv_bfloat162 &>(b)));
+        return reinterpret_cast<const uint32_t &>(m);
+    } else {
+        const __half2 m = __hmax2(reinterpret_cast<__half2 &>(a), __habs2(reinterpret_cast<__half2 &>(b)));
+        return reinterpret_cast<const uint32_t &>(m);
+    }
+}
 template <typename E, int D>
 __global__ void __launch_bounds__(128) c8_write_kernel(const E *k, const E *v, const int32_t *lens, uint8_t *kc, uint8_t *vc, float *kf,
-                                                       float *vf, Triple sk, Triple sv, int Hkv, int T, long long window, long long sinks,
+                                                       float *vf, Triple sk, Triple sv, int Hkv, int T, unsigned window, int sinks,
                                                        int blocks) {
-    constexpr int P = D / 16, N = kC8Block * P / 128;  // pieces of a slot, of a thread
+    constexpr bool BF = std::is_same<E, __nv_bfloat16>::value;
+    constexpr int P = D / 16, N = kC8Block * P / 128;  // pieces of 16 values of a slot, of a thread
     __shared__ float s_top[4];
-    const long long S = sinks + window;
-    const long long bh = blockIdx.x / blocks, first = (long long)(blockIdx.x % blocks) * kC8Block;
-    const int h = (int)(bh % Hkv), b = (int)(bh / Hkv), n = lens == nullptr ? T : min(max(lens[b], 0), T);
+    const long long S = (long long)sinks + window;
+    const unsigned bh = blockIdx.x / (unsigned)blocks;
+    const int first = (int)(blockIdx.x % (unsigned)blocks) * kC8Block;
+    const int h = (int)(bh % (unsigned)Hkv), b = (int)(bh / (unsigned)Hkv), n = lens == nullptr ? T : min(max(lens[b], 0), T);
     if (first >= n) return;  // no token reaches the block
     const bool of_v = blockIdx.y != 0;
     const Triple st = of_v ? sv : sk;
     const E *x = (of_v ? v : k) + b * st.b + h * st.h;
-    float val[N][16], top = 0.f;
+    uint4 val[N][2];
+    bool held[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int at = threadIdx.x + 128 * i;
-        const long long slot = first + at / P;
+        const int at = threadIdx.x + 128 * i, slot = first + at / P;
         long long p = slot;  // the last token that falls on the slot
-        if (slot >= sinks && slot < n) p += (n - 1 - slot) / window * window;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) val[i][j] = 0.f;
-        if (slot < S && p < n) load16(x + p * st.t + 16 * (at % P), val[i]);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(val[i][j]));
+        if (slot >= sinks && slot < n) p += (unsigned)(n - 1 - slot) / window * (long long)window;
+        held[i] = slot < S && slot < n;
+        const uint4 *row = reinterpret_cast<const uint4 *>(x + p * st.t) + 2 * (at % P);
+        val[i][0] = held[i] ? __ldcs(row) : make_uint4(0u, 0u, 0u, 0u);
+        val[i][1] = held[i] ? __ldcs(row + 1) : make_uint4(0u, 0u, 0u, 0u);
     }
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint4 w = val[i][e];
+            most = max_abs2<BF>(max_abs2<BF>(max_abs2<BF>(max_abs2<BF>(most, w.x), w.y), w.z), w.w);
+        }
+    const float2 two = unpack16<BF>(most);
+    float top = fmaxf(two.x, two.y);
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
     if (threadIdx.x % 32 == 0) s_top[threadIdx.x / 32] = top;
     __syncthreads();
     const float f = factor_of(fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]))), by = inverse(f);
-    uint8_t *to = (of_v ? vc : kc) + (bh * S + first) * D;
+    uint4 *to = reinterpret_cast<uint4 *>((of_v ? vc : kc) + (bh * S + first) * D) + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int at = threadIdx.x + 128 * i;
-        const long long slot = first + at / P;
-        if (slot < S && slot < n) reinterpret_cast<uint4 *>(to)[at] = code16(val[i], by);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint4 y = val[i][e / 2];
+            const float2 p = unpack16<BF>(e % 2 ? y.z : y.x), q = unpack16<BF>(e % 2 ? y.w : y.y);
+            w[e] = e4m3x2(p.x * by, p.y * by) | e4m3x2(q.x * by, q.y * by) << 16;
+        }
+        if (held[i]) to[128 * i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (threadIdx.x == 0) (of_v ? vf : kf)[blockIdx.x] = f;
 }
@@ -674,7 +700,7 @@ extern "C" int cla_window_cache8_write(const void *k, const void *v, const int32
     cudaStream_t s = (cudaStream_t)stream;
 #define CLA_C8_WRITE(E, D)                                                                                                       \
     c8_write_kernel<E, D><<<grid, 128, 0, s>>>((const E *)k, (const E *)v, lens, (uint8_t *)kcache, (uint8_t *)vcache, kscale, vscale, \
-                                               r[0], r[1], (int)Hkv, (int)T, window, sinks, blocks)
+                                               r[0], r[1], (int)Hkv, (int)T, (unsigned)window, (int)sinks, blocks)
     if (dtype == CLA_BF16) {
         if (d == 128) CLA_C8_WRITE(__nv_bfloat16, 128);
         else CLA_C8_WRITE(__nv_bfloat16, 64);
