@@ -937,6 +937,7 @@ def window_cache8_write(k, v, kcache, vcache, kscale, vscale, *, window, sinks=0
         _strides(k, v)), stream)
 
 
+@functools.lru_cache(maxsize=256)  # a number that the sizes fix; a step asks for it
 def window_attn_step8_workspace_size(B, H, Hkv, d, window, sinks=0) -> int:
     return int(lib().cla_window_attn_step8_workspace_size(B, H, Hkv, d, *_counts(window, sinks)))
 
@@ -988,14 +989,25 @@ def qk_norm_rope_fwd(q, k, wq=None, wk=None, freq=None, *, pos=None, lens=None, 
     return qo, ko
 
 
+@_own_memory
 def qk_norm_rope_step(q, k, wq, wk, freq, pos, *, eps=1e-6, interleaved=False, qo=None, ko=None, stream=None):
     """qk_norm_rope_fwd for one token of each of B sequences: q [B, H, d], k [B, Hkv, d], pos [B] int32 (what
     window_attn_step takes)."""
-    _dims(q, 3, "q"), _dims(k, 3, "k")
-    given = tuple(None if t is None else t.unsqueeze(2) for t in (qo, ko))
-    a, b = qk_norm_rope_fwd(q.unsqueeze(2), k.unsqueeze(2), wq, wk, freq, pos=None if pos is None else pos.unsqueeze(-1), eps=eps,
-                            interleaved=interleaved, qo=given[0], ko=given[1], stream=stream)
-    return a.squeeze(2) if qo is None else qo, b.squeeze(2) if ko is None else ko
+    B, H, d = _dims(q, 3, "q")
+    Hkv = _dims(k, 3, "k")[1]
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    code = _dtype_code(q, "q", _DTYPES)
+    hs, ks, rot = (B, H, d), (B, Hkv, d), _rot(freq)
+    qo, ko = _out(qo, hs, dt, dev), _out(ko, ks, dt, dev)
+    strides = None
+    if not (q.is_contiguous() and k.is_contiguous() and qo.is_contiguous() and ko.is_contiguous()):
+        flat = [s for t in (q, k, qo, ko) for s in (*t.stride()[:2], d)]  # no stride from token to token
+        strides = (ctypes.c_int64 * 12)(*flat)
+    _launch("cla_qk_norm_rope_fwd", dev, (
+        _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(wq, f32, "wq", (d,)), _T(wk, f32, "wk", (d,)),
+        _T(freq, f32, "freq", (rot // 2,)), _T(pos, torch.int32, "pos", (B,)), None, _T(qo, dt, "qo", hs, True),
+        _T(ko, dt, "ko", ks, True), float(eps), rot, int(bool(interleaved)), code, B, H, Hkv, 1, d, strides), stream)
+    return qo, ko
 
 
 def qk_norm_rope_bwd_workspace_size(B, H, Hkv, T, d) -> int:

@@ -29,7 +29,7 @@
 namespace cla {
 namespace {
 
-// Persistent blocks, for 152 multiprocessors: forward 2 for each, backward one (its lanes hold 16 sums of dw as well, 170
+// Blocks that run at once, for 152 multiprocessors: forward 2 for each, backward one (its lanes hold 16 sums of dw as well, 170
 // registers; with 128 they went to local memory and the backward took 100 us where it takes 70).
 constexpr int kFwdThreads = 256, kFwdBlocks = 304, kBwdThreads = 384, kBwdBlocks = 152;
 
@@ -38,7 +38,7 @@ struct QnArgs {
     const int32_t *pos, *lens;
     float eps, inv_d;
     int T, heads[2], d, rot;
-    long long tokens, tiles;  // tiles: of as many tokens as a warp has groups of lanes
+    long long tokens, groups;  // groups: of as many tokens as a block has groups of lanes
 };
 
 // freq / 2 pi as a signed fraction of a turn in 64 bits
@@ -158,25 +158,25 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// Where a lane is in its warp's list of rows: token (b, t), head.  The list has the tiles of 32 / G neighbouring tokens
-// one after the other, and in each its heads.
+// Where a lane is in its block's list of rows: token (b, t), head.  The list has the groups of neighbouring tokens, one for
+// every group of lanes of the block, one behind the other, and in each its heads.
 template <int G>
 struct At {
-    long long tile;
+    long long group;
     int head, b, t;
     bool on, live;  // there is such a token; it is of its sequence
     __device__ void token(const QnArgs &g) {
-        const long long n = tile * (32 / G) + threadIdx.x % 32 / G;
+        const long long n = group * (blockDim.x / G) + threadIdx.x / G;
         on = n < g.tokens;
         const unsigned i = on ? (unsigned)n : 0u;
         b = (int)(i / (unsigned)g.T), t = (int)(i % (unsigned)g.T);
         live = on && (g.lens == nullptr || t < g.lens[b]);
     }
-    __device__ At(const QnArgs &g, long long unit, int heads) : tile(unit / heads), head((int)(unit % heads)) { token(g); }
-    // to the next row: true where that is of another tile
+    __device__ At(const QnArgs &g, long long unit, int heads) : group(unit / heads), head((int)(unit % heads)) { token(g); }
+    // to the next row: true where that is of another group
     __device__ __forceinline__ bool next(const QnArgs &g, int heads) {
         if (++head < heads) return false;
-        head = 0, ++tile;
+        head = 0, ++group;
         token(g);
         return true;
     }
@@ -190,11 +190,11 @@ struct Queue {
     __device__ __forceinline__ Queue(const void *smem) : base((uint32_t)__cvta_generic_to_shared(smem) + 16 * threadIdx.x) {}
     __device__ __forceinline__ uint32_t at(int stage, int piece) const { return base + (stage * PIECES + piece) * (THREADS * 16); }
     template <typename E>
-    __device__ __forceinline__ void put(int stage, int first, const E *p, int apart) const {
+    __device__ __forceinline__ void put(int stage, int first, const E *p, int apart, bool in) const {  // zeros where it is not in
 #pragma unroll
         for (int i = 0; i < (int)sizeof(E); ++i)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(stage, first + i)),
-                         "l"(p + (i < (int)sizeof(E) / 2 ? 0 : apart) + (sizeof(E) == 4 && i % 2 ? 4 : 0))
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, first + i)),
+                         "l"(p + (i < (int)sizeof(E) / 2 ? 0 : apart) + (sizeof(E) == 4 && i % 2 ? 4 : 0)), "r"(in ? 16 : 0)
                          : "memory");
     }
     __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -227,11 +227,11 @@ __device__ __forceinline__ void angles(const QnArgs &g, const Lane<G, IL> &l, co
     }
 }
 
-// The warp's equal share of the list of all rows, queries before keys.
+// The block's equal share of the list of all rows, queries before keys.
 struct Share {
     long long at, end;
     __device__ Share(long long all) {
-        const long long w = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, n = (long long)gridDim.x * (blockDim.x / 32);
+        const long long w = blockIdx.x, n = gridDim.x;
         at = all / n * w + (all % n) * w / n;
         end = all / n * (w + 1) + (all % n) * (w + 1) / n;
     }
@@ -246,7 +246,7 @@ struct QnFwd {
 template <typename E>
 constexpr int qn_fwd_stages() { return sizeof(E) == 4 ? 4 : 8; }
 template <typename E>
-constexpr int qn_bwd_stages() { return sizeof(E) == 4 ? 2 : 4; }
+constexpr int qn_bwd_stages() { return 2; }
 
 template <typename E, int G, bool IL>
 __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs g) {
@@ -257,11 +257,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
     const Lane<G, IL> l(g);
     for (int i = threadIdx.x; i < g.rot / 2; i += kFwdThreads) s_turn[i] = turns(g.freq[i]);
     __syncthreads();
-    const Share share(g.tiles * (g.heads[0] + g.heads[1]));
+    const Share share(g.groups * (g.heads[0] + g.heads[1]));
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         const int heads = pick(g.heads, which);
-        const long long base = which == 0 ? 0 : g.tiles * g.heads[0], lo = max(share.at, base), hi = min(share.end, base + g.tiles * heads);
+        const long long base = which == 0 ? 0 : g.groups * g.heads[0], lo = max(share.at, base), hi = min(share.end, base + g.groups * heads);
         if (lo >= hi) continue;
         const Triple sx = pick(p.sx, which), so = pick(p.so, which);
         const E *x = static_cast<const E *>(pick(p.x, which)) + l.c0;
@@ -269,13 +269,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
         At<G> f(g, lo - base, heads), c = f;
         const E *xf = x + f.b * sx.b + f.t * sx.t + f.head * sx.h;
         E *oc = o + c.b * so.b + c.t * so.t + c.head * so.h;
-        long long fetched = lo;
+        int left = (int)(hi - lo), coming = left;  // rows to be finished, to be asked for
         auto fetch = [&](int stage) {
-            if (fetched < hi) {
-                if (f.live && l.in) queue.put(stage, 0, xf, l.apart);
-                ++fetched;
+            if (coming > 0) {
+                queue.put(stage, 0, xf, l.apart, f.live && l.in);
                 xf += sx.h;
-                if (fetched < hi && f.next(g, heads)) xf = x + f.b * sx.b + f.t * sx.t;
+                if (--coming > 0 && f.next(g, heads)) xf = x + f.b * sx.b + f.t * sx.t;
             }
             queue.commit();
         };
@@ -293,42 +292,40 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
                 was[i] = mul2(w.a[i], was[i]), wac[i] = mul2(w.a[i], wac[i]);
             }
         };
-        coefficients();
         int stage = 0;
-#pragma unroll 1
-        for (long long at = lo; at < hi; ++at) {
+        Row<E, IL> y, z;
+        float r = 0.f, r1 = 0.f;
+        auto begin = [&](Row<E, IL> &v, float &r) {  // the next row, and its reciprocal root
             queue.wait();
-            uint4 v[N];
+            uint4 u[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = queue.get(stage, i);
+            for (int i = 0; i < N; ++i) u[i] = queue.get(stage, i);
             fetch(stage);
             stage = stage + 1 == S ? 0 : stage + 1;
-            Row<E, IL> y;
-            y.unpack(v);
-            if (!l.in) {
+            v.unpack(u);
+            float2 q = both(0.f), q1 = both(0.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y.a[i] = y.b[i] = both(0.f);
-            }
-            float2 q = both(0.f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q = fma2(y.a[i], y.a[i], q), q = fma2(y.b[i], y.b[i], q);
-            const float r = c.live ? rsqrtf(row_sum<G>(q.x + q.y) * g.inv_d + g.eps) : 0.f;
+            for (int i = 0; i < 4; ++i) q = fma2(v.a[i], v.a[i], q), q1 = fma2(v.b[i], v.b[i], q1);
+            r = rsqrtf(row_sum<G>(q.x + q.y + (q1.x + q1.y)) * g.inv_d + g.eps);
+        };
+        begin(y, r);
+        coefficients();
+#pragma unroll 1
+        for (; left > 0; --left) {
+            begin(z, r1);  // beside the end of the row before it; behind the last, what an old stage holds
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 a = mul2(y.a[i], both(r)), b = mul2(y.b[i], both(r));
                 y.a[i] = fma2(a, wac[i], mul2(b, wbs[i]));
                 y.b[i] = fma2(b, wbc[i], mul2(a, was[i]));
             }
-            if (!c.live) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y.a[i] = y.b[i] = both(0.f);
-            }
             if (c.on && l.in) y.store(oc, l.apart);
             oc += so.h;
-            if (at + 1 < hi && c.next(g, heads)) {
+            if (left > 1 && c.next(g, heads)) {
                 oc = o + c.b * so.b + c.t * so.t;
                 coefficients();
             }
+            y = z, r = r1;
         }
     }
 }
@@ -351,11 +348,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     for (int i = threadIdx.x; i < g.rot / 2; i += kBwdThreads) s_turn[i] = turns(g.freq[i]);
     __syncthreads();
-    const Share share(g.tiles * (g.heads[0] + g.heads[1]));
+    const Share share(g.groups * (g.heads[0] + g.heads[1]));
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         const int heads = pick(g.heads, which);
-        const long long base = which == 0 ? 0 : g.tiles * g.heads[0], lo = max(share.at, base), hi = min(share.end, base + g.tiles * heads);
+        const long long base = which == 0 ? 0 : g.groups * g.heads[0], lo = max(share.at, base), hi = min(share.end, base + g.groups * heads);
         Row<E, IL> acc;
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc.a[i] = acc.b[i] = both(0.f);
@@ -366,13 +363,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
             At<G> f(g, lo - base, heads), c = f;
             const E *xf = x + f.b * sx.b + f.t * sx.t + f.head * sx.h, *yf = y + f.b * sg.b + f.t * sg.t + f.head * sg.h;
             E *dc = d + c.b * sd.b + c.t * sd.t + c.head * sd.h;
-            long long fetched = lo;
+            int left = (int)(hi - lo), coming = left;
             auto fetch = [&](int stage) {
-                if (fetched < hi) {
-                    if (f.live && l.in) queue.put(stage, 0, xf, l.apart), queue.put(stage, N, yf, l.apart);
-                    ++fetched;
+                if (coming > 0) {
+                    queue.put(stage, 0, xf, l.apart, f.live && l.in);
+                    queue.put(stage, N, yf, l.apart, f.live && l.in);
                     xf += sx.h, yf += sg.h;
-                    if (fetched < hi && f.next(g, heads)) xf = x + f.b * sx.b + f.t * sx.t, yf = y + f.b * sg.b + f.t * sg.t;
+                    if (--coming > 0 && f.next(g, heads)) xf = x + f.b * sx.b + f.t * sx.t, yf = y + f.b * sg.b + f.t * sg.t;
                 }
                 queue.commit();
             };
@@ -384,7 +381,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
             angles(g, l, c, s_turn, sn, cs);
             int stage = 0;
 #pragma unroll 1
-            for (long long at = lo; at < hi; ++at) {
+            for (; left > 0; --left) {
                 queue.wait();
                 uint4 v[N], u[N];
 #pragma unroll
@@ -394,10 +391,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
                 Row<E, IL> z, e;
                 z.unpack(v);
                 e.unpack(u);
-                if (!(c.live && l.in)) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) z.a[i] = z.b[i] = e.a[i] = e.b[i] = both(0.f);
-                }
                 float2 q = both(0.f), m = both(0.f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -417,7 +410,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
                 }
                 if (c.on && l.in) z.store(dc, l.apart);
                 dc += sd.h;
-                if (at + 1 < hi && c.next(g, heads)) {
+                if (left > 1 && c.next(g, heads)) {
                     dc = d + c.b * sd.b + c.t * sd.t;
                     angles(g, l, c, s_turn, sn, cs);
                 }
@@ -479,21 +472,28 @@ int qn_lanes(int64_t d) {
 }
 
 QnArgs qn_args(const float *wq, const float *wk, const float *freq, const int32_t *pos, const int32_t *lens, float eps, int64_t rot,
-               int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d) {
+               int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d, int threads) {
     QnArgs g = {};
     g.w[0] = wq, g.w[1] = wk, g.freq = freq, g.pos = pos, g.lens = lens;
     g.eps = eps, g.inv_d = 1.f / (float)d;
     g.T = (int)T, g.heads[0] = (int)H, g.heads[1] = (int)Hkv, g.d = (int)d, g.rot = (int)rot;
     g.tokens = B * T;
-    const long long per = 32 / qn_lanes(d);
-    g.tiles = (g.tokens + per - 1) / per;
+    const long long per = threads / qn_lanes(d);
+    g.groups = (g.tokens + per - 1) / per;
     return g;
 }
 
-// Blocks of the persistent kernels: a warp has one row at least.
-unsigned qn_blocks(const QnArgs &g, int threads, int most) {
-    const long long rows = g.tiles * (g.heads[0] + g.heads[1]), n = (rows + threads / 32 - 1) / (threads / 32);
-    return (unsigned)(n < most ? n : most);
+// Blocks that run at once, each with one row of each of its lanes' at least; forward more where each has 16, so that
+// multiprocessors that are further from memory take fewer (1 x 32/8 x 32768 x 128: 106 us with 2432 blocks against 119
+// with 304, 3 x 10/5 x 1531 x 96: 45 and 31 us with the backward).
+unsigned qn_blocks(const QnArgs &g, int most, int rows) {
+    const long long n = g.groups * (g.heads[0] + g.heads[1]), more = n / rows;
+    return (unsigned)(n < most ? n : more < most ? most : more < 0x7fffffff ? more : 0x7fffffff);
+}
+
+unsigned qn_bwd_blocks(const QnArgs &g) {
+    const long long n = g.groups * (g.heads[0] + g.heads[1]);
+    return (unsigned)(n < kBwdBlocks ? n : kBwdBlocks);
 }
 
 template <typename E, int G, bool IL>
@@ -501,7 +501,7 @@ int qn_fwd_g(const char *fn, const QnFwd &p, const QnArgs &g, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     constexpr int smem = Queue<kFwdThreads, qn_fwd_stages<E>(), Row<E, IL>::N>::BYTES;
     if (int st = set_max_dynamic_smem(done, (const void *)qn_fwd_kernel<E, G, IL>, smem)) return st;
-    qn_fwd_kernel<E, G, IL><<<qn_blocks(g, kFwdThreads, kFwdBlocks), kFwdThreads, smem, s>>>(p, g);
+    qn_fwd_kernel<E, G, IL><<<qn_blocks(g, kFwdBlocks, 16), kFwdThreads, smem, s>>>(p, g);
     return check_launch(fn);
 }
 
@@ -521,7 +521,7 @@ int qn_bwd_g(const char *fn, const QnBwd &p, const QnArgs &g, float *parts, cuda
     static std::atomic<unsigned long long> done{0};
     constexpr int smem = Queue<kBwdThreads, qn_bwd_stages<E>(), 2 * Row<E, IL>::N>::BYTES;
     if (int st = set_max_dynamic_smem(done, (const void *)qn_bwd_kernel<E, G, IL>, smem)) return st;
-    qn_bwd_kernel<E, G, IL><<<qn_blocks(g, kBwdThreads, kBwdBlocks), kBwdThreads, smem, s>>>(p, g, parts);
+    qn_bwd_kernel<E, G, IL><<<qn_bwd_blocks(g), kBwdThreads, smem, s>>>(p, g, parts);
     return check_launch(fn);
 }
 
@@ -536,7 +536,7 @@ int qn_bwd(const char *fn, const QnBwd &p, const QnArgs &g, float *dwq, float *d
         default: st = qn_bwd_g<E, 16, IL>(fn, p, g, parts, s);
     }
     if (st != CLA_OK || (dwq == nullptr && dwk == nullptr)) return st;
-    qn_join_kernel<<<(unsigned)((2 * g.d + 31) / 32), 256, 0, s>>>(parts, dwq, dwk, g.d, (int)qn_blocks(g, kBwdThreads, kBwdBlocks));
+    qn_join_kernel<<<(unsigned)((2 * g.d + 31) / 32), 256, 0, s>>>(parts, dwq, dwk, g.d, (int)qn_bwd_blocks(g));
     return check_launch(fn);
 }
 
@@ -562,7 +562,7 @@ extern "C" int cla_qk_norm_rope_fwd(const void *q, const void *k, const float *w
     Triple r[4];
     if (int st = view_strides(fn, strides, names, heads, ds, 4, B, T, (int64_t)(16 / dtype_bytes(dtype)), r)) return st;
     if (!any_q && !any_k) return CLA_OK;
-    const QnArgs g = qn_args(wq, wk, freq, pos, lens, eps, rot, B, H, Hkv, T, d);
+    const QnArgs g = qn_args(wq, wk, freq, pos, lens, eps, rot, B, H, Hkv, T, d, kFwdThreads);
     const QnFwd p = {{q, k}, {qo, ko}, {r[0], r[1]}, {r[2], r[3]}};
     cudaStream_t s = (cudaStream_t)stream;
     if (dtype == CLA_F32) return interleaved ? qn_fwd<float, true>(fn, p, g, s) : qn_fwd<float, false>(fn, p, g, s);
@@ -601,7 +601,7 @@ extern "C" int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *w
         if (dwk) CLA_CUDA_TRY(cudaMemsetAsync(dwk, 0, d * 4, s), fn);
         return CLA_OK;
     }
-    const QnArgs g = qn_args(wq, wk, freq, pos, lens, eps, rot, B, H, Hkv, T, d);
+    const QnArgs g = qn_args(wq, wk, freq, pos, lens, eps, rot, B, H, Hkv, T, d, kBwdThreads);
     const QnBwd p = {{q, k}, {dqo, dko}, {dq, dk}, {r[0], r[1]}, {r[2], r[3]}, {r[4], r[5]}};
     float *parts = static_cast<float *>(ws);
     if (dtype == CLA_F32)

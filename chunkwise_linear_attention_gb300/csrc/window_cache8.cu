@@ -278,7 +278,7 @@ __device__ __forceinline__ void put_token(uint32_t tile, uint8_t *kc, uint8_t *v
     __syncwarp();
 }
 
-constexpr int kC8Stages = 5;  // tiles of a warp on their way
+constexpr int kC8Stages = 4;  // tiles of a warp on their way
 
 template <int D, int NG>
 constexpr int c8_smem() {
@@ -307,21 +307,26 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
     float(*s_l)[NH] = s_m + kStepWarps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3, G = g.H / g.Hkv;
 
-    // this block's share
-    long long all = 0, before;
-    for (int b0 = 0; b0 < g.B; b0 += 128) all += block_scan(b0 + (int)threadIdx.x < g.B ? held_blocks(g, b0 + threadIdx.x) : 0, before, s_sum);
-    all *= g.Hkv;
+    // this block's share, and the pair in which it starts
+    long long all = 0, before = 0;
+    int held = 0;
+    for (int b0 = 0; b0 < g.B; b0 += 128) {
+        held = b0 + (int)threadIdx.x < g.B ? held_blocks(g, b0 + threadIdx.x) : 0;
+        all += block_scan((long long)held * g.Hkv, before, s_sum);
+    }
     long long at = share_of(all, blockIdx.x);
     const long long start = at, end = share_of(all, blockIdx.x + 1);
     if (threadIdx.x == 0) cuts[blockIdx.x].unit = -1;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits for this grid's end
     long long seen = 0;
     for (int b0 = 0; b0 < g.B && at < end && seen <= at; b0 += 128) {
-        const int mine = b0 + (int)threadIdx.x < g.B ? held_blocks(g, b0 + threadIdx.x) : 0;
-        const long long more = block_scan((long long)mine * g.Hkv, before, s_sum);
-        before += seen;
-        if (before <= at && at < before + (long long)mine * g.Hkv) s_at[0] = b0 + threadIdx.x, s_at[1] = at - before;
-        seen += more;
+        if (g.B > 128) {
+            held = b0 + (int)threadIdx.x < g.B ? held_blocks(g, b0 + threadIdx.x) : 0;
+            const long long more = block_scan((long long)held * g.Hkv, before, s_sum);
+            before += seen;
+            seen += more;
+        }
+        if (before <= at && at < before + (long long)held * g.Hkv) s_at[0] = b0 + threadIdx.x, s_at[1] = at - before;
     }
     __syncthreads();
     int b = 0, used = 1, hk = 0, first = 0;
@@ -574,43 +579,62 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 reinterpret_cast<uint32_t *>(o + (long long)b * g.H * D)[i] = 0u;
 }
 
-// Adds the parts of a cut (sequence, key head), for a query head of the group: warps take every eighth part, which meet
-// in a fixed order.
+// Adds the parts of a cut (sequence, key head), for a query head of the group, in a fixed order: their common maximum first,
+// then every eighth part by a warp.
 template <typename E, int D>
 __global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ parts, const Cut8 *__restrict__ cuts, E *__restrict__ o, int G) {
     constexpr int W = 8, N = D / 32;
-    __shared__ float s_o[W][D], s_m[W], s_l[W];
+    __shared__ float s_o[W][D], s_f[kC8MaxBlocks], s_m[W], s_l[W];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Cut8 cut = cuts[blockIdx.x];
     if (cut.unit < 0) return;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.y, n = cut.last - (int)blockIdx.x + 1;
-    float m = -INFINITY, l = 0.f, x[N];
+    auto part_of = [&](int i) { return parts + (i == 0 ? cut.slot : 2 * ((int)blockIdx.x + i)) * c8_part<D>(G); };
+    constexpr int K = (kC8MaxBlocks + 255) / 256;
+    float2 ml[K];
+    float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = 0.f;
-    for (int i = warp; i < n; i += W) {
+    for (int k = 0; k < K; ++k) {
+        const int i = threadIdx.x + 256 * k;
         const unsigned c = blockIdx.x + i;
-        if (share_of(cut.all, c) == share_of(cut.all, c + 1)) continue;  // more thread blocks than blocks of slots
-        const float *part = parts + (i == 0 ? cut.slot : 2 * (int)c) * c8_part<D>(G);
-        const float2 ml = reinterpret_cast<const float2 *>(part + G * D)[h];
-        const float mn = fmaxf(m, ml.x), a = mn == -INFINITY ? 0.f : ex2(m - mn), f = mn == -INFINITY ? 0.f : ex2(ml.x - mn);
-        m = mn;
-        l = l * a + ml.y * f;
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = x[e] * a + part[h * D + 32 * e + lane] * f;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (i < n && share_of(cut.all, c) < share_of(cut.all, c + 1))  // else: more thread blocks than blocks of slots
+            ml[k] = reinterpret_cast<const float2 *>(part_of(i) + G * D)[h];
+        m = fmaxf(m, ml[k].x);
     }
-    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+    if (lane == 0) s_m[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = fmaxf(m, s_m[w]);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        // a part without a maximum holds nothing, or NaN alone
+        const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : NAN) : ex2(ml[k].x - m);
+        if (threadIdx.x + 256 * k < kC8MaxBlocks) s_f[threadIdx.x + 256 * k] = f;
+        l += f * ml[k].y;
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(~0u, l, x);
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    float x[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < n; i += W) {
+        const float f = s_f[i], *part = part_of(i) + h * D + lane;
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = fmaf(f, f != 0.f ? part[32 * e] : 0.f, x[e]);
+    }
 #pragma unroll
     for (int e = 0; e < N; ++e) s_o[warp][32 * e + lane] = x[e];
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += 256) {
-        float mm = s_m[0], lt = 0.f, y = 0.f;
+        float lt = 0.f, y = 0.f;
 #pragma unroll
-        for (int w = 1; w < W; ++w) mm = fmaxf(mm, s_m[w]);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float f = ex2(s_m[w] - mm);
-            lt += f * s_l[w], y += f * s_o[w][d];
-        }
+        for (int w = 0; w < W; ++w) lt += s_l[w], y += s_o[w][d];
         o[((long long)cut.unit * G + h) * D + d] = from_f32<E>(y / lt);
     }
 }
@@ -662,6 +686,7 @@ int c8_step(const char *fn, const void *q, const void *k, const void *v, void *k
     c8_step_kernel<E, D, NG><<<grid, kStepWarps * 32, c8_smem<D, NG>(), s>>>(
         (const E *)q, (const E *)k, (const E *)v, (uint8_t *)kc, (uint8_t *)vc, kf, vf, (E *)o, parts, cuts, g);
     if (int st = check_launch(fn)) return st;
+    if (g.blocks == 1) return CLA_OK;  // nothing is cut
     // the join's launch goes beside the step's end
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at;

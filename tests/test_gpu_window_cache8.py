@@ -206,6 +206,30 @@ def test_step_over_an_empty_cache_as_made(cla):
     torch.testing.assert_close(o.float().cpu(), want.view(2, 1, 1).expand(2, 1, 64), rtol=2 ** -7, atol=0)
 
 
+def test_step_what_is_not_finite(cla):
+    """A NaN in a key or a query reaches the heads that see it and no others, wherever its slot lies in the split of the work;
+    one in a slot that no token has reached, or in a row without a sequence, reaches nothing."""
+    g = torch.Generator().manual_seed(15)
+    B, H, K, d, W = 3, 4, 2, 64, 3000
+    pos = torch.tensor([2500, 100, -1], dtype=torch.int32)
+    (kc, ks), (vc, vs) = filled(g, B, K, W, d, pos), filled(g, B, K, W, d, pos)
+    q, k, v = rnd(g, B, H, d, dtype=F16), rnd(g, B, K, d, dtype=F16), rnd(g, B, K, d, dtype=F16)
+    q[2], k[2] = float("nan"), float("inf")
+    want = cla.window_attn_step8(q, k, v, kc.clone(), vc.clone(), ks.clone(), vs.clone(), pos.cuda(), window=W)
+    assert bool(torch.isfinite(want).all()) and float(want[2].abs().max()) == 0
+    for slot in (0, 63, 64, 1000, 2047, 2499):
+        bad = kc.clone()
+        bad.view(torch.uint8)[0, 1, slot, 5] = 0x7f
+        got = cla.window_attn_step8(q, k, v, bad, vc.clone(), ks.clone(), vs.clone(), pos.cuda(), window=W)
+        assert bool(torch.isnan(got[0, 2:]).all()) and torch.equal(got[0, :2], want[0, :2]) and torch.equal(got[1:], want[1:])
+    bad = q.clone()
+    bad[1, 1, 3] = float("nan")
+    got = cla.window_attn_step8(bad, k, v, kc.clone(), vc.clone(), ks.clone(), vs.clone(), pos.cuda(), window=W)
+    assert bool(torch.isnan(got[1, 1]).all())
+    got[1, 1] = want[1, 1]
+    assert torch.equal(got, want)
+
+
 def test_step_strided(cla):
     g = torch.Generator().manual_seed(4)
     qkv = rnd(g, 3, 8, 64, dtype=BF16)
