@@ -10,7 +10,7 @@
 // a call brings.  A block holds 32 columns of a head's state in registers: a
 // thread 4 neighbouring columns of every 16th row, so that a warp's accesses
 // are whole 128-byte lines.  The sums over rows go through shuffles and shared
-// memory.
+// memory, with one barrier a token.
 #include "cla_internal.cuh"
 #include "elem_io.cuh"
 #include "strided.cuh"
@@ -18,7 +18,7 @@
 namespace cla {
 namespace {
 
-constexpr int kDsThreads = 128, kDsCols = 32;
+constexpr int kDsThreads = 128, kDsCols = 32, kDsTokens = 4;  // tokens whose inputs are fetched together
 
 struct DsArgs {
     const void *q, *k, *v;
@@ -33,83 +33,111 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 template <typename E, int DK>
 __global__ void __launch_bounds__(kDsThreads) delta_step_kernel(DsArgs g) {
-    constexpr int R = DK / 16;  // rows of a thread
-    __shared__ float s_q[DK], s_k[DK], s_part[kDsThreads / 32][3][kDsCols];
+    constexpr int R = DK / 16, W = kDsThreads / 32;  // rows of a thread
+    __shared__ __align__(16) float4 s_kq[kDsTokens][DK];  // k twice, q twice: operands of paired products as they are read
+    __shared__ __align__(16) float s_v[kDsTokens][kDsCols];
+    __shared__ float s_a[kDsTokens], s_b[kDsTokens];
+    __shared__ __align__(16) float2 s_part[2][W][2][8][2];  // the warps' sums: S^T k and S^T q of 4 columns, two and two
+    __shared__ float s_qk[kDsTokens];
+    static_assert(kDsTokens <= W && kDsCols == 32, "a warp for every token");
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, cg = lane % 8, rg = warp * 4 + lane / 8;
-    const int slice = blockIdx.x % g.slices;
-    const long long bh = blockIdx.x / g.slices;
-    const int b = (int)(bh / g.H), h = (int)(bh % g.H), hk = h / (g.H / g.Hk);
+    const unsigned bh = blockIdx.x / (unsigned)g.slices;
+    const int slice = (int)(blockIdx.x - bh * (unsigned)g.slices), b = (int)(bh / (unsigned)g.H), h = (int)(bh - (unsigned)b * (unsigned)g.H);
     const int col = slice * kDsCols + 4 * cg;
     const bool in = col < g.dv;
     const int n = g.lens == nullptr ? g.T : min(max(g.lens[b], 0), g.T);
-    float *S = g.S + bh * DK * g.dv + col, *o = g.o + bh * g.T * g.dv + col;
-    const E *q = static_cast<const E *>(g.q) + b * g.sq.b + hk * g.sq.h, *k = static_cast<const E *>(g.k) + b * g.sk.b + hk * g.sk.h;
-    const E *v = static_cast<const E *>(g.v) + b * g.sv.b + h * g.sv.h + col;
+    float *S = g.S + ((long long)bh * DK + rg) * g.dv + col;
+    float2 x[R][2];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const float4 f = in && n > 0 ? __ldcs(reinterpret_cast<const float4 *>(S + 16ll * i * g.dv)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[i][0] = make_float2(f.x, f.y), x[i][1] = make_float2(f.z, f.w);
+    }
+    const int hk = (int)((unsigned)h / (unsigned)(g.H / g.Hk));
+    float *o = g.o + (long long)bh * g.T * g.dv + col;
+    const E *q = static_cast<const E *>(g.q) + b * g.sq.b + hk * g.sq.h + lane, *k = static_cast<const E *>(g.k) + b * g.sk.b + hk * g.sk.h + lane;
+    const E *v = static_cast<const E *>(g.v) + b * g.sv.b + h * g.sv.h + slice * kDsCols + lane;
     const float *ld = g.log_decay + b * g.sl.b + h * g.sl.h, *be = g.beta + b * g.sb.b + h * g.sb.h;
-
-    float4 x[R];
+    for (int t0 = 0; t0 < n; t0 += kDsTokens) {
+        const int nt = min(kDsTokens, n - t0);
+        if (t0 > 0) __syncthreads();  // the tokens before have been used
+        if (warp < nt) {  // a token's inputs by a warp
+            const long long t = t0 + warp;
+            float qk = 0.f, kk[DK / 32], qq[DK / 32];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        x[i] = in && n > 0 ? __ldcs(reinterpret_cast<const float4 *>(S + (long long)(rg + 16 * i) * g.dv)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int t = 0; t < n; ++t) {
-        for (int i = threadIdx.x; i < DK; i += kDsThreads) {
-            s_q[i] = to_f32(q[t * g.sq.t + i]);
-            s_k[i] = to_f32(k[t * g.sk.t + i]);
-        }
-        const float a = expf(ld[t * g.sl.t]), beta = be[t * g.sb.t];
-        float vv[4];
+            for (int i = 0; i < DK / 32; ++i) kk[i] = to_f32(k[t * g.sk.t + 32 * i]), qq[i] = to_f32(q[t * g.sq.t + 32 * i]);
+            s_v[warp][lane] = slice * kDsCols + lane < g.dv ? to_f32(v[t * g.sv.t]) : 0.f;
+            if (lane == 0) s_a[warp] = expf(ld[t * g.sl.t]), s_b[warp] = be[t * g.sb.t];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) vv[e] = in ? to_f32(v[t * g.sv.t + e]) : 0.f;
-        __syncthreads();
-        float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f}, qk = 0.f;
+            for (int i = 0; i < DK / 32; ++i) {
+                s_kq[warp][lane + 32 * i] = make_float4(kk[i], kk[i], qq[i], qq[i]);
+                qk = fmaf(kk[i], qq[i], qk);
+            }
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float kk = s_k[rg + 16 * i], qq = s_q[rg + 16 * i];
-            x[i].x = a == 0.f ? 0.f : a * x[i].x;
-            x[i].y = a == 0.f ? 0.f : a * x[i].y;
-            x[i].z = a == 0.f ? 0.f : a * x[i].z;
-            x[i].w = a == 0.f ? 0.f : a * x[i].w;
-            sk[0] = fmaf(kk, x[i].x, sk[0]), sk[1] = fmaf(kk, x[i].y, sk[1]), sk[2] = fmaf(kk, x[i].z, sk[2]), sk[3] = fmaf(kk, x[i].w, sk[3]);
-            sq[0] = fmaf(qq, x[i].x, sq[0]), sq[1] = fmaf(qq, x[i].y, sq[1]), sq[2] = fmaf(qq, x[i].z, sq[2]), sq[3] = fmaf(qq, x[i].w, sq[3]);
-            qk = fmaf(qq, kk, qk);
-        }
-#pragma unroll
-        for (int w = 8; w < 32; w <<= 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sk[e] += __shfl_xor_sync(~0u, sk[e], w), sq[e] += __shfl_xor_sync(~0u, sq[e], w);
-            qk += __shfl_xor_sync(~0u, qk, w);
-        }
-        if (lane < 8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s_part[warp][0][4 * cg + e] = sk[e], s_part[warp][1][4 * cg + e] = sq[e];
-            s_part[warp][2][cg] = qk;
+            for (int w = 1; w < 32; w <<= 1) qk += __shfl_xor_sync(~0u, qk, w);
+            if (lane == 0) s_qk[warp] = qk;
         }
         __syncthreads();
-        float u[4], y[4];
-        qk = 0.f;
+        for (int t = 0; t < nt; ++t) {
+            const float a = s_a[t];
+            if (a == 0.f) {  // whatever the state holds
 #pragma unroll
-        for (int w = 0; w < kDsThreads / 32; ++w) qk += s_part[w][2][cg];
+                for (int i = 0; i < R; ++i) x[i][0] = x[i][1] = both(0.f);
+            }
+            float2 sk[2] = {both(0.f), both(0.f)}, sq[2] = {both(0.f), both(0.f)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float p = 0.f, r = 0.f;
+            for (int i = 0; i < R; ++i) {
+                const float4 kq = s_kq[t][rg + 16 * i];
+                const float2 kk = make_float2(kq.x, kq.y), qq = make_float2(kq.z, kq.w);
+                sk[0] = fma2(kk, x[i][0], sk[0]), sk[1] = fma2(kk, x[i][1], sk[1]);
+                sq[0] = fma2(qq, x[i][0], sq[0]), sq[1] = fma2(qq, x[i][1], sq[1]);
+            }
+            // the four lanes of a column group add up: one half of the sums goes to either pair of them, a half of that to each
+            const bool hi = lane & 16, odd = lane & 8;
+            float2 keep[2];
 #pragma unroll
-            for (int w = 0; w < kDsThreads / 32; ++w) p += s_part[w][0][4 * cg + e], r += s_part[w][1][4 * cg + e];
-            u[e] = beta * (vv[e] - p);
-            y[e] = fmaf(qk, u[e], r);
+            for (int e = 0; e < 2; ++e) {
+                const float2 give = hi ? sk[e] : sq[e];
+                keep[e] = hi ? sq[e] : sk[e];
+                keep[e].x += __shfl_xor_sync(~0u, give.x, 16), keep[e].y += __shfl_xor_sync(~0u, give.y, 16);
+            }
+            const float2 give = odd ? keep[0] : keep[1];
+            float2 sum = odd ? keep[1] : keep[0];
+            sum.x += __shfl_xor_sync(~0u, give.x, 8), sum.y += __shfl_xor_sync(~0u, give.y, 8);
+            float2(*part)[2][8][2] = s_part[t & 1];  // the other one may still be read
+            part[warp][hi][cg][odd] = sum;
+            __syncthreads();
+            const float qk = s_qk[t];
+            float4 p = *reinterpret_cast<const float4 *>(part[0][0][cg]), y = *reinterpret_cast<const float4 *>(part[0][1][cg]);
+#pragma unroll
+            for (int w = 1; w < W; ++w) {
+                const float4 f = *reinterpret_cast<const float4 *>(part[w][0][cg]), e = *reinterpret_cast<const float4 *>(part[w][1][cg]);
+                p.x += f.x, p.y += f.y, p.z += f.z, p.w += f.w;
+                y.x += e.x, y.y += e.y, y.z += e.z, y.w += e.w;
+            }
+            const float4 vv = *reinterpret_cast<const float4 *>(&s_v[t][4 * cg]);
+            const float beta = s_b[t];
+            const float2 u0 = make_float2(beta * fmaf(-a, p.x, vv.x), beta * fmaf(-a, p.y, vv.y));
+            const float2 u1 = make_float2(beta * fmaf(-a, p.z, vv.z), beta * fmaf(-a, p.w, vv.w));
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float2 kk = *reinterpret_cast<const float2 *>(&s_kq[t][rg + 16 * i]);
+                x[i][0] = fma2(kk, u0, mul2(both(a), x[i][0]));
+                x[i][1] = fma2(kk, u1, mul2(both(a), x[i][1]));
+            }
+            if (rg == 0 && in) *reinterpret_cast<float4 *>(o + (long long)(t0 + t) * g.dv) = make_float4(fmaf(qk, u0.x, a * y.x), fmaf(qk, u0.y, a * y.y), fmaf(qk, u1.x, a * y.z), fmaf(qk, u1.y, a * y.w));
         }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float kk = s_k[rg + 16 * i];
-            x[i].x = fmaf(kk, u[0], x[i].x), x[i].y = fmaf(kk, u[1], x[i].y), x[i].z = fmaf(kk, u[2], x[i].z), x[i].w = fmaf(kk, u[3], x[i].w);
-        }
-        if (rg == 0 && in) *reinterpret_cast<float4 *>(o + (long long)t * g.dv) = make_float4(y[0], y[1], y[2], y[3]);
-        __syncthreads();
     }
     if (in && n > 0) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) __stcs(reinterpret_cast<float4 *>(S + (long long)(rg + 16 * i) * g.dv), x[i]);
+        for (int i = 0; i < R; ++i)
+            __stcs(reinterpret_cast<float4 *>(S + 16ll * i * g.dv), make_float4(x[i][0].x, x[i][0].y, x[i][1].x, x[i][1].y));
     }
     if (in)
         for (int t = n + rg; t < g.T; t += 16) *reinterpret_cast<float4 *>(o + (long long)t * g.dv) = make_float4(0.f, 0.f, 0.f, 0.f);
