@@ -338,7 +338,7 @@ struct QnBwd {
 
 // A block leaves its rows' sums of dw in parts[block][2][d].
 template <typename E, int G, bool IL>
-__global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs g, float *parts) {
+__global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs g, float *parts, WsHeader *hdr) {
     constexpr int S = qn_bwd_stages<E>(), N = Row<E, IL>::N, W = kBwdThreads / 32;
     extern __shared__ __align__(16) char smem[];
     __shared__ unsigned long long s_turn[128];
@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
     const Queue<kBwdThreads, S, 2 * N> queue(smem);
     const Lane<G, IL> l(g);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (blockIdx.x == 0 && threadIdx.x < (int)sizeof(WsHeader) / 4) reinterpret_cast<uint32_t *>(hdr)[threadIdx.x] = 0u;  // nothing waits
     for (int i = threadIdx.x; i < g.rot / 2; i += kBwdThreads) s_turn[i] = turns(g.freq[i]);
     __syncthreads();
     const Share share(g.groups * (g.heads[0] + g.heads[1]));
@@ -521,7 +522,7 @@ int qn_bwd_g(const char *fn, const QnBwd &p, const QnArgs &g, float *parts, cuda
     static std::atomic<unsigned long long> done{0};
     constexpr int smem = Queue<kBwdThreads, qn_bwd_stages<E>(), 2 * Row<E, IL>::N>::BYTES;
     if (int st = set_max_dynamic_smem(done, (const void *)qn_bwd_kernel<E, G, IL>, smem)) return st;
-    qn_bwd_kernel<E, G, IL><<<qn_bwd_blocks(g), kBwdThreads, smem, s>>>(p, g, parts);
+    qn_bwd_kernel<E, G, IL><<<qn_bwd_blocks(g), kBwdThreads, smem, s>>>(p, g, parts, reinterpret_cast<WsHeader *>(parts) - 1);
     return check_launch(fn);
 }
 
@@ -572,7 +573,7 @@ extern "C" int cla_qk_norm_rope_fwd(const void *q, const void *k, const float *w
 
 extern "C" size_t cla_qk_norm_rope_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d) {
     if (qn_check("cla_qk_norm_rope_bwd_workspace_size", B, H, Hkv, T, d, 0, 1.f, CLA_F32) != CLA_OK) return 0;
-    return (size_t)kBwdBlocks * 2 * d * 4;
+    return sizeof(WsHeader) + (size_t)kBwdBlocks * 2 * d * 4;
 }
 
 extern "C" int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const float *wk, const float *freq,
@@ -597,13 +598,14 @@ extern "C" int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *w
     if (int st = view_strides(fn, strides, names, heads, ds, 6, B, T, (int64_t)(16 / dtype_bytes(dtype)), r)) return st;
     cudaStream_t s = (cudaStream_t)stream;
     if (!any_q && !any_k) {
+        CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(WsHeader), s), fn);
         if (dwq) CLA_CUDA_TRY(cudaMemsetAsync(dwq, 0, d * 4, s), fn);
         if (dwk) CLA_CUDA_TRY(cudaMemsetAsync(dwk, 0, d * 4, s), fn);
         return CLA_OK;
     }
     const QnArgs g = qn_args(wq, wk, freq, pos, lens, eps, rot, B, H, Hkv, T, d, kBwdThreads);
     const QnBwd p = {{q, k}, {dqo, dko}, {dq, dk}, {r[0], r[1]}, {r[2], r[3]}, {r[4], r[5]}};
-    float *parts = static_cast<float *>(ws);
+    float *parts = reinterpret_cast<float *>(static_cast<WsHeader *>(ws) + 1);
     if (dtype == CLA_F32)
         return interleaved ? qn_bwd<float, true>(fn, p, g, dwq, dwk, parts, s) : qn_bwd<float, false>(fn, p, g, dwq, dwk, parts, s);
     if (dtype == CLA_BF16)

@@ -291,10 +291,9 @@ constexpr size_t c8_part(size_t G) {  // floats of a part: G heads' sums, their 
 }
 
 template <typename E, int D, int NG>
-__global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q, const E *__restrict__ k,
-                                                                       const E *__restrict__ v, uint8_t *kc, uint8_t *vc, float *kf,
-                                                                       float *vf, E *__restrict__ o, float *__restrict__ parts,
-                                                                       Cut8 *__restrict__ cuts, Step8Args g) {
+__global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q, const E *__restrict__ k, const E *__restrict__ v,
+                                                         uint8_t *kc, uint8_t *vc, float *kf, float *vf, E *__restrict__ o,
+                                                         float *__restrict__ parts, Cut8 *__restrict__ cuts, WsHeader *hdr, Step8Args g) {
     constexpr int NH = 8 * NG, KC = D / 64, M = D / 16, P = D / 16;  // 64-column pieces; products of 16 columns of o; pieces of a slot
     constexpr bool BF = std::is_same<E, __nv_bfloat16>::value;
     extern __shared__ __align__(128) char smem[];
@@ -307,6 +306,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
     float(*s_l)[NH] = s_m + kStepWarps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3, G = g.H / g.Hkv;
 
+    if (blockIdx.x == 0 && threadIdx.x < (int)sizeof(WsHeader) / 4) reinterpret_cast<uint32_t *>(hdr)[threadIdx.x] = 0u;  // nothing waits
     // this block's share, and the pair in which it starts
     long long all = 0, before = 0;
     int held = 0;
@@ -681,10 +681,11 @@ int c8_step(const char *fn, const void *q, const void *k, const void *v, void *k
     if (int st = c8_resident<E, D, NG>(fn, &n)) return st;
     const long long most = (long long)g.B * g.Hkv * g.blocks;
     const unsigned grid = (unsigned)(most < n ? most : n);
-    Cut8 *cuts = static_cast<Cut8 *>(ws);
+    WsHeader *hdr = static_cast<WsHeader *>(ws);
+    Cut8 *cuts = reinterpret_cast<Cut8 *>(hdr + 1);
     float *parts = reinterpret_cast<float *>(cuts + kC8MaxBlocks);
     c8_step_kernel<E, D, NG><<<grid, kStepWarps * 32, c8_smem<D, NG>(), s>>>(
-        (const E *)q, (const E *)k, (const E *)v, (uint8_t *)kc, (uint8_t *)vc, kf, vf, (E *)o, parts, cuts, g);
+        (const E *)q, (const E *)k, (const E *)v, (uint8_t *)kc, (uint8_t *)vc, kf, vf, (E *)o, parts, cuts, hdr, g);
     if (int st = check_launch(fn)) return st;
     if (g.blocks == 1) return CLA_OK;  // nothing is cut
     // the join's launch goes beside the step's end
@@ -740,7 +741,7 @@ extern "C" int cla_window_cache8_write(const void *k, const void *v, const int32
 extern "C" size_t cla_window_attn_step8_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
     if (c8_check("cla_window_attn_step8_workspace_size", B, H, Hkv, 1, d, window, sinks, CLA_BF16, 1.f) != CLA_OK) return 0;
     const int64_t most = B * Hkv * ((sinks + window + kC8Block - 1) / kC8Block);  // a thread block has one block of slots at least
-    return sizeof(Cut8) * kC8MaxBlocks + (size_t)(2 * (most < kC8MaxBlocks ? most : kC8MaxBlocks) * (Hkv ? H / Hkv : 0) * (d + 2) * 4);
+    return sizeof(WsHeader) + sizeof(Cut8) * kC8MaxBlocks + (size_t)(2 * (most < kC8MaxBlocks ? most : kC8MaxBlocks) * (Hkv ? H / Hkv : 0) * (d + 2) * 4);
 }
 
 extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v, void *kcache, void *vcache, float *kscale,
@@ -750,9 +751,8 @@ extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v
     const char *fn = "cla_window_attn_step8";
     clear_error();
     if (int st = c8_check(fn, B, H, Hkv, 1, d, window, sinks, dtype, scale)) return st;
-    if (B * H == 0) return CLA_OK;
-    if (H / Hkv > 65535) return fail(CLA_ERR_UNSUPPORTED, "%s: %lld query heads of a key head", fn, (long long)(H / Hkv));
-    if (!q || !k || !v || !kcache || !vcache || !kscale || !vscale || !pos || !o)
+    if (H > 0 && H / Hkv > 65535) return fail(CLA_ERR_UNSUPPORTED, "%s: %lld query heads of a key head", fn, (long long)(H / Hkv));
+    if (B * H > 0 && (!q || !k || !v || !kcache || !vcache || !kscale || !vscale || !pos || !o))
         return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned_or_null({q, k, v, kcache, vcache, o}, 16) || !aligned_or_null({pos, kscale, vscale}, 4))
         return fail(CLA_ERR_INVALID_ARG, "%s: a pointer is misaligned", fn);
@@ -766,6 +766,10 @@ extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v
     if (strides != nullptr)
         for (int i = 0; i < 3; ++i) full[3 * i] = strides[2 * i], full[3 * i + 1] = strides[2 * i + 1], full[3 * i + 2] = d;
     if (int st = view_strides(fn, strides ? full : nullptr, names, heads, ds, 3, B, 1, 8, r)) return st;
+    if (B * H == 0) {
+        CLA_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(WsHeader), (cudaStream_t)stream), fn);
+        return CLA_OK;
+    }
     const Step8Args g{pos,      scale * 1.4426950408889634f, window, sinks, sinks + window, (int)B, (int)H, (int)Hkv,
                       (int)((sinks + window + kC8Block - 1) / kC8Block), r[0], r[1], r[2]};
     cudaStream_t s = (cudaStream_t)stream;

@@ -75,6 +75,21 @@ def test_nothing_to_do(cla, B, H, K, T):
     assert float(dwq.abs().max()) == 0 and float(dwk.abs().max()) == 0
 
 
+def test_workspace(cla):
+    """A workspace of the caller's, whatever it held and in use again; its status; one that is too small."""
+    n = cla.qk_norm_rope_bwd_workspace_size(2, 4, 2, 50, 64)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    for T in (50, 0, 50):
+        args, ups = inputs(2, 4, 2, T, 64, 64, BF16)
+        want = cla.qk_norm_rope_bwd(*args, *ups)
+        for a, b in zip(want, cla.qk_norm_rope_bwd(*args, *ups, workspace=ws)):
+            assert torch.equal(a, b)
+        cla.check_status(ws)
+        ws[100:].fill_(255)
+    with pytest.raises(ValueError, match="workspace"):
+        cla.qk_norm_rope_bwd(*args, *ups, workspace=ws[:n - 1])
+
+
 @pytest.mark.parametrize("which", ["none", "q", "k"])
 def test_weights_left_out(cla, which):
     (q, k, wq, wk, freq), ups = inputs(2, 3, 2, 20, 64, 32, BF16)

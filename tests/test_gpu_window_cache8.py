@@ -349,3 +349,43 @@ def test_caches_of_more_than_31_bits(cla):
         f = R.factor(torch.cat((v[b, 0].double().cpu(), torch.tensor([2.0 ** -8]))))
         assert float(vs[b, 0, j // 64]) == f
         same(vc[b, 0, j], R.rounded(v[b, 0].double().cpu() / f))
+
+
+@pytest.mark.parametrize("B,H,K,window", [(300, 2, 1, 100), (700, 1, 1, 63), (129, 2, 2, 200)])
+def test_many_sequences(cla, B, H, K, window):
+    """More sequences than a block has threads, most of them short or empty; and none at all."""
+    g = torch.Generator().manual_seed(B)
+    pos = torch.randint(-40, 2 * window, (B,), generator=g, dtype=torch.int32)
+    pos[:3], pos[B - 2:] = -1, -5
+    step(cla, g, B, H, K, 64, window, 2, BF16, pos)
+    pos[:] = -1
+    assert float(step(cla, g, B, H, K, 64, window, 2, BF16, pos).abs().max()) == 0
+    pos[B // 2] = 70
+    step(cla, g, B, H, K, 64, window, 2, BF16, pos)
+
+
+@pytest.mark.parametrize("B,K", [(0, 1), (2, 0)])
+def test_step_nothing_to_do(cla, B, K):
+    cache = cla.window_cache8(B, K, 64, window=100)
+    x = torch.zeros(B, K, 64, dtype=BF16, device="cuda")
+    ws = torch.full((cla.window_attn_step8_workspace_size(B, K, K, 64, 100),), 255, dtype=torch.uint8, device="cuda")
+    pos = torch.zeros(B, dtype=torch.int32, device="cuda")
+    assert cla.window_attn_step8(x, x, x, *cache, pos, window=100, workspace=ws).shape == x.shape
+    cla.check_status(ws)
+
+
+def test_step_workspace(cla):
+    """A workspace of the caller's, whatever it held and in use again; its status; one that is too small."""
+    g = torch.Generator().manual_seed(17)
+    B, H, K, d, W = 2, 6, 2, 64, 5000
+    pos = torch.tensor([4000, 4999], dtype=torch.int32)
+    (kc, ks), (vc, vs) = filled(g, B, K, W, d, pos), filled(g, B, K, W, d, pos)
+    q, k, v = rnd(g, B, H, d, dtype=BF16), rnd(g, B, K, d, dtype=BF16), rnd(g, B, K, d, dtype=BF16)
+    want = cla.window_attn_step8(q, k, v, kc, vc, ks, vs, pos.cuda(), window=W)
+    n = cla.window_attn_step8_workspace_size(B, H, K, d, W)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(want, cla.window_attn_step8(q, k, v, kc, vc, ks, vs, pos.cuda(), window=W, workspace=ws))
+        cla.check_status(ws)
+    with pytest.raises(ValueError, match="workspace"):
+        cla.window_attn_step8(q, k, v, kc, vc, ks, vs, pos.cuda(), window=W, workspace=ws[:n - 1])

@@ -58,7 +58,7 @@ def test_norm_refusals(lib, call, kw, status):
 def test_norm_workspace(lib):
     for kw, st in [(dict(ws=None), 5), (dict(ws=ODD), 5), (dict(n=100), 5), (dict(dw=ODD), 1)]:
         assert nbwd(lib, **kw) == st, kw
-    assert lib.cla_qk_norm_rope_bwd_workspace_size(2, 4, 2, 10, 64) >= 2 * 64 * 4
+    assert lib.cla_qk_norm_rope_bwd_workspace_size(2, 4, 2, 10, 64) >= 256 + 2 * 64 * 4
     assert lib.cla_qk_norm_rope_bwd_workspace_size(2, 4, 2, 10, 65) == 0
     assert lib.cla_qk_norm_rope_bwd_workspace_size(-2, 4, 2, 10, 64) == 0
     assert nfwd(lib, B=0) == 0 and nfwd(lib, H=0, K=0) == 0 and nfwd(lib, T=0, q=None, k=None, qo=None, ko=None, freq=None) == 0
@@ -93,10 +93,11 @@ def test_cache8_calls(lib):
                dict(lens=None), dict(o=ODD)):
         assert cstep(lib, **kw) == 1, kw
     assert cstep(lib, ws=None) == 5 and cstep(lib, ws=ODD) == 5 and cstep(lib, nbytes=1000) == 5 and cstep(lib, H=1 << 17, K=1) == 2
-    assert lib.cla_window_attn_step8_workspace_size(2, 4, 2, 64, 100, 2) > 8 * 2 * 66 * 4
+    assert lib.cla_window_attn_step8_workspace_size(2, 4, 2, 64, 100, 2) > 256 + 8 * 2 * 66 * 4
+    assert lib.cla_window_attn_step8_workspace_size(0, 0, 0, 64, 100, 2) >= 256
     assert lib.cla_window_attn_step8_workspace_size(2, 4, 3, 64, 100, 2) == 0
     assert cwrite(lib, T=-1) == 1 and cwrite(lib, T=1 << 31) == 2
-    assert cwrite(lib, B=0) == 0 and cwrite(lib, T=0) == 0 and cstep(lib, B=0) == 0 and cstep(lib, H=0, K=0) == 0
+    assert cwrite(lib, B=0) == 0 and cwrite(lib, T=0) == 0 and cstep(lib, B=0, ws=None) == 5
 
 
 def dstep(lib, q=A, v=A, ld=A, beta=A, lens=None, S=A, o=A, dtype=1, B=2, H=4, Hk=2, T=3, dk=64, dv=64, s=None):
