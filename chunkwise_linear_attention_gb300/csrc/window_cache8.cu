@@ -282,8 +282,7 @@ constexpr int kC8Stages = 4;  // tiles of a warp on their way
 
 template <int D, int NG>
 constexpr int c8_smem() {
-    const int ring = kStepWarps * kC8Stages * 32 * D, parts = kStepWarps * 8 * NG * (D + 2) * 4;
-    return ring > parts ? ring : parts;
+    return kStepWarps * (kC8Stages * 32 * D + 8 * NG * (D + 2) * 4);  // the ring of tiles, the parts of the result
 }
 template <int D>
 constexpr size_t c8_part(size_t G) {  // floats of a part: G heads' sums, their maxima and totals
@@ -300,9 +299,9 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
     __shared__ __align__(16) E s_new[2][D];
     __shared__ float s_top[2][kStepWarps];
     __shared__ long long s_sum[kStepWarps], s_at[2];
-    // the ring of tiles, and after the slots the parts of the result
-    float(*s_o)[NH][D] = reinterpret_cast<float(*)[NH][D]>(smem);
-    float(*s_m)[NH] = reinterpret_cast<float(*)[NH]>(smem + kStepWarps * NH * D * 4);
+    char *const s_parts = smem + kStepWarps * kC8Stages * 32 * D;
+    float(*s_o)[NH][D] = reinterpret_cast<float(*)[NH][D]>(s_parts);
+    float(*s_m)[NH] = reinterpret_cast<float(*)[NH]>(s_parts + kStepWarps * NH * D * 4);
     float(*s_l)[NH] = s_m + kStepWarps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3, G = g.H / g.Hkv;
 
@@ -335,43 +334,51 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
     const uint32_t ring = smem_u32(smem) + warp * (kC8Stages * 32 * D), ring_end = ring + kC8Stages * 32 * D;
     // where this lane's pieces go in a tile: the x-th 512 x bytes on, with the keys of tile_at the same for every other x
     uint32_t at_lane[2] = {tile_at<D>(lane / P, lane % P), tile_at<D>(lane / P + 32 / P, lane % P) - 512u};
-    while (at < end) {
-        const long long unit = (long long)b * g.Hkv + hk, p = g.pos[b];
-        const int mine = (int)(p < g.sinks ? p : g.sinks + (p - g.sinks) % g.window), n = (int)min(p + 1, g.slots);
-        const int cnt = (int)min((long long)(used - first), end - at);
-        const bool whole = cnt == used;
-        uint8_t *kb = kc + unit * g.slots * D, *vb = vc + unit * g.slots * D;
-        float *kfb = kf + unit * g.blocks + first, *vfb = vf + unit * g.blocks + first;
-        const int own = mine / kC8Block - first;  // the token's block, where that is of this segment
-        // the warp's 16 slots of block i, which lie one behind the other; zeros behind the last that holds a token
-        const uint8_t *kl = kb + ((long long)first * kC8Block + 16 * warp) * D + 16 * lane;
-        const uint8_t *vl = vb + ((long long)first * kC8Block + 16 * warp) * D + 16 * lane;
-        auto fetch = [&](int i, uint32_t to) {
-            constexpr int R = 32 / P;
-            const int s0 = (first + i) * kC8Block + 16 * warp;
-            const long long from = (long long)i * (kC8Block * D);
-            if (s0 + 16 <= n) {
+    // the segment: blocks [first, first + cnt) of pair (b, hk), whose n first slots hold tokens
+    int n = 0, cnt = 0, own = 0, mine = 0;
+    uint8_t *kb = nullptr, *vb = nullptr;
+    const uint8_t *kl = nullptr, *vl = nullptr;
+    auto locate = [&]() {
+        const long long p = g.pos[b], unit = (long long)b * g.Hkv + hk, from = ((long long)first * kC8Block + 16 * warp) * D + 16 * lane;
+        mine = (int)(p < g.sinks ? p : g.sinks + (p - g.sinks) % g.window), n = (int)min(p + 1, g.slots);
+        cnt = (int)min((long long)(used - first), end - at);
+        own = mine / kC8Block - first;  // the token's block, where that is of this segment
+        kb = kc + unit * g.slots * D, vb = vc + unit * g.slots * D;
+        kl = kb + from, vl = vb + from;
+    };
+    // the warp's 16 slots of block i, which lie one behind the other; zeros behind the last that holds a token
+    auto fetch = [&](int i, uint32_t to) {
+        constexpr int R = 32 / P;
+        const int s0 = (first + i) * kC8Block + 16 * warp;
+        const long long from = (long long)i * (kC8Block * D);
+        if (s0 + 16 <= n) {
 #pragma unroll
-                for (int x = 0; x < 16 / R; ++x) {
-                    cp_async16(to + at_lane[x & 1] + 512 * x, kl + from + 512 * x, 16u);
-                    cp_async16(to + 16 * D + at_lane[x & 1] + 512 * x, vl + from + 512 * x, 16u);
-                }
-            } else {
-#pragma unroll 1
-                for (int x = 0; x < 16 / R; ++x) {
-                    const bool in = s0 + lane / P + R * x < n;
-                    cp_async16(to + at_lane[x & 1] + 512 * x, in ? kl + from + 512 * x : kb, in ? 16u : 0u);
-                    cp_async16(to + 16 * D + at_lane[x & 1] + 512 * x, in ? vl + from + 512 * x : vb, in ? 16u : 0u);
-                }
+            for (int x = 0; x < 16 / R; ++x) {
+                cp_async16(to + at_lane[x & 1] + 512 * x, kl + from + 512 * x, 16u);
+                cp_async16(to + 16 * D + at_lane[x & 1] + 512 * x, vl + from + 512 * x, 16u);
             }
-        };
+        } else {
+#pragma unroll 1
+            for (int x = 0; x < 16 / R; ++x) {
+                const bool in = s0 + lane / P + R * x < n;
+                cp_async16(to + at_lane[x & 1] + 512 * x, in ? kl + from + 512 * x : kb, in ? 16u : 0u);
+                cp_async16(to + 16 * D + at_lane[x & 1] + 512 * x, in ? vl + from + 512 * x : vb, in ? 16u : 0u);
+            }
+        }
+    };
+    auto prefetch = [&]() {
+        __syncwarp();  // the warp has read its tiles, and written its part of the token's block
+#pragma unroll 1
+        for (int i = 0; i < kC8Stages; ++i) {
+            if (i < cnt) fetch(i, ring + i * (32 * D));
+            cp_async_commit();
+        }
+    };
+    if (at < end) locate(), prefetch();
+    while (at < end) {
+        float *kfb = kf + ((long long)b * g.Hkv + hk) * g.blocks + first, *vfb = vf + ((long long)b * g.Hkv + hk) * g.blocks + first;
         for (int h0 = 0; h0 < G; h0 += NH) {  // 16 heads at most, or the segment again (from L2)
             const int nh = min(NH, G - h0);
-#pragma unroll 1
-            for (int i = 0; i < kC8Stages; ++i) {
-                if (i < cnt) fetch(i, ring + i * (32 * D));
-                cp_async_commit();
-            }
             if (h0 == 0 && threadIdx.x < 2 * P * 2) {  // the token's key and value
                 const int which = threadIdx.x / (2 * P), c = threadIdx.x % (2 * P);
                 const E *x = which == 0 ? k + b * g.sk.b + hk * g.sk.h : v + b * g.sv.b + hk * g.sv.h;
@@ -520,7 +527,27 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                     }
                 }
             }
-            __syncthreads();  // the last tiles have been read: the parts take the ring's place
+            // the next segment, or this one for more heads, is on its way while the parts meet
+            const long long unit = (long long)b * g.Hkv + hk;
+            const int slot = 2 * blockIdx.x + (at != start);
+            const bool whole = cnt == used;
+            if (h0 + NH >= G) {
+                if (!whole && first == 0 && threadIdx.x == 0) {
+                    // the thread block that has the pair's last block of slots: the least c with share_of(c + 1) >= at + used
+                    const long long x = at + used;
+                    cuts[blockIdx.x] = Cut8{(int)unit, slot, (int)((x * gridDim.x + all - 1) / all) - 1, (int)all};
+                }
+                at += cnt;
+                first = 0;
+                if (at < end && ++hk == g.Hkv) {
+                    hk = 0;
+                    do used = held_blocks(g, ++b);
+                    while (used == 0);
+                }
+                if (at < end) locate(), prefetch();
+            } else {
+                prefetch();
+            }
             // product y, row r: column (D / 8) r + 2 y, row r + 8: the next one
 #pragma unroll
             for (int a = 0; a < NG; ++a)
@@ -536,7 +563,6 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 }
             __syncthreads();
             // the warps' parts together: the outputs of a whole segment, or a part for the join
-            const int slot = 2 * blockIdx.x + (at != start);
             float *part = parts + slot * c8_part<D>(G);
             for (int i = threadIdx.x; i < nh * D / 2; i += blockDim.x) {
                 const int h = i / (D / 2), d = i % (D / 2) * 2;
@@ -557,19 +583,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                     if (d == 0) reinterpret_cast<float2 *>(part + G * D)[h0 + h] = make_float2(mm, lt);
                 }
             }
-            __syncthreads();  // the ring is free again
-        }
-        if (!whole && first == 0 && threadIdx.x == 0) {
-            // the thread block that has the pair's last block of slots: the least c with share_of(c + 1) >= at + used
-            const long long x = at + used;
-            cuts[blockIdx.x] = Cut8{(int)unit, 2 * (int)blockIdx.x + (at != start), (int)((x * gridDim.x + all - 1) / all) - 1, (int)all};
-        }
-        at += cnt;
-        first = 0;
-        if (at < end && ++hk == g.Hkv) {
-            hk = 0;
-            do used = held_blocks(g, ++b);
-            while (used == 0);
+            __syncthreads();  // the parts have been read
         }
     }
     // rows without a sequence
