@@ -798,9 +798,14 @@ _HALF = (torch.bfloat16, torch.float16)
 
 def _strides(*tensors):
     """The tensors' outer strides as the C ABI takes them; None when all are dense."""
-    if all(t.is_contiguous() for t in tensors):
+    for t in tensors:
+        if not t.is_contiguous():
+            break
+    else:
         return None
-    flat = [s for t in tensors for s in t.stride()[:-1]]
+    flat = ()
+    for t in tensors:
+        flat += t.stride()[:-1]
     return (ctypes.c_int64 * len(flat))(*flat)
 
 
@@ -1001,8 +1006,8 @@ def qk_norm_rope_step(q, k, wq, wk, freq, pos, *, eps=1e-6, interleaved=False, q
     qo, ko = _out(qo, hs, dt, dev), _out(ko, ks, dt, dev)
     strides = None
     if not (q.is_contiguous() and k.is_contiguous() and qo.is_contiguous() and ko.is_contiguous()):
-        flat = [s for t in (q, k, qo, ko) for s in (*t.stride()[:2], d)]  # no stride from token to token
-        strides = (ctypes.c_int64 * 12)(*flat)
+        # there is no stride from token to token
+        strides = (ctypes.c_int64 * 12)(*q.stride()[:2], d, *k.stride()[:2], d, *qo.stride()[:2], d, *ko.stride()[:2], d)
     _launch("cla_qk_norm_rope_fwd", dev, (
         _T(q, dt, "q", hs, True), _T(k, dt, "k", ks, True), _T(wq, f32, "wq", (d,)), _T(wk, f32, "wk", (d,)),
         _T(freq, f32, "freq", (rot // 2,)), _T(pos, torch.int32, "pos", (B,)), None, _T(qo, dt, "qo", hs, True),
@@ -1010,6 +1015,7 @@ def qk_norm_rope_step(q, k, wq, wk, freq, pos, *, eps=1e-6, interleaved=False, q
     return qo, ko
 
 
+@functools.lru_cache(maxsize=256)  # a number that the sizes fix
 def qk_norm_rope_bwd_workspace_size(B, H, Hkv, T, d) -> int:
     return int(lib().cla_qk_norm_rope_bwd_workspace_size(B, H, Hkv, T, d))
 
