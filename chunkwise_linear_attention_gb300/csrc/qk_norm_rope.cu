@@ -11,9 +11,18 @@
 // What bounds them is memory: a row is read once and written once (backward:
 // two reads, one write).  A row is handled by the fewest lanes, a power of two,
 // that take 16 of its values each, as the two 8-value pieces whose pairs turn
-// into one another, so the rotation stays within a lane.  A group of such lanes
-// takes a token and walks over its heads: the sines and cosines are formed once
-// for all of them.
+// into one another, so the rotation stays within a lane.  A block's groups of
+// such lanes take neighbouring tokens and walk over their heads together: the
+// sines and cosines are formed once for all of them.  Queries come first and
+// keys after them, so that one set of weights and sums is held at a time.  Rows
+// come through asynchronous copies into a lane's own column of shared memory,
+// several rows ahead and without registers.  Arithmetic is on pairs of fp32.
+//
+// Measured on GB300 (bf16, every pass on other inputs): prefill 1 x 32/8 x
+// 32768 x 128 out of a fused projection 106 us for 671 MB (6.3 TB/s, 93% of the
+// measured copy rate; loads into registers four rows at a time 147); training
+// pass 4 x 16/16 x 8192 x 64 118 us for 671 MB (5.7 TB/s, 84%): backward 62 of
+// a floor of 59, forward 48 of 40, join and the gaps between launches the rest.
 //
 // Angles: positions reach 2^31 and an angle's 24 bits of fp32 would leave
 // nothing of its fraction of a turn.  freq / 2 pi is formed as a 64-bit

@@ -12,11 +12,17 @@
 // the block then holds; where that differs from the one it had, the block's
 // other numbers are written anew.
 //
-// The step is bound by reading the cache once.  As in window_step.cuh, the
-// blocks of threads of a cluster share the slots of a (sequence, key head), and
-// a warp takes 16 slots at a time from memory into the operands of m16n8k16
-// products:
+// The step is bound by reading the cache once.  The list of all blocks of slots
+// that hold tokens, over sequences and key heads, is cut into equal shares, one
+// for every thread block that runs at once, whatever the lengths: shares by
+// whole pairs left a third of the GPU idle at 512 pairs (146 us against 91).  A
+// warp takes 16 slots of each block of its thread block's share, which come
+// through a ring of asynchronous copies, into the operands of m16n8k16 products:
 //   scores^T [16 slots x 8 heads] = K Q^T,  o^T [16 columns x 8 heads] += V^T P^T.
+// A pair that lies within a share is finished by its thread block; the parts of
+// one that is cut go to the workspace and are added by a second kernel, which is
+// launched beside the first and waits for its end.
+//
 // e4m3 numbers turn into fp16 exactly, two with one instruction.  Queries turn
 // into fp16 too, each head's by a power of two of its own under which its
 // largest lies in [1, 2): exact for bf16 down to 2^-14 of that, and off by less
@@ -24,7 +30,18 @@
 // t = s + log2 f, the weights are 2^(t - m) with m the running maximum of t, and
 // the sum that divides takes each with 1 / f.  Weights are in [0, 2^15]
 // (2^7 at the maximum, 8 above before the maximum moves) as fp16 for their
-// product: rounded by 2^-12 of themselves, or 2^-32 of the largest.
+// product: rounded by 2^-11 of themselves at most, or 2^-32 of the largest.
+// Against bf16 outputs (2^-8) that is nothing; for fp16 outputs a second part
+// takes what the first leaves (error against 64 bits 2.0e-4, with one part 2.9e-4).
+//
+// Measured on GB300: 64 x 32/8 x 128, window 4096, sinks 4, bf16: 91 us for 539
+// MB (5.9 TB/s, 87% of the measured copy rate); 2 x 32/4 x 128, window 65536:
+// 33 us, of which the stream of 134 MB is 20 and the rest the start, the parts
+// and the join; 4 x 16/4, window 1024: 12 us.  Two thread blocks a
+// multiprocessor and tiles four deep: three with three or four deep 95 and 97
+// us, two of five and six deep 93 and 94.  Scores formed a block ahead of their
+// weights changed nothing (92 us), more shares than blocks that run at once
+// cost their starts (97 us at twice as many).
 #include <math.h>
 
 #include <type_traits>
@@ -219,6 +236,11 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
     return v;
 }
 
+// four e4m3 numbers without their signs; 0 for a NaN
+__device__ __forceinline__ uint32_t size4(uint32_t w) {
+    w &= 0x7f7f7f7fu;
+    return w & ~__vcmpeq4(w, 0x7f7f7f7fu);
+}
 // The token into the block of slots that the warps' tiles (K's 16 slots, then V's) hold, and into the caches: `row` of this
 // warp's 16 slots is its own, where that is one of them, and the first n of them hold tokens.  All threads of the block
 // call it together.  kfac, vfac: the block's factors, before and after.
@@ -235,11 +257,10 @@ __device__ __forceinline__ void put_token(uint32_t tile, uint8_t *kc, uint8_t *v
         for (int x = 0; x < 16 / R; ++x) {
             const int s = lane / P + R * x;
             const uint4 w = lds16(tile + which * 16 * D + tile_at<D>(s, c));
-            const uint32_t a = __vmaxu4(w.x & 0x7f7f7f7fu, w.y & 0x7f7f7f7fu), e = __vmaxu4(w.z & 0x7f7f7f7fu, w.w & 0x7f7f7f7fu);
-            if (s != row) most = __vmaxu4(most, __vmaxu4(a, e));
+            if (s != row) most = __vmaxu4(most, __vmaxu4(__vmaxu4(size4(w.x), size4(w.y)), __vmaxu4(size4(w.z), size4(w.w))));
         }
         most = __vmaxu4(most, most >> 16);
-        most = min(max(most & 0xffu, most >> 8 & 0xffu), 0x7eu);  // a NaN counts as the largest number
+        most = max(most & 0xffu, most >> 8 & 0xffu);
         float val[16], top = 0.f;
         load16(s_new[which] + 16 * c, val);
 #pragma unroll
@@ -593,7 +614,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 reinterpret_cast<uint32_t *>(o + (long long)b * g.H * D)[i] = 0u;
 }
 
-// Adds the parts of a cut (sequence, key head), for a query head of the group, in a fixed order: their common maximum first,
+// Adds the parts of a cut (sequence, key head), one query head of the group after the other, in a fixed order: their common maximum first,
 // then every eighth part by a warp.
 template <typename E, int D>
 __global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ parts, const Cut8 *__restrict__ cuts, E *__restrict__ o, int G) {
@@ -602,54 +623,57 @@ __global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Cut8 cut = cuts[blockIdx.x];
     if (cut.unit < 0) return;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.y, n = cut.last - (int)blockIdx.x + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = cut.last - (int)blockIdx.x + 1;
     auto part_of = [&](int i) { return parts + (i == 0 ? cut.slot : 2 * ((int)blockIdx.x + i)) * c8_part<D>(G); };
     constexpr int K = (kC8MaxBlocks + 255) / 256;
-    float2 ml[K];
-    float m = -INFINITY, l = 0.f;
+    for (int h = blockIdx.y; h < G; h += gridDim.y) {
+        float2 ml[K];
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int i = threadIdx.x + 256 * k;
-        const unsigned c = blockIdx.x + i;
-        ml[k] = make_float2(-INFINITY, 0.f);
-        if (i < n && share_of(cut.all, c) < share_of(cut.all, c + 1))  // else: more thread blocks than blocks of slots
-            ml[k] = reinterpret_cast<const float2 *>(part_of(i) + G * D)[h];
-        m = fmaxf(m, ml[k].x);
-    }
+        for (int k = 0; k < K; ++k) {
+            const int i = threadIdx.x + 256 * k;
+            const unsigned c = blockIdx.x + i;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (i < n && share_of(cut.all, c) < share_of(cut.all, c + 1))  // else: more thread blocks than blocks of slots
+                ml[k] = reinterpret_cast<const float2 *>(part_of(i) + G * D)[h];
+            m = fmaxf(m, ml[k].x);
+        }
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
-    if (lane == 0) s_m[warp] = m;
-    __syncthreads();
+        for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+        if (lane == 0) s_m[warp] = m;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < W; ++w) m = fmaxf(m, s_m[w]);
+        for (int w = 0; w < W; ++w) m = fmaxf(m, s_m[w]);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        // a part without a maximum holds nothing, or NaN alone
-        const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : NAN) : ex2(ml[k].x - m);
-        if (threadIdx.x + 256 * k < kC8MaxBlocks) s_f[threadIdx.x + 256 * k] = f;
-        l += f * ml[k].y;
-    }
+        for (int k = 0; k < K; ++k) {
+            // a part without a maximum holds nothing, or NaN alone
+            const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : NAN) : ex2(ml[k].x - m);
+            if (threadIdx.x + 256 * k < kC8MaxBlocks) s_f[threadIdx.x + 256 * k] = f;
+            l += f * ml[k].y;
+        }
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(~0u, l, x);
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    float x[N];
+        for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(~0u, l, x);
+        if (lane == 0) s_l[warp] = l;
+        __syncthreads();
+        float x[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = 0.f;
+        for (int e = 0; e < N; ++e) x[e] = 0.f;
 #pragma unroll 4
-    for (int i = warp; i < n; i += W) {
-        const float f = s_f[i], *part = part_of(i) + h * D + lane;
+        for (int i = warp; i < n; i += W) {
+            const float f = s_f[i], *part = part_of(i) + h * D + lane;
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = fmaf(f, f != 0.f ? part[32 * e] : 0.f, x[e]);
-    }
+            for (int e = 0; e < N; ++e) x[e] = fmaf(f, f != 0.f ? part[32 * e] : 0.f, x[e]);
+        }
 #pragma unroll
-    for (int e = 0; e < N; ++e) s_o[warp][32 * e + lane] = x[e];
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += 256) {
-        float lt = 0.f, y = 0.f;
+        for (int e = 0; e < N; ++e) s_o[warp][32 * e + lane] = x[e];
+        __syncthreads();
+        for (int d = threadIdx.x; d < D; d += 256) {
+            float lt = 0.f, y = 0.f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) lt += s_l[w], y += s_o[w][d];
-        o[((long long)cut.unit * G + h) * D + d] = from_f32<E>(y / lt);
+            for (int w = 0; w < W; ++w) lt += s_l[w], y += s_o[w][d];
+            o[((long long)cut.unit * G + h) * D + d] = from_f32<E>(y / lt);
+        }
+        __syncthreads();
     }
 }
 
@@ -705,7 +729,7 @@ int c8_step(const char *fn, const void *q, const void *k, const void *v, void *k
     // the join's launch goes beside the step's end
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at;
-    cfg.gridDim = dim3(grid, (unsigned)(g.H / g.Hkv));
+    cfg.gridDim = dim3(grid, (unsigned)(g.H / g.Hkv < 8 ? g.H / g.Hkv : 8));  // most of them have nothing to do
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -765,7 +789,6 @@ extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v
     const char *fn = "cla_window_attn_step8";
     clear_error();
     if (int st = c8_check(fn, B, H, Hkv, 1, d, window, sinks, dtype, scale)) return st;
-    if (H > 0 && H / Hkv > 65535) return fail(CLA_ERR_UNSUPPORTED, "%s: %lld query heads of a key head", fn, (long long)(H / Hkv));
     if (B * H > 0 && (!q || !k || !v || !kcache || !vcache || !kscale || !vscale || !pos || !o))
         return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned_or_null({q, k, v, kcache, vcache, o}, 16) || !aligned_or_null({pos, kscale, vscale}, 4))

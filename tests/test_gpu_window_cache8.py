@@ -138,7 +138,7 @@ def step(cla, g, B, H, K, d, window, sinks, dtype, pos, std=1.0, scale=None, new
                                                   (3, 6, 6, 128, 1500, 0), (2, 32, 2, 64, 5000, 16), (4, 5, 1, 64, 3, 100),
                                                   (2, 40, 1, 128, 130, 1), (1, 9, 1, 64, 33, 0), (9, 18, 9, 64, 3000, 2),
                                                   (1, 4, 1, 128, 20000, 0), (10, 22, 11, 128, 900, 5), (3, 3, 3, 64, 63, 1),
-                                                  (3, 3, 3, 64, 64, 1), (2, 48, 2, 64, 700, 0)])
+                                                  (3, 3, 3, 64, 64, 1), (2, 48, 2, 64, 700, 0), (1, 80, 1, 64, 3000, 5)])
 def test_step(cla, B, H, K, d, window, sinks, dtype):
     g = torch.Generator().manual_seed(9)
     S = sinks + window
@@ -228,6 +228,23 @@ def test_step_what_is_not_finite(cla):
     assert bool(torch.isnan(got[1, 1]).all())
     got[1, 1] = want[1, 1]
     assert torch.equal(got, want)
+
+
+def test_step_beside_a_nan(cla):
+    """A NaN that a block of the token holds does not count for its factor; the block's other numbers move as without it."""
+    g = torch.Generator().manual_seed(16)
+    pos = torch.tensor([40], dtype=torch.int32)
+    (kc, ks), (vc, vs) = filled(g, 1, 1, 200, 64, pos), filled(g, 1, 1, 200, 64, pos)
+    for new in (1e-3, 1.0, 500.0):
+        q, k, v = rnd(g, 1, 2, 64, dtype=F16), rnd(g, 1, 1, 64, dtype=F16, std=new), rnd(g, 1, 1, 64, dtype=F16)
+        a, b = ([x.clone() for x in (kc, vc, ks, vs)] for _ in range(2))
+        a[0].view(torch.uint8)[0, 0, 7, 9], b[0].view(torch.uint8)[0, 0, 7, 9] = 0x7f, 0
+        for x in (a, b):
+            cla.window_attn_step8(q, k, v, *x, pos.cuda(), window=200)
+        assert torch.equal(a[2][0, 0, :1], b[2][0, 0, :1])
+        assert torch.isnan(a[0][0, 0, 7, 9].float())
+        a[0].view(torch.uint8)[0, 0, 7, 9] = b[0].view(torch.uint8)[0, 0, 7, 9]
+        assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8))
 
 
 def test_step_strided(cla):
