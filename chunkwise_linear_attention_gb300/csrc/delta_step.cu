@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(kDsThreads) delta_step_kernel(DsArgs g) {
     static_assert(kDsTokens <= W && kDsCols == 32, "a warp for every token");
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, cg = lane % 8, rg = warp * 4 + lane / 8;
     const unsigned bh = blockIdx.x / (unsigned)g.slices;
-    const int slice = (int)(blockIdx.x - bh * (unsigned)g.slices), b = (int)(bh / (unsigned)g.H), h = (int)(bh - (unsigned)b * (unsigned)g.H);
+    const int slice = (int)(blockIdx.x - bh * (unsigned)g.slices);
+    const int b = (int)(bh / (unsigned)g.H), h = (int)(bh - (unsigned)b * (unsigned)g.H);
     const int col = slice * kDsCols + 4 * cg;
     const bool in = col < g.dv;
     const int n = g.lens == nullptr ? g.T : min(max(g.lens[b], 0), g.T);
@@ -67,7 +68,8 @@ __global__ void __launch_bounds__(kDsThreads) delta_step_kernel(DsArgs g) {
     }
     const int hk = (int)((unsigned)h / (unsigned)(g.H / g.Hk));
     float *o = g.o + (long long)bh * g.T * g.dv + col;
-    const E *q = static_cast<const E *>(g.q) + b * g.sq.b + hk * g.sq.h + lane, *k = static_cast<const E *>(g.k) + b * g.sk.b + hk * g.sk.h + lane;
+    const E *q = static_cast<const E *>(g.q) + b * g.sq.b + hk * g.sq.h + lane;
+    const E *k = static_cast<const E *>(g.k) + b * g.sk.b + hk * g.sk.h + lane;
     const E *v = static_cast<const E *>(g.v) + b * g.sv.b + h * g.sv.h + slice * kDsCols + lane;
     const float *ld = g.log_decay + b * g.sl.b + h * g.sl.h, *be = g.beta + b * g.sb.b + h * g.sb.h;
     for (int t0 = 0; t0 < n; t0 += kDsTokens) {
@@ -137,7 +139,9 @@ __global__ void __launch_bounds__(kDsThreads) delta_step_kernel(DsArgs g) {
                 x[i][0] = fma2(kk, u0, mul2(both(a), x[i][0]));
                 x[i][1] = fma2(kk, u1, mul2(both(a), x[i][1]));
             }
-            if (rg == 0 && in) *reinterpret_cast<float4 *>(o + (long long)(t0 + t) * g.dv) = make_float4(fmaf(qk, u0.x, a * y.x), fmaf(qk, u0.y, a * y.y), fmaf(qk, u1.x, a * y.z), fmaf(qk, u1.y, a * y.w));
+            if (rg == 0 && in)
+                *reinterpret_cast<float4 *>(o + (long long)(t0 + t) * g.dv) =
+                    make_float4(fmaf(qk, u0.x, a * y.x), fmaf(qk, u0.y, a * y.y), fmaf(qk, u1.x, a * y.z), fmaf(qk, u1.y, a * y.w));
         }
     }
     if (in && n > 0) {
@@ -175,7 +179,7 @@ extern "C" int cla_delta_step(const void *q, const void *k, const void *v, const
         return fail(CLA_ERR_UNSUPPORTED, "%s: head dimensions %lld, %lld: dim_k of 64 or 128 and dim_v a multiple of 4 are needed", fn,
                     (long long)dim_k, (long long)dim_v);
     const int64_t slices = (dim_v + kDsCols - 1) / kDsCols;
-    if (!product_below({B, H, slices}, 2147483648.0) || T >= (int64_t)1 << 31 || !product_below({B, H, T, dim_v}, 1e15))
+    if (!product_below({B, H, slices}, 2147483648.0) || T > 65536 || !product_below({B, H, T, dim_v}, 1e15))
         return fail(CLA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     const bool any = B * H * T > 0;
     if (any && (!q || !k || !v || !log_decay || !beta || !S || !o)) return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);

@@ -68,7 +68,9 @@ __device__ __forceinline__ void sincos_at(unsigned long long turn, int pos, floa
 }
 
 __device__ __forceinline__ float2 pair_f32(uint32_t u, float) { return make_float2(0.f, 0.f); }
-__device__ __forceinline__ float2 pair_f32(uint32_t u, __nv_bfloat16) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
+__device__ __forceinline__ float2 pair_f32(uint32_t u, __nv_bfloat16) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 __device__ __forceinline__ float2 pair_f32(uint32_t u, __half) { return __half22float2(reinterpret_cast<__half2 &>(u)); }
 __device__ __forceinline__ uint32_t pair_of(float2 v, float) { return 0u; }
 __device__ __forceinline__ uint32_t pair_of(float2 v, __nv_bfloat16) {
@@ -128,7 +130,8 @@ struct Row {
         for (int i = 0; i < N; ++i) {
             uint4 v;
             if constexpr (N == 4) {
-                v = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]));
+                const float *y = x + 4 * i;
+                v = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
             } else {
                 const float *y = x + 8 * i;
                 v = make_uint4(pair_of(make_float2(y[0], y[1]), E()), pair_of(make_float2(y[2], y[3]), E()),
@@ -210,7 +213,10 @@ struct Queue {
     __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory"); }
     __device__ __forceinline__ uint4 get(int stage, int piece) const {
         uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at(stage, piece)) : "memory");
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(at(stage, piece))
+                     : "memory");
         return v;
     }
 };
@@ -224,7 +230,8 @@ __device__ __forceinline__ float2 minus(float2 a) { return make_float2(-a.x, -a.
 
 // Sines and cosines of the lane's 8 angles at its token.
 template <int G, bool IL>
-__device__ __forceinline__ void angles(const QnArgs &g, const Lane<G, IL> &l, const At<G> &a, const unsigned long long *s_turn, float2 *s, float2 *c) {
+__device__ __forceinline__ void angles(const QnArgs &g, const Lane<G, IL> &l, const At<G> &a, const unsigned long long *s_turn,
+                                       float2 *s, float2 *c) {
     const int pos = !a.live ? 0 : g.pos != nullptr ? g.pos[(long long)a.b * g.T + a.t] : a.t;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -270,7 +277,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         const int heads = pick(g.heads, which);
-        const long long base = which == 0 ? 0 : g.groups * g.heads[0], lo = max(share.at, base), hi = min(share.end, base + g.groups * heads);
+        const long long base = which == 0 ? 0 : g.groups * g.heads[0];
+        const long long lo = max(share.at, base), hi = min(share.end, base + g.groups * heads);
         if (lo >= hi) continue;
         const Triple sx = pick(p.sx, which), so = pick(p.so, which);
         const E *x = static_cast<const E *>(pick(p.x, which)) + l.c0;
@@ -362,7 +370,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         const int heads = pick(g.heads, which);
-        const long long base = which == 0 ? 0 : g.groups * g.heads[0], lo = max(share.at, base), hi = min(share.end, base + g.groups * heads);
+        const long long base = which == 0 ? 0 : g.groups * g.heads[0];
+        const long long lo = max(share.at, base), hi = min(share.end, base + g.groups * heads);
         Row<E, IL> acc;
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc.a[i] = acc.b[i] = both(0.f);
@@ -468,8 +477,8 @@ int qn_check(const char *fn, int64_t B, int64_t H, int64_t Hkv, int64_t T, int64
     if (rot > d) return fail(CLA_ERR_INVALID_ARG, "%s: %lld rotated values of a head of %lld", fn, (long long)rot, (long long)d);
     if (dtype_bytes(dtype) == 0) return fail(CLA_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
     if (d < 16 || d > 256 || d % 16 != 0 || rot % 16 != 0)
-        return fail(CLA_ERR_UNSUPPORTED, "%s: head dimension %lld with %lld rotated: multiples of 16 up to 256 are needed", fn, (long long)d,
-                    (long long)rot);
+        return fail(CLA_ERR_UNSUPPORTED, "%s: head dimension %lld with %lld rotated: multiples of 16 up to 256 are needed", fn,
+                    (long long)d, (long long)rot);
     if (!product_below({B, T}, 2147483648.0) || !product_below({H + Hkv}, 1 << 20) || !product_below({B, T, H + Hkv}, 68719476736.0))
         return fail(CLA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     return CLA_OK;

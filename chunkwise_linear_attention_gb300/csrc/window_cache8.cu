@@ -288,8 +288,8 @@ __device__ __forceinline__ void put_token(uint32_t tile, uint8_t *kc, uint8_t *v
                 for (int j = 0; j < 16; ++j) val[j] *= old;
             }
             const uint4 code = code16(val, by);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile + which * 16 * D + tile_at<D>(s, c)), "r"(code.x), "r"(code.y),
-                         "r"(code.z), "r"(code.w)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile + which * 16 * D + tile_at<D>(s, c)), "r"(code.x),
+                         "r"(code.y), "r"(code.z), "r"(code.w)
                          : "memory");
             *reinterpret_cast<uint4 *>(to + s * D + 16 * c) = code;
         }
@@ -610,14 +610,15 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
     // rows without a sequence
     for (b = blockIdx.x; b < g.B; b += gridDim.x)
         if (g.pos[b] < 0)
-            for (int i = threadIdx.x; i < g.H * D / 2; i += blockDim.x)
+            for (long long i = threadIdx.x; i < (long long)g.H * D / 2; i += blockDim.x)
                 reinterpret_cast<uint32_t *>(o + (long long)b * g.H * D)[i] = 0u;
 }
 
-// Adds the parts of a cut (sequence, key head), one query head of the group after the other, in a fixed order: their common maximum first,
-// then every eighth part by a warp.
+// Adds the parts of a cut (sequence, key head), one query head of the group after the other, in a fixed order: their
+// common maximum first, then every eighth part by a warp.
 template <typename E, int D>
-__global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ parts, const Cut8 *__restrict__ cuts, E *__restrict__ o, int G) {
+__global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ parts, const Cut8 *__restrict__ cuts, E *__restrict__ o,
+                                                      int G) {
     constexpr int W = 8, N = D / 32;
     __shared__ float s_o[W][D], s_f[kC8MaxBlocks], s_m[W], s_l[W];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -689,7 +690,8 @@ int c8_check(const char *fn, int64_t B, int64_t H, int64_t Hkv, int64_t T, int64
     if (d != 64 && d != 128) return fail(CLA_ERR_UNSUPPORTED, "%s: head dimension %lld", fn, (long long)d);
     if (window > kMaxTokens || sinks > kMaxTokens - window || !product_below({B, Hkv, d, sinks + window}, 1e15))
         return fail(CLA_ERR_UNSUPPORTED, "%s: sinks + window must be at most 2^31 - 512, the cache below 10^15 elements", fn);
-    if (T > kMaxTokens || !product_below({B, H}, 1 << 27) || !product_below({B, Hkv, (sinks + window + kC8Block - 1) / kC8Block}, 2147483648.0))
+    if (T > kMaxTokens || !product_below({B, H}, 1 << 27) ||
+        !product_below({B, Hkv, (sinks + window + kC8Block - 1) / kC8Block}, 2147483648.0))
         return fail(CLA_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     return CLA_OK;
 }
@@ -779,7 +781,8 @@ extern "C" int cla_window_cache8_write(const void *k, const void *v, const int32
 extern "C" size_t cla_window_attn_step8_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
     if (c8_check("cla_window_attn_step8_workspace_size", B, H, Hkv, 1, d, window, sinks, CLA_BF16, 1.f) != CLA_OK) return 0;
     const int64_t most = B * Hkv * ((sinks + window + kC8Block - 1) / kC8Block);  // a thread block has one block of slots at least
-    return sizeof(WsHeader) + sizeof(Cut8) * kC8MaxBlocks + (size_t)(2 * (most < kC8MaxBlocks ? most : kC8MaxBlocks) * (Hkv ? H / Hkv : 0) * (d + 2) * 4);
+    const int64_t parts = 2 * (most < kC8MaxBlocks ? most : kC8MaxBlocks);
+    return sizeof(WsHeader) + sizeof(Cut8) * kC8MaxBlocks + (size_t)(parts * (Hkv ? H / Hkv : 0) * (d + 2) * 4);
 }
 
 extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v, void *kcache, void *vcache, float *kscale,

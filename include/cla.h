@@ -864,7 +864,8 @@ int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq,
  *   o      [B, H, T, dim_v] fp32 out, dense
  *   strides [opt]: {batch, head, token} triples of q, k, v, log_decay, beta, any
  *          positive number of elements below 2^39
- * dim_k 64 or 128, dim_v a multiple of 4; B * H * ceil(dim_v / 32) below 2^31. */
+ * dim_k 64 or 128, dim_v a multiple of 4; T at most 65536; B * H * ceil(dim_v /
+ * 32) below 2^31, B * H * T * dim_v below 10^15. */
 int cla_delta_step(const void *q, const void *k, const void *v,
                    const float *log_decay, const float *beta, const int32_t *lens,
                    float *S, float *o, int dtype, int64_t B, int64_t H, int64_t Hk,

@@ -110,7 +110,7 @@ def dstep(lib, q=A, v=A, ld=A, beta=A, lens=None, S=A, o=A, dtype=1, B=2, H=4, H
     (dict(H=0), 1), (dict(Hk=0), 1), (dict(dtype=3), 2), (dict(dk=32), 2), (dict(dk=256), 2), (dict(dv=66), 2), (dict(dv=0), 2),
     (dict(q=None), 1), (dict(v=None), 1), (dict(ld=None), 1), (dict(beta=None), 1), (dict(S=None), 1), (dict(o=None), 1),
     (dict(q=ODD1), 1), (dict(q=ODD, dtype=0), 1), (dict(ld=ODD), 1), (dict(lens=ODD), 1), (dict(S=ODD), 1), (dict(o=ODD), 1),
-    (dict(B=1 << 20, H=1 << 12, Hk=1), 2), (dict(T=1 << 31), 2), (dict(dv=1 << 40), 2), (dict(s=[64, 64, 0] * 5), 1),
+    (dict(B=1 << 20, H=1 << 12, Hk=1), 2), (dict(T=1 << 31), 2), (dict(T=65537), 2), (dict(dv=1 << 40), 2), (dict(s=[64, 64, 0] * 5), 1),
     (dict(s=[64, -1, 64] * 5), 1)])
 def test_delta_step_refusals(lib, kw, status):
     assert dstep(lib, **kw) == status
