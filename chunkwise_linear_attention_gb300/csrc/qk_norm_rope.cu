@@ -444,6 +444,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
             if (lane < G && l.in) s_w[warp][which][l.c0 + (i < 8 ? i : l.apart + i - 8)] = v[i];
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits for this grid's end
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * g.d; i += kBwdThreads) {
         float v = 0.f;
@@ -456,6 +457,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
 // dw = the blocks' parts, in a fixed order: 8 threads take every eighth of a column's
 __global__ void __launch_bounds__(256) qn_join_kernel(const float *__restrict__ parts, float *dwq, float *dwk, int d, int blocks) {
     __shared__ float s[8][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int col = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;
     float v = 0.f;
     if (col < 2 * d)
@@ -555,7 +557,17 @@ int qn_bwd(const char *fn, const QnBwd &p, const QnArgs &g, float *dwq, float *d
         default: st = qn_bwd_g<E, 16, IL>(fn, p, g, parts, s);
     }
     if (st != CLA_OK || (dwq == nullptr && dwk == nullptr)) return st;
-    qn_join_kernel<<<(unsigned)((2 * g.d + 31) / 32), 256, 0, s>>>(parts, dwq, dwk, g.d, (int)qn_bwd_blocks(g));
+    // the join's launch goes beside the backward's end
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at;
+    cfg.gridDim = dim3((unsigned)((2 * g.d + 31) / 32));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    CLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, qn_join_kernel, (const float *)parts, dwq, dwk, g.d, (int)qn_bwd_blocks(g)), fn);
     return check_launch(fn);
 }
 
