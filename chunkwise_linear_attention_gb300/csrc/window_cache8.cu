@@ -614,8 +614,9 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 reinterpret_cast<uint32_t *>(o + (long long)b * g.H * D)[i] = 0u;
 }
 
-// Adds the parts of a cut (sequence, key head), one query head of the group after the other, in a fixed order: their
-// common maximum first, then every eighth part by a warp.
+// Adds the parts of a cut (sequence, key head), for a query head of the group, in a fixed order: their common maximum first,
+// then every eighth part by a warp.  A block of it fits beside the step's two (32 registers; with 59 it did not, and the
+// step took 2 us more).
 template <typename E, int D>
 __global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ parts, const Cut8 *__restrict__ cuts, E *__restrict__ o,
                                                       int G) {
@@ -624,57 +625,54 @@ __global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Cut8 cut = cuts[blockIdx.x];
     if (cut.unit < 0) return;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = cut.last - (int)blockIdx.x + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.y, n = cut.last - (int)blockIdx.x + 1;
     auto part_of = [&](int i) { return parts + (i == 0 ? cut.slot : 2 * ((int)blockIdx.x + i)) * c8_part<D>(G); };
     constexpr int K = (kC8MaxBlocks + 255) / 256;
-    for (int h = blockIdx.y; h < G; h += gridDim.y) {
-        float2 ml[K];
-        float m = -INFINITY, l = 0.f;
+    float2 ml[K];
+    float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int i = threadIdx.x + 256 * k;
-            const unsigned c = blockIdx.x + i;
-            ml[k] = make_float2(-INFINITY, 0.f);
-            if (i < n && share_of(cut.all, c) < share_of(cut.all, c + 1))  // else: more thread blocks than blocks of slots
-                ml[k] = reinterpret_cast<const float2 *>(part_of(i) + G * D)[h];
-            m = fmaxf(m, ml[k].x);
-        }
+    for (int k = 0; k < K; ++k) {
+        const int i = threadIdx.x + 256 * k;
+        const unsigned c = blockIdx.x + i;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (i < n && share_of(cut.all, c) < share_of(cut.all, c + 1))  // else: more thread blocks than blocks of slots
+            ml[k] = reinterpret_cast<const float2 *>(part_of(i) + G * D)[h];
+        m = fmaxf(m, ml[k].x);
+    }
 #pragma unroll
-        for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
-        if (lane == 0) s_m[warp] = m;
-        __syncthreads();
+    for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+    if (lane == 0) s_m[warp] = m;
+    __syncthreads();
 #pragma unroll
-        for (int w = 0; w < W; ++w) m = fmaxf(m, s_m[w]);
+    for (int w = 0; w < W; ++w) m = fmaxf(m, s_m[w]);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            // a part without a maximum holds nothing, or NaN alone
-            const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : NAN) : ex2(ml[k].x - m);
-            if (threadIdx.x + 256 * k < kC8MaxBlocks) s_f[threadIdx.x + 256 * k] = f;
-            l += f * ml[k].y;
-        }
+    for (int k = 0; k < K; ++k) {
+        // a part without a maximum holds nothing, or NaN alone
+        const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : NAN) : ex2(ml[k].x - m);
+        if (threadIdx.x + 256 * k < kC8MaxBlocks) s_f[threadIdx.x + 256 * k] = f;
+        l += f * ml[k].y;
+    }
 #pragma unroll
-        for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(~0u, l, x);
-        if (lane == 0) s_l[warp] = l;
-        __syncthreads();
-        float x[N];
+    for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(~0u, l, x);
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    float x[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = 0.f;
+    for (int e = 0; e < N; ++e) x[e] = 0.f;
 #pragma unroll 4
-        for (int i = warp; i < n; i += W) {
-            const float f = s_f[i], *part = part_of(i) + h * D + lane;
+    for (int i = warp; i < n; i += W) {
+        const float f = s_f[i], *part = part_of(i) + h * D + lane;
 #pragma unroll
-            for (int e = 0; e < N; ++e) x[e] = fmaf(f, f != 0.f ? part[32 * e] : 0.f, x[e]);
-        }
+        for (int e = 0; e < N; ++e) x[e] = fmaf(f, f != 0.f ? part[32 * e] : 0.f, x[e]);
+    }
 #pragma unroll
-        for (int e = 0; e < N; ++e) s_o[warp][32 * e + lane] = x[e];
-        __syncthreads();
-        for (int d = threadIdx.x; d < D; d += 256) {
-            float lt = 0.f, y = 0.f;
+    for (int e = 0; e < N; ++e) s_o[warp][32 * e + lane] = x[e];
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += 256) {
+        float lt = 0.f, y = 0.f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) lt += s_l[w], y += s_o[w][d];
-            o[((long long)cut.unit * G + h) * D + d] = from_f32<E>(y / lt);
-        }
-        __syncthreads();
+        for (int w = 0; w < W; ++w) lt += s_l[w], y += s_o[w][d];
+        o[((long long)cut.unit * G + h) * D + d] = from_f32<E>(y / lt);
     }
 }
 
@@ -731,7 +729,7 @@ int c8_step(const char *fn, const void *q, const void *k, const void *v, void *k
     // the join's launch goes beside the step's end
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at;
-    cfg.gridDim = dim3(grid, (unsigned)(g.H / g.Hkv < 8 ? g.H / g.Hkv : 8));  // most of them have nothing to do
+    cfg.gridDim = dim3(grid, (unsigned)(g.H / g.Hkv));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -792,6 +790,7 @@ extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v
     const char *fn = "cla_window_attn_step8";
     clear_error();
     if (int st = c8_check(fn, B, H, Hkv, 1, d, window, sinks, dtype, scale)) return st;
+    if (H > 0 && H / Hkv > 65535) return fail(CLA_ERR_UNSUPPORTED, "%s: %lld query heads of a key head", fn, (long long)(H / Hkv));
     if (B * H > 0 && (!q || !k || !v || !kcache || !vcache || !kscale || !vscale || !pos || !o))
         return fail(CLA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
     if (!aligned_or_null({q, k, v, kcache, vcache, o}, 16) || !aligned_or_null({pos, kscale, vscale}, 4))

@@ -776,7 +776,8 @@ int cla_window_cache8_write(const void *k, const void *v, const int32_t *lens,
  * with the cache's numbers.
  * The arguments are cla_window_attn_step's, with the caches above; the order of
  * the sums is fixed by the sizes, the positions and the device model.
- * B * Hkv * ceil((sinks + window) / 64) is below 2^31, B * H below 2^27. */
+ * B * Hkv * ceil((sinks + window) / 64) is below 2^31, B * H below 2^27, H / Hkv
+ * below 2^16. */
 int cla_window_attn_step8(const void *q, const void *k, const void *v, void *kcache,
                           void *vcache, float *kscale, float *vscale,
                           const int32_t *pos, void *o, float scale, int64_t window,

@@ -93,7 +93,7 @@ def test_cache8_calls(lib):
                dict(lens=None), dict(o=ODD)):
         assert cstep(lib, **kw) == 1, kw
     assert cstep(lib, ws=None) == 5 and cstep(lib, ws=ODD) == 5 and cstep(lib, nbytes=1000) == 5
-    assert cstep(lib, H=1 << 26, K=1) == 2
+    assert cstep(lib, H=1 << 26, K=1) == 2 and cstep(lib, H=1 << 16, K=1) == 2
     assert lib.cla_window_attn_step8_workspace_size(2, 4, 2, 64, 100, 2) > 256 + 8 * 2 * 66 * 4
     assert lib.cla_window_attn_step8_workspace_size(0, 0, 0, 64, 100, 2) >= 256
     assert lib.cla_window_attn_step8_workspace_size(2, 4, 3, 64, 100, 2) == 0
