@@ -272,7 +272,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
     const Queue<kFwdThreads, S, N> queue(smem);
     const Lane<G, IL> l(g);
     for (int i = threadIdx.x; i < g.rot / 2; i += kFwdThreads) s_turn[i] = turns(g.freq[i]);
-    __syncthreads();
     const Share share(g.groups * (g.heads[0] + g.heads[1]));
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
@@ -326,6 +325,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
             r = rsqrtf(row_sum<G>(q.x + q.y + (q1.x + q1.y)) * g.inv_d + g.eps);
         };
         begin(y, r);
+        __syncthreads();  // s_turn is there
         coefficients();
 #pragma unroll 1
         for (; left > 0; --left) {
@@ -365,7 +365,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (blockIdx.x == 0 && threadIdx.x < (int)sizeof(WsHeader) / 4) reinterpret_cast<uint32_t *>(hdr)[threadIdx.x] = 0u;  // nothing waits
     for (int i = threadIdx.x; i < g.rot / 2; i += kBwdThreads) s_turn[i] = turns(g.freq[i]);
-    __syncthreads();
     const Share share(g.groups * (g.heads[0] + g.heads[1]));
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
@@ -397,6 +396,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
             Row<E, IL> w;
             l.weights(pick(g.w, which), w);
             float2 sn[4], cs[4];
+            __syncthreads();  // s_turn is there
             angles(g, l, c, s_turn, sn, cs);
             int stage = 0;
 #pragma unroll 1
