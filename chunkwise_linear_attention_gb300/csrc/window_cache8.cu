@@ -192,24 +192,25 @@ struct Step8Args {
 struct Cut8 {
     int unit, slot, last, all;  // unit: sequence Hkv + key head, or -1: nothing to do; all: blocks of slots in the list
 };
-__device__ __forceinline__ long long share_of(long long all, unsigned block) { return all * block / gridDim.x; }
+// Where thread block `c`'s share of the list begins: all c / blocks, rounded down (c is at most 608).
+__device__ __forceinline__ unsigned share_of(unsigned all, unsigned c) { return all / gridDim.x * c + all % gridDim.x * c / gridDim.x; }
 
 __device__ __forceinline__ long long held_slots(const Step8Args &g, int b) { return max(0ll, min((long long)g.pos[b] + 1, g.slots)); }
 __device__ __forceinline__ int held_blocks(const Step8Args &g, int b) { return (int)((held_slots(g, b) + kC8Block - 1) / kC8Block); }
 
 // Sum over a block's threads, and what the threads before this one add to it.
-__device__ __forceinline__ long long block_scan(long long v, long long &before, long long *s_sum) {
+__device__ __forceinline__ unsigned block_scan(unsigned v, unsigned &before, unsigned *s_sum) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    long long up = v;
+    unsigned up = v;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-        const long long y = __shfl_up_sync(~0u, up, x);
+        const unsigned y = __shfl_up_sync(~0u, up, x);
         if (lane >= x) up += y;
     }
     __syncthreads();
     if (lane == 31) s_sum[warp] = up;
     __syncthreads();
-    long long all = 0;
+    unsigned all = 0;
     before = up - v;
 #pragma unroll
     for (int w = 0; w < kStepWarps; ++w) {
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) E s_new[2][D];
     __shared__ float s_top[2][kStepWarps];
-    __shared__ long long s_sum[kStepWarps], s_at[2];
+    __shared__ unsigned s_sum[kStepWarps], s_at[2];
     char *const s_parts = smem + kStepWarps * kC8Stages * 32 * D;
     float(*s_o)[NH][D] = reinterpret_cast<float(*)[NH][D]>(s_parts);
     float(*s_m)[NH] = reinterpret_cast<float(*)[NH]>(s_parts + kStepWarps * NH * D * 4);
@@ -327,30 +328,29 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3, G = g.H / g.Hkv;
 
     if (blockIdx.x == 0 && threadIdx.x < (int)sizeof(WsHeader) / 4) reinterpret_cast<uint32_t *>(hdr)[threadIdx.x] = 0u;  // nothing waits
-    // this block's share, and the pair in which it starts
-    long long all = 0, before = 0;
-    int held = 0;
+    // this block's share, and the pair in which it starts (all counts of blocks of slots are below 2^31)
+    unsigned all = 0, before = 0, held = 0;
     for (int b0 = 0; b0 < g.B; b0 += 128) {
-        held = b0 + (int)threadIdx.x < g.B ? held_blocks(g, b0 + threadIdx.x) : 0;
-        all += block_scan((long long)held * g.Hkv, before, s_sum);
+        held = b0 + (int)threadIdx.x < g.B ? (unsigned)held_blocks(g, b0 + threadIdx.x) * g.Hkv : 0u;
+        all += block_scan(held, before, s_sum);
     }
-    long long at = share_of(all, blockIdx.x);
-    const long long start = at, end = share_of(all, blockIdx.x + 1);
+    unsigned at = share_of(all, blockIdx.x);
+    const unsigned start = at, end = share_of(all, blockIdx.x + 1);
     if (threadIdx.x == 0) cuts[blockIdx.x].unit = -1;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits for this grid's end
-    long long seen = 0;
+    unsigned seen = 0;
     for (int b0 = 0; b0 < g.B && at < end && seen <= at; b0 += 128) {
         if (g.B > 128) {
-            held = b0 + (int)threadIdx.x < g.B ? held_blocks(g, b0 + threadIdx.x) : 0;
-            const long long more = block_scan((long long)held * g.Hkv, before, s_sum);
+            held = b0 + (int)threadIdx.x < g.B ? (unsigned)held_blocks(g, b0 + threadIdx.x) * g.Hkv : 0u;
+            const unsigned more = block_scan(held, before, s_sum);
             before += seen;
             seen += more;
         }
-        if (before <= at && at < before + (long long)held * g.Hkv) s_at[0] = b0 + threadIdx.x, s_at[1] = at - before;
+        if (before <= at && at < before + held) s_at[0] = b0 + threadIdx.x, s_at[1] = at - before;
     }
     __syncthreads();
     int b = 0, used = 1, hk = 0, first = 0;
-    if (at < end) b = (int)s_at[0], used = held_blocks(g, b), hk = (int)(s_at[1] / used), first = (int)(s_at[1] % used);
+    if (at < end) b = (int)s_at[0], used = held_blocks(g, b), hk = (int)(s_at[1] / (unsigned)used), first = (int)(s_at[1] % (unsigned)used);
 
     const uint32_t ring = smem_u32(smem) + warp * (kC8Stages * 32 * D), ring_end = ring + kC8Stages * 32 * D;
     // where this lane's pieces go in a tile: the x-th 512 x bytes on, with the keys of tile_at the same for every other x
@@ -361,8 +361,9 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
     const uint8_t *kl = nullptr, *vl = nullptr;
     auto locate = [&]() {
         const long long p = g.pos[b], unit = (long long)b * g.Hkv + hk, from = ((long long)first * kC8Block + 16 * warp) * D + 16 * lane;
-        mine = (int)(p < g.sinks ? p : g.sinks + (p - g.sinks) % g.window), n = (int)min(p + 1, g.slots);
-        cnt = (int)min((long long)(used - first), end - at);
+        // positions and slots are below 2^31
+        mine = (int)(p < g.sinks ? p : g.sinks + (unsigned)(p - g.sinks) % (unsigned)g.window), n = (int)min(p + 1, g.slots);
+        cnt = min(used - first, (int)(end - at));
         own = mine / kC8Block - first;  // the token's block, where that is of this segment
         kb = kc + unit * g.slots * D, vb = vc + unit * g.slots * D;
         kl = kb + from, vl = vb + from;
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
             if (h0 + NH >= G) {
                 if (!whole && first == 0 && threadIdx.x == 0) {
                     // the thread block that has the pair's last block of slots: the least c with share_of(c + 1) >= at + used
-                    const long long x = at + used;
+                    const unsigned long long x = at + (unsigned)used;
                     cuts[blockIdx.x] = Cut8{(int)unit, slot, (int)((x * gridDim.x + all - 1) / all) - 1, (int)all};
                 }
                 at += cnt;
