@@ -21,7 +21,7 @@
 // Measured on GB300 (bf16, every pass on other inputs): prefill 1 x 32/8 x
 // 32768 x 128 out of a fused projection 106 us for 671 MB (6.3 TB/s, 93% of the
 // measured copy rate; loads into registers four rows at a time 147); training
-// pass 4 x 16/16 x 8192 x 64 118 us for 671 MB (5.7 TB/s, 84%): backward 62 of
+// pass 4 x 16/16 x 8192 x 64 116 us for 671 MB (5.8 TB/s, 85%): backward 62 of
 // a floor of 59, forward 48 of 40, join and the gaps between launches the rest.
 //
 // Angles: positions reach 2^31 and an angle's 24 bits of fp32 would leave
