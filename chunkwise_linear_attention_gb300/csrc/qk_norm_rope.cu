@@ -62,9 +62,34 @@ __device__ __forceinline__ unsigned long long turns(float f) {
     else t = e > -128 ? hi >> (-e - 64) : 0ull;
     return f < 0.f ? 0ull - t : t;
 }
-__device__ __forceinline__ void sincos_at(unsigned long long turn, int pos, float &s, float &c) {
-    const unsigned long long phase = turn * (unsigned long long)(long long)pos;
-    sincospif((float)(int)(unsigned int)(phase >> 32) * 0x1p-31f, &s, &c);
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 minus(float2 a) { return make_float2(-a.x, -a.y); }
+
+// Sines and cosines of two angles: the nearest quarter turn is taken off the 32-bit fraction of a turn exactly, what is left,
+// at most an eighth, goes through the Taylor series (terms up to x^9 and x^8: off by 2e-9 and 2.5e-8), and the quarters say
+// which of the two is which and with what sign.
+__device__ __forceinline__ void sincos_at(const unsigned long long *turn, int pos, float2 &s, float2 &c) {
+    unsigned q[2];
+    float left[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const unsigned phase = (unsigned)(turn[i] * (unsigned long long)(long long)pos >> 32);
+        q[i] = (phase + 0x20000000u) >> 30;
+        left[i] = (float)(int)(phase - (q[i] << 30));
+    }
+    const float2 x = mul2(make_float2(left[0], left[1]), both(6.283185307179586f * 0x1p-32f)), y = mul2(x, x);
+    float2 p = fma2(y, both(1.f / 362880.f), both(-1.f / 5040.f));
+    p = fma2(fma2(p, y, both(1.f / 120.f)), y, both(-1.f / 6.f));
+    p = fma2(mul2(p, y), x, x);
+    float2 r = fma2(y, both(1.f / 40320.f), both(-1.f / 720.f));
+    r = fma2(fma2(r, y, both(1.f / 24.f)), y, both(-0.5f));
+    r = fma2(r, y, both(1.f));
+    const float2 a = make_float2(q[0] & 1u ? r.x : p.x, q[1] & 1u ? r.y : p.y), b = make_float2(q[0] & 1u ? p.x : r.x, q[1] & 1u ? p.y : r.y);
+    s = make_float2(__uint_as_float(__float_as_uint(a.x) ^ (q[0] & 2u) << 30), __uint_as_float(__float_as_uint(a.y) ^ (q[1] & 2u) << 30));
+    c = make_float2(__uint_as_float(__float_as_uint(b.x) ^ (q[0] + 1u & 2u) << 30),
+                    __uint_as_float(__float_as_uint(b.y) ^ (q[1] + 1u & 2u) << 30));
 }
 
 __device__ __forceinline__ float2 pair_f32(uint32_t u, float) { return make_float2(0.f, 0.f); }
@@ -177,19 +202,25 @@ struct At {
     long long group;
     int head, b, t;
     bool on, live;  // there is such a token; it is of its sequence
-    __device__ void token(const QnArgs &g) {
-        const long long n = group * (blockDim.x / G) + threadIdx.x / G;
+    __device__ void token(const QnArgs &g, bool ahead) {  // ahead: of the group before, b and t are known
+        const int step = blockDim.x / G;
+        const long long n = group * step + threadIdx.x / G;
         on = n < g.tokens;
-        const unsigned i = on ? (unsigned)n : 0u;
-        b = (int)(i / (unsigned)g.T), t = (int)(i % (unsigned)g.T);
+        if (ahead && step <= g.T) {
+            if (t >= g.T - step) t -= g.T - step, ++b;
+            else t += step;
+        } else {
+            b = (int)((unsigned)n / (unsigned)g.T), t = (int)((unsigned)n % (unsigned)g.T);
+        }
+        if (!on) b = 0, t = 0;  // and stays so: what follows is not on either
         live = on && (g.lens == nullptr || t < g.lens[b]);
     }
-    __device__ At(const QnArgs &g, long long unit, int heads) : group(unit / heads), head((int)(unit % heads)) { token(g); }
+    __device__ At(const QnArgs &g, long long unit, int heads) : group(unit / heads), head((int)(unit % heads)) { token(g, false); }
     // to the next row: true where that is of another group
     __device__ __forceinline__ bool next(const QnArgs &g, int heads) {
         if (++head < heads) return false;
         head = 0, ++group;
-        token(g);
+        token(g, true);
         return true;
     }
 };
@@ -223,10 +254,6 @@ struct Queue {
 
 template <typename T>
 __device__ __forceinline__ T pick(const T (&a)[2], int which) { return which == 0 ? a[0] : a[1]; }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
-__device__ __forceinline__ float2 minus(float2 a) { return make_float2(-a.x, -a.y); }
 
 // Sines and cosines of the lane's 8 angles at its token.
 template <int G, bool IL>
@@ -236,10 +263,7 @@ __device__ __forceinline__ void angles(const QnArgs &g, const Lane<G, IL> &l, co
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         s[i] = both(0.f), c[i] = both(1.f);
-        if (l.turned) {
-            sincos_at(s_turn[8 * l.sub + 2 * i], pos, s[i].x, c[i].x);
-            sincos_at(s_turn[8 * l.sub + 2 * i + 1], pos, s[i].y, c[i].y);
-        }
+        if (l.turned) sincos_at(s_turn + 8 * l.sub + 2 * i, pos, s[i], c[i]);
     }
 }
 
@@ -298,9 +322,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
         for (int i = 0; i < S; ++i) fetch(i);
         // w_a cos, w_b sin, w_b cos, w_a sin
         float2 wac[4], wbs[4], wbc[4], was[4];
+        Row<E, IL> w;
+        l.weights(pick(g.w, which), w);
         auto coefficients = [&]() {
-            Row<E, IL> w;
-            l.weights(pick(g.w, which), w);
             angles(g, l, c, s_turn, was, wac);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -134,6 +134,27 @@ def test_far_positions(cla):
             assert abs(float(o[t, i]) - c) <= e and abs(float(o[t, i + 8]) - s) <= e, (p, f)
 
 
+def test_angles_densely(cla):
+    """fp32 rows at many positions, in every eighth of a turn and at their borders: sines and cosines within the form's bound."""
+    T = 30000
+    args, ups = inputs(1, 1, 1, T, 16, 16, F32, 7)
+    freq = torch.tensor([1.0, 0.7853981633974483, 1.5707963267948966, 3.141592653589793, 0.1, 6.283185307179586, 1e-3, 0.39269908],
+                        device="cuda")
+    g = torch.Generator().manual_seed(3)
+    pos = torch.cat((torch.arange(T // 2), torch.randint(-(1 << 21), 1 << 21, (T - T // 2,), generator=g))).to(torch.int32)
+    check(cla, args[:4] + (freq,), ups, pos=pos[None].cuda())
+
+
+@pytest.mark.parametrize("B,T", [(5, 7), (3, 64), (2, 65), (40, 1), (3, 700)])
+def test_groups_across_sequences(cla, B, T):
+    """Groups of tokens that end one sequence and begin another, or several."""
+    (q, k, wq, wk, freq), ups = inputs(B, 3, 1, T, 64, 64, BF16, B)
+    g = torch.Generator().manual_seed(T)
+    pos = torch.randint(0, 5000, (B, T), generator=g, dtype=torch.int32).cuda()
+    lens = torch.randint(0, T + 1, (B,), generator=g, dtype=torch.int32).cuda()
+    check(cla, (q, k, wq, wk, freq), ups, pos=pos, lens=lens)
+
+
 def test_odd_frequencies(cla):
     """Negative, subnormal and vast frequencies: an angle of the other sign, none, and one that is some angle."""
     (q, k, wq, wk, _), _ = inputs(1, 2, 1, 9, 16, 0, F32)
