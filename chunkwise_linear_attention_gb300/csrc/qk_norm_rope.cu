@@ -528,12 +528,12 @@ QnArgs qn_args(const float *wq, const float *wk, const float *freq, const int32_
     return g;
 }
 
-// Blocks that run at once, each with one row of each of its lanes' at least; forward more where each has 16, so that
-// multiprocessors that are further from memory take fewer (1 x 32/8 x 32768 x 128: 106 us with 2432 blocks against 119
-// with 304, 3 x 10/5 x 1531 x 96: 45 and 31 us with the backward).
-unsigned qn_blocks(const QnArgs &g, int most, int rows) {
-    const long long n = g.groups * (g.heads[0] + g.heads[1]), more = n / rows;
-    return (unsigned)(n < most ? n : more < most ? most : more < 0x7fffffff ? more : 0x7fffffff);
+// Blocks that run at once, each with one row of each of its lanes' at least; forward as many rounds of them as give each
+// 16, so that multiprocessors that are further from memory take fewer (1 x 32/8 x 32768 x 128: 106 us with 8 rounds against
+// 119 with one; 3 x 10/5 x 1531 x 96, 7 rows: 45 and 31 us with the backward).
+unsigned qn_fwd_blocks(const QnArgs &g) {
+    const long long n = g.groups * (g.heads[0] + g.heads[1]), rounds = n / (16 * kFwdBlocks);
+    return (unsigned)(n < kFwdBlocks ? n : rounds < 1 ? kFwdBlocks : rounds < 4096 ? rounds * kFwdBlocks : 4096 * kFwdBlocks);
 }
 
 unsigned qn_bwd_blocks(const QnArgs &g) {
@@ -546,7 +546,7 @@ int qn_fwd_g(const char *fn, const QnFwd &p, const QnArgs &g, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     constexpr int smem = Queue<kFwdThreads, qn_fwd_stages<E>(), Row<E, IL>::N>::BYTES;
     if (int st = set_max_dynamic_smem(done, (const void *)qn_fwd_kernel<E, G, IL>, smem)) return st;
-    qn_fwd_kernel<E, G, IL><<<qn_blocks(g, kFwdBlocks, 16), kFwdThreads, smem, s>>>(p, g);
+    qn_fwd_kernel<E, G, IL><<<qn_fwd_blocks(g), kFwdThreads, smem, s>>>(p, g);
     return check_launch(fn);
 }
 
