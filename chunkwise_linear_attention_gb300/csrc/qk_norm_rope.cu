@@ -19,10 +19,10 @@
 // several rows ahead and without registers.  Arithmetic is on pairs of fp32.
 //
 // Measured on GB300 (bf16, every pass on other inputs): prefill 1 x 32/8 x
-// 32768 x 128 out of a fused projection 106 us for 671 MB (6.3 TB/s, 93% of the
+// 32768 x 128 out of a fused projection 105 us for 671 MB (6.4 TB/s, 94% of the
 // measured copy rate; loads into registers four rows at a time 147); training
-// pass 4 x 16/16 x 8192 x 64 116 us for 671 MB (5.8 TB/s, 85%): backward 62 of
-// a floor of 59, forward 48 of 40, join and the gaps between launches the rest.
+// pass 4 x 16/16 x 8192 x 64 115 us for 671 MB (5.8 TB/s, 86%): backward 62 of
+// a floor of 59, forward 47 of 40, join and the gaps between launches the rest.
 //
 // Angles: positions reach 2^31 and an angle's 24 bits of fp32 would leave
 // nothing of its fraction of a turn.  freq / 2 pi is formed as a 64-bit
@@ -529,7 +529,7 @@ QnArgs qn_args(const float *wq, const float *wk, const float *freq, const int32_
 }
 
 // Blocks that run at once, each with one row of each of its lanes' at least; forward as many rounds of them as give each
-// 16, so that multiprocessors that are further from memory take fewer (1 x 32/8 x 32768 x 128: 106 us with 8 rounds against
+// 16, so that multiprocessors that are further from memory take fewer (1 x 32/8 x 32768 x 128: 105 us with 8 rounds against
 // 119 with one; 3 x 10/5 x 1531 x 96, 7 rows: 45 and 31 us with the backward).
 unsigned qn_fwd_blocks(const QnArgs &g) {
     const long long n = g.groups * (g.heads[0] + g.heads[1]), rounds = n / (16 * kFwdBlocks);
