@@ -27,8 +27,8 @@
 // Angles: positions reach 2^31 and an angle's 24 bits of fp32 would leave
 // nothing of its fraction of a turn.  freq / 2 pi is formed as a 64-bit
 // fraction of a turn from the integer product of freq's 24 bits and 2^64 / 2 pi;
-// its product with the position wraps around as turns do.  What is left of the
-// angle is off by less than 2^-33 (1 + |freq|) turns and is rounded to 24 bits.
+// its product with the position wraps around as turns do, and its upper 32 bits
+// are the angle: off by less than 2^-31 (1 + |freq|) turns.
 #include <math.h>
 
 #include "cla_internal.cuh"
@@ -39,7 +39,7 @@ namespace cla {
 namespace {
 
 // Blocks that run at once, for 152 multiprocessors: forward 2 for each, backward one (its lanes hold 16 sums of dw as well, 170
-// registers; with 128 they went to local memory and the backward took 100 us where it takes 70).
+// registers; with 128 they went to local memory and the backward took some 100 us where it takes 62).
 constexpr int kFwdThreads = 256, kFwdBlocks = 304, kBwdThreads = 384, kBwdBlocks = 152;
 
 struct QnArgs {
