@@ -167,17 +167,23 @@ struct Row {
     }
 };
 
-// What a lane has of a row, and its frequencies: the 8 from 8 sub on.
+// What a lane has of a row: 8 values from c0 on and 8 from c0 + apart on, so that neighbouring lanes' pieces of either lie
+// side by side (32 bytes in a row a lane would make two half sectors of each in every access).  Halves as pairs: the lanes of
+// the rotated values have both of a pair, the others halves of the rest.  Neighbours as pairs: halves of the row.
 template <int G, bool IL>
 struct Lane {
     int sub, c0, apart;
-    bool in, turned;
+    bool in;
     __device__ Lane(const QnArgs &g) {
+        const bool turned = 16 * (threadIdx.x % G) < g.rot;
         sub = threadIdx.x % G;
         in = 16 * sub < g.d;
-        turned = 16 * sub < g.rot;
-        c0 = turned && !IL ? 8 * sub : 16 * sub;
-        apart = turned && !IL ? g.rot / 2 : 8;
+        c0 = IL || turned ? 8 * sub : 8 * sub + g.rot / 2;
+        apart = IL ? g.d / 2 : turned ? g.rot / 2 : (g.d - g.rot) / 2;
+    }
+    // of its pairs 2 i and 2 i + 1: the first one's frequency
+    __device__ __forceinline__ int frequency(const QnArgs &g, int i) const {
+        return IL ? 4 * sub + (i < 2 ? 2 * i : g.d / 4 + 2 * i - 4) : 8 * sub + 2 * i;
     }
     template <typename E>
     __device__ __forceinline__ void weights(const float *w, Row<E, IL> &x) const {
@@ -263,7 +269,8 @@ __device__ __forceinline__ void angles(const QnArgs &g, const Lane<G, IL> &l, co
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         s[i] = both(0.f), c[i] = both(1.f);
-        if (l.turned) sincos_at(s_turn + 8 * l.sub + 2 * i, pos, s[i], c[i]);
+        const int f = l.frequency(g, i);
+        if (2 * f < g.rot) sincos_at(s_turn + f, pos, s[i], c[i]);
     }
 }
 
@@ -351,22 +358,29 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
         begin(y, r);
         __syncthreads();  // s_turn is there
         coefficients();
-#pragma unroll 1
-        for (; left > 0; --left) {
-            begin(z, r1);  // beside the end of the row before it; behind the last, what an old stage holds
+        auto finish = [&](Row<E, IL> &v, float r) {  // true behind the last row
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 a = mul2(y.a[i], both(r)), b = mul2(y.b[i], both(r));
-                y.a[i] = fma2(a, wac[i], mul2(b, wbs[i]));
-                y.b[i] = fma2(b, wbc[i], mul2(a, was[i]));
+                const float2 a = mul2(v.a[i], both(r)), b = mul2(v.b[i], both(r));
+                v.a[i] = fma2(a, wac[i], mul2(b, wbs[i]));
+                v.b[i] = fma2(b, wbc[i], mul2(a, was[i]));
             }
-            if (c.on && l.in) y.store(oc, l.apart);
+            if (c.on && l.in) v.store(oc, l.apart);
+            if (--left == 0) return true;
             oc += so.h;
-            if (left > 1 && c.next(g, heads)) {
+            if (c.next(g, heads)) {
                 oc = o + c.b * so.b + c.t * so.t;
                 coefficients();
             }
-            y = z, r = r1;
+            return false;
+        };
+        // a row begins beside the end of the one before it; behind the last, with what an old stage holds
+#pragma unroll 1
+        while (true) {
+            begin(z, r1);
+            if (finish(y, r)) break;
+            begin(y, r);
+            if (finish(z, r1)) break;
         }
     }
 }
