@@ -148,7 +148,7 @@ struct Row {
             (IL ? x[4 * i + 1] : x[8 + 2 * i]) = b[i].x, (IL ? x[4 * i + 3] : x[9 + 2 * i]) = b[i].y;
         }
     }
-    __device__ __forceinline__ void store(E *p, int apart) const {  // from c0 on; c1 = c0 + apart
+    __device__ __forceinline__ void store(E *p, int gap, int apart) const {
         float x[16];
         get(x);
 #pragma unroll
@@ -162,34 +162,36 @@ struct Row {
                 v = make_uint4(pair_of(make_float2(y[0], y[1]), E()), pair_of(make_float2(y[2], y[3]), E()),
                                pair_of(make_float2(y[4], y[5]), E()), pair_of(make_float2(y[6], y[7]), E()));
             }
-            *reinterpret_cast<uint4 *>(p + (i < N / 2 ? 0 : apart) + (N == 4 && i % 2 ? 4 : 0)) = v;
+            *reinterpret_cast<uint4 *>(p + (i < N / 2 ? 0 : apart) + (N == 4 && i % 2 ? gap : 0)) = v;
         }
     }
 };
 
-// What a lane has of a row: 8 values from c0 on and 8 from c0 + apart on, so that neighbouring lanes' pieces of either lie
-// side by side (32 bytes in a row a lane would make two half sectors of each in every access).  Halves as pairs: the lanes of
-// the rotated values have both of a pair, the others halves of the rest.  Neighbours as pairs: halves of the row.
-template <int G, bool IL>
+// What a lane has of a row: 8 values from c0 on and 8 from c0 + apart on, in fp32 four and four with a gap, so that
+// neighbouring lanes' 16-byte pieces lie side by side (32 bytes in a row a lane would make two half sectors of each in
+// every access).  Halves as pairs: the lanes of the rotated values have both of a pair, the others equal parts of the rest.
+// Neighbours as pairs: equal parts of the row.
+template <typename E, int G, bool IL>
 struct Lane {
-    int sub, c0, apart;
+    int sub, c0, gap, apart;
     bool in;
     __device__ Lane(const QnArgs &g) {
-        const bool turned = 16 * (threadIdx.x % G) < g.rot;
+        const bool turned = IL || 16 * (threadIdx.x % G) < g.rot;
+        const int from = turned ? 0 : g.rot, n = IL ? g.d : turned ? g.rot : g.d - g.rot;  // the values that such lanes share
         sub = threadIdx.x % G;
         in = 16 * sub < g.d;
-        c0 = IL || turned ? 8 * sub : 8 * sub + g.rot / 2;
-        apart = IL ? g.d / 2 : turned ? g.rot / 2 : (g.d - g.rot) / 2;
+        c0 = from + (sub - from / 16) * (sizeof(E) == 4 ? 4 : 8);
+        gap = sizeof(E) == 4 ? n / 4 : 4;
+        apart = n / 2;
     }
-    // of its pairs 2 i and 2 i + 1: the first one's frequency
-    __device__ __forceinline__ int frequency(const QnArgs &g, int i) const {
-        return IL ? 4 * sub + (i < 2 ? 2 * i : g.d / 4 + 2 * i - 4) : 8 * sub + 2 * i;
-    }
-    template <typename E>
+    // where the lane's i-th value lies
+    __device__ __forceinline__ int at(int i) const { return c0 + (i / 4 % 2) * gap + i / 8 * apart + i % 4; }
+    // the frequency of the first of its pairs 2 i and 2 i + 1
+    __device__ __forceinline__ int frequency(int i) const { return IL ? at(4 * i) / 2 : at(2 * i); }
     __device__ __forceinline__ void weights(const float *w, Row<E, IL> &x) const {
         float y[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = w != nullptr && in ? w[c0 + (i < 8 ? i : apart + i - 8)] : 1.f;
+        for (int i = 0; i < 16; ++i) y[i] = w != nullptr && in ? w[at(i)] : 1.f;
         x.set(y);
     }
 };
@@ -239,11 +241,11 @@ struct Queue {
     __device__ __forceinline__ Queue(const void *smem) : base((uint32_t)__cvta_generic_to_shared(smem) + 16 * threadIdx.x) {}
     __device__ __forceinline__ uint32_t at(int stage, int piece) const { return base + (stage * PIECES + piece) * (THREADS * 16); }
     template <typename E>
-    __device__ __forceinline__ void put(int stage, int first, const E *p, int apart, bool in) const {  // zeros where it is not in
+    __device__ __forceinline__ void put(int stage, int first, const E *p, int gap, int apart, bool in) const {  // zeros where it is not in
 #pragma unroll
         for (int i = 0; i < (int)sizeof(E); ++i)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, first + i)),
-                         "l"(p + (i < (int)sizeof(E) / 2 ? 0 : apart) + (sizeof(E) == 4 && i % 2 ? 4 : 0)), "r"(in ? 16 : 0)
+                         "l"(p + (i < (int)sizeof(E) / 2 ? 0 : apart) + (sizeof(E) == 4 && i % 2 ? gap : 0)), "r"(in ? 16 : 0)
                          : "memory");
     }
     __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -262,14 +264,14 @@ template <typename T>
 __device__ __forceinline__ T pick(const T (&a)[2], int which) { return which == 0 ? a[0] : a[1]; }
 
 // Sines and cosines of the lane's 8 angles at its token.
-template <int G, bool IL>
-__device__ __forceinline__ void angles(const QnArgs &g, const Lane<G, IL> &l, const At<G> &a, const unsigned long long *s_turn,
+template <typename E, int G, bool IL>
+__device__ __forceinline__ void angles(const QnArgs &g, const Lane<E, G, IL> &l, const At<G> &a, const unsigned long long *s_turn,
                                        float2 *s, float2 *c) {
     const int pos = !a.live ? 0 : g.pos != nullptr ? g.pos[(long long)a.b * g.T + a.t] : a.t;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         s[i] = both(0.f), c[i] = both(1.f);
-        const int f = l.frequency(g, i);
+        const int f = l.frequency(i);
         if (2 * f < g.rot) sincos_at(s_turn + f, pos, s[i], c[i]);
     }
 }
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
     extern __shared__ __align__(16) char smem[];
     __shared__ unsigned long long s_turn[128];
     const Queue<kFwdThreads, S, N> queue(smem);
-    const Lane<G, IL> l(g);
+    const Lane<E, G, IL> l(g);
     for (int i = threadIdx.x; i < g.rot / 2; i += kFwdThreads) s_turn[i] = turns(g.freq[i]);
     const Share share(g.groups * (g.heads[0] + g.heads[1]));
 #pragma unroll 1
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
         int left = (int)(hi - lo), coming = left;  // rows to be finished, to be asked for
         auto fetch = [&](int stage) {
             if (coming > 0) {
-                queue.put(stage, 0, xf, l.apart, f.live && l.in);
+                queue.put(stage, 0, xf, l.gap, l.apart, f.live && l.in);
                 xf += sx.h;
                 if (--coming > 0 && f.next(g, heads)) xf = x + f.b * sx.b + f.t * sx.t;
             }
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
                 v.a[i] = fma2(a, wac[i], mul2(b, wbs[i]));
                 v.b[i] = fma2(b, wbc[i], mul2(a, was[i]));
             }
-            if (c.on && l.in) v.store(oc, l.apart);
+            if (c.on && l.in) v.store(oc, l.gap, l.apart);
             if (--left == 0) return true;
             oc += so.h;
             if (c.next(g, heads)) {
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
     __shared__ unsigned long long s_turn[128];
     __shared__ float s_w[W][2][G * 16];
     const Queue<kBwdThreads, S, 2 * N> queue(smem);
-    const Lane<G, IL> l(g);
+    const Lane<E, G, IL> l(g);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (blockIdx.x == 0 && threadIdx.x < (int)sizeof(WsHeader) / 4) reinterpret_cast<uint32_t *>(hdr)[threadIdx.x] = 0u;  // nothing waits
     for (int i = threadIdx.x; i < g.rot / 2; i += kBwdThreads) s_turn[i] = turns(g.freq[i]);
@@ -422,8 +424,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
             int left = (int)(hi - lo), coming = left;
             auto fetch = [&](int stage) {
                 if (coming > 0) {
-                    queue.put(stage, 0, xf, l.apart, f.live && l.in);
-                    queue.put(stage, N, yf, l.apart, f.live && l.in);
+                    queue.put(stage, 0, xf, l.gap, l.apart, f.live && l.in);
+                    queue.put(stage, N, yf, l.gap, l.apart, f.live && l.in);
                     xf += sx.h, yf += sg.h;
                     if (--coming > 0 && f.next(g, heads)) xf = x + f.b * sx.b + f.t * sx.t, yf = y + f.b * sg.b + f.t * sg.t;
                 }
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
                     z.a[i] = mul2(both(r), fma2(z.a[i], both(-k), mul2(e.a[i], w.a[i])));
                     z.b[i] = mul2(both(r), fma2(z.b[i], both(-k), mul2(e.b[i], w.b[i])));
                 }
-                if (c.on && l.in) z.store(dc, l.apart);
+                if (c.on && l.in) z.store(dc, l.gap, l.apart);
                 dc += sd.h;
                 if (left > 1 && c.next(g, heads)) {
                     dc = d + c.b * sd.b + c.t * sd.t;
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
         for (int i = 0; i < 16; ++i) {
 #pragma unroll
             for (int x = G; x < 32; x <<= 1) v[i] += __shfl_xor_sync(~0u, v[i], x);
-            if (lane < G && l.in) s_w[warp][which][l.c0 + (i < 8 ? i : l.apart + i - 8)] = v[i];
+            if (lane < G && l.in) s_w[warp][which][l.at(i)] = v[i];
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits for this grid's end
