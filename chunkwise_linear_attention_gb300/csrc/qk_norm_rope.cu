@@ -10,19 +10,22 @@
 //
 // What bounds them is memory: a row is read once and written once (backward:
 // two reads, one write).  A row is handled by the fewest lanes, a power of two,
-// that take 16 of its values each, as the two 8-value pieces whose pairs turn
-// into one another, so the rotation stays within a lane.  A block's groups of
-// such lanes take neighbouring tokens and walk over their heads together: the
-// sines and cosines are formed once for all of them.  Queries come first and
+// that take 16 of its values each, both of each pair, so the rotation stays
+// within a lane, and in 16-byte pieces beside the neighbouring lanes', so every
+// access moves whole sectors.  A block's groups of such lanes take neighbouring
+// tokens and walk over their heads together: the sines and cosines are formed
+// once for all of them.  Queries come first and
 // keys after them, so that one set of weights and sums is held at a time.  Rows
 // come through asynchronous copies into a lane's own column of shared memory,
 // several rows ahead and without registers.  Arithmetic is on pairs of fp32.
 //
 // Measured on GB300 (bf16, every pass on other inputs): prefill 1 x 32/8 x
 // 32768 x 128 out of a fused projection 105 us for 671 MB (6.4 TB/s, 94% of the
-// measured copy rate; loads into registers four rows at a time 147); training
-// pass 4 x 16/16 x 8192 x 64 115 us for 671 MB (5.8 TB/s, 86%): backward 62 of
-// a floor of 59, forward 47 of 40, join and the gaps between launches the rest.
+// measured copy rate; loads into registers four rows at a time 147), with
+// neighbours as pairs 105 too (147 where a lane's 32 bytes lay in one piece) and
+// half of each head rotated 106 (125); training pass 4 x 16/16 x 8192 x 64 115 us
+// for 671 MB (5.8 TB/s, 86%): backward 62 of a floor of 59, forward 47 of 40,
+// join and the gaps between launches the rest.
 //
 // Angles: positions reach 2^31 and an angle's 24 bits of fp32 would leave
 // nothing of its fraction of a turn.  freq / 2 pi is formed as a 64-bit
@@ -38,8 +41,8 @@
 namespace cla {
 namespace {
 
-// Blocks that run at once, for 152 multiprocessors: forward 2 for each, backward one (its lanes hold 16 sums of dw as well, 170
-// registers; with 128 they went to local memory and the backward took some 100 us where it takes 62).
+// Blocks that run at once, for 152 multiprocessors: forward 2 for each, backward one (its lanes hold 16 sums of dw as well, up to
+// 156 registers; with 128 they went to local memory and the backward took some 100 us where it takes 62).
 constexpr int kFwdThreads = 256, kFwdBlocks = 304, kBwdThreads = 384, kBwdBlocks = 152;
 
 struct QnArgs {
@@ -546,7 +549,7 @@ QnArgs qn_args(const float *wq, const float *wk, const float *freq, const int32_
 
 // Blocks that run at once, each with one row of each of its lanes' at least; forward as many rounds of them as give each
 // 16, so that multiprocessors that are further from memory take fewer (1 x 32/8 x 32768 x 128: 105 us with 8 rounds against
-// 119 with one; 3 x 10/5 x 1531 x 96, 7 rows: 45 and 31 us with the backward).
+// 116 with one, 107 with 4 or 16, 143 with 33; 4/1 heads x 65536 x 128 with the backward: 99 with 2, 105 with one, 103 with 4).
 unsigned qn_fwd_blocks(const QnArgs &g) {
     const long long n = g.groups * (g.heads[0] + g.heads[1]), rounds = n / (16 * kFwdBlocks);
     return (unsigned)(n < kFwdBlocks ? n : rounds < 1 ? kFwdBlocks : rounds < 4096 ? rounds * kFwdBlocks : 4096 * kFwdBlocks);
