@@ -30,9 +30,9 @@
 // t = s + log2 f, the weights are 2^(t - m) with m the running maximum of t, and
 // the sum that divides takes each with 1 / f.  Weights are in [0, 2^15]
 // (2^7 at the maximum, 8 above before the maximum moves) as fp16 for their
-// product: rounded by 2^-11 of themselves at most, or 2^-32 of the largest.
-// Against bf16 outputs (2^-8) that is nothing; for fp16 outputs a second part
-// takes what the first leaves (error against 64 bits 2.0e-4, with one part 2.9e-4).
+// product, with a second part that takes what the first leaves: off by 2^-22 of
+// themselves at most, or 2^-32 of the largest.  One part would leave 2^-11, more
+// than fp32 loses for either type's outputs.
 //
 // Measured on GB300: 64 x 32/8 x 128, window 4096, sinks 4, bf16: 91 us for 539
 // MB (5.9 TB/s, 87% of the measured copy rate); 2 x 32/4 x 128, window 65536:
@@ -525,10 +525,8 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t h = pack16<false>(make_float2(z[2 * x], z[2 * x + 1]));
                         pw[a][x] = transpose8x8(h);
-                        if constexpr (!BF) {
-                            const float2 e = unpack16<false>(h);
-                            pl[a][x] = transpose8x8(pack16<false>(make_float2(z[2 * x] - e.x, z[2 * x + 1] - e.y)));
-                        }
+                        const float2 e = unpack16<false>(h);
+                        pl[a][x] = transpose8x8(pack16<false>(make_float2(z[2 * x] - e.x, z[2 * x + 1] - e.y)));
                     }
                 }
 #pragma unroll
@@ -542,10 +540,8 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                     for (int a = 0; a < NG; ++a) {
                         mma16x8<false>(acc[a][2 * y], f0, f1, f2, f3, pw[a][0], pw[a][1]);
                         mma16x8<false>(acc[a][2 * y + 1], f4, f5, f6, f7, pw[a][0], pw[a][1]);
-                        if constexpr (!BF) {
-                            mma16x8<false>(acc[a][2 * y], f0, f1, f2, f3, pl[a][0], pl[a][1]);
-                            mma16x8<false>(acc[a][2 * y + 1], f4, f5, f6, f7, pl[a][0], pl[a][1]);
-                        }
+                        mma16x8<false>(acc[a][2 * y], f0, f1, f2, f3, pl[a][0], pl[a][1]);
+                        mma16x8<false>(acc[a][2 * y + 1], f4, f5, f6, f7, pl[a][0], pl[a][1]);
                     }
                 }
             }

@@ -772,8 +772,7 @@ int cla_window_cache8_write(const void *k, const void *v, const int32_t *lens,
  * other numbers are rounded anew where a factor changes: exactly, but for those
  * that fall below e4m3's normal range), and the attention is over what the cache
  * then holds, the token's own key and value included.  Other blocks are read
- * only.  With bf16 tensors the weights are rounded to 11 bits for their product
- * with the cache's numbers.
+ * only.
  * The arguments are cla_window_attn_step's, with the caches above; the order of
  * the sums is fixed by the sizes, the positions and the device model.
  * B * Hkv * ceil((sinks + window) / 64) is below 2^31, B * H below 2^27, H / Hkv
