@@ -26,13 +26,18 @@
 // e4m3 numbers turn into fp16 exactly, two with one instruction.  Queries turn
 // into fp16 too, each head's by a power of two of its own under which its
 // largest lies in [1, 2): exact for bf16 down to 2^-14 of that, and off by less
-// than 2^-25 of it below.  The factors of v's blocks go into the exponent: with
-// t = s + log2 f, the weights are 2^(t - m) with m the running maximum of t, and
-// the sum that divides takes each with 1 / f.  Weights are in [0, 2^15]
-// (2^7 at the maximum, 8 above before the maximum moves) as fp16 for their
-// product, with a second part that takes what the first leaves: off by 2^-22 of
-// themselves at most, or 2^-32 of the largest.  One part would leave 2^-11, more
-// than fp32 loses for either type's outputs.
+// than 2^-25 of it below.
+//
+// The factors of v's blocks may lie 2^184 apart, so no weight is taken together
+// with one.  The total is held against the running maximum m of the scores
+// alone.  A tile's weights go into its product as 2^(s - t + 14), t the largest
+// score of its 16 slots (to bf16's accuracy, which one round of shuffles for two heads
+// finds), in two fp16 parts: off by 2^-22 of themselves at most, or 2^-38 of the
+// tile's largest, and no number of the tile is 2^18 above another that e4m3 has
+// not rounded to zero.  (One part would leave 2^-11.)  The product is added to
+// the sums in fp32 times f 2^(t - m - 14); the sums are held at 2^-32 of their value, so
+// that they stay finite whatever the number of slots.  Weights below
+// 2^-126 of the largest count as nothing, as in any fp32 softmax.
 //
 // Measured on GB300: 64 x 32/8 x 128, window 4096, sinks 4, bf16: 91 us for 539
 // MB (5.9 TB/s, 87% of the measured copy rate); 2 x 32/4 x 128, window 65536:
@@ -300,6 +305,15 @@ __device__ __forceinline__ void put_token(uint32_t tile, uint8_t *kc, uint8_t *v
     __syncwarp();
 }
 
+// acc += x times what belongs to its column
+__device__ __forceinline__ void add_times(float (&acc)[4], const float (&x)[4], float2 by) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float2 v = __ffma2_rn(make_float2(x[i], x[i + 1]), by, make_float2(acc[i], acc[i + 1]));
+        acc[i] = v.x, acc[i + 1] = v.y;
+    }
+}
+
 constexpr int kC8Stages = 4;  // tiles of a warp on their way
 
 template <int D, int NG>
@@ -430,7 +444,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 fac[a][0] = __shfl_sync(~0u, up, 8 * j) * g.c;  // of heads 2j, 2j + 1
                 fac[a][1] = __shfl_sync(~0u, up, 8 * j + 4) * g.c;
             }
-            // per head: the exponent's offset (the maximum less 7; infinity before there is one) and the total
+            // per head: the running maximum (8 less than the maximum at most) and the total; acc: 2^-32 of the sums
             float acc[NG][M][4], mu[NG][2], l[NG][2];
 #pragma unroll
             for (int a = 0; a < NG; ++a) {
@@ -439,25 +453,21 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
 #pragma unroll
                 for (int y = 0; y < M; ++y) acc[a][y][0] = acc[a][y][1] = acc[a][y][2] = acc[a][y][3] = 0.f;
             }
-            float kfs = 0.f, vfs = 0.f, lifts = 0.f, lesses = 0.f;  // the factors of 32 blocks, one in each lane
+            float kfs = 0.f, vfs = 0.f;  // the factors of 32 blocks, one in each lane
             uint32_t tile = ring;
 #pragma unroll 1
             for (int i = 0; i < cnt; ++i) {
-                if (i % 32 == 0 && i + lane < cnt) {
-                    kfs = __ldcg(kfb + i + lane), vfs = __ldcg(vfb + i + lane);
-                    lifts = __log2f(fmaxf(vfs, 0x1p-64f)), lesses = __frcp_rn(fmaxf(vfs, 0x1p-64f));
-                }
-                float kfac = __shfl_sync(~0u, kfs, i % 32), lift = __shfl_sync(~0u, lifts, i % 32), less = __shfl_sync(~0u, lesses, i % 32);
+                if (i % 32 == 0 && i + lane < cnt) kfs = __ldcg(kfb + i + lane), vfs = __ldcg(vfb + i + lane);
+                float kfac = __shfl_sync(~0u, kfs, i % 32), vfac = __shfl_sync(~0u, vfs, i % 32);
                 cp_async_wait<kC8Stages - 1>();
                 __syncwarp();
                 const int left = n - (first + i) * kC8Block - 16 * warp;  // slots from the warp's first that hold a token
                 if (h0 == 0 && i == own) {
-                    float vfac = __shfl_sync(~0u, vfs, i % 32);
                     const int s0 = n - left;
                     put_token<E, D>(tile, kb + (long long)s0 * D, vb + (long long)s0 * D, kfb + i, vfb + i, s_new, mine - s0, left, kfac,
                                     vfac, s_top);
-                    lift = __log2f(vfac), less = inverse(vfac);
                 }
+                const float part = vfac * 0x1p-32f;
                 uint4 kx[2][KC];
                 uint32_t vx[4][D / 32];
 #pragma unroll
@@ -479,6 +489,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 cp_async_commit();
                 tile = tile + 32 * D == ring_end ? ring : tile + 32 * D;
                 uint32_t pw[NG][2], pl[NG][2];
+                float2 by[NG];  // what the products of heads 2j, 2j + 1 are added with
 #pragma unroll
                 for (int a = 0; a < NG; ++a) {
                     float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -501,26 +512,32 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                             if (r + 8 >= left) z[2] = z[3] = -INFINITY;
                         }
                     };
-                    exponents(lift - mu[a][0], lift - mu[a][1]);
-                    if (__any_sync(~0u, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > 15.f)) {
-                        exponents(lift, lift);
+                    exponents(-mu[a][0], -mu[a][1]);
+                    if (__any_sync(~0u, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > 8.f)) {
+                        exponents(0.f, 0.f);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float top = fmaxf(z[e], z[2 + e]);
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-                            const float mn = fmaxf(mu[a][e], top - 7.f), f = mn == -INFINITY ? 1.f : ex2(mu[a][e] - mn);
+                            const float mn = fmaxf(mu[a][e], top), f = mn == -INFINITY ? 1.f : ex2(mu[a][e] - mn);
                             mu[a][e] = mn;
                             l[a][e] *= f;
 #pragma unroll
                             for (int y = 0; y < M; ++y) acc[a][y][e] *= f, acc[a][y][2 + e] *= f;
                         }
-                        exponents(lift - mu[a][0], lift - mu[a][1]);
+                        exponents(-mu[a][0], -mu[a][1]);
                     }
+                    // the largest of the tile, off by 1 at most from -512 up, where it still weighs anything
+                    __nv_bfloat162 two = __floats2bfloat162_rn(fmaxf(z[0], z[2]), fmaxf(z[1], z[3]));
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) z[x] = ex2(z[x]);
-                    l[a][0] = fmaf(z[0] + z[2], less, l[a][0]);
-                    l[a][1] = fmaf(z[1] + z[3], less, l[a][1]);
+                    for (int x = 4; x < 32; x <<= 1) two = __hmax2(two, __shfl_xor_sync(~0u, two, x));
+                    const float t0 = fmaxf(__low2float(two), -512.f) - 14.f, t1 = fmaxf(__high2float(two), -512.f) - 14.f;
+                    z[0] = ex2(z[0] - t0), z[1] = ex2(z[1] - t1), z[2] = ex2(z[2] - t0), z[3] = ex2(z[3] - t1);
+                    const float e0 = ex2(t0), e1 = ex2(t1);
+                    l[a][0] = fmaf(z[0] + z[2], e0, l[a][0]);
+                    l[a][1] = fmaf(z[1] + z[3], e1, l[a][1]);
+                    by[a] = make_float2(e0 * part, e1 * part);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t h = pack16<false>(make_float2(z[2 * x], z[2 * x + 1]));
@@ -538,10 +555,13 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                     const uint32_t f4 = f16x2_of(a1), f5 = f16x2_of(a1 >> 16), f6 = f16x2_of(b1), f7 = f16x2_of(b1 >> 16);
 #pragma unroll
                     for (int a = 0; a < NG; ++a) {
-                        mma16x8<false>(acc[a][2 * y], f0, f1, f2, f3, pw[a][0], pw[a][1]);
-                        mma16x8<false>(acc[a][2 * y + 1], f4, f5, f6, f7, pw[a][0], pw[a][1]);
-                        mma16x8<false>(acc[a][2 * y], f0, f1, f2, f3, pl[a][0], pl[a][1]);
-                        mma16x8<false>(acc[a][2 * y + 1], f4, f5, f6, f7, pl[a][0], pl[a][1]);
+                        float u[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma16x8<false>(u, f0, f1, f2, f3, pl[a][0], pl[a][1]);
+                        mma16x8<false>(w, f4, f5, f6, f7, pl[a][0], pl[a][1]);
+                        mma16x8<false>(u, f0, f1, f2, f3, pw[a][0], pw[a][1]);
+                        mma16x8<false>(w, f4, f5, f6, f7, pw[a][0], pw[a][1]);
+                        add_times(acc[a][2 * y], u, by[a]);
+                        add_times(acc[a][2 * y + 1], w, by[a]);
                     }
                 }
             }
@@ -595,7 +615,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                     lt = fmaf(f, s_l[w][h], lt), x = fmaf(f, e.x, x), y = fmaf(f, e.y, y);
                 }
                 if (whole) {
-                    reinterpret_cast<uint32_t *>(o + (unit * G + h0) * D)[i] = pack16<BF>(make_float2(x / lt, y / lt));
+                    reinterpret_cast<uint32_t *>(o + (unit * G + h0) * D)[i] = pack16<BF>(make_float2(x / lt * 0x1p32f, y / lt * 0x1p32f));
                 } else {
                     reinterpret_cast<float2 *>(part + h0 * D)[i] = make_float2(x, y);
                     if (d == 0) reinterpret_cast<float2 *>(part + G * D)[h0 + h] = make_float2(mm, lt);
@@ -669,7 +689,7 @@ __global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ 
         float lt = 0.f, y = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) lt += s_l[w], y += s_o[w][d];
-        o[((long long)cut.unit * G + h) * D + d] = from_f32<E>(y / lt);
+        o[((long long)cut.unit * G + h) * D + d] = from_f32<E>(y / lt * 0x1p32f);
     }
 }
 

@@ -760,7 +760,9 @@ int cla_window_attn_step(const void *q, const void *k, const void *v, void *kcac
 
 /* cla_window_cache_write into that cache.  Bytes of slots and factors of blocks
  * that no token reaches are left as they were.  An infinity is held as the
- * largest number, a NaN stays one and does not count for the factor. */
+ * largest number: its block's factor is 2^120, under which the block's other
+ * numbers of that key head become 0, for good (they are not rounded from the
+ * tensor again).  A NaN stays one and does not count for the factor. */
 int cla_window_cache8_write(const void *k, const void *v, const int32_t *lens,
                             void *kcache, void *vcache, float *kscale,
                             float *vscale, int64_t window, int64_t sinks,
@@ -772,7 +774,9 @@ int cla_window_cache8_write(const void *k, const void *v, const int32_t *lens,
  * other numbers are rounded anew where a factor changes: exactly, but for those
  * that fall below e4m3's normal range), and the attention is over what the cache
  * then holds, the token's own key and value included.  Other blocks are read
- * only.
+ * only.  Factors may lie as far apart as they can: what a block adds to a column
+ * is rounded relative to itself, as in fp32 sums, whatever other blocks and
+ * columns hold; weights below 2^-110 of the largest may count as nothing.
  * The arguments are cla_window_attn_step's, with the caches above; the order of
  * the sums is fixed by the sizes, the positions and the device model.
  * B * Hkv * ceil((sinks + window) / 64) is below 2^31, B * H below 2^27, H / Hkv
