@@ -47,6 +47,7 @@
 // us, two of five and six deep 93 and 94.  Scores formed a block ahead of their
 // weights changed nothing (92 us), more shares than blocks that run at once
 // cost their starts (97 us at twice as many).
+#include <float.h>
 #include <math.h>
 
 #include <type_traits>
@@ -444,11 +445,12 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 fac[a][0] = __shfl_sync(~0u, up, 8 * j) * g.c;  // of heads 2j, 2j + 1
                 fac[a][1] = __shfl_sync(~0u, up, 8 * j + 4) * g.c;
             }
-            // per head: the running maximum (8 less than the maximum at most) and the total; acc: 2^-32 of the sums
+            // per head: the running maximum (8 less than the maximum at most; finite from the start, so that a score of -inf
+            // weighs nothing wherever it comes) and the total; acc: 2^-32 of the sums
             float acc[NG][M][4], mu[NG][2], l[NG][2];
 #pragma unroll
             for (int a = 0; a < NG; ++a) {
-                mu[a][0] = mu[a][1] = -INFINITY;
+                mu[a][0] = mu[a][1] = -FLT_MAX;
                 l[a][0] = l[a][1] = 0.f;
 #pragma unroll
                 for (int y = 0; y < M; ++y) acc[a][y][0] = acc[a][y][1] = acc[a][y][2] = acc[a][y][3] = 0.f;
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                             float top = fmaxf(z[e], z[2 + e]);
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-                            const float mn = fmaxf(mu[a][e], top), f = mn == -INFINITY ? 1.f : ex2(mu[a][e] - mn);
+                            const float mn = fmaxf(mu[a][e], top), f = ex2(mu[a][e] - mn);
                             mu[a][e] = mn;
                             l[a][e] *= f;
 #pragma unroll
@@ -664,8 +666,7 @@ __global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ 
     for (int w = 0; w < W; ++w) m = fmaxf(m, s_m[w]);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        // a part without a maximum holds nothing, or NaN alone
-        const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : NAN) : ex2(ml[k].x - m);
+        const float f = ex2(ml[k].x - m);
         if (threadIdx.x + 256 * k < kC8MaxBlocks) s_f[threadIdx.x + 256 * k] = f;
         l += f * ml[k].y;
     }

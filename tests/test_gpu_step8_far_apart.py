@@ -134,3 +134,21 @@ def test_small_weights_of_large_values(cla, B, H, K, n, below, high):
         x = v.clone()
         x[:, :, large] *= 2.0 ** high
         M.assert_within("o", *both(cla, q, k, x, n, pos))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n", [1, 16, 64, 128, 1600])
+def test_a_score_of_minus_infinity(cla, n, dtype):
+    """A token whose key is the largest number in the direction away from the query: its score is -inf in fp32 and its weight
+    nothing, also where it is all that a tile holds."""
+    B, H, K, d = 2, 4, 2, 64
+    q = torch.zeros(B, H, d)
+    q[..., 3] = -1000.0
+    k, v = torch.zeros(B, K, n + 1, d), torch.ones(B, K, n + 1, d)
+    k[:, :, n, 3], v[:, :, n] = float("inf"), 5.0
+    q, k, v = (x.to(dtype).cuda() for x in (q, k, v))
+    cache = cla.window_cache8(B, K, d, window=n + 1)
+    cla.window_cache8_write(k[:, :, :n], v[:, :, :n], *cache, window=n + 1)
+    pos = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    got = cla.window_attn_step8(q, k[:, :, n], v[:, :, n], *cache, pos, window=n + 1)
+    assert torch.equal(got, torch.ones_like(got))
