@@ -666,8 +666,9 @@ __global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ 
     for (int w = 0; w < W; ++w) m = fmaxf(m, s_m[w]);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const float f = ex2(ml[k].x - m);
-        if (threadIdx.x + 256 * k < kC8MaxBlocks) s_f[threadIdx.x + 256 * k] = f;
+        const bool there = ml[k].x != -INFINITY;
+        const float f = there ? ex2(ml[k].x - m) : 0.f;
+        if (threadIdx.x + 256 * k < kC8MaxBlocks) s_f[threadIdx.x + 256 * k] = there ? f : -1.f;
         l += f * ml[k].y;
     }
 #pragma unroll
@@ -681,7 +682,8 @@ __global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ 
     for (int i = warp; i < n; i += W) {
         const float f = s_f[i], *part = part_of(i) + h * D + lane;
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = fmaf(f, f != 0.f ? part[32 * e] : 0.f, x[e]);
+        for (int e = 0; e < N; ++e)
+            if (f != -1.f) x[e] = fmaf(f, part[32 * e], x[e]);  // of a part that is there, were its weight 0: it may hold a NaN
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) s_o[warp][32 * e + lane] = x[e];

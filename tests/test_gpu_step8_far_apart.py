@@ -152,3 +152,21 @@ def test_a_score_of_minus_infinity(cla, n, dtype):
     pos = torch.full((B,), n, dtype=torch.int32, device="cuda")
     got = cla.window_attn_step8(q, k[:, :, n], v[:, :, n], *cache, pos, window=n + 1)
     assert torch.equal(got, torch.ones_like(got))
+
+
+@pytest.mark.parametrize("B,H,K,n", SPLITS)
+def test_a_nan_of_no_weight(cla, B, H, K, n):
+    """A NaN among the values reaches its column however small its slot's weight, whichever way the work is split."""
+    q, k, v = (torch.zeros(B, h, m, 64, dtype=BF16, device="cuda") for h, m in ((H, 1), (K, n), (K, n)))
+    q, pos = q[:, :, 0], torch.full((B,), n - 1, dtype=torch.int32, device="cuda")
+    q[..., 0] = 8.0
+    for slot in (5, 70):
+        k.zero_(), v.fill_(1.0)
+        k[:, :, slot // 64 * 64:slot // 64 * 64 + 64, 0] = -400.0
+        v[:, :, slot, 9] = float("nan")
+        cache = cla.window_cache8(B, K, 64, window=n)
+        cla.window_cache8_write(k[:, :, :n - 1], v[:, :, :n - 1], *cache, window=n)
+        got = cla.window_attn_step8(q, k[:, :, n - 1], v[:, :, n - 1], *cache, pos, window=n)
+        assert bool(torch.isnan(got[..., 9]).all())
+        got[..., 9] = 1.0
+        assert torch.equal(got, torch.ones_like(got))
