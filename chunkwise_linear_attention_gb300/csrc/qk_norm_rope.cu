@@ -497,8 +497,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
     }
 }
 
-// dw = the blocks' parts, in a fixed order: 8 threads take every eighth of a column's
-__global__ void __launch_bounds__(256) qn_join_kernel(const float *__restrict__ parts, float *dwq, float *dwk, int d, int blocks) {
+// dw = the blocks' parts, in a fixed order: 8 threads take every eighth of a column's.  It starts while the backward still
+// writes them, so they are no memory that stays as it is for the kernel's life: no __restrict__.
+__global__ void __launch_bounds__(256) qn_join_kernel(const float *parts, float *dwq, float *dwk, int d, int blocks) {
     __shared__ float s[8][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int col = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;

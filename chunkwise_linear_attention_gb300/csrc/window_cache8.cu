@@ -635,10 +635,10 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
 
 // Adds the parts of a cut (sequence, key head), for a query head of the group, in a fixed order: their common maximum first,
 // then every eighth part by a warp.  A block of it fits beside the step's two (32 registers; with 59 it did not, and the
-// step took 2 us more).
+// step took 2 us more).  It starts while the step still writes parts and cuts, so these are no memory that stays as it is
+// for the kernel's life: no __restrict__, and the wait keeps the loads behind it.
 template <typename E, int D>
-__global__ void __launch_bounds__(256) c8_join_kernel(const float *__restrict__ parts, const Cut8 *__restrict__ cuts, E *__restrict__ o,
-                                                      int G) {
+__global__ void __launch_bounds__(256) c8_join_kernel(const float *parts, const Cut8 *cuts, E *o, int G) {
     constexpr int W = 8, N = D / 32;
     __shared__ float s_o[W][D], s_f[kC8MaxBlocks], s_m[W], s_l[W];
     asm volatile("griddepcontrol.wait;" ::: "memory");
