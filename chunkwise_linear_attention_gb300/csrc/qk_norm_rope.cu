@@ -32,6 +32,7 @@
 // fraction of a turn from the integer product of freq's 24 bits and 2^64 / 2 pi;
 // its product with the position wraps around as turns do, and its upper 32 bits
 // are the angle: off by less than 2^-31 (1 + |freq|) turns.
+#include <float.h>
 #include <math.h>
 
 #include "cla_internal.cuh"
@@ -42,7 +43,7 @@ namespace cla {
 namespace {
 
 // Blocks that run at once, for 152 multiprocessors: forward 2 for each, backward one (its lanes hold 16 sums of dw as well, up to
-// 156 registers; with 128 they went to local memory and the backward took some 100 us where it takes 62).
+// 159 registers; with 128 they went to local memory and the backward took some 100 us where it takes 62).
 constexpr int kFwdThreads = 256, kFwdBlocks = 304, kBwdThreads = 384, kBwdBlocks = 152;
 
 struct QnArgs {
@@ -396,16 +397,57 @@ struct QnBwd {
     Triple sx[2], sg[2], sdx[2];
 };
 
-// A block leaves its rows' sums of dw in parts[block][2][d].
+// Sums of many rows go to pairs of fp32, 48 bits: x the sum, y what its roundings have left.
+__device__ __forceinline__ void add(float2 &s, float v) {
+    const float t = __fadd_rn(s.x, v), b = __fsub_rn(t, s.x);
+    s.y = __fadd_rn(s.y, __fadd_rn(__fsub_rn(s.x, __fsub_rn(t, b)), __fsub_rn(v, b)));
+    s.x = t;
+}
+__device__ __forceinline__ void add(float2 &s, float2 v) {
+    add(s, v.x);
+    s.y = __fadd_rn(s.y, v.y);
+}
+__device__ __forceinline__ float total(float2 s) { return fabsf(s.x) <= FLT_MAX ? s.x + s.y : s.x; }  // an infinity stays one
+
+// The sums of 16 values over the lanes of a warp that have the same columns (lane % G alike), scattered: a lane is left with
+// those of its values first, first + 1, ... in v[0 .. N), with G = 1 two lanes with the same one.
+template <int G>
+struct Scatter {
+    static constexpr int N = G > 2 ? G / 2 : 1;
+    static __device__ __forceinline__ int first(int lane) {
+        int at = 0;
+#pragma unroll
+        for (int x = 16, n = 8; x >= G && n > 0; x >>= 1, n >>= 1) at += lane & x ? n : 0;
+        return at;
+    }
+    static __device__ __forceinline__ void sum(float (&v)[16], int lane) {
+#pragma unroll
+        for (int x = 16, n = 8; x >= G; x >>= 1, n >>= 1) {
+            const bool up = lane & x;
+            if (n == 0) v[0] += __shfl_xor_sync(~0u, v[0], x);
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float give = up ? v[i] : v[i + n];
+                v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(~0u, give, x);
+            }
+        }
+    }
+};
+
+// A block leaves its rows' sums of dw in parts[block][2][d].  A lane adds kBwdRows rows at most in fp32, one after the other;
+// the warp's sums of them, the warps' and the blocks' go to pairs of fp32 (fp64 runs at a small share of fp32's rate here).  All
+// in fp32, 2300 rows a lane that are alike left 6 times what 64 rows can.
+constexpr int kBwdRows = 64;
 template <typename E, int G, bool IL>
-__global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs g, float *parts, WsHeader *hdr) {
+__global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs g, float2 *parts, WsHeader *hdr) {
     constexpr int S = qn_bwd_stages<E>(), N = Row<E, IL>::N, W = kBwdThreads / 32;
     extern __shared__ __align__(16) char smem[];
     __shared__ unsigned long long s_turn[128];
-    __shared__ float s_w[W][2][G * 16];
+    __shared__ float2 s_w[W][G * 16];
     const Queue<kBwdThreads, S, 2 * N> queue(smem);
     const Lane<E, G, IL> l(g);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, first = Scatter<G>::first(lane);
+    const bool owner = l.in && (G > 1 || lane % 2 == 0);  // of the sums that it is left with
     if (blockIdx.x == 0 && threadIdx.x < (int)sizeof(WsHeader) / 4) reinterpret_cast<uint32_t *>(hdr)[threadIdx.x] = 0u;  // nothing waits
     for (int i = threadIdx.x; i < g.rot / 2; i += kBwdThreads) s_turn[i] = turns(g.freq[i]);
     const Share share(g.groups * (g.heads[0] + g.heads[1]));
@@ -414,9 +456,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
         const int heads = pick(g.heads, which);
         const long long base = which == 0 ? 0 : g.groups * g.heads[0];
         const long long lo = max(share.at, base), hi = min(share.end, base + g.groups * heads);
-        Row<E, IL> acc;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc.a[i] = acc.b[i] = both(0.f);
+        for (int i = 0; i < Scatter<G>::N; ++i)
+            if (owner) s_w[warp][l.at(first + i)] = both(0.f);
         if (lo < hi) {
             const Triple sx = pick(p.sx, which), sg = pick(p.sg, which), sd = pick(p.sdx, which);
             const E *x = static_cast<const E *>(pick(p.x, which)) + l.c0, *y = static_cast<const E *>(pick(p.g, which)) + l.c0;
@@ -443,76 +485,82 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
             angles(g, l, c, s_turn, sn, cs);
             int stage = 0;
 #pragma unroll 1
-            for (; left > 0; --left) {
-                queue.wait();
-                uint4 v[N], u[N];
+            while (left > 0) {
+                Row<E, IL> acc;
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] = queue.get(stage, i), u[i] = queue.get(stage, N + i);
-                fetch(stage);
-                stage = stage + 1 == S ? 0 : stage + 1;
-                Row<E, IL> z, e;
-                z.unpack(v);
-                e.unpack(u);
-                float2 q = both(0.f), m = both(0.f);
+                for (int i = 0; i < 4; ++i) acc.a[i] = acc.b[i] = both(0.f);
+#pragma unroll 1
+                for (const int end = max(left - kBwdRows, 0); left > end; --left) {
+                    queue.wait();
+                    uint4 v[N], u[N];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 t = e.a[i];  // turned back
-                    e.a[i] = fma2(t, cs[i], mul2(e.b[i], sn[i]));
-                    e.b[i] = fma2(e.b[i], cs[i], mul2(t, minus(sn[i])));
-                    q = fma2(z.a[i], z.a[i], q), q = fma2(z.b[i], z.b[i], q);
-                    m = fma2(mul2(e.a[i], w.a[i]), z.a[i], m), m = fma2(mul2(e.b[i], w.b[i]), z.b[i], m);
-                }
-                const float r = rsqrtf(row_sum<G>(q.x + q.y) * g.inv_d + g.eps), k = row_sum<G>(m.x + m.y) * g.inv_d * r * r;
+                    for (int i = 0; i < N; ++i) v[i] = queue.get(stage, i), u[i] = queue.get(stage, N + i);
+                    fetch(stage);
+                    stage = stage + 1 == S ? 0 : stage + 1;
+                    Row<E, IL> z, e;
+                    z.unpack(v);
+                    e.unpack(u);
+                    float2 q = both(0.f), m = both(0.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc.a[i] = fma2(mul2(e.a[i], both(r)), z.a[i], acc.a[i]);
-                    acc.b[i] = fma2(mul2(e.b[i], both(r)), z.b[i], acc.b[i]);
-                    z.a[i] = mul2(both(r), fma2(z.a[i], both(-k), mul2(e.a[i], w.a[i])));
-                    z.b[i] = mul2(both(r), fma2(z.b[i], both(-k), mul2(e.b[i], w.b[i])));
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 t = e.a[i];  // turned back
+                        e.a[i] = fma2(t, cs[i], mul2(e.b[i], sn[i]));
+                        e.b[i] = fma2(e.b[i], cs[i], mul2(t, minus(sn[i])));
+                        q = fma2(z.a[i], z.a[i], q), q = fma2(z.b[i], z.b[i], q);
+                        m = fma2(mul2(e.a[i], w.a[i]), z.a[i], m), m = fma2(mul2(e.b[i], w.b[i]), z.b[i], m);
+                    }
+                    const float r = rsqrtf(row_sum<G>(q.x + q.y) * g.inv_d + g.eps), k = row_sum<G>(m.x + m.y) * g.inv_d * r * r;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc.a[i] = fma2(mul2(e.a[i], both(r)), z.a[i], acc.a[i]);
+                        acc.b[i] = fma2(mul2(e.b[i], both(r)), z.b[i], acc.b[i]);
+                        z.a[i] = mul2(both(r), fma2(z.a[i], both(-k), mul2(e.a[i], w.a[i])));
+                        z.b[i] = mul2(both(r), fma2(z.b[i], both(-k), mul2(e.b[i], w.b[i])));
+                    }
+                    if (c.on && l.in) z.store(dc, l.gap, l.apart);
+                    dc += sd.h;
+                    if (left > 1 && c.next(g, heads)) {
+                        dc = d + c.b * sd.b + c.t * sd.t;
+                        angles(g, l, c, s_turn, sn, cs);
+                    }
                 }
-                if (c.on && l.in) z.store(dc, l.gap, l.apart);
-                dc += sd.h;
-                if (left > 1 && c.next(g, heads)) {
-                    dc = d + c.b * sd.b + c.t * sd.t;
-                    angles(g, l, c, s_turn, sn, cs);
-                }
+                float v[16];
+                acc.get(v);
+                Scatter<G>::sum(v, lane);
+#pragma unroll
+                for (int i = 0; i < Scatter<G>::N; ++i)
+                    if (owner) add(s_w[warp][l.at(first + i)], v[i]);
             }
         }
-        float v[16];
-        acc.get(v);
+        // the join may take its place; it waits for this grid's end
+        if (which == 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        __syncthreads();
+        for (int i = threadIdx.x; i < g.d; i += kBwdThreads) {
+            float2 v = s_w[0][i];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-#pragma unroll
-            for (int x = G; x < 32; x <<= 1) v[i] += __shfl_xor_sync(~0u, v[i], x);
-            if (lane < G && l.in) s_w[warp][which][l.at(i)] = v[i];
+            for (int x = 1; x < W; ++x) add(v, s_w[x][i]);
+            parts[((long long)blockIdx.x * 2 + which) * g.d + i] = v;
         }
-    }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits for this grid's end
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * g.d; i += kBwdThreads) {
-        float v = 0.f;
-#pragma unroll
-        for (int x = 0; x < W; ++x) v += s_w[x][i / g.d][i % g.d];
-        parts[(long long)blockIdx.x * 2 * g.d + i] = v;
+        __syncthreads();  // the warps' sums have been read
     }
 }
 
-// dw = the blocks' parts, in a fixed order: 8 threads take every eighth of a column's.  It starts while the backward still
+// dw = the blocks' parts, in a fixed order: 16 threads take every 16th of a column's.  It starts while the backward still
 // writes them, so they are no memory that stays as it is for the kernel's life: no __restrict__.
-__global__ void __launch_bounds__(256) qn_join_kernel(const float *parts, float *dwq, float *dwk, int d, int blocks) {
-    __shared__ float s[8][32];
+__global__ void __launch_bounds__(256) qn_join_kernel(const float2 *parts, float *dwq, float *dwk, int d, int blocks) {
+    __shared__ float2 s[16][16];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int col = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;
-    float v = 0.f;
-    if (col < 2 * d)
-        for (int i = y; i < blocks; i += 8) v += parts[(long long)i * 2 * d + col];
-    s[y][threadIdx.x % 32] = v;
+    const int x = threadIdx.x % 16, col = blockIdx.x * 16 + x, y = threadIdx.x / 16;
+    float2 v = both(0.f);
+#pragma unroll 5
+    for (int i = y; i < blocks; i += 16) add(v, parts[(long long)i * 2 * d + col]);
+    s[y][x] = v;
     __syncthreads();
-    if (y == 0 && col < 2 * d) {
+    if (y == 0) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x];
+        for (int i = 1; i < 16; ++i) add(v, s[i][x]);
         float *to = col < d ? dwq : dwk;
-        if (to != nullptr) to[col < d ? col : col - d] = v;
+        if (to != nullptr) to[col < d ? col : col - d] = total(v);
     }
 }
 
@@ -582,7 +630,7 @@ int qn_fwd(const char *fn, const QnFwd &p, const QnArgs &g, cudaStream_t s) {
 }
 
 template <typename E, int G, bool IL>
-int qn_bwd_g(const char *fn, const QnBwd &p, const QnArgs &g, float *parts, cudaStream_t s) {
+int qn_bwd_g(const char *fn, const QnBwd &p, const QnArgs &g, float2 *parts, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     constexpr int smem = Queue<kBwdThreads, qn_bwd_stages<E>(), 2 * Row<E, IL>::N>::BYTES;
     if (int st = set_max_dynamic_smem(done, (const void *)qn_bwd_kernel<E, G, IL>, smem)) return st;
@@ -591,7 +639,7 @@ int qn_bwd_g(const char *fn, const QnBwd &p, const QnArgs &g, float *parts, cuda
 }
 
 template <typename E, bool IL>
-int qn_bwd(const char *fn, const QnBwd &p, const QnArgs &g, float *dwq, float *dwk, float *parts, cudaStream_t s) {
+int qn_bwd(const char *fn, const QnBwd &p, const QnArgs &g, float *dwq, float *dwk, float2 *parts, cudaStream_t s) {
     int st;
     switch (qn_lanes(g.d)) {
         case 1: st = qn_bwd_g<E, 1, IL>(fn, p, g, parts, s); break;
@@ -604,14 +652,14 @@ int qn_bwd(const char *fn, const QnBwd &p, const QnArgs &g, float *dwq, float *d
     // the join's launch goes beside the backward's end
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at;
-    cfg.gridDim = dim3((unsigned)((2 * g.d + 31) / 32));
+    cfg.gridDim = dim3((unsigned)(2 * g.d / 16));  // d is a multiple of 16
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    CLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, qn_join_kernel, (const float *)parts, dwq, dwk, g.d, (int)qn_bwd_blocks(g)), fn);
+    CLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, qn_join_kernel, (const float2 *)parts, dwq, dwk, g.d, (int)qn_bwd_blocks(g)), fn);
     return check_launch(fn);
 }
 
@@ -647,7 +695,7 @@ extern "C" int cla_qk_norm_rope_fwd(const void *q, const void *k, const float *w
 
 extern "C" size_t cla_qk_norm_rope_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d) {
     if (qn_check("cla_qk_norm_rope_bwd_workspace_size", B, H, Hkv, T, d, 0, 1.f, CLA_F32) != CLA_OK) return 0;
-    return sizeof(WsHeader) + (size_t)kBwdBlocks * 2 * d * 4;
+    return sizeof(WsHeader) + (size_t)kBwdBlocks * 2 * d * sizeof(float2);
 }
 
 extern "C" int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const float *wk, const float *freq,
@@ -679,7 +727,7 @@ extern "C" int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *w
     }
     const QnArgs g = qn_args(wq, wk, freq, pos, lens, eps, rot, B, H, Hkv, T, d, kBwdThreads);
     const QnBwd p = {{q, k}, {dqo, dko}, {dq, dk}, {r[0], r[1]}, {r[2], r[3]}, {r[4], r[5]}};
-    float *parts = reinterpret_cast<float *>(static_cast<WsHeader *>(ws) + 1);
+    float2 *parts = reinterpret_cast<float2 *>(static_cast<WsHeader *>(ws) + 1);
     if (dtype == CLA_F32)
         return interleaved ? qn_bwd<float, true>(fn, p, g, dwq, dwk, parts, s) : qn_bwd<float, false>(fn, p, g, dwq, dwk, parts, s);
     if (dtype == CLA_BF16)

@@ -835,7 +835,8 @@ size_t cla_qk_norm_rope_bwd_workspace_size(int64_t B, int64_t H, int64_t Hkv,
  *   dw = sum over rows of g n,  dx = r (g w - n mean(g w n)),  r = n / x.
  *   dqo, dko  gradients on qo and ko, dtype;  dq, dk dtype out, 0 behind a
  *             sequence's length
- *   dwq, dwk  [d] fp32 [opt] out, summed in an order that the sizes fix
+ *   dwq, dwk  [d] fp32 [opt] out, summed in an order that the sizes fix: 64 rows
+ *             and a warp's in fp32, those in 48 bits, rounded once
  *   strides [opt]: of q, k, dqo, dko, dq, dk
  * dq may be q or dqo, with the same strides, and so for dk.  The other arguments
  * are the forward's. */
