@@ -17,6 +17,8 @@
 // (6.3 TB/s, 92% of the measured copy rate); 8 tokens for 32 x 32 states: 49 us
 // where the states' traffic is 20: the chain of a token (sums, exchange, update)
 // at 24 warps a multiprocessor.
+#include <math.h>
+
 #include "cla_internal.cuh"
 #include "elem_io.cuh"
 #include "strided.cuh"
@@ -81,7 +83,11 @@ __global__ void __launch_bounds__(kDsThreads) delta_step_kernel(DsArgs g) {
 #pragma unroll
             for (int i = 0; i < DK / 32; ++i) kk[i] = to_f32(k[t * g.sk.t + 32 * i]), qq[i] = to_f32(q[t * g.sq.t + 32 * i]);
             s_v[warp][lane] = slice * kDsCols + lane < g.dv ? to_f32(v[t * g.sv.t]) : 0.f;
-            if (lane == 0) s_a[warp] = expf(ld[t * g.sl.t]), s_b[warp] = be[t * g.sb.t];
+            if (lane == 0) {
+                const float l = ld[t * g.sl.t];
+                s_a[warp] = l == -INFINITY ? -1.f : expf(l);  // -1: a reset, which a decay that underflows is not
+                s_b[warp] = be[t * g.sb.t];
+            }
 #pragma unroll
             for (int i = 0; i < DK / 32; ++i) {
                 s_kq[warp][lane + 32 * i] = make_float4(kk[i], kk[i], qq[i], qq[i]);
@@ -93,8 +99,9 @@ __global__ void __launch_bounds__(kDsThreads) delta_step_kernel(DsArgs g) {
         }
         __syncthreads();
         for (int t = 0; t < nt; ++t) {
-            const float a = s_a[t];
-            if (a == 0.f) {  // whatever the state holds
+            float a = s_a[t];
+            if (a < 0.f) {  // whatever the state holds
+                a = 0.f;
 #pragma unroll
                 for (int i = 0; i < R; ++i) x[i][0] = x[i][1] = both(0.f);
             }

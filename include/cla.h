@@ -862,7 +862,7 @@ int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq,
  *          H is a multiple of Hk: value head h takes query and key head
  *          h / (H / Hk).  Keys are used as given.
  *   log_decay, beta [B, H, T] fp32; a log decay of -inf drops the state, whatever
- *          it holds
+ *          it holds; a decay that underflows to 0 is a product like any other
  *   lens   [B] int32 [opt]: tokens of each sequence (clamped to [0, T]); behind
  *          them o is 0, the state is kept and the inputs are not used
  *   S      [B, H, dim_k, dim_v] fp32, dense, in and out
