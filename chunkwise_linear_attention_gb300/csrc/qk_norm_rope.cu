@@ -152,7 +152,8 @@ struct Row {
             (IL ? x[4 * i + 1] : x[8 + 2 * i]) = b[i].x, (IL ? x[4 * i + 3] : x[9 + 2 * i]) = b[i].y;
         }
     }
-    __device__ __forceinline__ void store(E *p, int gap, int apart) const {
+    // live: else zeros, whatever the weights have made of the row
+    __device__ __forceinline__ void store(E *p, int gap, int apart, bool live) const {
         float x[16];
         get(x);
 #pragma unroll
@@ -166,7 +167,7 @@ struct Row {
                 v = make_uint4(pair_of(make_float2(y[0], y[1]), E()), pair_of(make_float2(y[2], y[3]), E()),
                                pair_of(make_float2(y[4], y[5]), E()), pair_of(make_float2(y[6], y[7]), E()));
             }
-            *reinterpret_cast<uint4 *>(p + (i < N / 2 ? 0 : apart) + (N == 4 && i % 2 ? gap : 0)) = v;
+            *reinterpret_cast<uint4 *>(p + (i < N / 2 ? 0 : apart) + (N == 4 && i % 2 ? gap : 0)) = live ? v : make_uint4(0u, 0u, 0u, 0u);
         }
     }
 };
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) qn_fwd_kernel(QnFwd p, QnArgs 
                 v.a[i] = fma2(a, wac[i], mul2(b, wbs[i]));
                 v.b[i] = fma2(b, wbc[i], mul2(a, was[i]));
             }
-            if (c.on && l.in) v.store(oc, l.gap, l.apart);
+            if (c.on && l.in) v.store(oc, l.gap, l.apart, c.live);
             if (--left == 0) return true;
             oc += so.h;
             if (c.next(g, heads)) {
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) qn_bwd_kernel(QnBwd p, QnArgs 
                         z.a[i] = mul2(both(r), fma2(z.a[i], both(-k), mul2(e.a[i], w.a[i])));
                         z.b[i] = mul2(both(r), fma2(z.b[i], both(-k), mul2(e.b[i], w.b[i])));
                     }
-                    if (c.on && l.in) z.store(dc, l.gap, l.apart);
+                    if (c.on && l.in) z.store(dc, l.gap, l.apart, c.live);
                     dc += sd.h;
                     if (left > 1 && c.next(g, heads)) {
                         dc = d + c.b * sd.b + c.t * sd.t;
