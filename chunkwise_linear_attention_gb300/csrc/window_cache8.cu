@@ -30,14 +30,16 @@
 //
 // The factors of v's blocks may lie 2^184 apart, so no weight is taken together
 // with one.  The total is held against the running maximum m of the scores
-// alone.  A tile's weights go into its product as 2^(s - t + 14), t the largest
-// score of its 16 slots (to bf16's accuracy, which one round of shuffles for two heads
-// finds), in two fp16 parts: off by 2^-22 of themselves at most, or 2^-38 of the
-// tile's largest, and no number of the tile is 2^18 above another that e4m3 has
-// not rounded to zero.  (One part would leave 2^-11.)  The product is added to
-// the sums in fp32 times f 2^(t - m - 14); the sums are held at 2^-32 of their value, so
-// that they stay finite whatever the number of slots.  Weights below
-// 2^-126 of the largest count as nothing, as in any fp32 softmax.
+// alone.  A tile's weights go into its product as 2^(s - t + 15), t the largest
+// score of its 16 slots, in two fp16 parts: off by 2^-22 of themselves at most,
+// or 2^-40 of the tile's largest, and no number of the tile is 2^18 above
+// another that e4m3 has not rounded to zero.  (One part would leave 2^-11.)  Up
+// to four heads leave columns 4 to 7 of the product free: the second parts go
+// there, and one product does for both.  The
+// product is added to the sums in fp32 times f 2^(t - m - 15); the sums are held
+// at 2^-32 of their value, so that they stay finite whatever the number of
+// slots.  Weights below 2^-110 of the largest may count as nothing, much as in
+// any fp32 softmax.
 //
 // Measured on GB300: 64 x 32/8 x 128, window 4096, sinks 4, bf16: 91 us for 539
 // MB (5.9 TB/s, 87% of the measured copy rate); 2 x 32/4 x 128, window 65536:
@@ -317,29 +319,34 @@ __device__ __forceinline__ void add_times(float (&acc)[4], const float (&x)[4], 
 
 constexpr int kC8Stages = 4;  // tiles of a warp on their way
 
-template <int D, int NG>
+// NH query heads at once are the columns of NG products; four are in either half of one's.
+template <int NH>
+constexpr int c8_groups() { return NH <= 8 ? 1 : NH / 8; }
+template <int D, int NH>
 constexpr int c8_smem() {
-    return kStepWarps * (kC8Stages * 32 * D + 8 * NG * (D + 2) * 4);  // the ring of tiles, the parts of the result
+    return kStepWarps * (kC8Stages * 32 * D + 8 * c8_groups<NH>() * (D + 2) * 4);  // the ring of tiles, the parts of the result
 }
 template <int D>
 constexpr size_t c8_part(size_t G) {  // floats of a part: G heads' sums, their maxima and totals
     return G * (D + 2);
 }
 
-template <typename E, int D, int NG>
+template <typename E, int D, int NH>
 __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q, const E *__restrict__ k, const E *__restrict__ v,
                                                          uint8_t *kc, uint8_t *vc, float *kf, float *vf, E *__restrict__ o,
                                                          float *__restrict__ parts, Cut8 *__restrict__ cuts, WsHeader *hdr, Step8Args g) {
-    constexpr int NH = 8 * NG, KC = D / 64, M = D / 16, P = D / 16;  // 64-column pieces; products of 16 columns of o; pieces of a slot
+    constexpr int NG = c8_groups<NH>(), N = 8 * NG;  // columns
+    constexpr int KC = D / 64, M = D / 16, P = D / 16;  // 64-column pieces; products of 16 columns of o; pieces of a slot
+    constexpr bool HALVES = NH == 4;  // columns 4 to 7: the same heads, whose products take the weights' second parts
     constexpr bool BF = std::is_same<E, __nv_bfloat16>::value;
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) E s_new[2][D];
     __shared__ float s_top[2][kStepWarps];
     __shared__ unsigned s_sum[kStepWarps], s_at[2];
     char *const s_parts = smem + kStepWarps * kC8Stages * 32 * D;
-    float(*s_o)[NH][D] = reinterpret_cast<float(*)[NH][D]>(s_parts);
-    float(*s_m)[NH] = reinterpret_cast<float(*)[NH]>(s_parts + kStepWarps * NH * D * 4);
-    float(*s_l)[NH] = s_m + kStepWarps;
+    float(*s_o)[N][D] = reinterpret_cast<float(*)[N][D]>(s_parts);
+    float(*s_m)[N] = reinterpret_cast<float(*)[N]>(s_parts + kStepWarps * N * D * 4);
+    float(*s_l)[N] = s_m + kStepWarps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3, G = g.H / g.Hkv;
 
     if (blockIdx.x == 0 && threadIdx.x < (int)sizeof(WsHeader) / 4) reinterpret_cast<uint32_t *>(hdr)[threadIdx.x] = 0u;  // nothing waits
@@ -414,7 +421,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
     if (at < end) locate(), prefetch();
     while (at < end) {
         float *kfb = kf + ((long long)b * g.Hkv + hk) * g.blocks + first, *vfb = vf + ((long long)b * g.Hkv + hk) * g.blocks + first;
-        for (int h0 = 0; h0 < G; h0 += NH) {  // 16 heads at most, or the segment again (from L2)
+        for (int h0 = 0; h0 < G; h0 += NH) {  // NH heads at most, or the segment again (from L2)
             const int nh = min(NH, G - h0);
             if (h0 == 0 && threadIdx.x < 2 * P * 2) {  // the token's key and value
                 const int which = threadIdx.x / (2 * P), c = threadIdx.x % (2 * P);
@@ -430,7 +437,8 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 for (int c = 0; c < KC; ++c) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[c][i] = 0.f;
-                    if (8 * a + r < nh) load16(q + b * g.sq.b + (hk * G + h0 + 8 * a + r) * g.sq.h + 64 * c + 16 * j, x[c]);
+                    const int h = HALVES ? r & 3 : 8 * a + r;
+                    if (h < nh) load16(q + b * g.sq.b + (hk * G + h0 + h) * g.sq.h + 64 * c + 16 * j, x[c]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[c][i]));
                 }
@@ -494,59 +502,54 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 float2 by[NG];  // what the products of heads 2j, 2j + 1 are added with
 #pragma unroll
                 for (int a = 0; a < NG; ++a) {
-                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+                    float s[2][4] = {};  // two sums, so that products wait half as long for one another
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
                         const uint32_t w0[4] = {kx[0][c].x, kx[0][c].y, kx[0][c].z, kx[0][c].w};
                         const uint32_t w1[4] = {kx[1][c].x, kx[1][c].y, kx[1][c].z, kx[1][c].w};
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            mma16x8<false>(s, f16x2_of(w0[x]), f16x2_of(w1[x]), f16x2_of(w0[x] >> 16), f16x2_of(w1[x] >> 16),
+                            mma16x8<false>(s[x & 1], f16x2_of(w0[x]), f16x2_of(w1[x]), f16x2_of(w0[x] >> 16), f16x2_of(w1[x] >> 16),
                                            qf[a][c][2 * x], qf[a][c][2 * x + 1]);
                     }
-                    // s: (slot r, heads 2j, 2j + 1), (slot r + 8, the same heads); z: the weights' exponents
+                    // z: (slot r, heads 2j, 2j + 1), (slot r + 8, the same heads); top: the tile's largest
                     const float f0 = fac[a][0] * kfac, f1 = fac[a][1] * kfac;
-                    float z[4];
-                    auto exponents = [&](float by0, float by1) {
-                        z[0] = fmaf(s[0], f0, by0), z[1] = fmaf(s[1], f1, by1), z[2] = fmaf(s[2], f0, by0), z[3] = fmaf(s[3], f1, by1);
-                        if (left < 16) {
-                            if (r >= left) z[0] = z[1] = -INFINITY;
-                            if (r + 8 >= left) z[2] = z[3] = -INFINITY;
-                        }
-                    };
-                    exponents(-mu[a][0], -mu[a][1]);
-                    if (__any_sync(~0u, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > 8.f)) {
-                        exponents(0.f, 0.f);
+                    float z[4] = {(s[0][0] + s[1][0]) * f0, (s[0][1] + s[1][1]) * f1, (s[0][2] + s[1][2]) * f0, (s[0][3] + s[1][3]) * f1};
+                    if (left < 16) {
+                        if (r >= left) z[0] = z[1] = -INFINITY;
+                        if (r + 8 >= left) z[2] = z[3] = -INFINITY;
+                    }
+                    float top[2] = {fmaxf(z[0], z[2]), fmaxf(z[1], z[3])};
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) {
+                        top[0] = fmaxf(top[0], __shfl_xor_sync(~0u, top[0], x));
+                        top[1] = fmaxf(top[1], __shfl_xor_sync(~0u, top[1], x));
+                    }
+                    const float t0 = fmaxf(top[0], -FLT_MAX) - 15.f, t1 = fmaxf(top[1], -FLT_MAX) - 15.f;
+                    z[0] = ex2(z[0] - t0), z[1] = ex2(z[1] - t1), z[2] = ex2(z[2] - t0), z[3] = ex2(z[3] - t1);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t h = pack16<false>(make_float2(z[2 * x], z[2 * x + 1]));
+                        const float2 e = unpack16<false>(h);
+                        const uint32_t rest = pack16<false>(make_float2(z[2 * x] - e.x, z[2 * x + 1] - e.y));
+                        pw[a][x] = transpose8x8(HALVES && j >= 2 ? rest : h);
+                        if constexpr (!HALVES) pl[a][x] = transpose8x8(rest);
+                    }
+                    // behind the weights, which do not wait for it: the running maximum
+                    if (__any_sync(~0u, top[0] - mu[a][0] > 8.f || top[1] - mu[a][1] > 8.f)) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float top = fmaxf(z[e], z[2 + e]);
-#pragma unroll
-                            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-                            const float mn = fmaxf(mu[a][e], top), f = ex2(mu[a][e] - mn);
+                            const float mn = fmaxf(mu[a][e], top[e]), f = ex2(mu[a][e] - mn);
                             mu[a][e] = mn;
                             l[a][e] *= f;
 #pragma unroll
                             for (int y = 0; y < M; ++y) acc[a][y][e] *= f, acc[a][y][2 + e] *= f;
                         }
-                        exponents(-mu[a][0], -mu[a][1]);
                     }
-                    // the largest of the tile, off by 1 at most from -512 up, where it still weighs anything
-                    __nv_bfloat162 two = __floats2bfloat162_rn(fmaxf(z[0], z[2]), fmaxf(z[1], z[3]));
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) two = __hmax2(two, __shfl_xor_sync(~0u, two, x));
-                    const float t0 = fmaxf(__low2float(two), -512.f) - 14.f, t1 = fmaxf(__high2float(two), -512.f) - 14.f;
-                    z[0] = ex2(z[0] - t0), z[1] = ex2(z[1] - t1), z[2] = ex2(z[2] - t0), z[3] = ex2(z[3] - t1);
-                    const float e0 = ex2(t0), e1 = ex2(t1);
+                    const float e0 = ex2(t0 - mu[a][0]), e1 = ex2(t1 - mu[a][1]);
                     l[a][0] = fmaf(z[0] + z[2], e0, l[a][0]);
                     l[a][1] = fmaf(z[1] + z[3], e1, l[a][1]);
                     by[a] = make_float2(e0 * part, e1 * part);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t h = pack16<false>(make_float2(z[2 * x], z[2 * x + 1]));
-                        pw[a][x] = transpose8x8(h);
-                        const float2 e = unpack16<false>(h);
-                        pl[a][x] = transpose8x8(pack16<false>(make_float2(z[2 * x] - e.x, z[2 * x + 1] - e.y)));
-                    }
                 }
 #pragma unroll
                 for (int y = 0; y < D / 32; ++y) {
@@ -558,8 +561,10 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
 #pragma unroll
                     for (int a = 0; a < NG; ++a) {
                         float u[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma16x8<false>(u, f0, f1, f2, f3, pl[a][0], pl[a][1]);
-                        mma16x8<false>(w, f4, f5, f6, f7, pl[a][0], pl[a][1]);
+                        if constexpr (!HALVES) {
+                            mma16x8<false>(u, f0, f1, f2, f3, pl[a][0], pl[a][1]);
+                            mma16x8<false>(w, f4, f5, f6, f7, pl[a][0], pl[a][1]);
+                        }
                         mma16x8<false>(u, f0, f1, f2, f3, pw[a][0], pw[a][1]);
                         mma16x8<false>(w, f4, f5, f6, f7, pw[a][0], pw[a][1]);
                         add_times(acc[a][2 * y], u, by[a]);
@@ -613,7 +618,11 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
 #pragma unroll
                 for (int w = 0; w < kStepWarps; ++w) {
                     const float f = ex2(s_m[w][h] - mm);
-                    const float2 e = *reinterpret_cast<const float2 *>(&s_o[w][h][d]);
+                    float2 e = *reinterpret_cast<const float2 *>(&s_o[w][h][d]);
+                    if constexpr (HALVES) {
+                        const float2 rest = *reinterpret_cast<const float2 *>(&s_o[w][h + 4][d]);
+                        e.x += rest.x, e.y += rest.y;
+                    }
                     lt = fmaf(f, s_l[w][h], lt), x = fmaf(f, e.x, x), y = fmaf(f, e.y, y);
                 }
                 if (whole) {
@@ -715,34 +724,34 @@ int c8_check(const char *fn, int64_t B, int64_t H, int64_t Hkv, int64_t T, int64
 }
 
 // Blocks of the step that the current device runs at once, asked for once per device.
-template <typename E, int D, int NG>
+template <typename E, int D, int NH>
 int c8_resident(const char *fn, int *n) {
     static std::atomic<int> known[64];
     static std::atomic<unsigned long long> done{0};
-    constexpr int smem = c8_smem<D, NG>();
+    constexpr int smem = c8_smem<D, NH>();
     int dev = 0, sms = 0;
     CLA_CUDA_TRY(cudaGetDevice(&dev), fn);
     *n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
     if (*n != 0) return CLA_OK;
-    if (int st = set_max_dynamic_smem(done, (const void *)c8_step_kernel<E, D, NG>, smem)) return st;
+    if (int st = set_max_dynamic_smem(done, (const void *)c8_step_kernel<E, D, NH>, smem)) return st;
     if (int st = multiprocessors(fn, &sms)) return st;
-    CLA_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, c8_step_kernel<E, D, NG>, kStepWarps * 32, smem), fn);
+    CLA_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, c8_step_kernel<E, D, NH>, kStepWarps * 32, smem), fn);
     *n = *n * sms < kC8MaxBlocks ? *n * sms : kC8MaxBlocks;
     if (dev < 64) known[dev].store(*n, std::memory_order_relaxed);
     return CLA_OK;
 }
 
-template <typename E, int D, int NG>
+template <typename E, int D, int NH>
 int c8_step(const char *fn, const void *q, const void *k, const void *v, void *kc, void *vc, float *kf, float *vf, void *o,
             const Step8Args &g, void *ws, cudaStream_t s) {
     int n = 0;
-    if (int st = c8_resident<E, D, NG>(fn, &n)) return st;
+    if (int st = c8_resident<E, D, NH>(fn, &n)) return st;
     const long long most = (long long)g.B * g.Hkv * g.blocks;
     const unsigned grid = (unsigned)(most < n ? most : n);
     WsHeader *hdr = static_cast<WsHeader *>(ws);
     Cut8 *cuts = reinterpret_cast<Cut8 *>(hdr + 1);
     float *parts = reinterpret_cast<float *>(cuts + kC8MaxBlocks);
-    c8_step_kernel<E, D, NG><<<grid, kStepWarps * 32, c8_smem<D, NG>(), s>>>(
+    c8_step_kernel<E, D, NH><<<grid, kStepWarps * 32, c8_smem<D, NH>(), s>>>(
         (const E *)q, (const E *)k, (const E *)v, (uint8_t *)kc, (uint8_t *)vc, kf, vf, (E *)o, parts, cuts, hdr, g);
     if (int st = check_launch(fn)) return st;
     if (g.blocks == 1) return CLA_OK;  // nothing is cut
@@ -832,10 +841,15 @@ extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v
     const Step8Args g{pos,      scale * 1.4426950408889634f, window, sinks, sinks + window, (int)B, (int)H, (int)Hkv,
                       (int)((sinks + window + kC8Block - 1) / kC8Block), r[0], r[1], r[2]};
     cudaStream_t s = (cudaStream_t)stream;
-    const bool bf = dtype == CLA_BF16, wide = H / Hkv > 8;
-#define CLA_STEP8(E, D)                                                                                \
-    (wide ? c8_step<E, D, 2>(fn, q, k, v, kcache, vcache, kscale, vscale, o, g, ws, s) \
-          : c8_step<E, D, 1>(fn, q, k, v, kcache, vcache, kscale, vscale, o, g, ws, s))
+    // heads of a group at once: 16, 8, or 4 with both parts of the weights in one product (64 x 32/8, in graphs: x 128, window
+    // 4096 89 us, 91 with 8; x 64, window 8192 91 us, 95 with 8.  64 x 64/4 x 128, window 4096: 75 us with 16, 96 with 8,
+    // which reads the cache twice)
+    const bool bf = dtype == CLA_BF16;
+    const int64_t heads_of = H / Hkv;
+#define CLA_STEP8(E, D)                                                                                            \
+    (heads_of > 8   ? c8_step<E, D, 16>(fn, q, k, v, kcache, vcache, kscale, vscale, o, g, ws, s) \
+     : heads_of > 4 ? c8_step<E, D, 8>(fn, q, k, v, kcache, vcache, kscale, vscale, o, g, ws, s)  \
+                    : c8_step<E, D, 4>(fn, q, k, v, kcache, vcache, kscale, vscale, o, g, ws, s))
     if (d == 128) return bf ? CLA_STEP8(__nv_bfloat16, 128) : CLA_STEP8(__half, 128);
     return bf ? CLA_STEP8(__nv_bfloat16, 64) : CLA_STEP8(__half, 64);
 #undef CLA_STEP8
