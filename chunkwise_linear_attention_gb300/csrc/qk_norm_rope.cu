@@ -42,8 +42,10 @@
 namespace cla {
 namespace {
 
-// Blocks that run at once, for 152 multiprocessors: forward 2 for each, backward one (its lanes hold 16 sums of dw as well, up to
-// 159 registers; with 128 they went to local memory and the backward took some 100 us where it takes 62).
+// Blocks, chosen for a part with 152 multiprocessors, on which they all run at once: forward 2 for each, backward one (its lanes
+// hold 16 sums of dw as well, up to 159 registers; with 128 they went to local memory and the backward took some 100 us where
+// it takes 62).  Numbers of their own, not asked of the device: dw's sums are in an order that the sizes alone fix, and a part
+// with fewer multiprocessors takes two rounds.
 constexpr int kFwdThreads = 256, kFwdBlocks = 304, kBwdThreads = 384, kBwdBlocks = 152;
 
 struct QnArgs {
@@ -96,12 +98,10 @@ __device__ __forceinline__ void sincos_at(const unsigned long long *turn, int po
                     __uint_as_float(__float_as_uint(b.y) ^ (q[1] + 1u & 2u) << 30));
 }
 
-__device__ __forceinline__ float2 pair_f32(uint32_t u, float) { return make_float2(0.f, 0.f); }
 __device__ __forceinline__ float2 pair_f32(uint32_t u, __nv_bfloat16) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 __device__ __forceinline__ float2 pair_f32(uint32_t u, __half) { return __half22float2(reinterpret_cast<__half2 &>(u)); }
-__device__ __forceinline__ uint32_t pair_of(float2 v, float) { return 0u; }
 __device__ __forceinline__ uint32_t pair_of(float2 v, __nv_bfloat16) {
     const __nv_bfloat162 h = __float22bfloat162_rn(v);
     return reinterpret_cast<const uint32_t &>(h);
