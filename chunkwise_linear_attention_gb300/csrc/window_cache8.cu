@@ -41,14 +41,16 @@
 // slots.  Weights below 2^-110 of the largest may count as nothing, much as in
 // any fp32 softmax.
 //
-// Measured on GB300: 64 x 32/8 x 128, window 4096, sinks 4, bf16: 91 us for 539
+// Measured on GB300: 64 x 32/8 x 128, window 4096, sinks 4, bf16: 92 us for 539
 // MB (5.9 TB/s, 87% of the measured copy rate); 2 x 32/4 x 128, window 65536:
 // 33 us, of which the stream of 134 MB is 20 and the rest the start, the parts
-// and the join; 4 x 16/4, window 1024: 12 us.  Two thread blocks a
-// multiprocessor and tiles four deep: three with three or four deep 95 and 97
-// us, two of five and six deep 93 and 94.  Scores formed a block ahead of their
-// weights changed nothing (92 us), more shares than blocks that run at once
-// cost their starts (97 us at twice as many).
+// and the join; 4 x 16/4, window 1024: 12 us; 64 x 64/4 x 128, window 4096: 75 us for
+// 269 MB, where the products of 16 heads in two parts bound it.
+//   Against the first case's 91 us with weights in one part and the factors in
+// their exponents: two thread blocks a multiprocessor and tiles four deep; three
+// with three or four deep 95 and 97 us, two of five and six deep 93 and 94.
+// Scores formed a block ahead of their weights changed nothing (92 us), more
+// shares than blocks that run at once cost their starts (97 us at twice as many).
 #include <float.h>
 #include <math.h>
 
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
 }
 
 // Adds the parts of a cut (sequence, key head), for a query head of the group, in a fixed order: their common maximum first,
-// then every eighth part by a warp.  A block of it fits beside the step's two (32 registers; with 59 it did not, and the
+// then every eighth part by a warp.  A block of it fits beside the step's two (34 registers; with 59 it did not, and the
 // step took 2 us more).  It starts while the step still writes parts and cuts, so these are no memory that stays as it is
 // for the kernel's life: no __restrict__, and the wait keeps the loads behind it.
 template <typename E, int D>

@@ -857,7 +857,8 @@ int cla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq,
  * states that are updated in place (those that cla_delta_fwd leaves, S_T):
  *   S_t = a_t (I - beta_t k_t^T k_t) S_{t-1} + beta_t k_t^T v_t,  o_t = q_t S_t
  * The state is read and written once, however many tokens there are; prompts are
- * cla_delta_fwd's.
+ * cla_delta_fwd's.  Nothing of the state before is kept: a draft whose tokens may
+ * be rejected runs on a copy of it, or again from one with `lens` cut short.
  *   q, k   [B, Hk, T, dim_k] dtype (any cla_dtype);  v [B, H, T, dim_v] dtype.
  *          H is a multiple of Hk: value head h takes query and key head
  *          h / (H / Hk).  Keys are used as given.
