@@ -35,17 +35,17 @@
 // or 2^-40 of the tile's largest, and no number of the tile is 2^18 above
 // another that e4m3 has not rounded to zero.  (One part would leave 2^-11.)  Up
 // to four heads leave columns 4 to 7 of the product free: the second parts go
-// there, and one product does for both.  The
-// product is added to the sums in fp32 times f 2^(t - m - 15); the sums are held
-// at 2^-32 of their value, so that they stay finite whatever the number of
-// slots.  Weights below 2^-110 of the largest may count as nothing, much as in
-// any fp32 softmax.
+// there, and one product does for both.  The product is added to the sums in
+// fp32 times f 2^(t - m - 15); the sums are held at 2^-32 of their value, so that
+// they stay finite whatever the number of slots.  Weights below 2^-110 of the
+// largest may count as nothing, much as in any fp32 softmax, and 2^-90 of a sum
+// may be lost for every tile, where what is added leaves fp32's normal range.
 //
 // Measured on GB300: 64 x 32/8 x 128, window 4096, sinks 4, bf16: 92 us for 539
 // MB (5.9 TB/s, 87% of the measured copy rate); 2 x 32/4 x 128, window 65536:
 // 33 us, of which the stream of 134 MB is 20 and the rest the start, the parts
-// and the join; 4 x 16/4, window 1024: 12 us; 64 x 64/4 x 128, window 4096: 75 us for
-// 269 MB, where the products of 16 heads in two parts bound it.
+// and the join; 4 x 16/4, window 1024: 12 us; 64 x 64/4 x 128, window 4096: 75
+// us for 269 MB, where the products of 16 heads in two parts bound it.
 //   Against the first case's 91 us with weights in one part and the factors in
 // their exponents: two thread blocks a multiprocessor and tiles four deep; three
 // with three or four deep 95 and 97 us, two of five and six deep 93 and 94.

@@ -776,7 +776,8 @@ int cla_window_cache8_write(const void *k, const void *v, const int32_t *lens,
  * then holds, the token's own key and value included.  Other blocks are read
  * only.  Factors may lie as far apart as they can: what a block adds to a column
  * is rounded relative to itself, as in fp32 sums, whatever other blocks and
- * columns hold; weights below 2^-110 of the largest may count as nothing.
+ * columns hold; weights below 2^-110 of the largest may count as nothing, and
+ * 2^-90 for every 16 slots may be lost of any sum.
  * The arguments are cla_window_attn_step's, with the caches above; the order of
  * the sums is fixed by the sizes, the positions and the device model.
  * B * Hkv * ceil((sinks + window) / 64) is below 2^31, B * H below 2^27, H / Hkv
