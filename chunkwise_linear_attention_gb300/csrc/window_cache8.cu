@@ -44,7 +44,7 @@
 // Measured on GB300: 64 x 32/8 x 128, window 4096, sinks 4, bf16: 92 us for 539
 // MB (5.9 TB/s, 87% of the measured copy rate); 2 x 32/4 x 128, window 65536:
 // 33 us, of which the stream of 134 MB is 20 and the rest the start, the parts
-// and the join; 4 x 16/4, window 1024: 12 us; 64 x 64/4 x 128, window 4096: 75
+// and the join; 4 x 16/4, window 1024: 12 us; 64 x 64/4 x 128, window 4096: 71
 // us for 269 MB, where the products of 16 heads in two parts bound it.
 //   Against the first case's 91 us with weights in one part and the factors in
 // their exponents: two thread blocks a multiprocessor and tiles four deep; three
@@ -502,6 +502,7 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                 tile = tile + 32 * D == ring_end ? ring : tile + 32 * D;
                 uint32_t pw[NG][2], pl[NG][2];
                 float2 by[NG];  // what the products of heads 2j, 2j + 1 are added with
+                float most[NG][2], all[NG][2];  // the tile's largest score and its weights' sum
 #pragma unroll
                 for (int a = 0; a < NG; ++a) {
                     float s[2][4] = {};  // two sums, so that products wait half as long for one another
@@ -521,7 +522,8 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                         if (r >= left) z[0] = z[1] = -INFINITY;
                         if (r + 8 >= left) z[2] = z[3] = -INFINITY;
                     }
-                    float top[2] = {fmaxf(z[0], z[2]), fmaxf(z[1], z[3])};
+                    float(&top)[2] = most[a];
+                    top[0] = fmaxf(z[0], z[2]), top[1] = fmaxf(z[1], z[3]);
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) {
                         top[0] = fmaxf(top[0], __shfl_xor_sync(~0u, top[0], x));
@@ -537,8 +539,16 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                         pw[a][x] = transpose8x8(HALVES && j >= 2 ? rest : h);
                         if constexpr (!HALVES) pl[a][x] = transpose8x8(rest);
                     }
-                    // behind the weights, which do not wait for it: the running maximum
-                    if (__any_sync(~0u, top[0] - mu[a][0] > 8.f || top[1] - mu[a][1] > 8.f)) {
+                    all[a][0] = z[0] + z[2], all[a][1] = z[1] + z[3];
+                }
+                // behind the weights, which do not wait for it: the running maximum
+                bool up = false;
+#pragma unroll
+                for (int a = 0; a < NG; ++a) up = up || most[a][0] - mu[a][0] > 8.f || most[a][1] - mu[a][1] > 8.f;
+                if (__any_sync(~0u, up)) {
+#pragma unroll
+                    for (int a = 0; a < NG; ++a) {
+                        const float(&top)[2] = most[a];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const float mn = fmaxf(mu[a][e], top[e]), f = ex2(mu[a][e] - mn);
@@ -548,9 +558,13 @@ __global__ void __launch_bounds__(128, 2) c8_step_kernel(const E *__restrict__ q
                             for (int y = 0; y < M; ++y) acc[a][y][e] *= f, acc[a][y][2 + e] *= f;
                         }
                     }
-                    const float e0 = ex2(t0 - mu[a][0]), e1 = ex2(t1 - mu[a][1]);
-                    l[a][0] = fmaf(z[0] + z[2], e0, l[a][0]);
-                    l[a][1] = fmaf(z[1] + z[3], e1, l[a][1]);
+                }
+#pragma unroll
+                for (int a = 0; a < NG; ++a) {
+                    const float(&top)[2] = most[a];
+                    const float e0 = ex2(fmaxf(top[0], -FLT_MAX) - 15.f - mu[a][0]), e1 = ex2(fmaxf(top[1], -FLT_MAX) - 15.f - mu[a][1]);
+                    l[a][0] = fmaf(all[a][0], e0, l[a][0]);
+                    l[a][1] = fmaf(all[a][1], e1, l[a][1]);
                     by[a] = make_float2(e0 * part, e1 * part);
                 }
 #pragma unroll
@@ -844,7 +858,7 @@ extern "C" int cla_window_attn_step8(const void *q, const void *k, const void *v
                       (int)((sinks + window + kC8Block - 1) / kC8Block), r[0], r[1], r[2]};
     cudaStream_t s = (cudaStream_t)stream;
     // heads of a group at once: 16, 8, or 4 with both parts of the weights in one product (64 x 32/8, in graphs: x 128, window
-    // 4096 89 us, 91 with 8; x 64, window 8192 91 us, 95 with 8.  64 x 64/4 x 128, window 4096: 75 us with 16, 96 with 8,
+    // 4096 89 us, 91 with 8; x 64, window 8192 91 us, 95 with 8.  64 x 64/4 x 128, window 4096: 71 us with 16, 96 with 8,
     // which reads the cache twice)
     const bool bf = dtype == CLA_BF16;
     const int64_t heads_of = H / Hkv;
